@@ -12,11 +12,14 @@
 #include <vector>
 
 #include "gdn.h"
+#include "gdn_host.h"
 #include "gdn_internal.h"
 
-namespace {
+namespace gdn_host {
 
+namespace {
 thread_local std::string g_err;
+}
 
 gdn_status fail(gdn_status s, const char* fmt, ...) {
   char buf[512];
@@ -28,11 +31,10 @@ gdn_status fail(gdn_status s, const char* fmt, ...) {
   return s;
 }
 
-constexpr int CHUNK = gdn::CH;
+gdn_status hip_fail(hipError_t e, const char* what) {
+  return fail(GDN_E_HIP, "%s: %s", what, hipGetErrorString(e));
+}
 
-size_t align_up(size_t x) { return (x + 255) & ~size_t(255); }
-
-// Compute units of the current device, cached per device.
 int cu_count() {
   static int cache[64] = {0};
   int dev = 0;
@@ -44,6 +46,52 @@ int cu_count() {
   }
   return cache[dev];
 }
+
+// ---------------------------------------------------------------- per-kernel timing
+namespace {
+struct ProfTotal { const char* name; double ms; int n; };
+bool g_prof = false;
+std::vector<ProfRec> g_pending;
+std::vector<hipEvent_t> g_pool;
+std::vector<ProfTotal> g_totals;
+
+hipEvent_t prof_event() {
+  if (!g_pool.empty()) { hipEvent_t e = g_pool.back(); g_pool.pop_back(); return e; }
+  hipEvent_t e = nullptr;
+  if (hipEventCreate(&e) != hipSuccess) return nullptr;
+  return e;
+}
+
+// Set while an allocation-free call runs on this thread: no timing events are
+// created for it.
+thread_local bool t_noalloc = false;
+}  // namespace
+
+ProfRec prof_begin(const char* name, hipStream_t s) {
+  if (!g_prof || t_noalloc) return ProfRec{name, nullptr, nullptr, false, false};
+  ProfRec r{name, prof_event(), prof_event(), true, false};
+  r.ok_a = r.a && hipEventRecord(r.a, s) == hipSuccess;
+  return r;
+}
+
+void prof_end(ProfRec& r, hipStream_t s) {
+  if (!r.on) return;
+  const bool ok_b = r.b && hipEventRecord(r.b, s) == hipSuccess;
+  if (r.ok_a && ok_b) {
+    g_pending.push_back(r);
+  } else {  // an unrecorded pair is not timed; its events go back to the pool
+    if (r.a) g_pool.push_back(r.a);
+    if (r.b) g_pool.push_back(r.b);
+  }
+}
+
+}  // namespace gdn_host
+
+namespace {
+
+using namespace gdn_host;
+
+constexpr int CHUNK = gdn::CH;
 
 struct Plan {
   int N = 0;
@@ -61,8 +109,6 @@ bool supported(int dtype, int Dk, int Dv) {
   if (dtype == GDN_F32) return Dk == 64 && Dv == 64;
   return false;
 }
-
-bool aligned(const void* p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
 
 gdn_status check_prep(int qk_norm, int gate_act, const float* gate_scale) {
   if ((qk_norm != 0 && qk_norm != 1) || (gate_act != 0 && gate_act != 1))
@@ -201,49 +247,6 @@ Plan make_plan(const gdn_common_args& a, bool bwd, int cus, bool saved = false, 
   }
   p.total = off;
   return p;
-}
-
-template <class T>
-T* at(void* base, size_t off) { return reinterpret_cast<T*>(static_cast<char*>(base) + off); }
-
-// ---------------------------------------------------------------- per-kernel timing
-struct ProfRec { const char* name; hipEvent_t a, b; };
-struct ProfTotal { const char* name; double ms; int n; };
-bool g_prof = false;
-std::vector<ProfRec> g_pending;
-std::vector<hipEvent_t> g_pool;
-std::vector<ProfTotal> g_totals;
-
-hipEvent_t prof_event() {
-  if (!g_pool.empty()) { hipEvent_t e = g_pool.back(); g_pool.pop_back(); return e; }
-  hipEvent_t e = nullptr;
-  if (hipEventCreate(&e) != hipSuccess) return nullptr;
-  return e;
-}
-
-// Set while an allocation-free call runs on this thread: no timing events are
-// created for it.
-thread_local bool t_noalloc = false;
-
-// Launch through f() on stream s, bracketed by events when timing is enabled.
-template <class F>
-hipError_t timed(const char* name, hipStream_t s, F f) {
-  if (!g_prof || t_noalloc) return f();
-  ProfRec r{name, prof_event(), prof_event()};
-  const bool ok_a = r.a && hipEventRecord(r.a, s) == hipSuccess;
-  hipError_t e = f();
-  const bool ok_b = r.b && hipEventRecord(r.b, s) == hipSuccess;
-  if (ok_a && ok_b) {
-    g_pending.push_back(r);
-  } else {  // an unrecorded pair is not timed; its events go back to the pool
-    if (r.a) g_pool.push_back(r.a);
-    if (r.b) g_pool.push_back(r.b);
-  }
-  return e;
-}
-
-gdn_status hip_fail(hipError_t e, const char* what) {
-  return fail(GDN_E_HIP, "%s: %s", what, hipGetErrorString(e));
 }
 
 gdn::SeqInfo seq_info(const gdn_common_args& a, int segc) {
