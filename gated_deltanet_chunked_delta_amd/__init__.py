@@ -3,15 +3,20 @@
 The computation runs in hand-written HIP kernels behind the C ABI of
 ``include/gdn.h`` (``libgdn.so``); this package only marshals torch tensors
 into it.  ``chunk_gated_delta_rule`` wraps the two entry points in an
-autograd function.
+autograd function.  ``layers`` holds the operators a layer runs around the
+recurrence (short convolution, gated norm) and the selective scan.
 """
 from __future__ import annotations
 
 import torch
 
 from .binding import GDNError, gdn_chunk_bwd, gdn_chunk_fwd, gdn_decode_step, lib  # noqa: F401
+from .layers import (gated_group_norm, gdn_conv_bwd, gdn_conv_fwd, gdn_conv_step, gdn_norm_bwd,  # noqa: F401
+                     gdn_norm_fwd, gdn_scan_bwd, gdn_scan_fwd, gdn_scan_step, selective_scan, short_conv)
 
-__all__ = ["gdn_chunk_fwd", "gdn_chunk_bwd", "gdn_decode_step", "chunk_gated_delta_rule", "GDNError", "lib"]
+__all__ = ["gdn_chunk_fwd", "gdn_chunk_bwd", "gdn_decode_step", "chunk_gated_delta_rule", "GDNError", "lib",
+           "short_conv", "selective_scan", "gated_group_norm", "gdn_conv_fwd", "gdn_conv_bwd", "gdn_conv_step",
+           "gdn_scan_fwd", "gdn_scan_bwd", "gdn_scan_step", "gdn_norm_fwd", "gdn_norm_bwd"]
 
 
 class _ChunkGatedDeltaRule(torch.autograd.Function):

@@ -17,7 +17,8 @@ LIB = os.path.join(HERE, "libgdn.so")
 # The same kernels with per-phase cycle counters (bench.py --phase-clock)
 LIB_CLOCK = os.path.join(HERE, "libgdn_clock.so")
 OBJ = os.path.join(HERE, "_build")
-SOURCES = ["gdn_api.hip", "gdn_plan.hip", "gdn_tsolve.hip", "gdn_fwd.hip", "gdn_bwd.hip", "gdn_decode.hip"]
+SOURCES = ["gdn_api.hip", "gdn_plan.hip", "gdn_tsolve.hip", "gdn_fwd.hip", "gdn_bwd.hip", "gdn_decode.hip",
+           "layer/gdn_conv.hip", "layer/gdn_scan.hip", "layer/gdn_norm.hip", "layer/gdn_layer_api.hip"]
 ARCH = os.environ.get("GDN_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", INC, "-I", CSRC,
@@ -32,7 +33,7 @@ SAN_FLAGS = ["-Xarch_host", "-fsanitize=address", "-Xarch_host", "-fsanitize=und
 
 
 def _compile(src: str, obj_dir: str = OBJ, extra=()) -> str:
-    obj = os.path.join(obj_dir, src.replace(".hip", ".o"))
+    obj = os.path.join(obj_dir, os.path.basename(src).replace(".hip", ".o"))
     cmd = ["hipcc", "-c", *FLAGS, *extra, os.path.join(CSRC, src), "-o", obj]
     r = subprocess.run(cmd, capture_output=True, text=True)
     if r.returncode != 0:

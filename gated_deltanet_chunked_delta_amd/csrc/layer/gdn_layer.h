@@ -1,0 +1,244 @@
+// gdn_layer.h -- parameter blocks and launchers of the operators around the
+// recurrence: short causal convolution, selective state space scan, gated
+// group norm (not part of the ABI).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include "gdn.h"
+#include "gdn_device.h"
+#include "gdn_internal.h"
+
+namespace gdn {
+
+// ---------------------------------------------------------------- vectors of V elements
+template <class E, int V> struct VecIO;
+template <class E> struct VecIO<E, 1> {
+  typedef E raw;
+  static __device__ __forceinline__ raw load(const E* p) { return *p; }
+  static __device__ __forceinline__ raw zero() { return to_e<E>(0.f); }
+  static __device__ __forceinline__ void get(raw r, float (&f)[1]) { f[0] = to_f(r); }
+  static __device__ __forceinline__ void store(E* p, const float (&f)[1]) { *p = to_e<E>(f[0]); }
+};
+template <> struct VecIO<bf16, 8> {
+  typedef bf16x8 raw;
+  static __device__ __forceinline__ raw load(const bf16* p) { return *reinterpret_cast<const bf16x8*>(p); }
+  static __device__ __forceinline__ raw zero() { return raw{}; }
+  static __device__ __forceinline__ void get(const raw& r, float (&f)[8]) {
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (float)r[i];
+  }
+  static __device__ __forceinline__ void store(bf16* p, const float (&f)[8]) {
+    *reinterpret_cast<bf16x8*>(p) = bf16x8{(bf16)f[0], (bf16)f[1], (bf16)f[2], (bf16)f[3],
+                                           (bf16)f[4], (bf16)f[5], (bf16)f[6], (bf16)f[7]};
+  }
+};
+template <> struct VecIO<float, 4> {
+  typedef f32x4 raw;
+  static __device__ __forceinline__ raw load(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
+  static __device__ __forceinline__ raw zero() { return zero4(); }
+  static __device__ __forceinline__ void get(const raw& r, float (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = r[i];
+  }
+  static __device__ __forceinline__ void store(float* p, const float (&f)[4]) {
+    *reinterpret_cast<f32x4*>(p) = f32x4{f[0], f[1], f[2], f[3]};
+  }
+};
+// Elements of one 16-byte access.
+template <class E> constexpr int kVec = 16 / (int)sizeof(E);
+
+// ---------------------------------------------------------------- short causal convolution
+struct ConvParams {
+  const void* x;             // [tokens][D], x_stride elements between tokens
+  int64_t x_stride;
+  const void* w;             // [D][W]
+  const void* bias;          // nullable [D]
+  const void* init;          // nullable [N][W-1][D]
+  const int32_t* cu;         // nullable [N+1]
+  int B, T, D, N, silu;
+  int64_t tokens;            // B * T
+  int run;                   // tokens per thread
+  int64_t nruns;
+  // forward
+  void* y;                   // [tokens][D]
+  void* fin;                 // nullable [N][W-1][D]
+  // backward
+  const void* dy;            // [tokens][D]
+  const void* dfin;          // nullable [N][W-1][D]
+  void* dx;                  // [tokens][D]
+  void* dw;                  // [D][W]
+  void* dbias;               // nullable [D]
+  void* dinit;               // nullable [N][W-1][D]
+  float* part;               // [nruns][W+1][D] partial sums of dw and dbias
+};
+struct ConvStepParams {
+  const void* x;             // [N][D]
+  int64_t x_stride;
+  void* state;               // [slots][W-1][D], shifted in place
+  const int32_t* state_idx;
+  int num_slots;
+  const void* w;
+  const void* bias;
+  void* y;
+  int N, D, silu;
+};
+// vec: 16-byte accesses are possible (D, strides and pointers allow them)
+hipError_t launch_conv_fwd(int dtype, int W, bool vec, const ConvParams& p, hipStream_t st);
+hipError_t launch_conv_bwd(int dtype, int W, bool vec, const ConvParams& p, hipStream_t st);
+hipError_t launch_conv_dw(int dtype, int W, const ConvParams& p, hipStream_t st);
+hipError_t launch_conv_step(int dtype, int W, bool vec, const ConvStepParams& p, hipStream_t st);
+
+// ---------------------------------------------------------------- gated group norm
+struct NormParams {
+  const void* x;             // [R][G][D], x_stride elements between tokens
+  int64_t x_stride;
+  const void* z;             // nullable gate, z_stride
+  int64_t z_stride;
+  const void* w;             // [G][D], or [D] with shared
+  const void* bias;          // nullable, like w
+  int64_t R;
+  int G, D, shared, center, gate_first;
+  float eps;
+  void* y;                   // [R][G][D]
+  const void* dy;            // [R][G][D]
+  void* dx;
+  void* dz;                  // nullable (no gate)
+  void* dw;
+  void* dbias;               // nullable
+  float* part;               // [weight groups][blocks][1 or 2][D]
+  int blocks;                // workgroups per weight group (backward)
+};
+hipError_t launch_norm_fwd(int dtype, bool vec, const NormParams& p, hipStream_t st);
+hipError_t launch_norm_bwd(int dtype, bool vec, const NormParams& p, hipStream_t st);
+
+// ---------------------------------------------------------------- selective state space scan
+constexpr int PS = 64;       // value columns of one slice: a head of Dv columns is Dv / PS slices
+
+// One sweep over the tokens of every segment, forwards or backwards in time,
+// with a Dk x PS slice of the state per (segment, head, slice):
+//   state <- decay * state + sw_t K_t V_t^T
+//   out1_t = tw_t (state^T Q_t) + D_h V_t          (a value row)
+//   out2_t = tw_t (state W_t)                      (a key row, one part per slice)
+//   rt_t   = Q_t . (state before token t) W_t      (the decay gradient's row term)
+// Forwards in time K = B, Q = C, V = x, W = dy, sw = step, tw = 1: out1 = y,
+// out2 = dC.  Backwards K = C, Q = B, V = dy, W = x, sw = 1, tw = step:
+// out1 = dx, out2 = dB.
+struct SweepParams {
+  const void* q;             // [tokens][G][Dk]
+  const void* k;
+  int64_t q_stride, k_stride;
+  const void* v;             // [tokens][H][Dv]
+  const void* w;
+  int64_t v_stride, w_stride;
+  const void* dt;            // [tokens][H]
+  int64_t dt_stride;
+  int dt_f32, softplus;
+  const float* dt_bias;      // nullable [H]
+  const float* A;            // [H]
+  const float* D;            // nullable [H]
+  int H, G, Dk, Dv;
+  int64_t tokens;
+  SeqInfo seq;
+  const SegDesc* segs;
+  const int* seg_first;
+  const float* s_in;         // nullable: state entering each segment (by segment when per_seg, else by sequence)
+  int per_seg;
+  float* s_end;              // nullable: state leaving the last segment of each sequence in sweep order [N][H][Dk][Dv]
+  float* s_loc;              // sweeps without output: each segment's own end state [nseg][H][Dk][Dv]
+  float* s_dec;              // and its total decay [nseg][H]
+  void* out1;                // [tokens][H][Dv]
+  float* out2;               // [parts][tokens][Dk]
+  float* rt;                 // [H * Dv / PS][tokens]
+  float* xd;                 // nullable [H * Dv / PS][tokens]: x_t . dy_t over the slice
+  float* cb;                 // nullable [G][tokens]: C_t . B_t
+  // anchor of the decay gradient: <end state, gradient of the end state> of each segment
+  const float* g_end;        // nullable: as s_in, for the other direction
+  int g_per_seg;
+  float* anchor;             // [nseg][H * Dv / PS]
+};
+
+struct ScanJoinParams {      // end states of the segments -> states entering them
+  float* s_loc;
+  const float* s_dec;
+  const float* s0;           // nullable [N][H][Dk][Dv]
+  int H, Dk, Dv, rev;
+  SeqInfo seq;
+  const SegDesc* segs;
+  const int* seg_first;
+  int N;
+};
+
+struct ScanGradParams {      // ddt, dA, dD, ddt_bias from the row terms
+  const void* dt;
+  int64_t dt_stride;
+  int dt_f32, softplus;
+  const float* dt_bias;
+  const float* A;
+  int H, G, Dk, Dv;
+  int64_t tokens;
+  SeqInfo seq;
+  const SegDesc* segs;
+  const int* seg_first;
+  const float* rt;           // forward sweep's row terms [slices][tokens]
+  const float* ct;           // backward sweep's
+  const float* xd;
+  const float* cb;
+  const float* anchor;       // nullable
+  void* ddt;                 // [tokens][H], dtype of dt
+  float* part;               // [nseg][H][3]
+  float* dA;
+  float* dD;                 // nullable
+  float* ddt_bias;           // nullable
+};
+
+struct ScanReduceParams {    // parts of dB or dC -> sums over a group's slices
+  const float* part;         // [G * parts per group][tokens][Dk]
+  void* out;                 // [tokens][G][Dk]
+  int G, ppg, Dk;
+  int64_t tokens;
+  SeqInfo seq;
+  const SegDesc* segs;
+};
+
+struct ScanStepParams {
+  const void* x;             // [N][H][Dv]
+  const void* dt;            // [N][H]
+  const void* b;             // [N][G][Dk]
+  const void* c;
+  int64_t x_stride, dt_stride, b_stride, c_stride;
+  const float* A;
+  const float* D;
+  const float* dt_bias;
+  int dt_f32, softplus;
+  float* state;              // [slots][H][Dk][Dv]
+  const int32_t* state_idx;
+  int num_slots;
+  void* y;                   // [N][H][Dv]
+  int N, H, G;
+};
+
+// Outputs of a sweep.
+enum { SWEEP_STATE = 0, SWEEP_VALUE = 1, SWEEP_KEY = 2 };
+hipError_t launch_sweep(int dtype, int rev, int mode, const SweepParams& p, int nseg, hipStream_t st);
+hipError_t launch_scan_join(const ScanJoinParams& p, hipStream_t st);
+hipError_t launch_scan_grad(const ScanGradParams& p, int nseg, hipStream_t st);
+hipError_t launch_scan_reduce(int dtype, const ScanReduceParams& p, hipStream_t st);
+hipError_t launch_scan_step(int dtype, int Dk, int Dv, const ScanStepParams& p, hipStream_t st);
+// Parts of out2 per group of heads that a key sweep writes.
+int sweep_parts_per_group(int dtype, int H, int G, int Dv);
+
+// Step size and log decay of one token and head.
+__device__ __forceinline__ float scan_dt_raw(const void* dt, int f32, int64_t i) {
+  return f32 ? static_cast<const float*>(dt)[i] : to_f(static_cast<const bf16*>(dt)[i]);
+}
+// softplus as max(x, 0) + log1p(exp(-|x|)); the accurate exp and log: a step of
+// 1e-3 keeps its relative precision, and it is formed once per token and head.
+__device__ __forceinline__ float scan_softplus(float x) { return fmaxf(x, 0.f) + log1pf(expf(-fabsf(x))); }
+template <class P>
+__device__ __forceinline__ float scan_step_size(const P& p, int64_t row, int h) {
+  const float raw = scan_dt_raw(p.dt, p.dt_f32, row * p.dt_stride + h) + (p.dt_bias ? p.dt_bias[h] : 0.f);
+  return p.softplus ? scan_softplus(raw) : raw;
+}
+
+}  // namespace gdn

@@ -1,0 +1,424 @@
+// gdn_norm.hip -- gated group norm, channels last: every token's G groups of D
+// channels are normalised on their own.
+//
+//   v = x                      (gate after the norm, or no gate)
+//     = x silu(z)              (gate before it)
+//   n = (v - mean) / sqrt(mean((v - mean)^2) + eps),   mean = 0 unless centred
+//   o = n w + bias,   y = o silu(z) (gate after) or o
+//
+// Bound: memory -- x, z read and y written once (backward: x, z, dy read, dx,
+// dz written).  A row (token and group) is held in registers by TPR threads,
+// NV 16-byte vectors each, so that statistics, output and gradients take one
+// read; TPR is the smallest power of two that covers the row with as few
+// vectors as possible, so several short rows (a head of 64 or 128 channels)
+// share a wave.  Rows too long for that are re-read by a whole workgroup.
+#include "gdn_layer.h"
+
+namespace gdn {
+
+namespace {
+
+constexpr int NORM_NT = 256;
+
+__device__ __forceinline__ float silu_n(float u) { return u * sigmoid_f(u); }
+
+// Sum over the TPR threads of a row, in each of them.  red: one float per wave.
+template <int TPR>
+__device__ __forceinline__ float row_sum(float x, float* red) {
+#pragma unroll
+  for (int o = 1; o < (TPR < 64 ? TPR : 64); o <<= 1) x += __shfl_xor(x, o, 64);
+  if (TPR > 64) {
+    __syncthreads();
+    if (lane_id() == 0) red[wave_id()] = x;
+    __syncthreads();
+    x = 0.f;
+#pragma unroll
+    for (int w = 0; w < NORM_NT / 64; ++w) x += red[w];
+  }
+  return x;
+}
+
+template <class E, int V, int TPR, int NV>
+struct NormRow {
+  float v[NV][V];  // x
+  float z[NV][V];  // gate input
+  template <class P>
+  __device__ __forceinline__ void load(const P& p, int64_t tok, int g, int lane) {
+    typedef VecIO<E, V> IO;
+    const E* xp = static_cast<const E*>(p.x) + tok * p.x_stride + (int64_t)g * p.D;
+    const E* zp = static_cast<const E*>(p.z) + tok * p.z_stride + (int64_t)g * p.D;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + lane) * V;
+      if (c < p.D) {
+        IO::get(IO::load(xp + c), v[i]);
+        if (p.z) IO::get(IO::load(zp + c), z[i]);
+      } else {
+#pragma unroll
+        for (int e = 0; e < V; ++e) v[i][e] = z[i][e] = 0.f;
+      }
+    }
+  }
+};
+
+template <class E, int V, int TPR, int NV>
+__global__ __launch_bounds__(NORM_NT) void norm_fwd_kernel(NormParams p) {
+  typedef VecIO<E, V> IO;
+  __shared__ float red[NORM_NT / 64];
+  const int lane = threadIdx.x % TPR;
+  const int64_t rows = p.R * p.G;
+  int64_t r = blockIdx.x * (int64_t)(NORM_NT / TPR) + threadIdx.x / TPR;
+  const bool live = r < rows;
+  r = min(r, rows - 1);
+  const int64_t tok = r / p.G;
+  const int g = (int)(r - tok * p.G);
+  NormRow<E, V, TPR, NV> a;
+  a.load(p, tok, g, lane);
+  const bool before = p.z && p.gate_first, after = p.z && !p.gate_first;
+  const float inv = 1.f / p.D;
+  float s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i)
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      if (before) a.v[i][e] *= silu_n(a.z[i][e]);
+      s += a.v[i][e];
+    }
+  float mean = 0.f;
+  if (p.center) mean = row_sum<TPR>(s, red) * inv;
+  s = 0.f;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const bool in = (i * TPR + lane) * V < p.D;
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      a.v[i][e] = in ? a.v[i][e] - mean : 0.f;
+      s += a.v[i][e] * a.v[i][e];
+    }
+  }
+  const float rstd = 1.f / sqrtf(row_sum<TPR>(s, red) * inv + p.eps);
+  if (!live) return;
+  const int64_t wo = p.shared ? 0 : (int64_t)g * p.D;
+  E* yp = static_cast<E*>(p.y) + r * p.D;
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * TPR + lane) * V;
+    if (c >= p.D) continue;
+    float w[V], b[V], y[V];
+    IO::get(IO::load(static_cast<const E*>(p.w) + wo + c), w);
+    if (p.bias) IO::get(IO::load(static_cast<const E*>(p.bias) + wo + c), b);
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      y[e] = a.v[i][e] * rstd * w[e];
+      if (p.bias) y[e] += b[e];
+      if (after) y[e] *= silu_n(a.z[i][e]);
+    }
+    IO::store(yp + c, y);
+  }
+}
+
+// Gradient.  With do = dy silu(z) (gate after) or dy, dn = do w:
+//   dv = (dn - n mean(dn n) - [centred] mean(dn)) rstd
+//   dx = dv (silu(z) with the gate before),  dw = sum do n,  dbias = sum do
+//   dz = silu'(z) (dv x  with the gate before,  dy o  after it)
+// p.blocks workgroups per weight group walk that group's rows, each thread
+// always on the same columns, and keep dw and dbias in registers; their parts
+// are joined by norm_dw_kernel in a fixed order.
+template <class E, int V, int TPR, int NV>
+__global__ __launch_bounds__(NORM_NT) void norm_bwd_kernel(NormParams p) {
+  typedef VecIO<E, V> IO;
+  constexpr int RPB = NORM_NT / TPR;
+  __shared__ float red[NORM_NT / 64];
+  __shared__ float cols[RPB > 1 ? RPB * TPR * V : 1];
+  const int lane = threadIdx.x % TPR, sub = threadIdx.x / TPR;
+  const int wg = p.shared ? 0 : blockIdx.x / p.blocks, blk = blockIdx.x % p.blocks;
+  const int64_t rows = p.shared ? p.R * p.G : p.R;  // of this weight group
+  const bool before = p.z && p.gate_first, after = p.z && !p.gate_first;
+  const float inv = 1.f / p.D;
+  float w[NV][V], b[NV][V], dw[NV][V] = {}, db[NV][V] = {};
+#pragma unroll
+  for (int i = 0; i < NV; ++i) {
+    const int c = (i * TPR + lane) * V;
+#pragma unroll
+    for (int e = 0; e < V; ++e) w[i][e] = b[i][e] = 0.f;
+    if (c < p.D) {
+      IO::get(IO::load(static_cast<const E*>(p.w) + (int64_t)wg * p.D + c), w[i]);
+      if (p.bias) IO::get(IO::load(static_cast<const E*>(p.bias) + (int64_t)wg * p.D + c), b[i]);
+    }
+  }
+  for (int64_t base = (int64_t)blk * RPB; base < rows; base += (int64_t)p.blocks * RPB) {
+    const int64_t rr = min(base + sub, rows - 1);
+    const bool live = base + sub < rows;
+    const int64_t tok = p.shared ? rr / p.G : rr;
+    const int g = p.shared ? (int)(rr - tok * p.G) : wg;
+    const int64_t off = (tok * p.G + g) * p.D;
+    NormRow<E, V, TPR, NV> a;
+    a.load(p, tok, g, lane);
+    float gy[NV][V];
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + lane) * V;
+#pragma unroll
+      for (int e = 0; e < V; ++e) gy[i][e] = 0.f;
+      if (c < p.D) IO::get(IO::load(static_cast<const E*>(p.dy) + off + c), gy[i]);
+    }
+    float n[NV][V];
+    float s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        n[i][e] = before ? a.v[i][e] * silu_n(a.z[i][e]) : a.v[i][e];
+        s += n[i][e];
+      }
+    float mean = 0.f;
+    if (p.center) mean = row_sum<TPR>(s, red) * inv;
+    s = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const bool in = (i * TPR + lane) * V < p.D;
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        n[i][e] = in ? n[i][e] - mean : 0.f;
+        s += n[i][e] * n[i][e];
+      }
+    }
+    const float rstd = 1.f / sqrtf(row_sum<TPR>(s, red) * inv + p.eps);
+    float c1 = 0.f, c2 = 0.f;
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        n[i][e] *= rstd;
+        const float dout = after ? gy[i][e] * silu_n(a.z[i][e]) : gy[i][e];
+        const float dn = dout * w[i][e];
+        c1 += dn * n[i][e];
+        c2 += dn;
+        if (live) {
+          dw[i][e] += dout * n[i][e];
+          db[i][e] += dout;
+        }
+      }
+    c1 = row_sum<TPR>(c1, red) * inv;
+    c2 = p.center ? row_sum<TPR>(c2, red) * inv : 0.f;
+    if (live) {
+#pragma unroll
+      for (int i = 0; i < NV; ++i) {
+        const int c = (i * TPR + lane) * V;
+        if (c >= p.D) continue;
+        float dx[V], dz[V];
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float sg = p.z ? sigmoid_f(a.z[i][e]) : 0.f, act = a.z[i][e] * sg;
+          const float dn = (after ? gy[i][e] * act : gy[i][e]) * w[i][e];
+          const float dv = (dn - n[i][e] * c1 - c2) * rstd;
+          dx[e] = before ? dv * act : dv;
+          const float dact = before ? dv * a.v[i][e] : gy[i][e] * (n[i][e] * w[i][e] + b[i][e]);
+          dz[e] = dact * sg * (1.f + a.z[i][e] * (1.f - sg));
+        }
+        IO::store(static_cast<E*>(p.dx) + off + c, dx);
+        if (p.z) IO::store(static_cast<E*>(p.dz) + off + c, dz);
+      }
+    }
+  }
+  // this workgroup's column sums: over its RPB rows' threads, then out
+  const int kinds = p.dbias ? 2 : 1;
+  float* part = p.part + ((int64_t)wg * p.blocks + blk) * kinds * p.D;
+  for (int kind = 0; kind < kinds; ++kind) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      const int c = (i * TPR + lane) * V;
+      float s[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) s[e] = kind ? db[i][e] : dw[i][e];
+      if (RPB > 1) {
+        __syncthreads();
+#pragma unroll
+        for (int e = 0; e < V; ++e) cols[(sub * V + e) * TPR + lane] = s[e];
+        __syncthreads();
+        if (sub == 0) {
+#pragma unroll
+          for (int e = 0; e < V; ++e) {
+            s[e] = 0.f;
+            for (int r = 0; r < RPB; ++r) s[e] += cols[(r * V + e) * TPR + lane];
+          }
+        }
+      }
+      if (sub == 0 && c < p.D) {
+#pragma unroll
+        for (int e = 0; e < V; ++e) part[(int64_t)kind * p.D + c + e] = s[e];
+      }
+    }
+  }
+}
+
+// Rows too long for registers: a workgroup per row re-reads it for each pass.
+template <class E>
+struct LongRow {
+  const E *x, *z, *w, *b, *dy;
+  bool before, after;
+  float mean, rstd;
+  __device__ __forceinline__ float gated(int c) const {
+    const float v = to_f(x[c]);
+    return before ? v * silu_n(to_f(z[c])) : v;
+  }
+  __device__ __forceinline__ void stats(const NormParams& p, float* red) {
+    const float inv = 1.f / p.D;
+    mean = 0.f;
+    float s = 0.f;
+    if (p.center) {
+      for (int c = threadIdx.x; c < p.D; c += NORM_NT) s += gated(c);
+      mean = row_sum<NORM_NT>(s, red) * inv;
+      s = 0.f;
+    }
+    for (int c = threadIdx.x; c < p.D; c += NORM_NT) {
+      const float v = gated(c) - mean;
+      s += v * v;
+    }
+    rstd = 1.f / sqrtf(row_sum<NORM_NT>(s, red) * inv + p.eps);
+  }
+};
+template <class E>
+__device__ __forceinline__ LongRow<E> long_row(const NormParams& p, int64_t tok, int g) {
+  LongRow<E> a;
+  a.x = static_cast<const E*>(p.x) + tok * p.x_stride + (int64_t)g * p.D;
+  a.z = static_cast<const E*>(p.z) + (p.z ? tok * p.z_stride + (int64_t)g * p.D : 0);
+  const int64_t wo = p.shared ? 0 : (int64_t)g * p.D;
+  a.w = static_cast<const E*>(p.w) + wo;
+  a.b = p.bias ? static_cast<const E*>(p.bias) + wo : nullptr;
+  a.dy = p.dy ? static_cast<const E*>(p.dy) + (tok * p.G + g) * p.D : nullptr;
+  a.before = p.z && p.gate_first;
+  a.after = p.z && !p.gate_first;
+  return a;
+}
+
+template <class E>
+__global__ __launch_bounds__(NORM_NT) void norm_fwd_long_kernel(NormParams p) {
+  __shared__ float red[NORM_NT / 64];
+  const int64_t r = blockIdx.x, tok = r / p.G;
+  LongRow<E> a = long_row<E>(p, tok, (int)(r - tok * p.G));
+  a.stats(p, red);
+  E* y = static_cast<E*>(p.y) + r * p.D;
+  for (int c = threadIdx.x; c < p.D; c += NORM_NT) {
+    float o = (a.gated(c) - a.mean) * a.rstd * to_f(a.w[c]);
+    if (a.b) o += to_f(a.b[c]);
+    if (a.after) o *= silu_n(to_f(a.z[c]));
+    y[c] = to_e<E>(o);
+  }
+}
+
+template <class E>
+__global__ __launch_bounds__(NORM_NT) void norm_bwd_long_kernel(NormParams p) {
+  __shared__ float red[NORM_NT / 64];
+  const int wg = p.shared ? 0 : blockIdx.x / p.blocks, blk = blockIdx.x % p.blocks;
+  const int64_t rows = p.shared ? p.R * p.G : p.R;
+  const float inv = 1.f / p.D;
+  const int kinds = p.dbias ? 2 : 1;
+  float* part = p.part + ((int64_t)wg * p.blocks + blk) * kinds * p.D;  // thread-owned columns
+  for (int c = threadIdx.x; c < p.D; c += NORM_NT)
+    for (int k = 0; k < kinds; ++k) part[(int64_t)k * p.D + c] = 0.f;
+  for (int64_t r = blk; r < rows; r += p.blocks) {
+    const int64_t tok = p.shared ? r / p.G : r;
+    const int g = p.shared ? (int)(r - tok * p.G) : wg;
+    LongRow<E> a = long_row<E>(p, tok, g);
+    a.stats(p, red);
+    float c1 = 0.f, c2 = 0.f;
+    for (int c = threadIdx.x; c < p.D; c += NORM_NT) {
+      const float gd = to_f(a.dy[c]) * (a.after ? silu_n(to_f(a.z[c])) : 1.f);
+      const float n = (a.gated(c) - a.mean) * a.rstd, dn = gd * to_f(a.w[c]);
+      c1 += dn * n;
+      c2 += dn;
+      part[c] += gd * n;
+      if (p.dbias) part[p.D + c] += gd;
+    }
+    c1 = row_sum<NORM_NT>(c1, red) * inv;
+    c2 = p.center ? row_sum<NORM_NT>(c2, red) * inv : 0.f;
+    E* dx = static_cast<E*>(p.dx) + (tok * p.G + g) * p.D;
+    E* dz = p.z ? static_cast<E*>(p.dz) + (tok * p.G + g) * p.D : nullptr;
+    for (int c = threadIdx.x; c < p.D; c += NORM_NT) {
+      const float z = p.z ? to_f(a.z[c]) : 0.f, sg = sigmoid_f(z), act = z * sg, dy = to_f(a.dy[c]);
+      const float n = (a.gated(c) - a.mean) * a.rstd;
+      const float dn = (a.after ? dy * act : dy) * to_f(a.w[c]);
+      const float dv = (dn - n * c1 - c2) * a.rstd;
+      dx[c] = to_e<E>(a.before ? dv * act : dv);
+      if (dz) {
+        const float dact = a.before ? dv * to_f(a.x[c]) : dy * (n * to_f(a.w[c]) + (a.b ? to_f(a.b[c]) : 0.f));
+        dz[c] = to_e<E>(dact * sg * (1.f + z * (1.f - sg)));
+      }
+    }
+  }
+}
+
+// dw and dbias: sums of the workgroups' parts, 32 columns a workgroup, eight
+// threads a column.
+template <class E>
+__global__ __launch_bounds__(NORM_NT) void norm_dw_kernel(NormParams p) {
+  __shared__ float red[8][33];
+  const int kinds = p.dbias ? 2 : 1;
+  const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
+  const int64_t cols = (int64_t)kinds * p.D, col = blockIdx.x * 32ll + cl;
+  const int wg = blockIdx.y;
+  float s = 0.f;
+  if (col < cols)
+    for (int b = rl; b < p.blocks; b += 8) s += p.part[((int64_t)wg * p.blocks + b) * cols + col];
+  red[rl][cl] = s;
+  __syncthreads();
+  if (rl == 0 && col < cols) {
+    s = 0.f;
+#pragma unroll
+    for (int r = 0; r < 8; ++r) s += red[r][cl];
+    if (col < p.D) static_cast<E*>(p.dw)[(int64_t)wg * p.D + col] = to_e<E>(s);
+    else static_cast<E*>(p.dbias)[(int64_t)wg * p.D + col - p.D] = to_e<E>(s);
+  }
+}
+
+template <class E, int V, int TPR, int NV>
+hipError_t norm_run(const NormParams& p, bool bwd, hipStream_t st) {
+  const int64_t rows = p.R * p.G;
+  if (bwd) {
+    hipLaunchKernelGGL((norm_bwd_kernel<E, V, TPR, NV>), dim3(p.blocks * (p.shared ? 1 : p.G)), dim3(NORM_NT), 0, st, p);
+  } else {
+    constexpr int RPB = NORM_NT / TPR;
+    hipLaunchKernelGGL((norm_fwd_kernel<E, V, TPR, NV>), dim3((rows + RPB - 1) / RPB), dim3(NORM_NT), 0, st, p);
+  }
+  return hipGetLastError();
+}
+
+template <class E, int V>
+hipError_t norm_pick(const NormParams& p, bool bwd, hipStream_t st) {
+  const int nv = (p.D + V - 1) / V;  // vectors in a row
+  if (nv <= 8) return norm_run<E, V, 8, 1>(p, bwd, st);
+  if (nv <= 16) return norm_run<E, V, 16, 1>(p, bwd, st);
+  if (nv <= 32) return norm_run<E, V, 32, 1>(p, bwd, st);
+  if (nv <= 64) return norm_run<E, V, 64, 1>(p, bwd, st);
+  if (nv <= 128) return norm_run<E, V, 64, 2>(p, bwd, st);
+  if (nv <= 256) return norm_run<E, V, 256, 1>(p, bwd, st);
+  if (nv <= 512) return norm_run<E, V, 256, 2>(p, bwd, st);
+  if (nv <= 1024) return norm_run<E, V, 256, 4>(p, bwd, st);
+  if (bwd)
+    hipLaunchKernelGGL((norm_bwd_long_kernel<E>), dim3(p.blocks * (p.shared ? 1 : p.G)), dim3(NORM_NT), 0, st, p);
+  else
+    hipLaunchKernelGGL((norm_fwd_long_kernel<E>), dim3(p.R * p.G), dim3(NORM_NT), 0, st, p);
+  return hipGetLastError();
+}
+
+template <class E>
+hipError_t norm_any(bool vec, const NormParams& p, bool bwd, hipStream_t st) {
+  hipError_t e = vec ? norm_pick<E, kVec<E>>(p, bwd, st) : norm_pick<E, 1>(p, bwd, st);
+  if (e != hipSuccess || !bwd) return e;
+  const int kinds = p.dbias ? 2 : 1;
+  hipLaunchKernelGGL((norm_dw_kernel<E>), dim3((kinds * (int64_t)p.D + 31) / 32, p.shared ? 1 : p.G), dim3(NORM_NT), 0,
+                     st, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_norm_fwd(int dtype, bool vec, const NormParams& p, hipStream_t st) {
+  return dtype == GDN_BF16 ? norm_any<bf16>(vec, p, false, st) : norm_any<float>(vec, p, false, st);
+}
+hipError_t launch_norm_bwd(int dtype, bool vec, const NormParams& p, hipStream_t st) {
+  return dtype == GDN_BF16 ? norm_any<bf16>(vec, p, true, st) : norm_any<float>(vec, p, true, st);
+}
+
+}  // namespace gdn

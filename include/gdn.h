@@ -274,6 +274,198 @@ typedef struct {
 
 gdn_status gdn_decode_step(const gdn_decode_args* args, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators around the recurrence: what a layer built on it runs beside it --
+ * a short causal convolution of its inputs, a selective state space scan in
+ * the recurrence's place, a gated group norm of its outputs.  dtype, alignment,
+ * ownership, streams and errors follow the rules above; bf16 and fp32 inputs
+ * throughout, sums and states in fp32.  These functions were added beside the
+ * chunk calls without changing any struct of theirs.
+ *
+ * Token strides (*_stride, in elements) let an input be a slice of a wider row:
+ * token t of the flattened [B * T] tokens starts at pointer + t * stride, its
+ * own entries contiguous.  A stride below the row's own width is invalid.
+ * 16-byte accesses are used where pointers, widths and strides allow them, and
+ * element accesses elsewhere; only the scan requires them (below). */
+
+/* Short causal depthwise convolution over [B, T, D], channels last:
+ *     u_t = bias + sum_{k < W} w_k x_{t-W+1+k},    y_t = u_t, or u_t sigmoid(u_t) with silu
+ * per channel, W in 2..4.  The W-1 inputs before a sequence's start are its
+ * initial state (rows oldest first; zero when NULL); its final state is its
+ * last W-1 inputs, initial state included when it is shorter.  cu_seqlens
+ * (device, int32 [num_seqs + 1], B == 1) packs sequences; tokens at or past
+ * cu_seqlens[N] belong to none: their y and dx are left as they were. */
+typedef struct {
+  int32_t dtype;
+  int32_t B, T, D, W;
+  const void* x;               /* [B, T, D] */
+  int64_t x_stride;
+  const void* w;               /* [D, W] */
+  const void* bias;            /* nullable [D] */
+  const void* init;            /* nullable [N, W-1, D] */
+  const int32_t* cu_seqlens;   /* nullable */
+  int32_t num_seqs;            /* N; B when cu_seqlens is NULL */
+  int32_t silu;                /* 0 or 1 */
+} gdn_conv_args;
+
+typedef struct {
+  gdn_conv_args a;
+  void* y;                     /* [B, T, D], written */
+  void* final_state;           /* nullable [N, W-1, D], written */
+} gdn_conv_fwd_args;
+
+typedef struct {
+  gdn_conv_args a;
+  const void* dy;              /* [B, T, D] */
+  const void* dfinal;          /* nullable [N, W-1, D]: gradient of the final state */
+  void* dx;                    /* [B, T, D], written */
+  void* dw;                    /* [D, W], written */
+  void* dbias;                 /* nullable [D], written */
+  void* dinit;                 /* nullable [N, W-1, D], written */
+  void* workspace;             /* gdn_conv_bwd_workspace_size bytes, 16-byte aligned */
+  size_t workspace_bytes;
+} gdn_conv_bwd_args;
+
+typedef struct {               /* one token for each of N sequences */
+  int32_t dtype;
+  int32_t N, D, W;
+  const void* x;               /* [N, D] */
+  int64_t x_stride;
+  void* state;                 /* [num_slots, W-1, D], advanced in place */
+  const int32_t* state_idx;    /* nullable [N]; out of range: padding, skipped (as gdn_decode_step) */
+  int32_t num_slots;
+  const void* w;
+  const void* bias;            /* nullable */
+  int32_t silu;
+  void* y;                     /* [N, D], written */
+} gdn_conv_step_args;
+
+gdn_status gdn_conv_fwd(const gdn_conv_fwd_args* args, void* stream);
+size_t gdn_conv_bwd_workspace_size(const gdn_conv_bwd_args* args);
+gdn_status gdn_conv_bwd(const gdn_conv_bwd_args* args, void* stream);
+gdn_status gdn_conv_step(const gdn_conv_step_args* args, void* stream);
+
+/* Selective state space scan, per sequence and head h of group g = h / (H / G):
+ *     d_t = dt_t, or softplus(dt_t + dt_bias[h]) with dt_softplus  (dt_bias is added either way)
+ *     h_t = exp(d_t A[h]) h_{t-1} + d_t B_t x_t^T      (Dk x Dv),   h_0 = h0
+ *     y_t = h_t^T C_t + D[h] x_t,                                  hT = the last h_t
+ * A <= 0 and d_t >= 0 in the intended domain (the decay never exceeds 1); a
+ * token with d_t = 0 leaves the state as it is.  Dk in {64, 128}; Dv a
+ * multiple of 64 up to 256; H a multiple of G.  x, B and C need 16-byte
+ * aligned pointers and token strides of whole 16 bytes.
+ * cu_seqlens / cu_seqlens_host as for the chunk calls.  seg_mode: sequences
+ * are cut into segments that run side by side and are joined exactly
+ * (0 = automatic, -1 = off, k > 0 = segments of k chunks of 64 tokens). */
+typedef struct {
+  int32_t dtype;               /* of x, B, C (and y, dy, dx, dB, dC) */
+  int32_t dt_dtype;            /* of dt (and ddt): GDN_F32, or GDN_BF16 */
+  int32_t B, T, H, G, Dk, Dv;
+  const void* x;               /* [B, T, H, Dv] */
+  const void* dt;              /* [B, T, H] */
+  const void* b;               /* [B, T, G, Dk] */
+  const void* c;               /* [B, T, G, Dk] */
+  int64_t x_stride, dt_stride, b_stride, c_stride;
+  const float* A;              /* [H] */
+  const float* D;              /* nullable [H] */
+  const float* dt_bias;        /* nullable [H] */
+  int32_t dt_softplus;
+  const float* h0;             /* nullable [N, H, Dk, Dv] */
+  const int32_t* cu_seqlens;
+  const int32_t* cu_seqlens_host;
+  int32_t num_seqs;
+  int32_t seg_mode;
+  void* workspace;
+  size_t workspace_bytes;
+} gdn_scan_args;
+
+typedef struct {
+  gdn_scan_args a;
+  void* y;                     /* [B, T, H, Dv], written */
+  float* hT;                   /* nullable [N, H, Dk, Dv], written */
+  float* h_save;               /* nullable, gdn_scan_states_bytes(&a) bytes: the state entering every
+                                  segment, for gdn_scan_bwd */
+} gdn_scan_fwd_args;
+
+typedef struct {
+  gdn_scan_args a;
+  const float* h_saved;        /* nullable: h_save of the forward on the same inputs (else recomputed) */
+  const void* dy;              /* [B, T, H, Dv], 16-byte aligned */
+  const float* dhT;            /* nullable [N, H, Dk, Dv] */
+  void* dx;                    /* [B, T, H, Dv], written */
+  void* ddt;                   /* [B, T, H], written */
+  void* db;                    /* [B, T, G, Dk], written */
+  void* dc;                    /* [B, T, G, Dk], written */
+  float* dA;                   /* [H], written */
+  float* dD;                   /* nullable [H], written */
+  float* ddt_bias;             /* nullable [H], written */
+  float* dh0;                  /* nullable [N, H, Dk, Dv], written */
+} gdn_scan_bwd_args;
+
+typedef struct {               /* one token for each of N sequences */
+  int32_t dtype, dt_dtype;
+  int32_t N, H, G, Dk, Dv;     /* Dk, Dv in {64, 128} */
+  const void* x;               /* [N, H, Dv] */
+  const void* dt;              /* [N, H] */
+  const void* b;               /* [N, G, Dk] */
+  const void* c;
+  int64_t x_stride, dt_stride, b_stride, c_stride;
+  const float* A;
+  const float* D;
+  const float* dt_bias;
+  int32_t dt_softplus;
+  float* state;                /* [num_slots, H, Dk, Dv], advanced in place */
+  const int32_t* state_idx;    /* nullable [N], as gdn_decode_step */
+  int32_t num_slots;
+  void* y;                     /* [N, H, Dv], written */
+} gdn_scan_step_args;
+
+size_t gdn_scan_fwd_workspace_size(const gdn_scan_fwd_args* args);
+size_t gdn_scan_bwd_workspace_size(const gdn_scan_bwd_args* args);
+size_t gdn_scan_states_bytes(const gdn_scan_args* a);  /* 0 when no sequence is cut */
+gdn_status gdn_scan_fwd(const gdn_scan_fwd_args* args, void* stream);
+gdn_status gdn_scan_bwd(const gdn_scan_bwd_args* args, void* stream);
+gdn_status gdn_scan_step(const gdn_scan_step_args* args, void* stream);
+
+/* Gated group norm over [R, G, D], channels last: every token's groups of D
+ * channels are normalised on their own.
+ *     v = x silu(z) with z and gate_first, else x
+ *     n = (v - m) / sqrt(mean((v - m)^2) + eps),   m = mean(v) with center, else 0
+ *     y = n w + bias,  times silu(z) with z and not gate_first
+ * w and bias are [G, D], or [D] for all groups with shared. */
+typedef struct {
+  int32_t dtype;
+  int64_t R;
+  int32_t G, D;
+  const void* x;               /* [R, G, D] */
+  int64_t x_stride;
+  const void* z;               /* nullable [R, G, D] */
+  int64_t z_stride;
+  const void* w;
+  const void* bias;            /* nullable */
+  int32_t shared, center, gate_first;
+  float eps;                   /* > 0 */
+} gdn_norm_args;
+
+typedef struct {
+  gdn_norm_args a;
+  void* y;                     /* [R, G, D], written */
+} gdn_norm_fwd_args;
+
+typedef struct {
+  gdn_norm_args a;
+  const void* dy;              /* [R, G, D] */
+  void* dx;                    /* [R, G, D], written */
+  void* dz;                    /* [R, G, D], written; needed with z */
+  void* dw;                    /* like w, written */
+  void* dbias;                 /* like bias, written; needed with bias */
+  void* workspace;
+  size_t workspace_bytes;
+} gdn_norm_bwd_args;
+
+gdn_status gdn_norm_fwd(const gdn_norm_fwd_args* args, void* stream);
+size_t gdn_norm_bwd_workspace_size(const gdn_norm_bwd_args* args);
+gdn_status gdn_norm_bwd(const gdn_norm_bwd_args* args, void* stream);
+
 /* Per-kernel timing, for benchmarks (off by default).  While enabled, every
  * kernel the library launches is bracketed by a pair of HIP events recorded on
  * the call's stream.  gdn_profile_read waits for the recorded events, adds
