@@ -18,7 +18,8 @@ LIB = os.path.join(HERE, "libgdn.so")
 LIB_CLOCK = os.path.join(HERE, "libgdn_clock.so")
 OBJ = os.path.join(HERE, "_build")
 SOURCES = ["gdn_api.hip", "gdn_plan.hip", "gdn_tsolve.hip", "gdn_fwd.hip", "gdn_bwd.hip", "gdn_decode.hip",
-           "layer/gdn_conv.hip", "layer/gdn_scan.hip", "layer/gdn_norm.hip", "layer/gdn_layer_api.hip"]
+           "layer/gdn_conv.hip", "layer/gdn_scan.hip", "layer/gdn_scan_ops.hip",
+           "layer/gdn_norm.hip", "layer/gdn_layer_api.hip"]
 ARCH = os.environ.get("GDN_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", INC, "-I", CSRC,

@@ -114,6 +114,7 @@ hipError_t launch_norm_bwd(int dtype, bool vec, const NormParams& p, hipStream_t
 
 // ---------------------------------------------------------------- selective state space scan
 constexpr int PS = 64;       // value columns of one slice: a head of Dv columns is Dv / PS slices
+constexpr int AB = 2;        // chunks between two anchors of the decay gradient
 
 // One sweep over the tokens of every segment, forwards or backwards in time,
 // with a Dk x PS slice of the state per (segment, head, slice):
@@ -152,10 +153,12 @@ struct SweepParams {
   float* rt;                 // [H * Dv / PS][tokens]
   float* xd;                 // nullable [H * Dv / PS][tokens]: x_t . dy_t over the slice
   float* cb;                 // nullable [G][tokens]: C_t . B_t
-  // anchor of the decay gradient: <end state, gradient of the end state> of each segment
-  const float* g_end;        // nullable: as s_in, for the other direction
-  int g_per_seg;
-  float* anchor;             // [nseg][H * Dv / PS]
+  // anchors of the decay gradient: the forward key sweep leaves its state at the
+  // end of every AB chunks of a segment, the backward one writes <it, its gradient>
+  float* dump;               // [nseg][blocks][H * Dv / PS][Dk * PS] in the key sweep's own order
+  double* anchor;            // [nseg][blocks][H * Dv / PS]
+  const float* h0;           // nullable: the backward key sweep also writes <h0, its gradient>
+  double* anchor0;           // [N][H * Dv / PS]
 };
 
 struct ScanJoinParams {      // end states of the segments -> states entering them
@@ -184,9 +187,10 @@ struct ScanGradParams {      // ddt, dA, dD, ddt_bias from the row terms
   const float* ct;           // backward sweep's
   const float* xd;
   const float* cb;
-  const float* anchor;       // nullable
+  const double* anchor;      // [nseg][blocks][H * Dv / PS]
+  const double* anchor0;     // nullable (no h0) [N][H * Dv / PS]
   void* ddt;                 // [tokens][H], dtype of dt
-  float* part;               // [nseg][H][3]
+  double* part;              // [nseg][blocks][H][3]
   float* dA;
   float* dD;                 // nullable
   float* ddt_bias;           // nullable

@@ -75,7 +75,7 @@ struct ScanPlan {
   int nseg = 0, nchunk = 0, segc = 1;
   bool multi = false;  // some sequence has more than one segment
   size_t o_chunk_first = 0, o_seg_first = 0, o_segs = 0, o_chunk_tab = 0;
-  size_t o_state = 0, o_dec = 0, o_grad = 0, o_rt = 0, o_ct = 0, o_xd = 0, o_cb = 0, o_anchor = 0, o_sums = 0,
+  size_t o_state = 0, o_dec = 0, o_grad = 0, o_rt = 0, o_ct = 0, o_xd = 0, o_cb = 0, o_anchor = 0, o_anchor0 = 0, o_dump = 0, o_sums = 0,
          o_part = 0, total = 0;
 };
 
@@ -126,8 +126,11 @@ ScanPlan scan_plan(const gdn_scan_args& a, bool bwd, bool own_states) {
     p.o_ct = take(sizeof(float) * vh * tokens);
     p.o_xd = take(sizeof(float) * vh * tokens);
     p.o_cb = take(sizeof(float) * a.G * tokens);
-    p.o_anchor = take(sizeof(float) * vh * p.nseg);
-    p.o_sums = take(sizeof(float) * 3 * a.H * (size_t)p.nseg);
+    const size_t blocks = (size_t)p.nseg * ((p.segc + gdn::AB - 1) / gdn::AB);
+    p.o_anchor = take(sizeof(double) * vh * blocks);
+    p.o_anchor0 = take(sizeof(double) * vh * a.num_seqs);
+    p.o_dump = take(sizeof(float) * state_elems(a) * blocks);
+    p.o_sums = take(sizeof(double) * 3 * a.H * blocks);
     p.o_part = take(sizeof(float) * gdn::sweep_parts_per_group(a.dtype, a.H, a.G, a.Dv) * (size_t)a.G * tokens * a.Dk);
   }
   p.total = off;
@@ -433,16 +436,14 @@ gdn_status gdn_scan_bwd(const gdn_scan_bwd_args* args, void* stream) {
   gdn::ScanReduceParams red{};
   red.part = at<float>(ws, pl.o_part);
   red.G = a.G; red.ppg = gdn::sweep_parts_per_group(a.dtype, a.H, a.G, a.Dv); red.Dk = a.Dk; red.tokens = (int64_t)a.B * a.T;
-  // dC, and the forward row terms with the segments' anchors
+  // dC, the forward row terms, and the states at the anchors
   gdn::SweepParams p = sweep_base(a, pl);
   sweep_dir(p, a, false, args->dy);
   red.seq = p.seq; red.segs = p.segs;
   p.s_in = hs;
   p.out2 = at<float>(ws, pl.o_part);
   p.rt = at<float>(ws, pl.o_rt);
-  p.g_end = gs;
-  p.g_per_seg = pl.multi;
-  p.anchor = at<float>(ws, pl.o_anchor);
+  p.dump = at<float>(ws, pl.o_dump);
   hipError_t e = timed("scan_dc", s, [&] { return gdn::launch_sweep(a.dtype, 0, gdn::SWEEP_KEY, p, pl.nseg, s); });
   if (e != hipSuccess) return hip_fail(e, "scan dC launch");
   red.out = args->dc;
@@ -456,6 +457,10 @@ gdn_status gdn_scan_bwd(const gdn_scan_bwd_args* args, void* stream) {
   p.rt = at<float>(ws, pl.o_ct);
   p.xd = at<float>(ws, pl.o_xd);
   p.cb = at<float>(ws, pl.o_cb);
+  p.dump = at<float>(ws, pl.o_dump);
+  p.anchor = at<double>(ws, pl.o_anchor);
+  p.h0 = a.h0;
+  p.anchor0 = at<double>(ws, pl.o_anchor0);
   e = timed("scan_db", s, [&] { return gdn::launch_sweep(a.dtype, 1, gdn::SWEEP_KEY, p, pl.nseg, s); });
   if (e != hipSuccess) return hip_fail(e, "scan dB launch");
   red.out = args->db;
@@ -473,8 +478,9 @@ gdn_status gdn_scan_bwd(const gdn_scan_bwd_args* args, void* stream) {
   g.dt_bias = a.dt_bias; g.A = a.A; g.H = a.H; g.G = a.G; g.Dk = a.Dk; g.Dv = a.Dv; g.tokens = (int64_t)a.B * a.T;
   g.seq = p.seq; g.segs = p.segs; g.seg_first = p.seg_first;
   g.rt = at<float>(ws, pl.o_rt); g.ct = at<float>(ws, pl.o_ct); g.xd = at<float>(ws, pl.o_xd); g.cb = at<float>(ws, pl.o_cb);
-  g.anchor = at<float>(ws, pl.o_anchor);
-  g.ddt = args->ddt; g.part = at<float>(ws, pl.o_sums); g.dA = args->dA; g.dD = args->dD; g.ddt_bias = args->ddt_bias;
+  g.anchor = at<double>(ws, pl.o_anchor);
+  g.anchor0 = a.h0 ? at<double>(ws, pl.o_anchor0) : nullptr;
+  g.ddt = args->ddt; g.part = at<double>(ws, pl.o_sums); g.dA = args->dA; g.dD = args->dD; g.ddt_bias = args->ddt_bias;
   e = timed("scan_ddt", s, [&] { return gdn::launch_scan_grad(g, pl.nseg, s); });
   return e == hipSuccess ? GDN_OK : hip_fail(e, "scan step gradient launch");
 }

@@ -1,0 +1,230 @@
+// gdn_scan_ops.hip -- the scan's smaller kernels: joins between segments, the
+// gradients of step sizes and decays, the sums of dB and dC over a group's
+// parts, and the single-token step.
+#include "gdn_layer.h"
+#include "gdn_scan_device.h"
+
+namespace gdn {
+
+namespace {
+
+template <class E> __device__ __forceinline__ float ldE(const void* p, int64_t i) { return to_f(static_cast<const E*>(p)[i]); }
+
+// Per (sequence, head): end states of the segments, each from a zero start,
+// become the states entering them (in sweep order).
+__global__ __launch_bounds__(256) void scan_join_kernel(ScanJoinParams p) {
+  const int n = blockIdx.z, h = blockIdx.y;
+  if (plan_invalid(p.seq, p.segs)) return;
+  const int64_t ss = (int64_t)p.Dk * p.Dv, e = blockIdx.x * 256 + threadIdx.x;
+  const int j0 = p.seq.cu ? p.seg_first[n] : n * p.seq.nseg_per_seq();
+  const int ns = p.seq.nseg_of(p.seg_first, n);
+  float carry = p.s0 ? p.s0[((int64_t)n * p.H + h) * ss + e] : 0.f;
+  for (int i = 0; i < ns; ++i) {
+    const int64_t j = j0 + (p.rev ? ns - 1 - i : i);
+    float* s = p.s_loc + (j * p.H + h) * ss + e;
+    const float loc = i + 1 < ns ? *s : 0.f;
+    *s = carry;
+    if (i + 1 < ns) carry = p.s_dec[j * p.H + h] * carry + loc;
+  }
+}
+
+// rt_t - D_t ct_t of token t of a segment (0 past the end t1).
+__device__ __forceinline__ double diff_at(const ScanGradParams& p, const SegRange& r, int t, int t1, int h, float bias) {
+  if (t >= t1) return 0.;
+  const int nsl = p.Dv / PS;
+  const int64_t row = r.row0 + t;
+  const float raw = scan_dt_raw(p.dt, p.dt_f32, row * p.dt_stride + h) + bias;
+  const float d = p.softplus ? scan_softplus(raw) : raw;
+  double rt = 0., ct = 0.;
+  for (int s = 0; s < nsl; ++s) {
+    const int64_t o = ((int64_t)h * nsl + s) * p.tokens + row;
+    rt += p.rt[o];
+    ct += p.ct[o];
+  }
+  return rt - d * ct;
+}
+
+// ddt of every token and each anchor block's sums for dA, dD and ddt_bias: a
+// wave per (anchor block of AB chunks, head) walks the block's 64-token pieces
+// backwards.  The suffix sum of differences is undamped (a rounding stays in it
+// to the block's start), so it and the sums over tokens are held in 64 bits, and
+// the sums are made to meet the next anchor.
+__global__ __launch_bounds__(64) void scan_grad_kernel(ScanGradParams p, int nab) {
+  const int j = blockIdx.x / nab, blk = blockIdx.x % nab, h = blockIdx.y, l = lane_id();
+  const int nsl = p.Dv / PS, g = h / (p.H / p.G);
+  SegRange r;
+  if (!seg_range(p.seq, p.segs, p.seg_first, j, r)) return;
+  double sA = 0., sD = 0., sb = 0.;
+  const int t0 = blk * AB * CH, t1 = min(r.len, t0 + AB * CH);
+  if (t0 < t1) {
+    // <h, dh> at the block's end, and at its start (the end of the block before)
+    double carry = 0., start = 0.;
+    for (int s = 0; s < nsl; ++s) {
+      carry += p.anchor[((int64_t)blockIdx.x * p.H + h) * nsl + s];
+      if (blk > 0) start += p.anchor[((int64_t)(blockIdx.x - 1) * p.H + h) * nsl + s];
+      else if (r.s > 0) start += p.anchor[((int64_t)(j * nab - nab + (p.seq.segc - 1) / AB) * p.H + h) * nsl + s];
+      else if (p.anchor0) start += p.anchor0[((int64_t)r.n * p.H + h) * nsl + s];
+    }
+    // the differences of the block's tokens, and their suffix sums in each 64-token piece
+    const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+    double sum = 0.;
+    for (int b = t0; b < t1; b += 64) sum += wave_sum_d(diff_at(p, r, b + l, t1, h, bias));
+    // what the sums miss the start's product by, per token
+    const double miss = (start - carry - sum) / (t1 - t0);
+    for (int b = t0 + (t1 - t0 - 1) / 64 * 64; b >= t0; b -= 64) {
+      const int t = b + l;
+      const bool in = t < t1;
+      const int64_t row = r.row0 + min(t, t1 - 1);
+      const float raw = scan_dt_raw(p.dt, p.dt_f32, row * p.dt_stride + h) + bias;
+      const float d = p.softplus ? scan_softplus(raw) : raw;
+      double ct = 0., xd = 0.;
+      for (int s = 0; s < nsl; ++s) {
+        const int64_t o = ((int64_t)h * nsl + s) * p.tokens + row;
+        ct += p.ct[o];
+        xd += p.xd[o];
+      }
+      double suf = diff_at(p, r, t, t1, h, bias) + (in ? miss : 0.);
+#pragma unroll
+      for (int o = 1; o < 64; o <<= 1) {
+        const double y = __shfl_down(suf, o, 64);
+        if (l + o < 64) suf += y;
+      }
+      const double da = carry + suf;
+      carry += __shfl(suf, 0, 64);
+      double dd = ct + p.cb[(int64_t)g * p.tokens + row] * xd + A * da;
+      if (p.softplus) dd *= 1.f / (1.f + expf(-raw));
+      if (in) {
+        if (p.dt_f32) static_cast<float*>(p.ddt)[row * p.H + h] = (float)dd;
+        else static_cast<bf16*>(p.ddt)[row * p.H + h] = to_e<bf16>((float)dd);
+        sA += d * da;
+        sD += xd;
+        sb += dd;
+      }
+    }
+  }
+  sA = wave_sum_d(sA);
+  sD = wave_sum_d(sD);
+  sb = wave_sum_d(sb);
+  if (l == 0) {
+    double* o = p.part + ((int64_t)blockIdx.x * p.H + h) * 3;
+    o[0] = sA;
+    o[1] = sD;
+    o[2] = sb;
+  }
+}
+__global__ __launch_bounds__(64) void scan_grad_sum_kernel(ScanGradParams p, int nblk) {
+  const int h = blockIdx.x, l = lane_id();
+  if (plan_invalid(p.seq, p.segs)) return;
+  if (plan_invalid(p.seq, p.segs)) return;
+  double s[3] = {0., 0., 0.};
+  for (int j = l; j < nblk; j += 64)
+    for (int i = 0; i < 3; ++i) s[i] += p.part[((int64_t)j * p.H + h) * 3 + i];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1)
+    for (int i = 0; i < 3; ++i) s[i] += __shfl_xor(s[i], o, 64);
+  if (l == 0) {
+    p.dA[h] = (float)s[0];
+    if (p.dD) p.dD[h] = (float)s[1];
+    if (p.ddt_bias) p.ddt_bias[h] = (float)s[2];
+  }
+}
+
+// dB or dC from the parts: four columns a thread.
+template <class E>
+__global__ __launch_bounds__(256) void scan_reduce_kernel(ScanReduceParams p) {
+  const int64_t i = blockIdx.x * 256ll + threadIdx.x;
+  const int q = p.Dk / 4;
+  const int64_t row = i / (q * p.G);
+  if (row >= p.tokens || plan_invalid(p.seq, p.segs)) return;
+  const int rem = (int)(i - row * q * p.G), g = rem / q, c = (rem % q) * 4;
+  f32x4 s = zero4();
+  for (int v = 0; v < p.ppg; ++v)
+    s += *reinterpret_cast<const f32x4*>(p.part + (((int64_t)g * p.ppg + v) * p.tokens + row) * p.Dk + c);
+  st4f<E>(static_cast<E*>(p.out) + (row * p.G + g) * p.Dk + c, s);
+}
+
+// Single-token step: a workgroup owns 32 columns of one (sequence, head) state,
+// its 256 threads 4 columns x Dk/32 rows each, as the delta rule's step does.
+// Bound: the fp32 state, read and written once, non-temporal.
+constexpr int STEP_COLS = 32;
+template <class E, int DK, int DV>
+__global__ __launch_bounds__(256) void scan_step_kernel(ScanStepParams p) {
+  constexpr int RPT = DK / 32;
+  __shared__ float red[32][STEP_COLS + 1];
+  const int tid = threadIdx.x, tc = tid & 7, tr = tid >> 3;
+  const int nh = blockIdx.x, n = nh / p.H, h = nh - n * p.H, g = h / (p.H / p.G);
+  const int slot = p.state_idx ? p.state_idx[n] : n;
+  if (slot < 0 || slot >= p.num_slots) return;  // padding entry
+  const int c0 = blockIdx.y * STEP_COLS + 4 * tc;
+  float* hs = p.state + ((int64_t)slot * p.H + h) * DK * DV;
+  f32x4 hv[RPT];
+  float bv[RPT], cv[RPT];
+#pragma unroll
+  for (int m = 0; m < RPT; ++m) {
+    const int i = tr + 32 * m;
+    hv[m] = __builtin_nontemporal_load(reinterpret_cast<const f32x4*>(hs + (int64_t)i * DV + c0));
+    bv[m] = ldE<E>(p.b, n * p.b_stride + (int64_t)g * DK + i);
+    cv[m] = ldE<E>(p.c, n * p.c_stride + (int64_t)g * DK + i);
+  }
+  const float d = scan_step_size(p, n, h), a = expf(d * p.A[h]);
+  const f32x4 x4 = ld4f<E>(static_cast<const E*>(p.x) + n * p.x_stride + (int64_t)h * DV + c0);
+  const f32x4 dx = x4 * d;
+  f32x4 part = zero4();
+#pragma unroll
+  for (int m = 0; m < RPT; ++m) {
+    const int i = tr + 32 * m;
+    const f32x4 hn = hv[m] * a + dx * bv[m];
+    __builtin_nontemporal_store(hn, reinterpret_cast<f32x4*>(hs + (int64_t)i * DV + c0));
+    part += hn * cv[m];
+  }
+#pragma unroll
+  for (int e = 0; e < 4; ++e) red[tr][4 * tc + e] = part[e];
+  __syncthreads();
+  if (tid < STEP_COLS) {
+    float s = 0.f;
+#pragma unroll 8
+    for (int r = 0; r < 32; ++r) s += red[r][tid];
+    const int j = blockIdx.y * STEP_COLS + tid;
+    if (p.D) s += p.D[h] * ldE<E>(p.x, n * p.x_stride + (int64_t)h * DV + j);
+    static_cast<E*>(p.y)[(int64_t)nh * DV + j] = to_e<E>(s);
+  }
+}
+
+template <class E>
+hipError_t step_any(int Dk, int Dv, const ScanStepParams& p, hipStream_t st) {
+  const dim3 g(p.N * p.H, Dv / STEP_COLS), b(256);
+  if (Dk == 128 && Dv == 128) hipLaunchKernelGGL((scan_step_kernel<E, 128, 128>), g, b, 0, st, p);
+  else if (Dk == 64 && Dv == 64) hipLaunchKernelGGL((scan_step_kernel<E, 64, 64>), g, b, 0, st, p);
+  else if (Dk == 64 && Dv == 128) hipLaunchKernelGGL((scan_step_kernel<E, 64, 128>), g, b, 0, st, p);
+  else if (Dk == 128 && Dv == 64) hipLaunchKernelGGL((scan_step_kernel<E, 128, 64>), g, b, 0, st, p);
+  else return hipErrorInvalidValue;
+  return hipGetLastError();
+}
+
+}  // namespace
+
+hipError_t launch_scan_join(const ScanJoinParams& p, hipStream_t st) {
+  hipLaunchKernelGGL(scan_join_kernel, dim3(p.Dk * p.Dv / 256, p.H, p.N), dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+hipError_t launch_scan_grad(const ScanGradParams& p, int nseg, hipStream_t st) {
+  const int nab = (p.seq.segc + AB - 1) / AB;
+  hipLaunchKernelGGL(scan_grad_kernel, dim3(nseg * nab, p.H), dim3(64), 0, st, p, nab);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(scan_grad_sum_kernel, dim3(p.H), dim3(64), 0, st, p, nseg * nab);
+  return hipGetLastError();
+}
+hipError_t launch_scan_reduce(int dtype, const ScanReduceParams& p, hipStream_t st) {
+  const int64_t n = p.tokens * p.G * (p.Dk / 4);
+  if (n == 0) return hipSuccess;
+  if (dtype == GDN_BF16) hipLaunchKernelGGL((scan_reduce_kernel<bf16>), dim3((n + 255) / 256), dim3(256), 0, st, p);
+  else hipLaunchKernelGGL((scan_reduce_kernel<float>), dim3((n + 255) / 256), dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+hipError_t launch_scan_step(int dtype, int Dk, int Dv, const ScanStepParams& p, hipStream_t st) {
+  if (p.N * p.H == 0) return hipSuccess;
+  return dtype == GDN_BF16 ? step_any<bf16>(Dk, Dv, p, st) : step_any<float>(Dk, Dv, p, st);
+}
+
+}  // namespace gdn
