@@ -159,6 +159,8 @@ gdn_status check_scan(const gdn_scan_args& a) {
     return fail(GDN_E_INVALID, "a token stride is below its row's width");
   if (a.x_stride % v || a.b_stride % v || a.c_stride % v)
     return fail(GDN_E_INVALID, "the token strides of x, b and c must be whole 16 bytes");
+  const int64_t most = std::max({a.x_stride, a.b_stride, a.c_stride, a.dt_stride, (int64_t)a.H * a.Dv});
+  if (most >= (1 << 22)) return fail(GDN_E_INVALID, "a token's row of %lld elements is too wide", (long long)most);
   if (!aligned(a.dt, esize(a.dt_dtype)) || !aligned(a.A, 4) || !aligned(a.D, 4) || !aligned(a.dt_bias, 4) ||
       !aligned(a.h0, 4))
     return fail(GDN_E_INVALID, "dt, A, D, dt_bias or h0 misaligned");

@@ -111,6 +111,10 @@ __device__ __forceinline__ void frag_f32(const Frag<float>& f, f32x4& lo, f32x4&
   hi = f.hi;
 }
 
+// Keeps the instruction scheduler from moving work across: without it the reads
+// of every unrolled step are hoisted to the front and registers spill.
+__device__ __forceinline__ void sched_fence() { __builtin_amdgcn_sched_barrier(0); }
+
 // a times a value held in two parts (about 16 bits of it).
 __device__ __forceinline__ void mma_hi_lo(f32x4& acc, const Frag<bf16>& a, const PFrag<bf16>& b) {
   mma(acc, a, b.lo);
@@ -132,8 +136,11 @@ struct ChunkRows {
   int64_t base;  // first token (global row)
   int nt;        // tokens, 1 .. CH
 };
+// Token of row r relative to the chunk's first.
 template <bool REV>
-__device__ __forceinline__ int64_t row_of(const ChunkRows& c, int r) { return c.base + (REV ? c.nt - 1 - r : r); }
+__device__ __forceinline__ int tok_of(const ChunkRows& c, int r) { return REV ? c.nt - 1 - r : r; }
+template <bool REV>
+__device__ __forceinline__ int64_t row_of(const ChunkRows& c, int r) { return c.base + tok_of<REV>(c, r); }
 // Chunk i of a segment in sweep order.
 template <bool REV>
 __device__ __forceinline__ ChunkRows chunk_rows(const SegRange& s, int i) {
@@ -142,6 +149,46 @@ __device__ __forceinline__ ChunkRows chunk_rows(const SegRange& s, int i) {
   r.base = s.row0 + (int64_t)c * CH;
   r.nt = min(CH, s.len - c * CH);
   return r;
+}
+// The segment, its fields known to be the same in every lane.
+__device__ __forceinline__ void make_uniform(SegRange& r) {
+  r.n = __builtin_amdgcn_readfirstlane(r.n);
+  r.s = __builtin_amdgcn_readfirstlane(r.s);
+  r.ns = __builtin_amdgcn_readfirstlane(r.ns);
+  r.len = __builtin_amdgcn_readfirstlane(r.len);
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)r.row0);
+  const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(r.row0 >> 32));
+  r.row0 = (int64_t)((uint64_t)hi << 32 | lo);
+}
+
+// DPP moves of 64-bit values (rows of 16 lanes; lanes without a source get 0).
+template <int CTRL>
+__device__ __forceinline__ double dpp_mov_d(double x) {
+  typedef int i32x2 __attribute__((__vector_size__(8)));
+  i32x2 v = __builtin_bit_cast(i32x2, x);
+  v[0] = dpp_mov<CTRL>(v[0]);
+  v[1] = dpp_mov<CTRL>(v[1]);
+  return __builtin_bit_cast(double, v);
+}
+__device__ __forceinline__ double readlane_d(double x, int lane) {
+  typedef int i32x2 __attribute__((__vector_size__(8)));
+  i32x2 v = __builtin_bit_cast(i32x2, x);
+  v[0] = __builtin_amdgcn_readlane(v[0], lane);
+  v[1] = __builtin_amdgcn_readlane(v[1], lane);
+  return __builtin_bit_cast(double, v);
+}
+// Sums over the four 16-lane groups of four values at once: lane 16 g + t gets
+// the sum of x[g] over lanes t, 16 + t, 32 + t, 48 + t.  Exchanging odd with even
+// lane rows of two values puts the halves of both sums side by side.
+__device__ __forceinline__ float sum_groups4(const float (&x)[4]) {
+  auto add = [](unsigned a, unsigned b) { return __builtin_bit_cast(float, a) + __builtin_bit_cast(float, b); };
+  auto add16 = [&](float a, float b) {
+    const auto r = __builtin_amdgcn_permlane16_swap(__builtin_bit_cast(unsigned, a), __builtin_bit_cast(unsigned, b), false, false);
+    return add(r[0], r[1]);
+  };
+  const float ab = add16(x[0], x[1]), cd = add16(x[2], x[3]);
+  const auto r = __builtin_amdgcn_permlane32_swap(__builtin_bit_cast(unsigned, ab), __builtin_bit_cast(unsigned, cd), false, false);
+  return add(r[0], r[1]);
 }
 
 // Decay factors of one head's chunk, in LDS.
@@ -180,52 +227,62 @@ struct HeadConst {
     bias = p.dt_bias ? p.dt_bias[h] : 0.f;
   }
 };
+// The bits of a row's dt, converted only where they are used (a conversion here
+// would wait for the load).
 template <bool REV, class P>
-__device__ __forceinline__ float load_dt(const P& p, const ChunkRows& c, int h) {
-  const int r = lane_id();
-  return r < c.nt ? scan_dt_raw(p.dt, p.dt_f32, row_of<REV>(c, r) * p.dt_stride + h) : 0.f;
+__device__ __forceinline__ uint32_t load_dt(const P& p, const ChunkRows& c, int h) {
+  const int r = lane_id(), t = tok_of<REV>(c, r);
+  const int64_t at = c.base * p.dt_stride + h;
+  const uint32_t off = r < c.nt ? (uint32_t)(t * (int)p.dt_stride) : 0u;
+  return p.dt_f32 ? (static_cast<const uint32_t*>(p.dt) + at)[off] : (static_cast<const uint16_t*>(p.dt) + at)[off];
+}
+template <class P>
+__device__ __forceinline__ float dt_value(const P& p, uint32_t bits) {
+  return __builtin_bit_cast(float, p.dt_f32 ? bits : bits << 16);
 }
 template <bool REV, class P>
-__device__ __forceinline__ void fill_decay(ChunkDecay& o, const P& p, const HeadConst& hc, float raw, int nt) {
+__device__ __forceinline__ void fill_decay(ChunkDecay& o, const P& p, const HeadConst& hc, uint32_t bits, int nt) {
   const int r = lane_id();
-  raw += hc.bias;
+  const float raw = dt_value(p, bits) + hc.bias;
   const float d = r < nt ? (p.softplus ? scan_softplus(raw) : raw) : 0.f;
-  const double a = (double)d * hc.A * 1.4426950408889634;
-  double step = a;
+  const double A2 = (double)hc.A * 1.4426950408889634;
+  double step = d * A2, fin = 0.;
   if (REV) {
-    step = __shfl_up(a, 1, 64);
-    if (r == 0) step = 0.;
+    fin = readlane_d(step, 63);
+    const float dp = __shfl_up(d, 1, 64);
+    step = r == 0 ? 0. : dp * A2;
   }
-  const int q = r & 15;
-  double pre = step;   // inclusive prefix in the 16-row block
-  double suf = step;   // inclusive suffix
-#pragma unroll
-  for (int o2 = 1; o2 < 16; o2 <<= 1) {
-    const double y = __shfl_up(pre, o2, 16), z = __shfl_down(suf, o2, 16);
-    if (q >= o2) pre += y;
-    if (q + o2 < 16) suf += z;
-  }
-  double after = __shfl_down(suf, 1, 16);
-  if (q == 15) after = 0.;
-  const double b0 = __shfl(pre, 15, 64), b1 = __shfl(pre, 31, 64), b2 = __shfl(pre, 47, 64), b3 = __shfl(pre, 63, 64);
-  const double fin = REV ? __shfl(a, 63, 64) : 0.;
+  // inclusive prefix and exclusive suffix sums in 16-row blocks
+  double pre = step;
+  pre += dpp_mov_d<0x111>(pre);
+  pre += dpp_mov_d<0x112>(pre);
+  pre += dpp_mov_d<0x114>(pre);
+  pre += dpp_mov_d<0x118>(pre);
+  double after = dpp_mov_d<0x101>(step);
+  after += dpp_mov_d<0x101>(after);
+  after += dpp_mov_d<0x102>(after);
+  after += dpp_mov_d<0x104>(after);
+  after += dpp_mov_d<0x108>(after);
+  const double b0 = readlane_d(pre, 15), b1 = readlane_d(pre, 31), b2 = readlane_d(pre, 47), b3 = readlane_d(pre, 63);
   const int blk = r >> 4;
   const double before = blk == 0 ? 0. : blk == 1 ? b0 : blk == 2 ? b0 + b1 : b0 + b1 + b2;
   const double later = (blk == 0 ? b1 + b2 + b3 : blk == 1 ? b2 + b3 : blk == 2 ? b3 : 0.) + fin;
-  const float w = r < nt ? 1.f : 0.f;
+  const float w = r < nt ? 1.f : 0.f, sw = REV ? w : d;
+  const float row = exp2_sum(pre), col = exp2_sum(after) * sw;
   o.p16[r] = pre;
-  o.sw[r] = REV ? w : d;
+  o.sw[r] = sw;
   o.tw[r] = REV ? d : w;
-  o.tf[r] = exp2_sum(before + pre);
-  o.row[r] = exp2_sum(pre);
-  o.col[r] = exp2_sum(after) * (REV ? w : d);
-  o.end[r] = exp2_sum(after + later) * (REV ? w : d);
+  o.tf[r] = exp2_sum(before) * row;
+  o.row[r] = row;
+  o.col[r] = col;
+  o.end[r] = exp2_sum(later) * col;
   if (r < 4) {
     const double t = r == 0 ? b1 : r == 1 ? b2 : r == 2 ? b1 + b2 : b0 + b1 + b2 + b3 + fin;
     o.btw[r] = exp2_sum(t);
   }
 }
 // The factors L o sw of tile (tb, sb) for this lane's entries (s = 4g + i, t = lane % 16).
+template <bool PRECISE>
 __device__ __forceinline__ f32x4 tile_decay(const ChunkDecay& d, int tb, int sb) {
   const int l = lane_id(), t = l & 15, g = l >> 4;
   f32x4 f;
@@ -236,34 +293,68 @@ __device__ __forceinline__ f32x4 tile_decay(const ChunkDecay& d, int tb, int sb)
     const double* ps = &d.p16[16 * sb + 4 * g];
     const f32x4 sw = *reinterpret_cast<const f32x4*>(&d.sw[16 * sb + 4 * g]);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = 4 * g + i <= t ? exp2_sum(pt - ps[i]) * sw[i] : 0.f;
+    for (int i = 0; i < 4; ++i) {
+      const double x = pt - ps[i];
+      f[i] = 4 * g + i <= t ? (PRECISE ? exp2_sum(x) : __builtin_amdgcn_exp2f((float)x)) * sw[i] : 0.f;
+    }
   }
   return f;
 }
 
-// ---------------------------------------------------------------- staging
-// A chunk's [CH][C] tile from global rows into registers, then into LDS, by NT
-// threads; rows past the end are zero.
-template <class E, int C, int NT>
+// ---------------------------------------------------------------- a chunk's rows in memory
+// The rows of a chunk as a buffer: base at the chunk's first token, its length
+// the chunk's own tokens.  Lane offsets are 32 bits; a row past the end lies
+// past the buffer, and backwards, where rows run down from the last token, at a
+// negative (huge unsigned) offset: loads give 0 there and stores do nothing, so
+// ragged chunks need no branch.  64 rows of a legal stride are below 2^31 bytes.
+typedef uint32_t u32x4 __attribute__((__vector_size__(16)));
+struct RowBuf {
+  __amdgpu_buffer_rsrc_t rsrc;
+  int shift;  // bytes that the offsets of a full chunk run past this one's (backwards)
+};
+template <bool REV, class E>
+__device__ __forceinline__ RowBuf row_buf(const E* base, int64_t stride, int width, int nt, bool live = true) {
+  RowBuf b;
+  const int bytes = live ? ((nt - 1) * (int)stride + width) * (int)sizeof(E) : 0;
+  b.rsrc = __builtin_amdgcn_make_buffer_rsrc(const_cast<E*>(base), 0, bytes, 0x00027000);
+  b.shift = REV ? (CH - nt) * (int)stride * (int)sizeof(E) : 0;
+  return b;
+}
+// Offset of row r (of a full chunk), entry e.
+template <bool REV, class E>
+__device__ __forceinline__ int row_off(int r, int64_t stride, int e) {
+  return ((REV ? CH - 1 - r : r) * (int)stride + e) * (int)sizeof(E);
+}
+__device__ __forceinline__ u32x4 ld16(const RowBuf& b, int off) {
+  return __builtin_bit_cast(u32x4, __builtin_amdgcn_raw_buffer_load_b128(b.rsrc, off - b.shift, 0, 0));
+}
+template <class V>
+__device__ __forceinline__ void st16(const RowBuf& b, int off, const V& v) {
+  static_assert(sizeof(V) == 16, "one 16-byte store");
+  typedef unsigned u4 __attribute__((ext_vector_type(4)));
+  __builtin_amdgcn_raw_buffer_store_b128(__builtin_bit_cast(u4, v), b.rsrc, off - b.shift, 0, 0);
+}
+
+// A chunk's [CH][C] tile into registers, then into LDS, by NT threads.
+template <class E, int C, int NT, bool REV>
 struct TileStage {
-  typedef uint32_t u32x4 __attribute__((__vector_size__(16)));
-  static constexpr int PPR = C * (int)sizeof(E) / 16, PIECES = CH * PPR, PER = (PIECES + NT - 1) / NT;
+  static constexpr int PPR = C * (int)sizeof(E) / 16, PIECES = CH * PPR, PER = PIECES / NT, RPS = NT / PPR;
+  static_assert(PIECES % NT == 0 && NT % PPR == 0, "whole rows a step");
   u32x4 v[PER];
-  template <bool REV>
-  __device__ __forceinline__ void load(const E* base, int64_t stride, const ChunkRows& c, int tid) {
+  // base: the chunk's first token; off: row_off of this thread's first piece
+  __device__ __forceinline__ void load(const E* base, int64_t stride, int nt, int off) {
+    const RowBuf b = row_buf<REV>(base, stride, C, nt);
+    const int step = (REV ? -1 : 1) * RPS * (int)stride * (int)sizeof(E);
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int i = tid + k * NT, r = i / PPR, pc = i % PPR;
-      v[k] = u32x4{0, 0, 0, 0};
-      if (r < c.nt) v[k] = *reinterpret_cast<const u32x4*>(base + row_of<REV>(c, r) * stride + pc * (16 / (int)sizeof(E)));
-    }
+    for (int k = 0; k < PER; ++k) v[k] = ld16(b, off + k * step);
   }
-  __device__ __forceinline__ void store(E* lds, int ld, int tid) const {
+  static __device__ __forceinline__ int first_off(int64_t stride, int tid) {
+    return row_off<REV, E>(tid / PPR, stride, tid % PPR * (16 / (int)sizeof(E)));
+  }
+  __device__ __forceinline__ void store(E* base, int ld, int tid) const {
+    E* d = base + tid / PPR * ld + tid % PPR * (16 / (int)sizeof(E));
 #pragma unroll
-    for (int k = 0; k < PER; ++k) {
-      const int i = tid + k * NT, r = i / PPR, pc = i % PPR;
-      if (PIECES % NT == 0 || i < PIECES) *reinterpret_cast<u32x4*>(lds + r * ld + pc * (16 / (int)sizeof(E))) = v[k];
-    }
+    for (int k = 0; k < PER; ++k) *reinterpret_cast<u32x4*>(d + k * RPS * ld) = v[k];
   }
 };
 
@@ -271,8 +362,10 @@ struct TileStage {
 // A workgroup of NW waves takes NW units of one group of heads in one segment;
 // a unit is VC = 32 value columns of one head, its state Dk x 32 in the wave's
 // accumulators for the whole segment.  K and Q are staged once for all waves,
-// and Q K^T, which has no head in it, is formed once by all waves together.
-// OUT = false: the state sweep (no Q, no output).
+// and Q K^T, which has no head in it, is formed once by all waves together; the
+// two waves of a pair belong to one head and share its decays and its chunk
+// matrix, of which each forms half.  OUT = false: the state sweep (no Q, no
+// output).
 constexpr int VC = 32;
 
 template <class E, int DK, int NW>
@@ -281,11 +374,20 @@ struct ValueLds {
   E q[CH * row_ld<E>(DK)];
   E v[NW][CH * row_ld<E>(VC)];
   f32x4 cb[10][64];
-  ChunkDecay dec[NW];
+  E m[NW / 2][10][64][4];
+  ChunkDecay dec[2][NW / 2];  // of this chunk and the next
 };
 
+// Tile idx of the head's chunk matrix from Q K^T and the decays.
+template <class E, int DK, int NW, int IDX>
+__device__ __forceinline__ void chunk_matrix_tile(ValueLds<E, DK, NW>& sh, const ChunkDecay& dec, int pair) {
+  constexpr int tb = IDX >= 6 ? 3 : IDX >= 3 ? 2 : IDX >= 1 ? 1 : 0, sb = IDX - tb * (tb + 1) / 2;
+  const int l = lane_id();
+  st4f<E>(sh.m[pair][IDX][l], sh.cb[IDX][l] * tile_decay<sizeof(E) == 4>(dec, tb, sb));
+}
+
 template <class E, int DK, int NW, bool REV, bool OUT>
-__global__ __launch_bounds__(NW * 64) void sweep_value_kernel(SweepParams p, int parts) {
+__global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, int parts) {
   extern __shared__ __align__(16) char smem[];
   typedef ValueLds<E, DK, NW> Lds;
   Lds* const sh0 = reinterpret_cast<Lds*>(smem);
@@ -294,6 +396,7 @@ __global__ __launch_bounds__(NW * 64) void sweep_value_kernel(SweepParams p, int
   const int part = blockIdx.x % parts, grp = blockIdx.x / parts % p.G, j = blockIdx.x / parts / p.G;
   SegRange r;
   if (!seg_range(p.seq, p.segs, p.seg_first, j, r)) return;
+  make_uniform(r);
   const bool first = REV ? r.s == r.ns - 1 : r.s == 0, last = REV ? r.s == 0 : r.s == r.ns - 1;
   if (!OUT && last) return;  // nothing follows this segment
   const int rep = p.H / p.G, upg = rep * (p.Dv / VC);
@@ -320,20 +423,32 @@ __global__ __launch_bounds__(NW * 64) void sweep_value_kernel(SweepParams p, int
 #pragma unroll
         for (int i = 0; i < 4; ++i) S[nt][pt][i] = s0[(int64_t)(key_of(nt) + i) * p.Dv + 4 * pt];
   }
+  // The state leaves as fp32 from the state sweep and from a sequence's last
+  // segment; elsewhere only bf16 outputs read it, and two parts (16 bits) of
+  // the values are enough.
+  const int np = !OUT || (last && p.s_end) ? Parts<E>::N : min(Parts<E>::N, 2);
   const int nch = (r.len + CH - 1) / CH;
-  TileStage<E, DK, NTH> tk, tq;
-  TileStage<E, VC, 64> tv;
+  TileStage<E, DK, NTH, REV> tk, tq;
+  TileStage<E, VC, 64, REV> tv;
+  const int ko = tk.first_off(p.k_stride, tid), qo = OUT ? tq.first_off(p.q_stride, tid) : 0;
+  const int vo = tv.first_off(p.v_stride, l), oo = row_off<REV, E>(t16, p.H * p.Dv, 8 * g4);
   HeadConst hc;
   hc.load(p, h);
-  float dt = 0.f;
+  uint32_t dt = 0;  // of the next chunk
   auto request = [&](int i) {
     const ChunkRows c = chunk_rows<REV>(r, i);
-    dt = load_dt<REV>(p, c, h);
-    tk.template load<REV>(static_cast<const E*>(p.k) + (int64_t)grp * DK, p.k_stride, c, tid);
-    if (OUT) tq.template load<REV>(static_cast<const E*>(p.q) + (int64_t)grp * DK, p.q_stride, c, tid);
-    tv.template load<REV>(static_cast<const E*>(p.v) + (int64_t)h * p.Dv + col, p.v_stride, c, l);
+    tk.load(static_cast<const E*>(p.k) + c.base * p.k_stride + (int64_t)grp * DK, p.k_stride, c.nt, ko);
+    if (OUT) tq.load(static_cast<const E*>(p.q) + c.base * p.q_stride + (int64_t)grp * DK, p.q_stride, c.nt, qo);
+    tv.load(static_cast<const E*>(p.v) + c.base * p.v_stride + (int64_t)h * p.Dv + col, p.v_stride, c.nt, vo);
   };
-  if (nch > 0) request(0);
+  if (nch > 0) {
+    request(0);
+    if ((w & 1) == 0) {
+      const ChunkRows c = chunk_rows<REV>(r, 0);
+      fill_decay<REV>(sh0->dec[0][w >> 1], p, hc, load_dt<REV>(p, c, h), c.nt);
+      if (nch > 1) dt = load_dt<REV>(p, chunk_rows<REV>(r, 1), h);
+    }
+  }
   float total = 1.f;
   for (int i = 0; i < nch; ++i) {
     const ChunkRows c = chunk_rows<REV>(r, i);
@@ -344,13 +459,18 @@ __global__ __launch_bounds__(NW * 64) void sweep_value_kernel(SweepParams p, int
       if (OUT) tq.store(sh.q, LDK, tid);
       tv.store(sh.v[w], LDV, l);
     }
-    const float raw = dt;
+    const uint32_t dt1 = dt;
+    if (i + 2 < nch && (w & 1) == 0) dt = load_dt<REV>(p, chunk_rows<REV>(r, i + 2), h);
     if (i + 1 < nch) request(i + 1);
-    fill_decay<REV>(lds_opaque(sh0)->dec[w], p, hc, raw, c.nt);
     __syncthreads();
+    // even waves, once a chunk: the next chunk's decays
+    auto next_decay = [&] {
+      if (i + 1 < nch) fill_decay<REV>(lds_opaque(sh0)->dec[(i + 1) & 1][w >> 1], p, hc, dt1, chunk_rows<REV>(r, i + 1).nt);
+    };
+    Frag<E> vf[2][2];  // V down its columns: rows 32 kb.., columns of tile pt
     if (OUT) {
-      Lds& sh = *lds_opaque(sh0);
       for (int idx = w; idx < 10; idx += NW) {
+        Lds& sh = *lds_opaque(sh0);
         int tb, sb;
         tri_tile(idx, tb, sb);
         f32x4 a = zero4();
@@ -359,18 +479,33 @@ __global__ __launch_bounds__(NW * 64) void sweep_value_kernel(SweepParams p, int
           mma(a, ld_frag8(sh.k, LDK, 16 * sb + t16, 32 * kb), ld_frag8(sh.q, LDK, 16 * tb + t16, 32 * kb));
         sh.cb[idx][l] = a;
       }
-    }
-    Frag<E> vf[2][2];  // V down its columns: rows 32 kb.., columns of tile pt
-#pragma unroll
-    for (int kb = 0; kb < 2; ++kb)
-#pragma unroll
-      for (int pt = 0; pt < 2; ++pt) vf[kb][pt] = ld_col(lds_opaque(sh0)->v[w], LDV, 32 * kb, 0, pt);
-    if (OUT) {
+      __syncthreads();
+      // the head's chunk matrix: the even wave four tiles below the diagonal
+      // blocks and the next decays, the odd one the other two and the diagonal
+      {
+        Lds& sh = *lds_opaque(sh0);
+        const ChunkDecay& dec = sh.dec[i & 1][w >> 1];
+        if ((w & 1) == 0) {
+          chunk_matrix_tile<E, DK, NW, 1>(sh, dec, w >> 1);
+          chunk_matrix_tile<E, DK, NW, 3>(sh, dec, w >> 1);
+          chunk_matrix_tile<E, DK, NW, 4>(sh, dec, w >> 1);
+          chunk_matrix_tile<E, DK, NW, 6>(sh, dec, w >> 1);
+          next_decay();
+        } else {
+          chunk_matrix_tile<E, DK, NW, 7>(sh, dec, w >> 1);
+          chunk_matrix_tile<E, DK, NW, 8>(sh, dec, w >> 1);
+          chunk_matrix_tile<E, DK, NW, 0>(sh, dec, w >> 1);
+          chunk_matrix_tile<E, DK, NW, 2>(sh, dec, w >> 1);
+          chunk_matrix_tile<E, DK, NW, 5>(sh, dec, w >> 1);
+          chunk_matrix_tile<E, DK, NW, 9>(sh, dec, w >> 1);
+        }
+      }
       f32x4 o[4][2];
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) o[tb][0] = o[tb][1] = zero4();
 #pragma unroll
       for (int kb = 0; kb < DK / 32; ++kb) {
+        sched_fence();
         Lds& sh = *lds_opaque(sh0);
         Frag<E> sf[2];
 #pragma unroll
@@ -382,43 +517,67 @@ __global__ __launch_bounds__(NW * 64) void sweep_value_kernel(SweepParams p, int
           mma(o[tb][1], sf[1], q);
         }
       }
-      __syncthreads();  // Q K^T of all waves
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt) vf[kb][pt] = ld_col(lds_opaque(sh0)->v[w], LDV, 32 * kb, 0, pt);
+      __syncthreads();
+      const RowBuf out = row_buf<REV>(static_cast<const E*>(p.out1) + c.base * p.H * p.Dv + (int64_t)h * p.Dv + col,
+                                      p.H * p.Dv, VC, c.nt, active);
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
+        sched_fence();
         Lds& sh = *lds_opaque(sh0);
-        const ChunkDecay& dec = sh.dec[w];
+        const ChunkDecay& dec = sh.dec[i & 1][w >> 1];
         const float tf = dec.tf[16 * tb + t16];
         o[tb][0] *= tf;
         o[tb][1] *= tf;
 #pragma unroll
         for (int kb = 0; kb <= tb / 2; ++kb) {
-          const f32x4 m0 = sh.cb[tb * (tb + 1) / 2 + 2 * kb][l] * tile_decay(dec, tb, 2 * kb);
-          f32x4 m1 = zero4();
-          if (2 * kb + 1 <= tb) m1 = sh.cb[tb * (tb + 1) / 2 + 2 * kb + 1][l] * tile_decay(dec, tb, 2 * kb + 1);
+          const int i0 = tb * (tb + 1) / 2 + 2 * kb;
           Frag<E> m;
-          pack_frag(m, m0, m1);
+          if constexpr (sizeof(E) == 2) {
+            const bf16x4 x = *reinterpret_cast<const bf16x4*>(sh.m[w >> 1][i0][l]);
+            bf16x4 y = bf16x4{};
+            if (2 * kb + 1 <= tb) y = *reinterpret_cast<const bf16x4*>(sh.m[w >> 1][i0 + (2 * kb + 1 <= tb)][l]);
+            m.v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+          } else {
+            m.lo = *reinterpret_cast<const f32x4*>(sh.m[w >> 1][i0][l]);
+            m.hi = 2 * kb + 1 <= tb ? *reinterpret_cast<const f32x4*>(sh.m[w >> 1][i0 + (2 * kb + 1 <= tb)][l]) : zero4();
+          }
           mma(o[tb][0], vf[kb][0], m);
           mma(o[tb][1], vf[kb][1], m);
         }
         const int row = 16 * tb + t16;
-        if (active && row < c.nt) {
+        const E* vr = sh.v[w] + row * LDV + 8 * g4;
+        f32x4 y0 = o[tb][0], y1 = o[tb][1];
+        if (REV) {  // forwards the target weight is 1
           const float tw = dec.tw[row];
-          const E* vr = sh.v[w] + row * LDV + 8 * g4;
-          const f32x4 y0 = o[tb][0] * tw + ld4f<E>(vr) * Dh, y1 = o[tb][1] * tw + ld4f<E>(vr + 4) * Dh;
-          E* dst = static_cast<E*>(p.out1) + (row_of<REV>(c, row) * p.H + h) * p.Dv + col + 8 * g4;
-          if constexpr (sizeof(E) == 2) {
-            Frag<bf16> f;
-            pack_frag(f, y0, y1);
-            *reinterpret_cast<bf16x8*>(dst) = f.v;
-          } else {
-            st4f<E>(dst, y0);
-            st4f<E>(dst + 4, y1);
-          }
+          y0 *= tw;
+          y1 *= tw;
+        }
+        y0 += ld4f<E>(vr) * Dh;
+        y1 += ld4f<E>(vr + 4) * Dh;
+        const int off = oo + (REV ? -tb : tb) * 16 * p.H * p.Dv * (int)sizeof(E);
+        if constexpr (sizeof(E) == 2) {
+          Frag<bf16> f;
+          pack_frag(f, y0, y1);
+          st16(out, off, f.v);
+        } else {
+          st16(out, off, y0);
+          st16(out, off + 16, y1);
         }
       }
+    } else {
+      if ((w & 1) == 0) next_decay();
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+        for (int pt = 0; pt < 2; ++pt) vf[kb][pt] = ld_col(lds_opaque(sh0)->v[w], LDV, 32 * kb, 0, pt);
     }
+    sched_fence();
     // S' = exp(tot) S + K^T (end V)
-    const ChunkDecay& dec = lds_opaque(sh0)->dec[w];
+    const ChunkDecay& dec = lds_opaque(sh0)->dec[i & 1][w >> 1];
     const float tot = dec.btw[3];
     if (!OUT) total *= tot;
     Parts<E> vp[2][2];
@@ -434,18 +593,27 @@ __global__ __launch_bounds__(NW * 64) void sweep_value_kernel(SweepParams p, int
       }
     }
 #pragma unroll
-    for (int nt = 0; nt < NT; ++nt) {
+    for (int n2 = 0; n2 < NT; n2 += 2) {  // four accumulator chains at a time
+      sched_fence();
       Lds& sh = *lds_opaque(sh0);
-      S[nt][0] *= tot;
-      S[nt][1] *= tot;
+      Frag<E> kf[2][2];
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        const Frag<E> kf = ld_col(sh.k, LDK, 32 * kb, 32 * (nt >> 1), nt & 1);
+      for (int e = 0; e < 2; ++e) {
+        S[n2 + e][0] *= tot;
+        S[n2 + e][1] *= tot;
 #pragma unroll
-        for (int q = Parts<E>::N - 1; q >= 0; --q) {
-          mma(S[nt][0], kf, vp[kb][0].p[q]);
-          mma(S[nt][1], kf, vp[kb][1].p[q]);
-        }
+        for (int kb = 0; kb < 2; ++kb) kf[e][kb] = ld_col(sh.k, LDK, 32 * kb, 16 * n2, e);
+      }
+#pragma unroll
+      for (int q = Parts<E>::N - 1; q >= 0; --q) {
+        if (q >= np) continue;
+#pragma unroll
+        for (int kb = 0; kb < 2; ++kb)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            mma(S[n2 + e][0], kf[e][kb], vp[kb][0].p[q]);
+            mma(S[n2 + e][1], kf[e][kb], vp[kb][1].p[q]);
+          }
       }
     }
   }
@@ -477,8 +645,8 @@ struct KeyLds {
   f32x4 z[10][64];               // sum over slices of the decayed chunk matrix, by tile and lane
   float rti[4][HS][CH];          // row terms of the chunk itself, by source block
   float rtx[DK / 16][HS][CH];    // row terms of the state, by key tile
-  double anc[DK / 16][HS];
-  ChunkDecay dec[HS];
+  float anc[DK / 16][HS];
+  ChunkDecay dec[2][HS];         // of this chunk and the next
 };
 
 template <class E, int DK, int HS, bool REV>
@@ -491,6 +659,7 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
   const int part = blockIdx.x % parts, grp = blockIdx.x / parts % p.G, j = blockIdx.x / parts / p.G;
   SegRange r;
   if (!seg_range(p.seq, p.segs, p.seg_first, j, r)) return;
+  make_uniform(r);
   const bool first = REV ? r.s == r.ns - 1 : r.s == 0;
   const int rep = p.H / p.G, spg = rep * (p.Dv / PS), spv = p.Dv / PS;
   const int64_t st_off = (int64_t)DK * p.Dv;
@@ -521,52 +690,47 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
   auto dump_of = [&](int b, int s) {
     return reinterpret_cast<f32x4*>(p.dump) + ((((int64_t)j * nab + b) * nsl + slice_of(s)) * NW + nt) * 256 + l;
   };
-  TileStage<E, DK, NTH> tk, tq;
-  TileStage<E, PS, NTH> tv[HS], tw[HS];
+  TileStage<E, DK, NTH, REV> tk, tq;
+  TileStage<E, PS, NTH, REV> tv[HS], tw[HS];
   static_assert(HS <= NW, "one wave a slice forms its decays");
+  const int ko = tk.first_off(p.k_stride, tid), qo = tq.first_off(p.q_stride, tid);
+  const int vo = tv[0].first_off(p.v_stride, tid), wo = tw[0].first_off(p.w_stride, tid);
+  const int oo = row_off<REV, float>(t16, DK, krow);
+  // the last HS waves form the decays, one slice each
+  const int ds = nt - (NW - HS), dh = slice_of(max(ds, 0)) / spv;
   HeadConst hc;
-  hc.load(p, slice_of(nt) / spv);
-  float dt = 0.f;
+  hc.load(p, dh);
+  uint32_t dt = 0;  // of the next chunk
   auto request = [&](int i) {
     const ChunkRows c = chunk_rows<REV>(r, i);
-    dt = load_dt<REV>(p, c, slice_of(nt) / spv);
-    tk.template load<REV>(static_cast<const E*>(p.k) + (int64_t)grp * DK, p.k_stride, c, tid);
-    tq.template load<REV>(static_cast<const E*>(p.q) + (int64_t)grp * DK, p.q_stride, c, tid);
+    tk.load(static_cast<const E*>(p.k) + c.base * p.k_stride + (int64_t)grp * DK, p.k_stride, c.nt, ko);
+    tq.load(static_cast<const E*>(p.q) + c.base * p.q_stride + (int64_t)grp * DK, p.q_stride, c.nt, qo);
 #pragma unroll
     for (int s = 0; s < HS; ++s) {
-      tv[s].template load<REV>(static_cast<const E*>(p.v) + (int64_t)slice_of(s) * PS, p.v_stride, c, tid);
-      tw[s].template load<REV>(static_cast<const E*>(p.w) + (int64_t)slice_of(s) * PS, p.w_stride, c, tid);
+      tv[s].load(static_cast<const E*>(p.v) + c.base * p.v_stride + (int64_t)slice_of(s) * PS, p.v_stride, c.nt, vo);
+      tw[s].load(static_cast<const E*>(p.w) + c.base * p.w_stride + (int64_t)slice_of(s) * PS, p.w_stride, c.nt, wo);
     }
   };
-  if (nch > 0) request(0);
+  if (nch > 0) {
+    request(0);
+    if (ds >= 0) {
+      const ChunkRows c = chunk_rows<REV>(r, 0);
+      fill_decay<REV>(sh0->dec[0][ds], p, hc, load_dt<REV>(p, c, dh), c.nt);
+      if (nch > 1) dt = load_dt<REV>(p, chunk_rows<REV>(r, 1), dh);
+    }
+  }
   for (int i = 0; i < nch; ++i) {
     const ChunkRows c = chunk_rows<REV>(r, i);
     const int ci = REV ? nch - 1 - i : i;  // chunk within the segment
-    if (REV && ((ci + 1) % AB == 0 || i == 0)) {
-      Lds& sh = *lds_opaque(sh0);
-      // the state entering the chunk is the gradient of the state at its end
+    // backwards: the state entering the chunk is the gradient of the state at its end
+    const bool anchor = REV && ((ci + 1) % AB == 0 || i == 0);
+    f32x4 dump[4];  // of the next slice
+    auto request_dump = [&](int s) {
+      const f32x4* d = dump_of(ci / AB, s);
 #pragma unroll
-      for (int s = 0; s < HS; ++s) {
-        double a = 0.;
-        if (s < ns) {
-          const f32x4* d = dump_of(ci / AB, s);
-#pragma unroll
-          for (int pt = 0; pt < 4; ++pt) {
-            const f32x4 x = d[pt * 64];
-#pragma unroll
-            for (int e = 0; e < 4; ++e) a += (double)x[e] * T[s][pt][e];
-          }
-        }
-        a = wave_sum_d(a);
-        if (l == 0) sh.anc[nt][s] = a;
-      }
-      __syncthreads();
-      if (tid < ns) {
-        double a = 0.;
-        for (int n = 0; n < NW; ++n) a += sh.anc[n][tid];
-        p.anchor[((int64_t)j * nab + ci / AB) * nsl + slice_of(tid)] = a;
-      }
-    }
+      for (int pt = 0; pt < 4; ++pt) dump[pt] = d[pt * 64];
+    };
+    float anc[4] = {0.f, 0.f, 0.f, 0.f};
     __syncthreads();  // the previous chunk's reads are done
     {
       Lds& sh = *lds_opaque(sh0);
@@ -578,13 +742,17 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
         tw[s].store(sh.w[s], LDV, tid);
       }
     }
-    const float raw = dt;
+    const uint32_t dt1 = dt;
+    if (i + 2 < nch && ds >= 0) dt = load_dt<REV>(p, chunk_rows<REV>(r, i + 2), dh);
+    if (anchor) request_dump(0);
     if (i + 1 < nch) request(i + 1);
-    if (nt < HS) fill_decay<REV>(lds_opaque(sh0)->dec[nt], p, hc, raw, c.nt);
     __syncthreads();
-    // the chunk's own part: tiles of (rows s, columns t)
-    for (int idx = nt; idx < 10; idx += NW) {
+    // the chunk's own part: tiles of (rows s, columns t), the diagonal ones, which
+    // cost more, on the first four waves; of eight waves the others take the rest
+    // and the next chunk's decays
+    for (int n = nt; n < 10; n += NW == 8 && n < 4 ? 10 : 4) {
       Lds& sh = *lds_opaque(sh0);
+      const int idx = n == 0 ? 0 : n == 1 ? 2 : n == 2 ? 5 : n == 3 ? 9 : n == 4 ? 1 : n < 7 ? n - 2 : n - 1;
       int tb, sb;
       tri_tile(idx, tb, sb);
       f32x4 cb = zero4(), zs = zero4();
@@ -599,8 +767,10 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
         for (int e = 0; e < 4; ++e)
           if (4 * g4 + e == t16 && live) p.cb[(int64_t)grp * p.tokens + grow] = cb[e];
       }
+      float rts[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < HS; ++s) {
+        sched_fence();
         Lds& sh = *lds_opaque(sh0);
         f32x4 x = zero4();
 #pragma unroll
@@ -611,25 +781,29 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
           for (int e = 0; e < 4; ++e)
             if (4 * g4 + e == t16 && live) p.xd[(int64_t)slice_of(s) * p.tokens + grow] = x[e];
         }
-        const f32x4 z = x * tile_decay(sh.dec[s], tb, sb);
+        const f32x4 z = x * tile_decay<true>(sh.dec[i & 1][s], tb, sb);
         float rt = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (sb < tb || 4 * g4 + e < t16) rt += z[e] * cb[e];
-        rt += __shfl_xor(rt, 16, 64);
-        rt += __shfl_xor(rt, 32, 64);
-        if (g4 == 0) sh.rti[sb][s][row] = rt;
-        if (s < ns) zs += z * sh.dec[s].tw[row];
+        rts[s] = rt;
+        if (s < ns) zs += z * sh.dec[i & 1][s].tw[row];
       }
+      const float rt = sum_groups4(rts);  // slice g
+      if (g4 < HS) sh.rti[sb][g4][row] = rt;
       sh.z[idx][l] = zs;
     }
+    if (ds >= 0 && i + 1 < nch)
+      fill_decay<REV>(lds_opaque(sh0)->dec[(i + 1) & 1][ds], p, hc, dt1, chunk_rows<REV>(r, i + 1).nt);
     __syncthreads();
     Frag<E> kf[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) kf[kb] = ld_col(lds_opaque(sh0)->k, LDK, 32 * kb, 32 * (nt >> 1), nt & 1);
+    Parts<E> kp[2];  // K times its decay to the chunk's end, of the current slice's head
     f32x4 o[4];
 #pragma unroll
     for (int tb = 0; tb < 4; ++tb) {
+      sched_fence();
       Lds& sh = *lds_opaque(sh0);
       o[tb] = zero4();
 #pragma unroll
@@ -642,57 +816,76 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
 #pragma unroll
     for (int s = 0; s < HS; ++s) {
       if (s >= ns) break;
-      Parts<E> tp[2];
+      sched_fence();
+      if (anchor) {  // <state at the chunk's end, its gradient>, this lane's part
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) split(tp[kb], T[s][2 * kb], T[s][2 * kb + 1]);
+        for (int pt = 0; pt < 4; ++pt)
+          anc[s] += (dump[pt][0] * T[s][pt][0] + dump[pt][1] * T[s][pt][1]) + (dump[pt][2] * T[s][pt][2] + dump[pt][3] * T[s][pt][3]);
+        anc[s] = row16_sum(anc[s]);
+        if (s + 1 < ns) request_dump(s + 1);
+      }
+      // u = W T^T of the state before the chunk, four row blocks side by side
+      f32x4 u[4];
+#pragma unroll
+      for (int tb = 0; tb < 4; ++tb) u[tb] = zero4();
+#pragma unroll
+      for (int kb = 0; kb < 2; ++kb) {
+        Lds& sh = *lds_opaque(sh0);
+        Frag<E> wf[4];
+#pragma unroll
+        for (int tb = 0; tb < 4; ++tb) wf[tb] = ld_frag8(sh.w[s], LDV, 16 * tb + t16, 32 * kb);
+        Parts<E> tp;
+        split(tp, T[s][2 * kb], T[s][2 * kb + 1]);
+#pragma unroll
+        for (int q = Parts<E>::N - 1; q >= 0; --q)
+#pragma unroll
+          for (int tb = 0; tb < 4; ++tb) mma(u[tb], tp.p[q], wf[tb]);
+      }
+      sched_fence();
+      Lds& sh = *lds_opaque(sh0);
+      const ChunkDecay& dec = sh.dec[i & 1][s];
+      float rts[4];
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
-        Lds& sh = *lds_opaque(sh0);
-        const ChunkDecay& dec = sh.dec[s];
-        f32x4 u = zero4();
-#pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          const Frag<E> wf = ld_frag8(sh.w[s], LDV, 16 * tb + t16, 32 * kb);
-#pragma unroll
-          for (int q = Parts<E>::N - 1; q >= 0; --q) mma(u, tp[kb].p[q], wf);
-        }
         const int row = 16 * tb + t16;
         const float tf = dec.tf[row];
         const f32x4 q4 = ld4f<E>(sh.q + row * LDK + krow);
-        float rt = (u[0] * q4[0] + u[1] * q4[1]) + (u[2] * q4[2] + u[3] * q4[3]);
-        rt += __shfl_xor(rt, 16, 64);
-        rt += __shfl_xor(rt, 32, 64);
-        if (g4 == 0) sh.rtx[nt][s][row] = rt * tf;
-        o[tb] += u * (tf * dec.tw[row]);
+        rts[tb] = tf * ((u[tb][0] * q4[0] + u[tb][1] * q4[1]) + (u[tb][2] * q4[2] + u[tb][3] * q4[3]));
+        o[tb] += u[tb] * (REV ? tf * dec.tw[row] : tf);  // forwards the target weight is 1
       }
+      sh.rtx[nt][s][l] = sum_groups4(rts);  // block g: row l
       // T' = exp(tot) T + V^T (end K)
-      Lds& sh = *lds_opaque(sh0);
-      const ChunkDecay& dec = sh.dec[s];
-      Parts<E> kp[2];
+      if (s == 0 || slice_of(s) % spv == 0) {
 #pragma unroll
-      for (int kb = 0; kb < 2; ++kb) {
-        f32x4 lo, hi;
-        frag_f32(kf[kb], lo, hi);
-        split(kp[kb], lo * *reinterpret_cast<const f32x4*>(&dec.end[32 * kb + 4 * g4]),
-              hi * *reinterpret_cast<const f32x4*>(&dec.end[32 * kb + 16 + 4 * g4]));
+        for (int kb = 0; kb < 2; ++kb) {
+          f32x4 lo, hi;
+          frag_f32(ld_col(sh.k, LDK, 32 * kb, 32 * (nt >> 1), nt & 1), lo, hi);
+          split(kp[kb], lo * *reinterpret_cast<const f32x4*>(&dec.end[32 * kb + 4 * g4]),
+                hi * *reinterpret_cast<const f32x4*>(&dec.end[32 * kb + 16 + 4 * g4]));
+        }
       }
       const float tot = dec.btw[3];
 #pragma unroll
-      for (int pt = 0; pt < 4; ++pt) {
-        T[s][pt] *= tot;
+      for (int pt = 0; pt < 4; ++pt) T[s][pt] *= tot;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) {
-          const Frag<E> vf = ld_col(sh.v[s], LDV, 32 * kb, 32 * (pt >> 1), pt & 1);
+      for (int kb = 0; kb < 2; ++kb) {
+        Frag<E> vf[4];
 #pragma unroll
-          for (int q = Parts<E>::N - 1; q >= 0; --q) mma(T[s][pt], vf, kp[kb].p[q]);
-        }
+        for (int pt = 0; pt < 4; ++pt) vf[pt] = ld_col(sh.v[s], LDV, 32 * kb, 32 * (pt >> 1), pt & 1);
+#pragma unroll
+        for (int q = Parts<E>::N - 1; q >= 0; --q)
+#pragma unroll
+          for (int pt = 0; pt < 4; ++pt) mma(T[s][pt], vf[pt], kp[kb].p[q]);
       }
     }
+    if (anchor) {
+      const float a = sum_groups4(anc);  // slice g
+      if (t16 == 0 && g4 < HS) lds_opaque(sh0)->anc[nt][g4] = a;
+    }
+    {
+      const RowBuf out = row_buf<REV>(p.out2 + ((int64_t)(grp * parts + part) * p.tokens + c.base) * DK, DK, DK, c.nt);
 #pragma unroll
-    for (int tb = 0; tb < 4; ++tb) {
-      const int row = 16 * tb + t16;
-      if (row < c.nt)
-        *reinterpret_cast<f32x4*>(p.out2 + ((int64_t)(grp * parts + part) * p.tokens + row_of<REV>(c, row)) * DK + krow) = o[tb];
+      for (int tb = 0; tb < 4; ++tb) st16(out, oo + (REV ? -tb : tb) * 16 * DK * 4, o[tb]);
     }
     if (!REV && ((ci + 1) % AB == 0 || ci + 1 == nch)) {
 #pragma unroll
@@ -705,6 +898,11 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
     }
     __syncthreads();
     Lds& sh = *lds_opaque(sh0);
+    if (anchor && tid < ns) {
+      double a = 0.;
+      for (int n = 0; n < NW; ++n) a += sh.anc[n][tid];
+      p.anchor[((int64_t)j * nab + ci / AB) * nsl + slice_of(tid)] = a;
+    }
     for (int k = tid; k < ns * CH; k += NTH) {
       const int s = k / CH, row = k % CH;
       if (row < c.nt) {
@@ -719,20 +917,21 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
   if (REV && p.h0 && r.s == 0) {
     Lds& sh = *sh0;
     // <h0, its gradient>: the anchor at the sequence's start
+    float anc[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-    for (int s = 0; s < HS; ++s) {
-      double a = 0.;
+    for (int s = 0; s < HS; ++s)
       if (s < ns) {
         const int sl = slice_of(s);
         const float* s0 = p.h0 + ((int64_t)r.n * p.H + sl / spv) * st_off + (int64_t)kcol * p.Dv + sl % spv * PS;
 #pragma unroll
         for (int pt = 0; pt < 4; ++pt)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) a += (double)T[s][pt][i] * s0[32 * (pt >> 1) + 8 * g4 + 4 * (pt & 1) + i];
+          for (int i = 0; i < 4; ++i) anc[s] += T[s][pt][i] * s0[32 * (pt >> 1) + 8 * g4 + 4 * (pt & 1) + i];
+        anc[s] = row16_sum(anc[s]);
       }
-      a = wave_sum_d(a);
-      if (l == 0) sh.anc[nt][s] = a;
-    }
+    __syncthreads();
+    const float part_sum = sum_groups4(anc);
+    if (t16 == 0 && g4 < HS) sh.anc[nt][g4] = part_sum;
     __syncthreads();
     if (tid < ns) {
       double a = 0.;
