@@ -28,20 +28,28 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanJoinParams p) {
   }
 }
 
-// rt_t - D_t ct_t of token t of a segment (0 past the end t1).
-__device__ __forceinline__ double diff_at(const ScanGradParams& p, const SegRange& r, int t, int t1, int h, float bias) {
-  if (t >= t1) return 0.;
+// A token's step in the recursion of da: da_t = da_{t+1} + v, or v alone (cut)
+// where the token's own decay is below fp32's unit round-off: what is left of
+// da_{t+1} - D_t ct_t = <., exp(a_t) h_{t-1}> there is below the rounding of
+// its two parts, which the step |A| in ddt would multiply.
+struct DaStep { double v; bool cut; };
+__device__ __forceinline__ DaStep da_step(const ScanGradParams& p, const SegRange& r, int t, int t1, int h, float A,
+                                          float bias) {
+  DaStep o{0., false};
+  if (t >= t1) return o;
   const int nsl = p.Dv / PS;
   const int64_t row = r.row0 + t;
   const float raw = scan_dt_raw(p.dt, p.dt_f32, row * p.dt_stride + h) + bias;
   const float d = p.softplus ? scan_softplus(raw) : raw;
   double rt = 0., ct = 0.;
   for (int s = 0; s < nsl; ++s) {
-    const int64_t o = ((int64_t)h * nsl + s) * p.tokens + row;
-    rt += p.rt[o];
-    ct += p.ct[o];
+    const int64_t at = ((int64_t)h * nsl + s) * p.tokens + row;
+    rt += p.rt[at];
+    ct += p.ct[at];
   }
-  return rt - d * ct;
+  o.cut = d * A < LN_EPS;
+  o.v = o.cut ? rt : rt - d * ct;
+  return o;
 }
 
 // ddt of every token and each anchor block's sums for dA, dD and ddt_bias: a
@@ -68,9 +76,14 @@ __global__ __launch_bounds__(64) void scan_grad_kernel(ScanGradParams p, int nab
     // the differences of the block's tokens, and their suffix sums in each 64-token piece
     const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
     double sum = 0.;
-    for (int b = t0; b < t1; b += 64) sum += wave_sum_d(diff_at(p, r, b + l, t1, h, bias));
+    bool cut = false;
+    for (int b = t0; b < t1; b += 64) {
+      const DaStep st = da_step(p, r, b + l, t1, h, A, bias);
+      sum += wave_sum_d(st.v);
+      cut |= __any(st.cut);
+    }
     // what the sums miss the start's product by, per token
-    const double miss = (start - carry - sum) / (t1 - t0);
+    const double miss = cut ? 0. : (start - carry - sum) / (t1 - t0);
     for (int b = t0 + (t1 - t0 - 1) / 64 * 64; b >= t0; b -= 64) {
       const int t = b + l;
       const bool in = t < t1;
@@ -83,14 +96,20 @@ __global__ __launch_bounds__(64) void scan_grad_kernel(ScanGradParams p, int nab
         ct += p.ct[o];
         xd += p.xd[o];
       }
-      double suf = diff_at(p, r, t, t1, h, bias) + (in ? miss : 0.);
+      const DaStep st = da_step(p, r, t, t1, h, A, bias);
+      double suf = st.v + (in ? miss : 0.);
+      int ended = st.cut;  // a cut at or behind this token, within the piece
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const double y = __shfl_down(suf, o, 64);
-        if (l + o < 64) suf += y;
+        const int f = __shfl_down(ended, o, 64);
+        if (l + o < 64 && !ended) {
+          suf += y;
+          ended = f;
+        }
       }
-      const double da = carry + suf;
-      carry += __shfl(suf, 0, 64);
+      const double da = ended ? suf : carry + suf;
+      carry = __shfl(da, 0, 64);
       double dd = ct + p.cb[(int64_t)g * p.tokens + row] * xd + A * da;
       if (p.softplus) dd *= 1.f / (1.f + expf(-raw));
       if (in) {
