@@ -33,6 +33,18 @@ template <> struct VecIO<bf16, 8> {
                                            (bf16)f[4], (bf16)f[5], (bf16)f[6], (bf16)f[7]};
   }
 };
+template <> struct VecIO<bf16, 4> {
+  typedef bf16x4 raw;
+  static __device__ __forceinline__ raw load(const bf16* p) { return *reinterpret_cast<const bf16x4*>(p); }
+  static __device__ __forceinline__ raw zero() { return raw{}; }
+  static __device__ __forceinline__ void get(const raw& r, float (&f)[4]) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = (float)r[i];
+  }
+  static __device__ __forceinline__ void store(bf16* p, const float (&f)[4]) {
+    *reinterpret_cast<bf16x4*>(p) = bf16x4{(bf16)f[0], (bf16)f[1], (bf16)f[2], (bf16)f[3]};
+  }
+};
 template <> struct VecIO<float, 4> {
   typedef f32x4 raw;
   static __device__ __forceinline__ raw load(const float* p) { return *reinterpret_cast<const f32x4*>(p); }
@@ -47,6 +59,17 @@ template <> struct VecIO<float, 4> {
 };
 // Elements of one 16-byte access.
 template <class E> constexpr int kVec = 16 / (int)sizeof(E);
+
+// sigmoid(x) and the SiLU gate with the hardware's exponential and reciprocal
+// (each within about one unit in the last place of fp32): the exact division of
+// sigmoid_f takes ten instructions, a third of what these memory-bound kernels
+// spend on an element.  exp overflow gives 1 / inf = 0.
+__device__ __forceinline__ float fast_sigmoid(float x) {
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * x));
+}
+__device__ __forceinline__ float silu_gate(float x) { return x * fast_sigmoid(x); }
+// its derivative, from x and sigmoid(x)
+__device__ __forceinline__ float dsilu_gate(float x, float s) { return s + x * (s - s * s); }
 
 // ---------------------------------------------------------------- short causal convolution
 struct ConvParams {

@@ -21,7 +21,8 @@ gdn_status check_conv(const gdn_conv_args& a) {
   if (a.W < 2 || a.W > 4) return fail(GDN_E_UNSUPPORTED, "unsupported convolution width %d (2 to 4)", a.W);
   if (a.silu != 0 && a.silu != 1) return fail(GDN_E_INVALID, "silu must be 0 or 1");
   const size_t es = esize(a.dtype);
-  if ((long long)a.B * a.T >= (1LL << 40) / a.D) return fail(GDN_E_INVALID, "problem too large");
+  // (token indices plus a run and its halo stay below 2^31)
+  if ((long long)a.B * a.T >= std::min((1LL << 40) / a.D, (1LL << 31) - 1024)) return fail(GDN_E_INVALID, "problem too large");
   if (a.cu_seqlens) {
     if (a.B != 1) return fail(GDN_E_INVALID, "cu_seqlens requires B == 1 (got %d)", a.B);
     if (a.num_seqs < 1) return fail(GDN_E_INVALID, "num_seqs must be >= 1 with cu_seqlens");
@@ -62,7 +63,8 @@ int conv_run(const gdn_conv_args& a, bool vec, int lo, int hi, int waves_per_cu)
   return run;
 }
 bool conv_vec(const gdn_conv_args& a) {
-  return vec_row(a.x, a.D, a.dtype) && vec_row(a.x, a.x_stride, a.dtype) && vec_row(a.init, a.D, a.dtype);
+  return vec_row(a.x, a.D, a.dtype) && vec_row(a.x, a.x_stride, a.dtype) && aligned(a.init, 16) && aligned(a.w, 16) &&
+         aligned(a.bias, 16);
 }
 int64_t runs_of(const gdn_conv_args& a, int run) { return ((int64_t)a.B * a.T + run - 1) / run; }
 
@@ -271,11 +273,14 @@ gdn::NormParams norm_params(const gdn_norm_args& a) {
   p.R = a.R; p.G = a.G; p.D = a.D; p.shared = a.shared; p.center = a.center; p.gate_first = a.gate_first; p.eps = a.eps;
   return p;
 }
-// Workgroups of the gradient: about four a compute unit, but no more than a
-// weight group has rows; each writes one row of parts.
+// Workgroups of the gradient, per weight group: each walks many rows and writes
+// one row of parts, so about as many as are resident at once (rows of up to 64
+// vectors: four a compute unit; longer ones, with more registers: two), but no
+// more than there are rows.
 int norm_blocks(const gdn_norm_args& a) {
   const int64_t groups = a.shared ? 1 : a.G, rows = a.shared ? a.R * a.G : a.R;
-  return (int)std::max<int64_t>(1, std::min<int64_t>(rows, 4LL * cu_count() / groups));
+  const int64_t per_cu = a.D * (int64_t)esize(a.dtype) <= 64 * 16 ? 4 : 2;
+  return (int)std::max<int64_t>(1, std::min<int64_t>(rows, per_cu * cu_count() / groups));
 }
 size_t norm_part_bytes(const gdn_norm_args& a) {
   return sizeof(float) * (a.shared ? 1 : a.G) * (size_t)norm_blocks(a) * (a.bias ? 2 : 1) * a.D;
@@ -355,7 +360,8 @@ gdn_status gdn_conv_step(const gdn_conv_step_args* args, void* stream) {
   gdn::ConvStepParams p{};
   p.x = a.x; p.x_stride = a.x_stride; p.state = a.state; p.state_idx = a.state_idx; p.num_slots = a.num_slots;
   p.w = a.w; p.bias = a.bias; p.y = a.y; p.N = a.N; p.D = a.D; p.silu = a.silu;
-  const bool vec = vec_row(a.x, a.D, a.dtype) && vec_row(a.x, a.x_stride, a.dtype) && aligned(a.state, 16) && aligned(a.y, 16);
+  const bool vec = vec_row(a.x, a.D, a.dtype) && vec_row(a.x, a.x_stride, a.dtype) && aligned(a.state, 16) && aligned(a.y, 16) &&
+                   aligned(a.w, 16) && aligned(a.bias, 16);
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = timed("conv_step", s, [&] { return gdn::launch_conv_step(a.dtype, a.W, vec, p, s); });
   return e == hipSuccess ? GDN_OK : hip_fail(e, "convolution step launch");

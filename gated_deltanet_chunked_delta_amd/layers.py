@@ -16,17 +16,19 @@ is free.  Tensors of a call share one device, whose current stream it uses.
 """
 from __future__ import annotations
 
+import contextlib
 import ctypes
 from typing import Optional
 
 import torch
 from torch.autograd.function import once_differentiable
 
-from .binding import GDNError, _check, _dtype_code, _ptr, _stream, _vp, lib as _load
+from .binding import GDNError, _check, _dtype_code, _ptr, _vp, lib as _load
 
 __all__ = ["short_conv", "selective_scan", "gated_group_norm", "gdn_conv_fwd", "gdn_conv_bwd", "gdn_conv_step",
            "gdn_scan_fwd", "gdn_scan_bwd", "gdn_scan_step", "gdn_norm_fwd", "gdn_norm_bwd"]
 
+_NO_SWITCH = contextlib.nullcontext()
 _i32, _i64, _sz = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
 
 
@@ -114,6 +116,8 @@ def lib():
 # ------------------------------------------------------------------ argument checks
 def _t(name, t, shape, dtype, dev, optional=False):
     """A contiguous tensor of this shape, dtype and device (or None)."""
+    if t is not None and t.shape == shape and t.dtype is dtype and t.device == dev and t.is_contiguous():
+        return t
     if t is None:
         if optional:
             return None
@@ -132,13 +136,17 @@ def _t(name, t, shape, dtype, dev, optional=False):
 def _rows(name, t, shape, inner, dtype, dev):
     """The token stride of a tensor of this shape whose last `inner` dimensions are
     contiguous and whose tokens (the dimensions before) lie evenly apart."""
-    if tuple(t.shape) != tuple(shape):
+    if t.shape != shape:
         raise GDNError(f"{name} must be {list(shape)}, got {list(t.shape)}")
     if t.dtype != dtype:
         raise GDNError(f"{name} must be {dtype}, got {t.dtype}")
     if t.device != dev:
         raise GDNError(f"{name} must be on {dev}, got {t.device}")
     nd, width = t.dim(), 1
+    if t.is_contiguous():
+        for n in shape[nd - inner:]:
+            width *= n
+        return width
     for d in range(nd - 1, nd - 1 - inner, -1):
         if t.shape[d] != 1 and t.stride(d) != width:
             raise GDNError(f"the entries of one token of {name} must be contiguous")
@@ -192,9 +200,16 @@ def _on_gpu(name, t):
     return t.device
 
 
+def _on(dev):
+    """The device made current for a call, where it is not already."""
+    return _NO_SWITCH if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
+
+
 def _call(fn, args, dev):
-    with torch.cuda.device(dev):
-        _check(fn(ctypes.byref(args), _vp(_stream(dev))))
+    with _on(dev):
+        status = fn(ctypes.byref(args), torch.cuda.current_stream(dev).cuda_stream)
+    if status:
+        _check(status)
 
 
 # ------------------------------------------------------------------ short causal convolution
@@ -253,7 +268,7 @@ def gdn_conv_bwd(x, weight, dy, bias=None, silu: bool = True, initial_state=None
     args = ConvBwdArgs()
     args.a = a
     args.dy, args.dfinal, args.dx, args.dw, args.dbias, args.dinit = map(_ptr, (dy, dfinal, dx, dw, db, di))
-    with torch.cuda.device(dev):
+    with _on(dev):
         ws = _workspace(lib().gdn_conv_bwd_workspace_size(ctypes.byref(args)), dev)
     args.workspace, args.workspace_bytes = ws.data_ptr(), ws.numel()
     _call(lib().gdn_conv_bwd, args, dev)
@@ -358,7 +373,7 @@ def gdn_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus: bool = False
     args = ScanFwdArgs()
     args.a, args.y, args.hT = a, _ptr(y), _ptr(hT)
     states = None
-    with torch.cuda.device(dev):
+    with _on(dev):
         if save_states:
             states = torch.empty(max(4, L.gdn_scan_states_bytes(ctypes.byref(a)) // 4), dtype=torch.float32, device=dev)
             args.h_save = _ptr(states)
@@ -383,7 +398,7 @@ def gdn_scan_bwd(x, dt, A, B, C, dy, D=None, dt_bias=None, dt_softplus: bool = F
     args.a = a
     args.dy, args.dhT, args.dx, args.ddt, args.db, args.dc, args.dA, args.dD, args.ddt_bias, args.dh0 = map(
         _ptr, (dy, dhT, dx, ddt, db, dc, dA, dD, dbias, dh0))
-    with torch.cuda.device(dev):
+    with _on(dev):
         if states is not None:
             _t("states", states, states.shape, torch.float32, dev)
             if states.numel() * 4 < L.gdn_scan_states_bytes(ctypes.byref(a)):
@@ -518,7 +533,7 @@ def gdn_norm_bwd(x, weight, dy, z=None, bias=None, eps: float = 1e-5, center: bo
     new = lambda t: None if t is None else torch.empty(t.shape, dtype=t.dtype, device=dev)
     dx, dw, dz, db = map(new, (x, weight, z, bias))
     args.dy, args.dx, args.dw, args.dz, args.dbias = map(_ptr, (dy, dx, dw, dz, db))
-    with torch.cuda.device(dev):
+    with _on(dev):
         ws = _workspace(lib().gdn_norm_bwd_workspace_size(ctypes.byref(args)), dev)
     args.workspace, args.workspace_bytes = ws.data_ptr(), ws.numel()
     _call(lib().gdn_norm_bwd, args, dev)
