@@ -137,7 +137,7 @@ hipError_t launch_norm_bwd(int dtype, bool vec, const NormParams& p, hipStream_t
 
 // ---------------------------------------------------------------- selective state space scan
 constexpr int PS = 64;       // value columns of one slice: a head of Dv columns is Dv / PS slices
-constexpr int AB = 2;        // chunks between two anchors of the decay gradient
+constexpr int AB = 1;        // chunks between two anchors of the decay gradient
 
 // One sweep over the tokens of every segment, forwards or backwards in time,
 // with a Dk x PS slice of the state per (segment, head, slice):

@@ -56,18 +56,20 @@ template <> struct Parts<float> {
   static constexpr int N = 1;
   Frag<float> p[1];
 };
+template <int NP = 3>
 __device__ __forceinline__ void split(Parts<float>& o, const f32x4& lo, const f32x4& hi) { pack_frag(o.p[0], lo, hi); }
+template <int NP = 3>
 __device__ __forceinline__ void split(Parts<bf16>& o, const f32x4& lo, const f32x4& hi) {
   typedef uint32_t u32x4 __attribute__((__vector_size__(16)));
   float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
-  for (int part = 0; part < 3; ++part) {
+  for (int part = 0; part < NP; ++part) {
     u32x4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t a = __builtin_bit_cast(uint32_t, x[2 * i]), b = __builtin_bit_cast(uint32_t, x[2 * i + 1]);
       v[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);  // the two high halves
-      if (part < 2) {
+      if (part < NP - 1) {
         x[2 * i] -= __builtin_bit_cast(float, a & 0xFFFF0000u);
         x[2 * i + 1] -= __builtin_bit_cast(float, b & 0xFFFF0000u);
       }
@@ -110,6 +112,14 @@ __device__ __forceinline__ void frag_f32(const Frag<float>& f, f32x4& lo, f32x4&
   lo = f.lo;
   hi = f.hi;
 }
+
+// The matrix cores' sums come out low by a fraction of a unit in the last place
+// on average, whatever their sign.  A state gathers such errors chunk by chunk,
+// and dA and the bias's gradient add products of two states over all tokens: 1e-6
+// of dA at 16,384 tokens, of one sign in every head.  So a state is kept with its
+// sign turned over from chunk to chunk (sign_of is the sign before chunk i) and
+// the errors of neighbouring chunks cancel: 3e-7, the fp32 terms' own noise.
+__device__ __forceinline__ float sign_of(int i) { return i & 1 ? -1.f : 1.f; }
 
 // Keeps the instruction scheduler from moving work across: without it the reads
 // of every unrolled step are hoisted to the front and registers spill.
@@ -368,9 +378,19 @@ struct TileStage {
 // output).
 constexpr int VC = 32;
 
+// Four floats at a 4-byte aligned address (a caller's state).
+typedef f32x4 __attribute__((aligned(4))) f32x4_u;
+__device__ __forceinline__ f32x4 ld_f32x4(const float* p) { return *reinterpret_cast<const f32x4_u*>(p); }
+__device__ __forceinline__ void st_f32x4(float* p, const f32x4& v) { *reinterpret_cast<f32x4_u*>(p) = v; }
+
+// bf16: the next chunk's K has a place of its own, so that it (and Q and V,
+// whose last reads come earlier) is staged during a chunk and one barrier
+// stands between chunks; in fp32 LDS does not hold it.
+template <class E> constexpr int kKeyBufs = sizeof(E) == 2 ? 2 : 1;
+
 template <class E, int DK, int NW>
 struct ValueLds {
-  E k[CH * row_ld<E>(DK)];
+  E k[kKeyBufs<E>][CH * row_ld<E>(DK)];
   E q[CH * row_ld<E>(DK)];
   E v[NW][CH * row_ld<E>(VC)];
   f32x4 cb[10][64];
@@ -406,23 +426,6 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
   const int64_t st_off = (int64_t)DK * p.Dv;
   const float Dh = OUT && p.D ? p.D[h] : 0.f;
 
-  // state tile (nt, pt), entry i: key 32 (nt / 2) + 8 g + 4 (nt % 2) + i, value col + 8 a + 4 pt + b (lane 16 g + 4 a + b)
-  f32x4 S[NT][2];
-  const int vcol = col + 8 * (t16 >> 2) + (t16 & 3);
-  auto key_of = [&](int nt) { return 32 * (nt >> 1) + 8 * g4 + 4 * (nt & 1); };
-#pragma unroll
-  for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-    for (int pt = 0; pt < 2; ++pt) S[nt][pt] = zero4();
-  if (OUT && p.s_in && (p.per_seg || first)) {
-    const float* s0 = p.s_in + ((int64_t)(p.per_seg ? j : r.n) * p.H + h) * st_off + vcol;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) S[nt][pt][i] = s0[(int64_t)(key_of(nt) + i) * p.Dv + 4 * pt];
-  }
   // The state leaves as fp32 from the state sweep and from a sequence's last
   // segment; elsewhere only bf16 outputs read it, and two parts (16 bits) of
   // the values are enough.
@@ -441,28 +444,61 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
     if (OUT) tq.load(static_cast<const E*>(p.q) + c.base * p.q_stride + (int64_t)grp * DK, p.q_stride, c.nt, qo);
     tv.load(static_cast<const E*>(p.v) + c.base * p.v_stride + (int64_t)h * p.Dv + col, p.v_stride, c.nt, vo);
   };
-  if (nch > 0) {
+  constexpr bool AHEAD = kKeyBufs<E> == 2;
+  auto stage_q = [&] { if (OUT) tq.store(lds_opaque(sh0)->q, LDK, tid); };
+  auto stage_k = [&](int i) { tk.store(lds_opaque(sh0)->k[AHEAD ? i & 1 : 0], LDK, tid); };
+  auto stage_v = [&] { tv.store(lds_opaque(sh0)->v[w], LDV, l); };
+  uint32_t dt0 = 0;
+  if (nch > 0) {  // the first chunk's requests before the state's
+    if ((w & 1) == 0) dt0 = load_dt<REV>(p, chunk_rows<REV>(r, 0), h);
     request(0);
+  }
+  // state tile (nt, pt), entry i: key 32 (nt / 2) + 8 g + 4 (nt % 2) + i, value
+  // col + 8 a + 4 pt + b (lane 16 g + 4 a + b); in memory a lane moves four
+  // values of key + b, turned over within the four lanes.
+  f32x4 S[NT][2];
+  const int64_t srow = (int64_t)(8 * g4 + (l & 3)) * p.Dv + col + 8 * (t16 >> 2);
+  auto key0 = [&](int nt) { return 32 * (nt >> 1) + 4 * (nt & 1); };
+#pragma unroll
+  for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+    for (int pt = 0; pt < 2; ++pt) S[nt][pt] = zero4();
+  if (OUT && p.s_in && (p.per_seg || first)) {
+    const float* s0 = p.s_in + ((int64_t)(p.per_seg ? j : r.n) * p.H + h) * st_off + srow;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < 2; ++pt) S[nt][pt] = ld_f32x4(s0 + key0(nt) * p.Dv + 4 * pt);
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int pt = 0; pt < 2; ++pt) S[nt][pt] = quad_transpose(S[nt][pt]);
+  }
+  if (nch > 0) {
     if ((w & 1) == 0) {
-      const ChunkRows c = chunk_rows<REV>(r, 0);
-      fill_decay<REV>(sh0->dec[0][w >> 1], p, hc, load_dt<REV>(p, c, h), c.nt);
+      fill_decay<REV>(sh0->dec[0][w >> 1], p, hc, dt0, chunk_rows<REV>(r, 0).nt);
       if (nch > 1) dt = load_dt<REV>(p, chunk_rows<REV>(r, 1), h);
     }
+    stage_k(0);
+    stage_q();
+    stage_v();
+    if (nch > 1) request(1);
   }
   float total = 1.f;
   for (int i = 0; i < nch; ++i) {
     const ChunkRows c = chunk_rows<REV>(r, i);
-    __syncthreads();  // the previous chunk's reads are done
-    {
-      Lds& sh = *lds_opaque(sh0);
-      tk.store(sh.k, LDK, tid);
-      if (OUT) tq.store(sh.q, LDK, tid);
-      tv.store(sh.v[w], LDV, l);
+    __syncthreads();  // this chunk's tiles are in place, the previous one's are read
+    if (!AHEAD && i > 0) {
+      stage_k(i);
+      stage_q();
+      stage_v();
+      if (i + 1 < nch) request(i + 1);
+      __syncthreads();
     }
+    const int kb_ = AHEAD ? i & 1 : 0;
+    const float sg = sign_of(i);
     const uint32_t dt1 = dt;
     if (i + 2 < nch && (w & 1) == 0) dt = load_dt<REV>(p, chunk_rows<REV>(r, i + 2), h);
-    if (i + 1 < nch) request(i + 1);
-    __syncthreads();
     // even waves, once a chunk: the next chunk's decays
     auto next_decay = [&] {
       if (i + 1 < nch) fill_decay<REV>(lds_opaque(sh0)->dec[(i + 1) & 1][w >> 1], p, hc, dt1, chunk_rows<REV>(r, i + 1).nt);
@@ -476,7 +512,7 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
         f32x4 a = zero4();
 #pragma unroll
         for (int kb = 0; kb < DK / 32; ++kb)
-          mma(a, ld_frag8(sh.k, LDK, 16 * sb + t16, 32 * kb), ld_frag8(sh.q, LDK, 16 * tb + t16, 32 * kb));
+          mma(a, ld_frag8(sh.k[kb_], LDK, 16 * sb + t16, 32 * kb), ld_frag8(sh.q, LDK, 16 * tb + t16, 32 * kb));
         sh.cb[idx][l] = a;
       }
       __syncthreads();
@@ -522,6 +558,10 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
 #pragma unroll
         for (int pt = 0; pt < 2; ++pt) vf[kb][pt] = ld_col(lds_opaque(sh0)->v[w], LDV, 32 * kb, 0, pt);
       __syncthreads();
+      if (AHEAD && i + 1 < nch) {  // Q has been read, the other K buffer is free
+        stage_q();
+        stage_k(i + 1);
+      }
       const RowBuf out = row_buf<REV>(static_cast<const E*>(p.out1) + c.base * p.H * p.Dv + (int64_t)h * p.Dv + col,
                                       p.H * p.Dv, VC, c.nt, active);
 #pragma unroll
@@ -529,7 +569,7 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
         sched_fence();
         Lds& sh = *lds_opaque(sh0);
         const ChunkDecay& dec = sh.dec[i & 1][w >> 1];
-        const float tf = dec.tf[16 * tb + t16];
+        const float tf = dec.tf[16 * tb + t16] * sg;
         o[tb][0] *= tf;
         o[tb][1] *= tf;
 #pragma unroll
@@ -570,26 +610,32 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
       }
     } else {
       if ((w & 1) == 0) next_decay();
+      if (AHEAD && i + 1 < nch) stage_k(i + 1);
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
 #pragma unroll
         for (int pt = 0; pt < 2; ++pt) vf[kb][pt] = ld_col(lds_opaque(sh0)->v[w], LDV, 32 * kb, 0, pt);
     }
+    if (AHEAD && i + 1 < nch) {
+      stage_v();  // (the wave's own)
+      if (i + 2 < nch) request(i + 2);
+    }
     sched_fence();
     // S' = exp(tot) S + K^T (end V)
     const ChunkDecay& dec = lds_opaque(sh0)->dec[i & 1][w >> 1];
-    const float tot = dec.btw[3];
-    if (!OUT) total *= tot;
+    const float tot = -dec.btw[3];
+    if (!OUT) total *= -tot;
     Parts<E> vp[2][2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) {
-      const f32x4 e0 = *reinterpret_cast<const f32x4*>(&dec.end[32 * kb + 4 * g4]);
-      const f32x4 e1 = *reinterpret_cast<const f32x4*>(&dec.end[32 * kb + 16 + 4 * g4]);
+      const f32x4 e0 = *reinterpret_cast<const f32x4*>(&dec.end[32 * kb + 4 * g4]) * -sg;
+      const f32x4 e1 = *reinterpret_cast<const f32x4*>(&dec.end[32 * kb + 16 + 4 * g4]) * -sg;
 #pragma unroll
       for (int pt = 0; pt < 2; ++pt) {
         f32x4 lo, hi;
         frag_f32(vf[kb][pt], lo, hi);
-        split(vp[kb][pt], lo * e0, hi * e1);
+        if (np == Parts<E>::N) split(vp[kb][pt], lo * e0, hi * e1);
+        else split<2>(vp[kb][pt], lo * e0, hi * e1);
       }
     }
 #pragma unroll
@@ -602,7 +648,7 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
         S[n2 + e][0] *= tot;
         S[n2 + e][1] *= tot;
 #pragma unroll
-        for (int kb = 0; kb < 2; ++kb) kf[e][kb] = ld_col(sh.k, LDK, 32 * kb, 16 * n2, e);
+        for (int kb = 0; kb < 2; ++kb) kf[e][kb] = ld_col(sh.k[kb_], LDK, 32 * kb, 16 * n2, e);
       }
 #pragma unroll
       for (int q = Parts<E>::N - 1; q >= 0; --q) {
@@ -619,13 +665,11 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
   }
   float* dst = OUT ? (last ? p.s_end : nullptr) : p.s_loc;
   if (!dst || !active) return;
-  dst += ((int64_t)(OUT ? r.n : j) * p.H + h) * st_off + vcol;
+  dst += ((int64_t)(OUT ? r.n : j) * p.H + h) * st_off + srow;
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int pt = 0; pt < 2; ++pt)
-#pragma unroll
-      for (int i = 0; i < 4; ++i) dst[(int64_t)(key_of(nt) + i) * p.Dv + 4 * pt] = S[nt][pt][i];
+    for (int pt = 0; pt < 2; ++pt) st_f32x4(dst + key0(nt) * p.Dv + 4 * pt, quad_transpose(S[nt][pt] * sign_of(nch)));
   if (!OUT && l == 0 && col == 0) p.s_dec[(int64_t)j * p.H + h] = total;
 }
 
@@ -669,21 +713,6 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
   const int kcol = 32 * (nt >> 1) + 8 * (t16 >> 2) + 4 * (nt & 1) + (t16 & 3);
   const int krow = 32 * (nt >> 1) + 8 * g4 + 4 * (nt & 1);
 
-  // state tile pt of slice s, entry i: value 32 (pt / 2) + 8 g + 4 (pt % 2) + i, key kcol
-  f32x4 T[HS][4];
-#pragma unroll
-  for (int s = 0; s < HS; ++s) {
-#pragma unroll
-    for (int pt = 0; pt < 4; ++pt) T[s][pt] = zero4();
-    if (s < ns && p.s_in && (p.per_seg || first)) {
-      const int sl = slice_of(s);
-      const float* s0 = p.s_in + ((int64_t)(p.per_seg ? j : r.n) * p.H + sl / spv) * st_off + (int64_t)kcol * p.Dv + sl % spv * PS;
-#pragma unroll
-      for (int pt = 0; pt < 4; ++pt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) T[s][pt][i] = s0[32 * (pt >> 1) + 8 * g4 + 4 * (pt & 1) + i];
-    }
-  }
   const int nch = (r.len + CH - 1) / CH, nab = (p.seq.segc + AB - 1) / AB;
   const int nsl = p.H * spv;  // slices of all heads
   // the state at anchor block b of this segment: [tile of 16 keys][pt][lane] per slice
@@ -696,8 +725,12 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
   const int ko = tk.first_off(p.k_stride, tid), qo = tq.first_off(p.q_stride, tid);
   const int vo = tv[0].first_off(p.v_stride, tid), wo = tw[0].first_off(p.w_stride, tid);
   const int oo = row_off<REV, float>(t16, DK, krow);
-  // the last HS waves form the decays, one slice each
-  const int ds = nt - (NW - HS), dh = slice_of(max(ds, 0)) / spv;
+  // heads of the slices: their decays are formed by one wave each, of eight waves
+  // first the last two, which have the least of the chunk matrix
+  const int head0 = slice_of(0) / spv, nheads = slice_of(ns - 1) / spv - head0 + 1;
+  auto head_of = [&](int s) { return slice_of(s) / spv - head0; };
+  const int dw = NW == 8 ? (nt >= 6 ? nt - 6 : nt >= 4 ? HS : 5 - nt) : nt;
+  const int ds = dw < nheads ? dw : -1, dh = head0 + max(ds, 0);
   HeadConst hc;
   hc.load(p, dh);
   uint32_t dt = 0;  // of the next chunk
@@ -711,17 +744,47 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
       tw[s].load(static_cast<const E*>(p.w) + c.base * p.w_stride + (int64_t)slice_of(s) * PS, p.w_stride, c.nt, wo);
     }
   };
-  if (nch > 0) {
+  auto stage = [&] {
+    Lds& sh = *lds_opaque(sh0);
+    tk.store(sh.k, LDK, tid);
+    tq.store(sh.q, LDK, tid);
+#pragma unroll
+    for (int s = 0; s < HS; ++s) {
+      tv[s].store(sh.v[s], LDV, tid);
+      tw[s].store(sh.w[s], LDV, tid);
+    }
+  };
+  uint32_t dt0 = 0;
+  if (nch > 0) {  // the first chunk's requests before the state's
+    if (ds >= 0) dt0 = load_dt<REV>(p, chunk_rows<REV>(r, 0), dh);
     request(0);
+  }
+  // state tile pt of slice s, entry i: value 32 (pt / 2) + 8 g + 4 (pt % 2) + i, key kcol
+  f32x4 T[HS][4];
+#pragma unroll
+  for (int s = 0; s < HS; ++s) {
+#pragma unroll
+    for (int pt = 0; pt < 4; ++pt) T[s][pt] = zero4();
+    if (s < ns && p.s_in && (p.per_seg || first)) {
+      const int sl = slice_of(s);
+      const float* s0 = p.s_in + ((int64_t)(p.per_seg ? j : r.n) * p.H + sl / spv) * st_off + (int64_t)kcol * p.Dv + sl % spv * PS;
+#pragma unroll
+      for (int pt = 0; pt < 4; ++pt)
+        T[s][pt] = ld_f32x4(s0 + 32 * (pt >> 1) + 8 * g4 + 4 * (pt & 1));
+    }
+  }
+  if (nch > 0) {
     if (ds >= 0) {
-      const ChunkRows c = chunk_rows<REV>(r, 0);
-      fill_decay<REV>(sh0->dec[0][ds], p, hc, load_dt<REV>(p, c, dh), c.nt);
+      fill_decay<REV>(sh0->dec[0][ds], p, hc, dt0, chunk_rows<REV>(r, 0).nt);
       if (nch > 1) dt = load_dt<REV>(p, chunk_rows<REV>(r, 1), dh);
     }
+    stage();
+    if (nch > 1) request(1);
   }
   for (int i = 0; i < nch; ++i) {
     const ChunkRows c = chunk_rows<REV>(r, i);
     const int ci = REV ? nch - 1 - i : i;  // chunk within the segment
+    const float sg = sign_of(i);
     // backwards: the state entering the chunk is the gradient of the state at its end
     const bool anchor = REV && ((ci + 1) % AB == 0 || i == 0);
     f32x4 dump[4];  // of the next slice
@@ -731,22 +794,8 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
       for (int pt = 0; pt < 4; ++pt) dump[pt] = d[pt * 64];
     };
     float anc[4] = {0.f, 0.f, 0.f, 0.f};
-    __syncthreads();  // the previous chunk's reads are done
-    {
-      Lds& sh = *lds_opaque(sh0);
-      tk.store(sh.k, LDK, tid);
-      tq.store(sh.q, LDK, tid);
-#pragma unroll
-      for (int s = 0; s < HS; ++s) {
-        tv[s].store(sh.v[s], LDV, tid);
-        tw[s].store(sh.w[s], LDV, tid);
-      }
-    }
-    const uint32_t dt1 = dt;
-    if (i + 2 < nch && ds >= 0) dt = load_dt<REV>(p, chunk_rows<REV>(r, i + 2), dh);
     if (anchor) request_dump(0);
-    if (i + 1 < nch) request(i + 1);
-    __syncthreads();
+    __syncthreads();  // this chunk's tiles and decays are in place
     // the chunk's own part: tiles of (rows s, columns t), the diagonal ones, which
     // cost more, on the first four waves; of eight waves the others take the rest
     // and the next chunk's decays
@@ -755,7 +804,7 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
       const int idx = n == 0 ? 0 : n == 1 ? 2 : n == 2 ? 5 : n == 3 ? 9 : n == 4 ? 1 : n < 7 ? n - 2 : n - 1;
       int tb, sb;
       tri_tile(idx, tb, sb);
-      f32x4 cb = zero4(), zs = zero4();
+      f32x4 cb = zero4(), zs = zero4(), f = zero4();  // f: the decays of the current slice's head
 #pragma unroll
       for (int kb = 0; kb < DK / 32; ++kb)
         mma(cb, ld_frag8(sh.k, LDK, 16 * sb + t16, 32 * kb), ld_frag8(sh.q, LDK, 16 * tb + t16, 32 * kb));
@@ -770,7 +819,7 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
       float rts[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
       for (int s = 0; s < HS; ++s) {
-        sched_fence();
+        if (s == 2) sched_fence();
         Lds& sh = *lds_opaque(sh0);
         f32x4 x = zero4();
 #pragma unroll
@@ -781,29 +830,32 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
           for (int e = 0; e < 4; ++e)
             if (4 * g4 + e == t16 && live) p.xd[(int64_t)slice_of(s) * p.tokens + grow] = x[e];
         }
-        const f32x4 z = x * tile_decay<true>(sh.dec[i & 1][s], tb, sb);
+        if (s == 0 || slice_of(s) % spv == 0) f = tile_decay<true>(sh.dec[i & 1][head_of(s)], tb, sb);
+        const f32x4 z = x * f;
         float rt = 0.f;
 #pragma unroll
         for (int e = 0; e < 4; ++e)
           if (sb < tb || 4 * g4 + e < t16) rt += z[e] * cb[e];
         rts[s] = rt;
-        if (s < ns) zs += z * sh.dec[i & 1][s].tw[row];
+        if (s < ns) zs += z * sh.dec[i & 1][head_of(s)].tw[row];
       }
       const float rt = sum_groups4(rts);  // slice g
       if (g4 < HS) sh.rti[sb][g4][row] = rt;
       sh.z[idx][l] = zs;
     }
     if (ds >= 0 && i + 1 < nch)
-      fill_decay<REV>(lds_opaque(sh0)->dec[(i + 1) & 1][ds], p, hc, dt1, chunk_rows<REV>(r, i + 1).nt);
+      fill_decay<REV>(lds_opaque(sh0)->dec[(i + 1) & 1][ds], p, hc, dt, chunk_rows<REV>(r, i + 1).nt);
     __syncthreads();
     Frag<E> kf[2];
 #pragma unroll
     for (int kb = 0; kb < 2; ++kb) kf[kb] = ld_col(lds_opaque(sh0)->k, LDK, 32 * kb, 32 * (nt >> 1), nt & 1);
-    Parts<E> kp[2];  // K times its decay to the chunk's end, of the current slice's head
+    // K times its decay to the chunk's end, of the current slice's head (backwards,
+    // with the anchors' registers, formed for every slice instead of held)
+    Parts<E> kp[2];
     f32x4 o[4];
 #pragma unroll
     for (int tb = 0; tb < 4; ++tb) {
-      sched_fence();
+      if (tb > 1) sched_fence();
       Lds& sh = *lds_opaque(sh0);
       o[tb] = zero4();
 #pragma unroll
@@ -821,7 +873,7 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
 #pragma unroll
         for (int pt = 0; pt < 4; ++pt)
           anc[s] += (dump[pt][0] * T[s][pt][0] + dump[pt][1] * T[s][pt][1]) + (dump[pt][2] * T[s][pt][2] + dump[pt][3] * T[s][pt][3]);
-        anc[s] = row16_sum(anc[s]);
+        anc[s] = sg * row16_sum(anc[s]);
         if (s + 1 < ns) request_dump(s + 1);
       }
       // u = W T^T of the state before the chunk, four row blocks side by side
@@ -843,28 +895,28 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
       }
       sched_fence();
       Lds& sh = *lds_opaque(sh0);
-      const ChunkDecay& dec = sh.dec[i & 1][s];
+      const ChunkDecay& dec = sh.dec[i & 1][head_of(s)];
       float rts[4];
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) {
         const int row = 16 * tb + t16;
         const float tf = dec.tf[row];
         const f32x4 q4 = ld4f<E>(sh.q + row * LDK + krow);
-        rts[tb] = tf * ((u[tb][0] * q4[0] + u[tb][1] * q4[1]) + (u[tb][2] * q4[2] + u[tb][3] * q4[3]));
-        o[tb] += u[tb] * (REV ? tf * dec.tw[row] : tf);  // forwards the target weight is 1
+        rts[tb] = (sg * tf) * ((u[tb][0] * q4[0] + u[tb][1] * q4[1]) + (u[tb][2] * q4[2] + u[tb][3] * q4[3]));
+        o[tb] += u[tb] * (sg * (REV ? tf * dec.tw[row] : tf));  // forwards the target weight is 1
       }
       sh.rtx[nt][s][l] = sum_groups4(rts);  // block g: row l
       // T' = exp(tot) T + V^T (end K)
-      if (s == 0 || slice_of(s) % spv == 0) {
+      if (REV || s == 0 || slice_of(s) % spv == 0) {
 #pragma unroll
         for (int kb = 0; kb < 2; ++kb) {
           f32x4 lo, hi;
           frag_f32(ld_col(sh.k, LDK, 32 * kb, 32 * (nt >> 1), nt & 1), lo, hi);
-          split(kp[kb], lo * *reinterpret_cast<const f32x4*>(&dec.end[32 * kb + 4 * g4]),
-                hi * *reinterpret_cast<const f32x4*>(&dec.end[32 * kb + 16 + 4 * g4]));
+          split(kp[kb], lo * (*reinterpret_cast<const f32x4*>(&dec.end[32 * kb + 4 * g4]) * -sg),
+                hi * (*reinterpret_cast<const f32x4*>(&dec.end[32 * kb + 16 + 4 * g4]) * -sg));
         }
       }
-      const float tot = dec.btw[3];
+      const float tot = -dec.btw[3];
 #pragma unroll
       for (int pt = 0; pt < 4; ++pt) T[s][pt] *= tot;
 #pragma unroll
@@ -882,6 +934,15 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
       const float a = sum_groups4(anc);  // slice g
       if (t16 == 0 && g4 < HS) lds_opaque(sh0)->anc[nt][g4] = a;
     }
+    __syncthreads();  // the chunk's tiles are read, its row terms are in place
+    // The next chunk's tiles into LDS and the requests of the one after it come
+    // before this chunk's stores: the wait for a requested tile covers every
+    // older store.
+    if (i + 1 < nch) stage();
+    if (i + 2 < nch) {
+      if (ds >= 0) dt = load_dt<REV>(p, chunk_rows<REV>(r, i + 2), dh);
+      request(i + 2);
+    }
     {
       const RowBuf out = row_buf<REV>(p.out2 + ((int64_t)(grp * parts + part) * p.tokens + c.base) * DK, DK, DK, c.nt);
 #pragma unroll
@@ -893,10 +954,9 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
         if (s < ns) {
           f32x4* d = dump_of(ci / AB, s);
 #pragma unroll
-          for (int pt = 0; pt < 4; ++pt) d[pt * 64] = T[s][pt];
+          for (int pt = 0; pt < 4; ++pt) d[pt * 64] = T[s][pt] * -sg;
         }
     }
-    __syncthreads();
     Lds& sh = *lds_opaque(sh0);
     if (anchor && tid < ns) {
       double a = 0.;
@@ -905,13 +965,15 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
     }
     for (int k = tid; k < ns * CH; k += NTH) {
       const int s = k / CH, row = k % CH;
-      if (row < c.nt) {
-        float a = 0.f;
-        for (int sb = 0; sb <= row / 16; ++sb) a += sh.rti[sb][s][row];
+      float a = sh.rti[0][s][row];
 #pragma unroll
-        for (int n = 0; n < NW; ++n) a += sh.rtx[n][s][row];
-        p.rt[(int64_t)slice_of(s) * p.tokens + row_of<REV>(c, row)] = a;
+      for (int sb = 1; sb < 4; ++sb) {
+        const float v = sh.rti[sb][s][row];  // (left from another chunk above the diagonal)
+        a += sb <= row / 16 ? v : 0.f;
       }
+#pragma unroll
+      for (int n = 0; n < NW; ++n) a += sh.rtx[n][s][row];
+      if (row < c.nt) p.rt[(int64_t)slice_of(s) * p.tokens + row_of<REV>(c, row)] = a;
     }
   }
   if (REV && p.h0 && r.s == 0) {
@@ -927,7 +989,7 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
         for (int pt = 0; pt < 4; ++pt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) anc[s] += T[s][pt][i] * s0[32 * (pt >> 1) + 8 * g4 + 4 * (pt & 1) + i];
-        anc[s] = row16_sum(anc[s]);
+        anc[s] = sign_of(nch) * row16_sum(anc[s]);
       }
     __syncthreads();
     const float part_sum = sum_groups4(anc);

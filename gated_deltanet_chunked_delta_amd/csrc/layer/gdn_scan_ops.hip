@@ -11,52 +11,53 @@ namespace {
 template <class E> __device__ __forceinline__ float ldE(const void* p, int64_t i) { return to_f(static_cast<const E*>(p)[i]); }
 
 // Per (sequence, head): end states of the segments, each from a zero start,
-// become the states entering them (in sweep order).
+// become the states entering them (in sweep order).  Four entries a thread; the
+// states of JOIN_AHEAD segments are requested together, since the chain through
+// them is only a multiply-add each.
+constexpr int JOIN_AHEAD = 8;
 __global__ __launch_bounds__(256) void scan_join_kernel(ScanJoinParams p) {
   const int n = blockIdx.z, h = blockIdx.y;
   if (plan_invalid(p.seq, p.segs)) return;
-  const int64_t ss = (int64_t)p.Dk * p.Dv, e = blockIdx.x * 256 + threadIdx.x;
+  const int64_t ss = (int64_t)p.Dk * p.Dv, e = (blockIdx.x * 256 + threadIdx.x) * 4;
   const int j0 = p.seq.cu ? p.seg_first[n] : n * p.seq.nseg_per_seq();
   const int ns = p.seq.nseg_of(p.seg_first, n);
-  float carry = p.s0 ? p.s0[((int64_t)n * p.H + h) * ss + e] : 0.f;
-  for (int i = 0; i < ns; ++i) {
-    const int64_t j = j0 + (p.rev ? ns - 1 - i : i);
-    float* s = p.s_loc + (j * p.H + h) * ss + e;
-    const float loc = i + 1 < ns ? *s : 0.f;
-    *s = carry;
-    if (i + 1 < ns) carry = p.s_dec[j * p.H + h] * carry + loc;
+  typedef f32x4 __attribute__((aligned(4))) f32x4_u;
+  f32x4 carry = zero4();
+  if (p.s0) carry = *reinterpret_cast<const f32x4_u*>(p.s0 + ((int64_t)n * p.H + h) * ss + e);
+  for (int i0 = 0; i0 < ns; i0 += JOIN_AHEAD) {
+    f32x4 loc[JOIN_AHEAD];
+    float dec[JOIN_AHEAD];
+    float* at[JOIN_AHEAD];
+#pragma unroll
+    for (int k = 0; k < JOIN_AHEAD; ++k) {
+      const int i = min(i0 + k, ns - 1);
+      const int64_t j = j0 + (p.rev ? ns - 1 - i : i);
+      at[k] = p.s_loc + (j * p.H + h) * ss + e;
+      loc[k] = zero4();
+      dec[k] = 0.f;
+      if (i0 + k + 1 < ns) {  // the last segment's own end state is not formed
+        loc[k] = *reinterpret_cast<const f32x4_u*>(at[k]);
+        dec[k] = p.s_dec[j * p.H + h];
+      }
+    }
+#pragma unroll
+    for (int k = 0; k < JOIN_AHEAD; ++k) {
+      if (i0 + k >= ns) break;
+      *reinterpret_cast<f32x4_u*>(at[k]) = carry;
+      carry = carry * dec[k] + loc[k];
+    }
   }
-}
-
-// A token's step in the recursion of da: da_t = da_{t+1} + v, or v alone (cut)
-// where the token's own decay is below fp32's unit round-off: what is left of
-// da_{t+1} - D_t ct_t = <., exp(a_t) h_{t-1}> there is below the rounding of
-// its two parts, which the step |A| in ddt would multiply.
-struct DaStep { double v; bool cut; };
-__device__ __forceinline__ DaStep da_step(const ScanGradParams& p, const SegRange& r, int t, int t1, int h, float A,
-                                          float bias) {
-  DaStep o{0., false};
-  if (t >= t1) return o;
-  const int nsl = p.Dv / PS;
-  const int64_t row = r.row0 + t;
-  const float raw = scan_dt_raw(p.dt, p.dt_f32, row * p.dt_stride + h) + bias;
-  const float d = p.softplus ? scan_softplus(raw) : raw;
-  double rt = 0., ct = 0.;
-  for (int s = 0; s < nsl; ++s) {
-    const int64_t at = ((int64_t)h * nsl + s) * p.tokens + row;
-    rt += p.rt[at];
-    ct += p.ct[at];
-  }
-  o.cut = d * A < LN_EPS;
-  o.v = o.cut ? rt : rt - d * ct;
-  return o;
 }
 
 // ddt of every token and each anchor block's sums for dA, dD and ddt_bias: a
-// wave per (anchor block of AB chunks, head) walks the block's 64-token pieces
-// backwards.  The suffix sum of differences is undamped (a rounding stays in it
-// to the block's start), so it and the sums over tokens are held in 64 bits, and
-// the sums are made to meet the next anchor.
+// wave per (anchor block of AB chunks, head), lane = token of a 64-token piece,
+// everything the block reads requested at once.  The recursion of da is a
+// suffix sum of v_t = rt_t - D_t ct_t, undamped (a rounding stays in it to the
+// block's start), so it and the sums over tokens are held in 64 bits, and what
+// the sums miss the next anchor by is spread evenly over the tokens.  Where a
+// token's own decay is below fp32's unit round-off the recursion restarts with
+// v_t = rt_t (cut): what is left of da_{t+1} - D_t ct_t = <., exp(a_t) h_{t-1}>
+// there is below the rounding of its two parts, which |A| in ddt would multiply.
 __global__ __launch_bounds__(64) void scan_grad_kernel(ScanGradParams p, int nab) {
   const int j = blockIdx.x / nab, blk = blockIdx.x % nab, h = blockIdx.y, l = lane_id();
   const int nsl = p.Dv / PS, g = h / (p.H / p.G);
@@ -65,6 +66,25 @@ __global__ __launch_bounds__(64) void scan_grad_kernel(ScanGradParams p, int nab
   double sA = 0., sD = 0., sb = 0.;
   const int t0 = blk * AB * CH, t1 = min(r.len, t0 + AB * CH);
   if (t0 < t1) {
+    const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
+    float raw[AB], d[AB], cb[AB];
+    double v[AB], ct[AB], xd[AB];
+    bool in[AB], cut[AB];
+#pragma unroll
+    for (int k = 0; k < AB; ++k) {
+      const int t = t0 + k * CH + l;
+      in[k] = t < t1;
+      const int64_t row = r.row0 + min(t, t1 - 1);
+      raw[k] = scan_dt_raw(p.dt, p.dt_f32, row * p.dt_stride + h) + bias;
+      cb[k] = p.cb[(int64_t)g * p.tokens + row];
+      v[k] = ct[k] = xd[k] = 0.;
+      for (int s = 0; s < nsl; ++s) {
+        const int64_t at = ((int64_t)h * nsl + s) * p.tokens + row;
+        v[k] += p.rt[at];
+        ct[k] += p.ct[at];
+        xd[k] += p.xd[at];
+      }
+    }
     // <h, dh> at the block's end, and at its start (the end of the block before)
     double carry = 0., start = 0.;
     for (int s = 0; s < nsl; ++s) {
@@ -73,32 +93,22 @@ __global__ __launch_bounds__(64) void scan_grad_kernel(ScanGradParams p, int nab
       else if (r.s > 0) start += p.anchor[((int64_t)(j * nab - nab + (p.seq.segc - 1) / AB) * p.H + h) * nsl + s];
       else if (p.anchor0) start += p.anchor0[((int64_t)r.n * p.H + h) * nsl + s];
     }
-    // the differences of the block's tokens, and their suffix sums in each 64-token piece
-    const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
     double sum = 0.;
-    bool cut = false;
-    for (int b = t0; b < t1; b += 64) {
-      const DaStep st = da_step(p, r, b + l, t1, h, A, bias);
-      sum += wave_sum_d(st.v);
-      cut |= __any(st.cut);
+    bool any_cut = false;
+#pragma unroll
+    for (int k = 0; k < AB; ++k) {
+      d[k] = p.softplus ? scan_softplus(raw[k]) : raw[k];
+      cut[k] = in[k] && d[k] * A < LN_EPS;
+      if (!cut[k]) v[k] -= d[k] * ct[k];
+      if (!in[k]) v[k] = 0.;
+      any_cut |= cut[k];
+      sum += v[k];
     }
-    // what the sums miss the start's product by, per token
-    const double miss = cut ? 0. : (start - carry - sum) / (t1 - t0);
-    for (int b = t0 + (t1 - t0 - 1) / 64 * 64; b >= t0; b -= 64) {
-      const int t = b + l;
-      const bool in = t < t1;
-      const int64_t row = r.row0 + min(t, t1 - 1);
-      const float raw = scan_dt_raw(p.dt, p.dt_f32, row * p.dt_stride + h) + bias;
-      const float d = p.softplus ? scan_softplus(raw) : raw;
-      double ct = 0., xd = 0.;
-      for (int s = 0; s < nsl; ++s) {
-        const int64_t o = ((int64_t)h * nsl + s) * p.tokens + row;
-        ct += p.ct[o];
-        xd += p.xd[o];
-      }
-      const DaStep st = da_step(p, r, t, t1, h, A, bias);
-      double suf = st.v + (in ? miss : 0.);
-      int ended = st.cut;  // a cut at or behind this token, within the piece
+    const double miss = __any(any_cut) ? 0. : (start - carry - wave_sum_d(sum)) / (t1 - t0);
+#pragma unroll
+    for (int k = AB - 1; k >= 0; --k) {
+      double suf = v[k] + (in[k] ? miss : 0.);
+      int ended = cut[k];  // a cut at or behind this token, within the piece
 #pragma unroll
       for (int o = 1; o < 64; o <<= 1) {
         const double y = __shfl_down(suf, o, 64);
@@ -110,13 +120,14 @@ __global__ __launch_bounds__(64) void scan_grad_kernel(ScanGradParams p, int nab
       }
       const double da = ended ? suf : carry + suf;
       carry = __shfl(da, 0, 64);
-      double dd = ct + p.cb[(int64_t)g * p.tokens + row] * xd + A * da;
-      if (p.softplus) dd *= 1.f / (1.f + expf(-raw));
-      if (in) {
+      double dd = ct[k] + cb[k] * xd[k] + A * da;
+      if (p.softplus) dd *= 1.f / (1.f + expf(-raw[k]));
+      if (in[k]) {
+        const int64_t row = r.row0 + t0 + k * CH + l;
         if (p.dt_f32) static_cast<float*>(p.ddt)[row * p.H + h] = (float)dd;
         else static_cast<bf16*>(p.ddt)[row * p.H + h] = to_e<bf16>((float)dd);
-        sA += d * da;
-        sD += xd;
+        sA += d[k] * da;
+        sD += xd[k];
         sb += dd;
       }
     }
@@ -223,7 +234,7 @@ hipError_t step_any(int Dk, int Dv, const ScanStepParams& p, hipStream_t st) {
 }  // namespace
 
 hipError_t launch_scan_join(const ScanJoinParams& p, hipStream_t st) {
-  hipLaunchKernelGGL(scan_join_kernel, dim3(p.Dk * p.Dv / 256, p.H, p.N), dim3(256), 0, st, p);
+  hipLaunchKernelGGL(scan_join_kernel, dim3(p.Dk * p.Dv / 1024, p.H, p.N), dim3(256), 0, st, p);
   return hipGetLastError();
 }
 hipError_t launch_scan_grad(const ScanGradParams& p, int nseg, hipStream_t st) {
