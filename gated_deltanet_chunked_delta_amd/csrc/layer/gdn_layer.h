@@ -254,6 +254,8 @@ hipError_t launch_scan_reduce(int dtype, const ScanReduceParams& p, hipStream_t 
 hipError_t launch_scan_step(int dtype, int Dk, int Dv, const ScanStepParams& p, hipStream_t st);
 // Parts of out2 per group of heads that a key sweep writes.
 int sweep_parts_per_group(int dtype, int H, int G, int Dv);
+// Workgroups of a sweep per segment.
+int sweep_workgroups(int dtype, int H, int G, int Dv);
 
 // Step size and log decay of one token and head.
 __device__ __forceinline__ float scan_dt_raw(const void* dt, int f32, int64_t i) {

@@ -1014,11 +1014,14 @@ hipError_t value_launch(const SweepParams& p, int nseg, hipStream_t st) {
   hipLaunchKernelGGL((sweep_value_kernel<E, DK, NW, REV, OUT>), dim3(nseg * p.G * parts), dim3(NW * 64), lds, st, p, parts);
   return hipGetLastError();
 }
+// Waves of a value sweep's workgroup: as many units as the group has, up to
+// eight (fp32: four, by LDS).
+int value_waves(int dtype, int upg) { return upg >= 8 && dtype == GDN_BF16 ? 8 : upg >= 4 ? 4 : 2; }
 template <class E, int DK, bool REV, bool OUT>
 hipError_t value_nw(const SweepParams& p, int nseg, hipStream_t st) {
-  const int upg = p.H / p.G * (p.Dv / VC);
-  if (upg >= 8 && sizeof(E) == 2) return value_launch<E, DK, sizeof(E) == 2 ? 8 : 4, REV, OUT>(p, nseg, st);
-  if (upg >= 4) return value_launch<E, DK, 4, REV, OUT>(p, nseg, st);
+  const int nw = value_waves(sizeof(E) == 2 ? GDN_BF16 : GDN_F32, p.H / p.G * (p.Dv / VC));
+  if (nw == 8) return value_launch<E, DK, sizeof(E) == 2 ? 8 : 4, REV, OUT>(p, nseg, st);
+  if (nw == 4) return value_launch<E, DK, 4, REV, OUT>(p, nseg, st);
   return value_launch<E, DK, 2, REV, OUT>(p, nseg, st);
 }
 
@@ -1060,6 +1063,10 @@ hipError_t launch_sweep(int dtype, int rev, int mode, const SweepParams& p, int 
 int sweep_parts_per_group(int dtype, int H, int G, int Dv) {
   const int spg = H / G * (Dv / PS), hs = key_slices(dtype, spg);
   return (spg + hs - 1) / hs;
+}
+int sweep_workgroups(int dtype, int H, int G, int Dv) {
+  const int upg = H / G * (Dv / VC), nw = value_waves(dtype, upg);
+  return G * max((upg + nw - 1) / nw, sweep_parts_per_group(dtype, H, G, Dv));
 }
 
 }  // namespace gdn
