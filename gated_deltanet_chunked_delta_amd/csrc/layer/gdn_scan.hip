@@ -117,9 +117,9 @@ __device__ __forceinline__ void frag_f32(const Frag<float>& f, f32x4& lo, f32x4&
 // on average, whatever their sign.  A state gathers such errors chunk by chunk,
 // and dA and the bias's gradient add products of two states over all tokens: 1e-6
 // of dA at 16,384 tokens, of one sign in every head.  So a state is kept with its
-// sign turned over from chunk to chunk (sign_of is the sign before chunk i) and
-// the errors of neighbouring chunks cancel: 3e-7, the fp32 terms' own noise.
-__device__ __forceinline__ float sign_of(int i) { return i & 1 ? -1.f : 1.f; }
+// sign turned over from chunk to chunk of its sequence (sign_of chunk boundary b)
+// and the errors of neighbouring chunks cancel: 3e-7, the fp32 terms' own noise.
+__device__ __forceinline__ float sign_of(int b) { return b & 1 ? -1.f : 1.f; }
 
 // Keeps the instruction scheduler from moving work across: without it the reads
 // of every unrolled step are hoisted to the front and registers spill.
@@ -160,12 +160,17 @@ __device__ __forceinline__ ChunkRows chunk_rows(const SegRange& s, int i) {
   r.nt = min(CH, s.len - c * CH);
   return r;
 }
+// The chunk boundary (within the sequence) that a sweep's state stands at before
+// its chunk i of nch.
+template <bool REV>
+__device__ __forceinline__ int boundary(const SegRange& s, int nch, int i) { return REV ? s.c0 + nch - i : s.c0 + i; }
 // The segment, its fields known to be the same in every lane.
 __device__ __forceinline__ void make_uniform(SegRange& r) {
   r.n = __builtin_amdgcn_readfirstlane(r.n);
   r.s = __builtin_amdgcn_readfirstlane(r.s);
   r.ns = __builtin_amdgcn_readfirstlane(r.ns);
   r.len = __builtin_amdgcn_readfirstlane(r.len);
+  r.c0 = __builtin_amdgcn_readfirstlane(r.c0);
   const uint32_t lo = __builtin_amdgcn_readfirstlane((int)(uint32_t)r.row0);
   const uint32_t hi = __builtin_amdgcn_readfirstlane((int)(uint32_t)(r.row0 >> 32));
   r.row0 = (int64_t)((uint64_t)hi << 32 | lo);
@@ -368,13 +373,21 @@ struct TileStage {
   }
 };
 
+// Workgroups go to the eight XCDs round-robin; this numbering gives each XCD a
+// contiguous run of work items, so that the workgroups of one segment and group,
+// which read the same K and Q, find them in one L2.
+__device__ __forceinline__ int xcd_item() {
+  const int n = gridDim.x, b = blockIdx.x, x = b & 7, per = n >> 3, rem = n & 7;
+  return x * per + min(x, rem) + (b >> 3);
+}
+
 // ---------------------------------------------------------------- value sweep
 // A workgroup of NW waves takes NW units of one group of heads in one segment;
 // a unit is VC = 32 value columns of one head, its state Dk x 32 in the wave's
-// accumulators for the whole segment.  K and Q are staged once for all waves,
-// and Q K^T, which has no head in it, is formed once by all waves together; the
-// two waves of a pair belong to one head and share its decays and its chunk
-// matrix, of which each forms half.  OUT = false: the state sweep (no Q, no
+// accumulators for the whole segment.  K and Q are staged once for all waves;
+// the waves of one head (a team: two, or four where a head has 128 or 256
+// columns) share its decays and its chunk matrix, the tiles of which, Q K^T
+// included, they form between them.  OUT = false: the state sweep (no Q, no
 // output).
 constexpr int VC = 32;
 
@@ -393,17 +406,20 @@ struct ValueLds {
   E k[kKeyBufs<E>][CH * row_ld<E>(DK)];
   E q[CH * row_ld<E>(DK)];
   E v[NW][CH * row_ld<E>(VC)];
-  f32x4 cb[10][64];
-  E m[NW / 2][10][64][4];
+  E m[NW / 2][10][64][4];     // by team
   ChunkDecay dec[2][NW / 2];  // of this chunk and the next
 };
 
-// Tile idx of the head's chunk matrix from Q K^T and the decays.
-template <class E, int DK, int NW, int IDX>
-__device__ __forceinline__ void chunk_matrix_tile(ValueLds<E, DK, NW>& sh, const ChunkDecay& dec, int pair) {
-  constexpr int tb = IDX >= 6 ? 3 : IDX >= 3 ? 2 : IDX >= 1 ? 1 : 0, sb = IDX - tb * (tb + 1) / 2;
-  const int l = lane_id();
-  st4f<E>(sh.m[pair][IDX][l], sh.cb[IDX][l] * tile_decay<sizeof(E) == 4>(dec, tb, sb));
+// Tile IDX of the head's chunk matrix: Q K^T, then the decays.
+template <int IDX, class E, int DK, int NW>
+__device__ __forceinline__ void chunk_matrix_tile(ValueLds<E, DK, NW>& sh, const E* k, const ChunkDecay& dec, int team) {
+  constexpr int tb = IDX >= 6 ? 3 : IDX >= 3 ? 2 : IDX >= 1 ? 1 : 0, sb = IDX - tb * (tb + 1) / 2, LDK = row_ld<E>(DK);
+  const int l = lane_id(), t16 = l & 15;
+  f32x4 a = zero4();
+#pragma unroll
+  for (int kb = 0; kb < DK / 32; ++kb)
+    mma(a, ld_frag8(k, LDK, 16 * sb + t16, 32 * kb), ld_frag8(sh.q, LDK, 16 * tb + t16, 32 * kb));
+  st4f<E>(sh.m[team][IDX][l], a * tile_decay<sizeof(E) == 4>(dec, tb, sb));
 }
 
 template <class E, int DK, int NW, bool REV, bool OUT>
@@ -413,7 +429,7 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
   Lds* const sh0 = reinterpret_cast<Lds*>(smem);
   constexpr int LDK = row_ld<E>(DK), LDV = row_ld<E>(VC), NT = DK / 16, NTH = NW * 64;
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), t16 = l & 15, g4 = l >> 4;
-  const int part = blockIdx.x % parts, grp = blockIdx.x / parts % p.G, j = blockIdx.x / parts / p.G;
+  const int item = xcd_item(), part = item % parts, grp = item / parts % p.G, j = item / parts / p.G;
   SegRange r;
   if (!seg_range(p.seq, p.segs, p.seg_first, j, r)) return;
   make_uniform(r);
@@ -423,6 +439,7 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
   const int unit = min(part * NW + w, upg - 1);
   const bool active = part * NW + w < upg;  // a wave without a unit repeats the last one and stores nothing
   const int h = grp * rep + unit / (p.Dv / VC), col = unit % (p.Dv / VC) * VC;
+  const int team_size = NW >= 4 && p.Dv % 128 == 0 ? 4 : 2, team = w / team_size, sub = w % team_size;
   const int64_t st_off = (int64_t)DK * p.Dv;
   const float Dh = OUT && p.D ? p.D[h] : 0.f;
 
@@ -450,7 +467,7 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
   auto stage_v = [&] { tv.store(lds_opaque(sh0)->v[w], LDV, l); };
   uint32_t dt0 = 0;
   if (nch > 0) {  // the first chunk's requests before the state's
-    if ((w & 1) == 0) dt0 = load_dt<REV>(p, chunk_rows<REV>(r, 0), h);
+    if (sub == 0) dt0 = load_dt<REV>(p, chunk_rows<REV>(r, 0), h);
     request(0);
   }
   // state tile (nt, pt), entry i: key 32 (nt / 2) + 8 g + 4 (nt % 2) + i, value
@@ -472,11 +489,11 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-      for (int pt = 0; pt < 2; ++pt) S[nt][pt] = quad_transpose(S[nt][pt]);
+      for (int pt = 0; pt < 2; ++pt) S[nt][pt] = quad_transpose(S[nt][pt]) * sign_of(boundary<REV>(r, nch, 0));
   }
   if (nch > 0) {
-    if ((w & 1) == 0) {
-      fill_decay<REV>(sh0->dec[0][w >> 1], p, hc, dt0, chunk_rows<REV>(r, 0).nt);
+    if (sub == 0) {
+      fill_decay<REV>(sh0->dec[0][team], p, hc, dt0, chunk_rows<REV>(r, 0).nt);
       if (nch > 1) dt = load_dt<REV>(p, chunk_rows<REV>(r, 1), h);
     }
     stage_k(0);
@@ -496,44 +513,49 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
       __syncthreads();
     }
     const int kb_ = AHEAD ? i & 1 : 0;
-    const float sg = sign_of(i);
+    const float sg = sign_of(boundary<REV>(r, nch, i));
     const uint32_t dt1 = dt;
-    if (i + 2 < nch && (w & 1) == 0) dt = load_dt<REV>(p, chunk_rows<REV>(r, i + 2), h);
-    // even waves, once a chunk: the next chunk's decays
+    if (i + 2 < nch && sub == 0) dt = load_dt<REV>(p, chunk_rows<REV>(r, i + 2), h);
+    // a team's first wave, once a chunk: the next chunk's decays
     auto next_decay = [&] {
-      if (i + 1 < nch) fill_decay<REV>(lds_opaque(sh0)->dec[(i + 1) & 1][w >> 1], p, hc, dt1, chunk_rows<REV>(r, i + 1).nt);
+      if (i + 1 < nch) fill_decay<REV>(lds_opaque(sh0)->dec[(i + 1) & 1][team], p, hc, dt1, chunk_rows<REV>(r, i + 1).nt);
     };
     Frag<E> vf[2][2];  // V down its columns: rows 32 kb.., columns of tile pt
     if (OUT) {
-      for (int idx = w; idx < 10; idx += NW) {
-        Lds& sh = *lds_opaque(sh0);
-        int tb, sb;
-        tri_tile(idx, tb, sb);
-        f32x4 a = zero4();
-#pragma unroll
-        for (int kb = 0; kb < DK / 32; ++kb)
-          mma(a, ld_frag8(sh.k[kb_], LDK, 16 * sb + t16, 32 * kb), ld_frag8(sh.q, LDK, 16 * tb + t16, 32 * kb));
-        sh.cb[idx][l] = a;
-      }
-      __syncthreads();
-      // the head's chunk matrix: the even wave four tiles below the diagonal
-      // blocks and the next decays, the odd one the other two and the diagonal
       {
         Lds& sh = *lds_opaque(sh0);
-        const ChunkDecay& dec = sh.dec[i & 1][w >> 1];
-        if ((w & 1) == 0) {
-          chunk_matrix_tile<E, DK, NW, 1>(sh, dec, w >> 1);
-          chunk_matrix_tile<E, DK, NW, 3>(sh, dec, w >> 1);
-          chunk_matrix_tile<E, DK, NW, 4>(sh, dec, w >> 1);
-          chunk_matrix_tile<E, DK, NW, 6>(sh, dec, w >> 1);
+        const ChunkDecay& dec = sh.dec[i & 1][team];
+        const E* k = sh.k[kb_];
+        if (team_size == 4) {
+          if (sub == 0) {
+            chunk_matrix_tile<1>(sh, k, dec, team);
+            next_decay();
+          } else if (sub == 1) {
+            chunk_matrix_tile<0>(sh, k, dec, team);
+            chunk_matrix_tile<2>(sh, k, dec, team);
+            chunk_matrix_tile<4>(sh, k, dec, team);
+          } else if (sub == 2) {
+            chunk_matrix_tile<5>(sh, k, dec, team);
+            chunk_matrix_tile<9>(sh, k, dec, team);
+            chunk_matrix_tile<3>(sh, k, dec, team);
+          } else {
+            chunk_matrix_tile<6>(sh, k, dec, team);
+            chunk_matrix_tile<7>(sh, k, dec, team);
+            chunk_matrix_tile<8>(sh, k, dec, team);
+          }
+        } else if (sub == 0) {
+          chunk_matrix_tile<1>(sh, k, dec, team);
+          chunk_matrix_tile<3>(sh, k, dec, team);
+          chunk_matrix_tile<4>(sh, k, dec, team);
+          chunk_matrix_tile<6>(sh, k, dec, team);
           next_decay();
         } else {
-          chunk_matrix_tile<E, DK, NW, 7>(sh, dec, w >> 1);
-          chunk_matrix_tile<E, DK, NW, 8>(sh, dec, w >> 1);
-          chunk_matrix_tile<E, DK, NW, 0>(sh, dec, w >> 1);
-          chunk_matrix_tile<E, DK, NW, 2>(sh, dec, w >> 1);
-          chunk_matrix_tile<E, DK, NW, 5>(sh, dec, w >> 1);
-          chunk_matrix_tile<E, DK, NW, 9>(sh, dec, w >> 1);
+          chunk_matrix_tile<7>(sh, k, dec, team);
+          chunk_matrix_tile<8>(sh, k, dec, team);
+          chunk_matrix_tile<0>(sh, k, dec, team);
+          chunk_matrix_tile<2>(sh, k, dec, team);
+          chunk_matrix_tile<5>(sh, k, dec, team);
+          chunk_matrix_tile<9>(sh, k, dec, team);
         }
       }
       f32x4 o[4][2];
@@ -568,7 +590,7 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
       for (int tb = 0; tb < 4; ++tb) {
         sched_fence();
         Lds& sh = *lds_opaque(sh0);
-        const ChunkDecay& dec = sh.dec[i & 1][w >> 1];
+        const ChunkDecay& dec = sh.dec[i & 1][team];
         const float tf = dec.tf[16 * tb + t16] * sg;
         o[tb][0] *= tf;
         o[tb][1] *= tf;
@@ -577,13 +599,13 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
           const int i0 = tb * (tb + 1) / 2 + 2 * kb;
           Frag<E> m;
           if constexpr (sizeof(E) == 2) {
-            const bf16x4 x = *reinterpret_cast<const bf16x4*>(sh.m[w >> 1][i0][l]);
+            const bf16x4 x = *reinterpret_cast<const bf16x4*>(sh.m[team][i0][l]);
             bf16x4 y = bf16x4{};
-            if (2 * kb + 1 <= tb) y = *reinterpret_cast<const bf16x4*>(sh.m[w >> 1][i0 + (2 * kb + 1 <= tb)][l]);
+            if (2 * kb + 1 <= tb) y = *reinterpret_cast<const bf16x4*>(sh.m[team][i0 + (2 * kb + 1 <= tb)][l]);
             m.v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
           } else {
-            m.lo = *reinterpret_cast<const f32x4*>(sh.m[w >> 1][i0][l]);
-            m.hi = 2 * kb + 1 <= tb ? *reinterpret_cast<const f32x4*>(sh.m[w >> 1][i0 + (2 * kb + 1 <= tb)][l]) : zero4();
+            m.lo = *reinterpret_cast<const f32x4*>(sh.m[team][i0][l]);
+            m.hi = 2 * kb + 1 <= tb ? *reinterpret_cast<const f32x4*>(sh.m[team][i0 + (2 * kb + 1 <= tb)][l]) : zero4();
           }
           mma(o[tb][0], vf[kb][0], m);
           mma(o[tb][1], vf[kb][1], m);
@@ -609,7 +631,7 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
         }
       }
     } else {
-      if ((w & 1) == 0) next_decay();
+      if (sub == 0) next_decay();
       if (AHEAD && i + 1 < nch) stage_k(i + 1);
 #pragma unroll
       for (int kb = 0; kb < 2; ++kb)
@@ -622,7 +644,7 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
     }
     sched_fence();
     // S' = exp(tot) S + K^T (end V)
-    const ChunkDecay& dec = lds_opaque(sh0)->dec[i & 1][w >> 1];
+    const ChunkDecay& dec = lds_opaque(sh0)->dec[i & 1][team];
     const float tot = -dec.btw[3];
     if (!OUT) total *= -tot;
     Parts<E> vp[2][2];
@@ -669,7 +691,7 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
 #pragma unroll
   for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-    for (int pt = 0; pt < 2; ++pt) st_f32x4(dst + key0(nt) * p.Dv + 4 * pt, quad_transpose(S[nt][pt] * sign_of(nch)));
+    for (int pt = 0; pt < 2; ++pt) st_f32x4(dst + key0(nt) * p.Dv + 4 * pt, quad_transpose(S[nt][pt] * sign_of(boundary<REV>(r, nch, nch))));
   if (!OUT && l == 0 && col == 0) p.s_dec[(int64_t)j * p.H + h] = total;
 }
 
@@ -700,7 +722,7 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
   Lds* const sh0 = reinterpret_cast<Lds*>(smem);
   constexpr int LDK = row_ld<E>(DK), LDV = row_ld<E>(PS), NW = DK / 16, NTH = DK * 4;
   const int tid = threadIdx.x, nt = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), t16 = l & 15, g4 = l >> 4;
-  const int part = blockIdx.x % parts, grp = blockIdx.x / parts % p.G, j = blockIdx.x / parts / p.G;
+  const int item = xcd_item(), part = item % parts, grp = item / parts % p.G, j = item / parts / p.G;
   SegRange r;
   if (!seg_range(p.seq, p.segs, p.seg_first, j, r)) return;
   make_uniform(r);
@@ -770,7 +792,7 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
       const float* s0 = p.s_in + ((int64_t)(p.per_seg ? j : r.n) * p.H + sl / spv) * st_off + (int64_t)kcol * p.Dv + sl % spv * PS;
 #pragma unroll
       for (int pt = 0; pt < 4; ++pt)
-        T[s][pt] = ld_f32x4(s0 + 32 * (pt >> 1) + 8 * g4 + 4 * (pt & 1));
+        T[s][pt] = ld_f32x4(s0 + 32 * (pt >> 1) + 8 * g4 + 4 * (pt & 1)) * sign_of(boundary<REV>(r, nch, 0));
     }
   }
   if (nch > 0) {
@@ -784,14 +806,14 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
   for (int i = 0; i < nch; ++i) {
     const ChunkRows c = chunk_rows<REV>(r, i);
     const int ci = REV ? nch - 1 - i : i;  // chunk within the segment
-    const float sg = sign_of(i);
+    const float sg = sign_of(boundary<REV>(r, nch, i));
     // backwards: the state entering the chunk is the gradient of the state at its end
     const bool anchor = REV && ((ci + 1) % AB == 0 || i == 0);
     f32x4 dump[4];  // of the next slice
     auto request_dump = [&](int s) {
       const f32x4* d = dump_of(ci / AB, s);
 #pragma unroll
-      for (int pt = 0; pt < 4; ++pt) dump[pt] = d[pt * 64];
+      for (int pt = 0; pt < 4; ++pt) dump[pt] = __builtin_nontemporal_load(d + pt * 64);
     };
     float anc[4] = {0.f, 0.f, 0.f, 0.f};
     if (anchor) request_dump(0);
@@ -954,7 +976,7 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
         if (s < ns) {
           f32x4* d = dump_of(ci / AB, s);
 #pragma unroll
-          for (int pt = 0; pt < 4; ++pt) d[pt * 64] = T[s][pt] * -sg;
+          for (int pt = 0; pt < 4; ++pt) __builtin_nontemporal_store(T[s][pt] * -sg, d + pt * 64);
         }
     }
     Lds& sh = *lds_opaque(sh0);
@@ -989,7 +1011,7 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
         for (int pt = 0; pt < 4; ++pt)
 #pragma unroll
           for (int i = 0; i < 4; ++i) anc[s] += T[s][pt][i] * s0[32 * (pt >> 1) + 8 * g4 + 4 * (pt & 1) + i];
-        anc[s] = sign_of(nch) * row16_sum(anc[s]);
+        anc[s] = sign_of(boundary<REV>(r, nch, nch)) * row16_sum(anc[s]);
       }
     __syncthreads();
     const float part_sum = sum_groups4(anc);

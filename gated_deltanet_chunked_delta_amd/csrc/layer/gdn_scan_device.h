@@ -9,6 +9,7 @@ struct SegRange {
   int n, s, ns;     // sequence, segment within it, segments of the sequence
   int64_t row0;     // first token of the segment (global row)
   int len;          // its tokens
+  int c0;           // its first chunk within the sequence
 };
 __device__ __forceinline__ bool seg_range(const SeqInfo& seq, const SegDesc* segs, const int* seg_first, int j,
                                           SegRange& r) {
@@ -20,6 +21,7 @@ __device__ __forceinline__ bool seg_range(const SeqInfo& seq, const SegDesc* seg
   const int t0 = min(d.c_begin * CH, seq.len(d.n)), t1 = min(d.c_end * CH, seq.len(d.n));
   r.row0 = seq.start(d.n) + t0;
   r.len = t1 - t0;
+  r.c0 = d.c_begin;
   return true;
 }
 

@@ -212,6 +212,11 @@ def _call(fn, args, dev):
         _check(status)
 
 
+def _wants_grad(*tensors):
+    """Whether a call has to go through autograd; one that has not calls the library directly."""
+    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+
+
 # ------------------------------------------------------------------ short causal convolution
 def _conv_args(x, weight, bias, silu, initial_state, cu_seqlens, cu_seqlens_host):
     if x.dim() != 3:
@@ -328,8 +333,11 @@ def short_conv(x, weight, bias=None, silu: bool = True, initial_state=None, outp
     optional bias [D] and SiLU, differentiable in x, weight, bias and initial_state.
     Returns y, or (y, final_state [N, W-1, D]).  cu_seqlens (int32, B = 1) packs
     sequences; cu_seqlens_host, when given, is checked against T."""
-    y, fin = _ShortConv.apply(x, weight, bias, initial_state, bool(silu), cu_seqlens, cu_seqlens_host,
-                              bool(output_final_state))
+    if _wants_grad(x, weight, bias, initial_state):
+        y, fin = _ShortConv.apply(x, weight, bias, initial_state, bool(silu), cu_seqlens, cu_seqlens_host,
+                                  bool(output_final_state))
+    else:
+        y, fin = gdn_conv_fwd(x, weight, bias, silu, initial_state, cu_seqlens, cu_seqlens_host, output_final_state)
     return (y, fin) if output_final_state else y
 
 
@@ -447,12 +455,12 @@ def gdn_scan_step(x, dt, A, B, C, state, D=None, dt_bias=None, dt_softplus: bool
 
 class _SelectiveScan(torch.autograd.Function):
     @staticmethod
-    def forward(ctx, x, dt, A, B, C, D, dt_bias, h0, dt_softplus, cu_seqlens, cu_seqlens_host, final, seg_mode, grad):
+    def forward(ctx, x, dt, A, B, C, D, dt_bias, h0, dt_softplus, cu_seqlens, cu_seqlens_host, final, seg_mode):
         if cu_seqlens is not None and cu_seqlens_host is None:
             cu_seqlens_host = cu_seqlens.cpu()
         res = gdn_scan_fwd(x, dt, A, B, C, D, dt_bias, dt_softplus, h0, cu_seqlens, cu_seqlens_host, final,
-                           save_states=grad, seg_mode=seg_mode)
-        ctx.save_for_backward(x, dt, A, B, C, D, dt_bias, h0, cu_seqlens, res[2] if grad else None)
+                           save_states=True, seg_mode=seg_mode)
+        ctx.save_for_backward(x, dt, A, B, C, D, dt_bias, h0, cu_seqlens, res[2])
         ctx.dt_softplus, ctx.cu_host, ctx.seg_mode = dt_softplus, cu_seqlens_host, seg_mode
         ctx.set_materialize_grads(False)
         return res[0], res[1]
@@ -463,12 +471,12 @@ class _SelectiveScan(torch.autograd.Function):
         x, dt, A, B, C, D, dt_bias, h0, cu, states = ctx.saved_tensors
         if dy is None:
             if dhT is None:
-                return (None,) * 14
+                return (None,) * 13
             dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
         dx, ddt, dA, dB, dC, dD, dbias, dh0 = gdn_scan_bwd(
             x, dt, A, B, C, dy.contiguous(), D, dt_bias, ctx.dt_softplus, h0,
             None if dhT is None else dhT.contiguous(), cu, ctx.cu_host, states, ctx.seg_mode)
-        return dx, ddt, dA, dB, dC, dD, dbias, dh0, None, None, None, None, None, None
+        return dx, ddt, dA, dB, dC, dD, dbias, dh0, None, None, None, None, None
 
 
 def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus: bool = False, initial_state=None,
@@ -482,10 +490,12 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus: bool = Fal
     [B, T, G, Dk] shared by H / G heads, states [N, H, Dk, Dv] fp32.  Returns y, or
     (y, hT).  cu_seqlens (int32, B = 1) packs sequences; without its host copy
     cu_seqlens_host it is read back once (a device synchronisation)."""
-    grad = torch.is_grad_enabled() and any(
-        t is not None and t.requires_grad for t in (x, dt, A, B, C, D, dt_bias, initial_state))
-    y, hT = _SelectiveScan.apply(x, dt, A, B, C, D, dt_bias, initial_state, bool(dt_softplus), cu_seqlens,
-                                 cu_seqlens_host, bool(output_final_state), int(seg_mode), grad)
+    if _wants_grad(x, dt, A, B, C, D, dt_bias, initial_state):
+        y, hT = _SelectiveScan.apply(x, dt, A, B, C, D, dt_bias, initial_state, bool(dt_softplus), cu_seqlens,
+                                     cu_seqlens_host, bool(output_final_state), int(seg_mode))
+    else:
+        y, hT = gdn_scan_fwd(x, dt, A, B, C, D, dt_bias, dt_softplus, initial_state, cu_seqlens, cu_seqlens_host,
+                             output_final_state, seg_mode=seg_mode)
     return (y, hT) if output_final_state else y
 
 
@@ -565,4 +575,6 @@ def gated_group_norm(x, weight, z: Optional[torch.Tensor] = None, bias=None, eps
         y = y silu(z) with a gate and not gate_first
 
     weight and bias are [G, D], or [D] shared by all groups."""
+    if not _wants_grad(x, weight, z, bias):
+        return gdn_norm_fwd(x, weight, z, bias, eps, center, gate_first)
     return _GatedGroupNorm.apply(x, weight, z, bias, float(eps), bool(center), bool(gate_first))
