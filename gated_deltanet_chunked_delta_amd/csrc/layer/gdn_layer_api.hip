@@ -337,7 +337,7 @@ gdn_status gdn_conv_fwd(const gdn_conv_fwd_args* args, void* stream) {
   p.y = args->y;
   p.fin = args->final_state;
   const bool vec = conv_vec(a) && aligned(p.y, 16) && aligned(p.fin, 16);
-  p.run = conv_run(a, vec, 4, 64, 8);
+  p.run = conv_run(a, vec, 4, 32, 16);
   p.nruns = runs_of(a, p.run);
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = timed("conv_fwd", s, [&] { return gdn::launch_conv_fwd(a.dtype, a.W, vec, p, s); });
