@@ -148,7 +148,6 @@ hipError_t launch_norm_bwd(int dtype, bool vec, const NormParams& p, hipStream_t
 
 // ---------------------------------------------------------------- selective state space scan
 constexpr int PS = 64;       // value columns of one slice: a head of Dv columns is Dv / PS slices
-constexpr int AB = 1;        // chunks between two anchors of the decay gradient
 
 // One sweep over the tokens of every segment, forwards or backwards in time,
 // with a Dk x PS slice of the state per (segment, head, slice):
@@ -188,9 +187,10 @@ struct SweepParams {
   float* xd;                 // nullable [H * Dv / PS][tokens]: x_t . dy_t over the slice
   float* cb;                 // nullable [G][tokens]: C_t . B_t
   // anchors of the decay gradient: the forward key sweep leaves its state at the
-  // end of every AB chunks of a segment, the backward one writes <it, its gradient>
-  float* dump;               // [nseg][blocks][H * Dv / PS][Dk * PS] in the key sweep's own order
-  double* anchor;            // [nseg][blocks][H * Dv / PS]
+  // end of every chunk, the backward one writes <it, its gradient>
+  const int* chunk_first;    // first chunk of each sequence
+  float* dump;               // [chunks][H * Dv / PS][Dk * PS] in the key sweep's own order
+  double* anchor;            // [chunks][H * Dv / PS]
   const float* h0;           // nullable: the backward key sweep also writes <h0, its gradient>
   double* anchor0;           // [N][H * Dv / PS]
 };
@@ -216,15 +216,15 @@ struct ScanGradParams {      // ddt, dA, dD, ddt_bias from the row terms
   int64_t tokens;
   SeqInfo seq;
   const SegDesc* segs;
-  const int* seg_first;
   const float* rt;           // forward sweep's row terms [slices][tokens]
   const float* ct;           // backward sweep's
   const float* xd;
   const float* cb;
-  const double* anchor;      // [nseg][blocks][H * Dv / PS]
+  const int2* chunk_tab;
+  const double* anchor;      // [chunks][H * Dv / PS]
   const double* anchor0;     // nullable (no h0) [N][H * Dv / PS]
   void* ddt;                 // [tokens][H], dtype of dt
-  double* part;              // [nseg][blocks][H][3]
+  double* part;              // [chunks][H][3]
   float* dA;
   float* dD;                 // nullable
   float* ddt_bias;           // nullable
@@ -260,7 +260,7 @@ struct ScanStepParams {
 enum { SWEEP_STATE = 0, SWEEP_VALUE = 1, SWEEP_KEY = 2 };
 hipError_t launch_sweep(int dtype, int rev, int mode, const SweepParams& p, int nseg, hipStream_t st);
 hipError_t launch_scan_join(const ScanJoinParams& p, hipStream_t st);
-hipError_t launch_scan_grad(const ScanGradParams& p, int nseg, hipStream_t st);
+hipError_t launch_scan_grad(const ScanGradParams& p, int nchunk, hipStream_t st);
 hipError_t launch_scan_reduce(int dtype, const ScanReduceParams& p, hipStream_t st);
 hipError_t launch_scan_step(int dtype, int Dk, int Dv, const ScanStepParams& p, hipStream_t st);
 // Parts of out2 per group of heads that a key sweep writes.

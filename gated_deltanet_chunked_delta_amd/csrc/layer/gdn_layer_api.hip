@@ -87,35 +87,38 @@ int seq_len(const gdn_scan_args& a, int n) {
 int64_t state_elems(const gdn_scan_args& a) { return (int64_t)a.H * a.Dk * a.Dv; }
 
 // Chunks per segment.  A sweep runs one workgroup a compute unit at a time, so
-// its time goes as rounds x chunks per segment; cutting adds a sweep for the
-// segments' states (0.6 of an output chunk per chunk, measured) and a join, about
-// two and a half chunks' time in all, and a round a chunk's time to start.  Among
-// the segment lengths that just fill 1, 2, .. rounds, and no cut at all, the
-// cheapest.  Measured, forward, 16 heads of 128 x 128: 1,024 tokens in segments of
-// 1 chunk 38 us, 4 62 us, uncut 106 us; 8,192 tokens in 4 chunks (one round) 84 us,
-// 2 118 us, 8 106 us; 32,768 tokens in 16 (one round) 206 us, 8 236 us, 32 340 us;
-// 128 tokens uncut 21 us, cut 31 us.
-int auto_segment(const gdn_scan_args& a, int maxc) {
+// its time goes as the larger of its work's share and its longest segment, in
+// chunks (of segments alike: rounds x chunks per segment), and a round takes a
+// chunk's time to start.  Cutting adds a sweep for the segments' states (0.6 of an
+// output chunk per chunk, measured) and a join, about two and a half chunks' time
+// in all.  Among the shortest segments of a few round counts, and no cut at all,
+// the cheapest.  Measured, forward, 16 heads of 128 x 128: 1,024 tokens in segments
+// of 1 chunk 38 us, 4 62 us, uncut 106 us; 8,192 tokens in 4 chunks (one round)
+// 84 us, 2 118 us, 8 106 us; 32,768 tokens in 16 (one round) 206 us, 8 236 us,
+// 32 340 us; 128 tokens uncut 21 us, cut 31 us.
+int auto_segment(const gdn_scan_args& a, int maxc, long long chunks) {
   if (maxc <= 1) return 1;
   const long long cus = cu_count(), per = gdn::sweep_workgroups(a.dtype, a.H, a.G, a.Dv);
   auto rounds = [&](int sc) {
     long long w = 0;
-    for (int n = 0; n < a.num_seqs; ++n) {
-      const int nc = (seq_len(a, n) + gdn::CH - 1) / gdn::CH;
-      w += nc == 0 ? 1 : (nc + sc - 1) / sc;
-    }
+    if (!a.cu_seqlens) w = (long long)a.B * ((maxc + sc - 1) / sc);
+    else
+      for (int n = 0; n < a.num_seqs; ++n) w += std::max(1, ((seq_len(a, n) + gdn::CH - 1) / gdn::CH + sc - 1) / sc);
     return (w * per + cus - 1) / cus;
   };
+  const double share = (double)chunks * per / cus;
+  auto sweep = [&](long long r, int sc) { return std::min((double)r * sc, share + sc); };
   int best = maxc;
-  double least = (double)rounds(maxc) * (maxc + 1);
-  for (long long r = 1; r <= 16; ++r) {
+  const long long uncut = rounds(maxc);
+  double least = sweep(uncut, maxc) + uncut;
+  for (int more : {0, 1, 2, 3, 5, 7, 11, 15}) {
+    const long long r = uncut + more;
     int lo = 1, hi = maxc;  // the shortest segments with at most r rounds
-    if (rounds(hi) > r) continue;
     while (lo < hi) {
       const int mid = lo + (hi - lo) / 2;
       if (rounds(mid) <= r) hi = mid; else lo = mid + 1;
     }
-    const double cost = lo >= maxc ? least : r * (1.6 * lo + 1) + 2.5;
+    const double cost = lo >= maxc ? least : 1.6 * sweep(r, lo) + r + 2.5;
     if (cost < least) {
       least = cost;
       best = lo;
@@ -137,9 +140,9 @@ ScanPlan scan_plan(const gdn_scan_args& a, bool bwd, bool own_states) {
   if (a.seg_mode == -1) {
     p.segc = std::max(1, maxc);
   } else if (a.seg_mode > 0) {
-    p.segc = a.seg_mode;
+    p.segc = std::min(a.seg_mode, std::max(1, maxc));
   } else {
-    p.segc = auto_segment(a, maxc);
+    p.segc = auto_segment(a, maxc, total);
   }
   long long nseg = 0;
   for (int n = 0; n < a.num_seqs; ++n) {
@@ -164,11 +167,11 @@ ScanPlan scan_plan(const gdn_scan_args& a, bool bwd, bool own_states) {
     p.o_ct = take(sizeof(float) * vh * tokens);
     p.o_xd = take(sizeof(float) * vh * tokens);
     p.o_cb = take(sizeof(float) * a.G * tokens);
-    const size_t blocks = (size_t)p.nseg * ((p.segc + gdn::AB - 1) / gdn::AB);
-    p.o_anchor = take(sizeof(double) * vh * blocks);
+    const size_t chunks = (size_t)p.nchunk;
+    p.o_anchor = take(sizeof(double) * vh * chunks);
     p.o_anchor0 = take(sizeof(double) * vh * a.num_seqs);
-    p.o_dump = take(sizeof(float) * state_elems(a) * blocks);
-    p.o_sums = take(sizeof(double) * 3 * a.H * blocks);
+    p.o_dump = take(sizeof(float) * state_elems(a) * chunks);
+    p.o_sums = take(sizeof(double) * 3 * a.H * chunks);
     p.o_part = take(sizeof(float) * gdn::sweep_parts_per_group(a.dtype, a.H, a.G, a.Dv) * (size_t)a.G * tokens * a.Dk);
   }
   p.total = off;
@@ -221,6 +224,13 @@ gdn_status check_scan(const gdn_scan_args& a) {
   return GDN_OK;
 }
 
+// A launch has fewer than 2^32 threads.
+gdn_status check_grid(const gdn_scan_args& a, const ScanPlan& pl) {
+  if ((long long)pl.nseg * gdn::sweep_workgroups(a.dtype, a.H, a.G, a.Dv) >= (1LL << 32) / 512)
+    return fail(GDN_E_INVALID, "problem too large: %d segments", pl.nseg);
+  return GDN_OK;
+}
+
 gdn_status check_ws(const void* ws, size_t have, size_t need) {
   if (!ws || have < need)
     return fail(GDN_E_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, ws ? have : (size_t)0);
@@ -238,6 +248,7 @@ gdn::SweepParams sweep_base(const gdn_scan_args& a, const ScanPlan& pl) {
   p.seq.cu = a.cu_seqlens; p.seq.T = a.T; p.seq.segc = pl.segc;
   p.segs = at<gdn::SegDesc>(ws, pl.o_segs);
   p.seg_first = at<int>(ws, pl.o_seg_first);
+  p.chunk_first = at<int>(ws, pl.o_chunk_first);
   p.per_seg = pl.multi;
   p.s_dec = at<float>(ws, pl.o_dec);
   return p;
@@ -383,7 +394,7 @@ gdn_status gdn_conv_step(const gdn_conv_step_args* args, void* stream) {
   if (a.N < 0 || a.D < 1) return fail(GDN_E_INVALID, "bad sizes N=%d D=%d", a.N, a.D);
   if (a.W < 2 || a.W > 4) return fail(GDN_E_UNSUPPORTED, "unsupported convolution width %d (2 to 4)", a.W);
   if (a.silu != 0 && a.silu != 1) return fail(GDN_E_INVALID, "silu must be 0 or 1");
-  if ((long long)a.N * a.D >= (1LL << 36)) return fail(GDN_E_INVALID, "problem too large");
+  if ((long long)a.N * a.D >= (1LL << 32) - 64) return fail(GDN_E_INVALID, "problem too large");
   if (a.N == 0) return GDN_OK;
   if (!a.x || !a.state || !a.w || !a.y) return fail(GDN_E_INVALID, "null pointer");
   if (a.x_stride < a.D) return fail(GDN_E_INVALID, "x_stride %lld below D = %d", (long long)a.x_stride, a.D);
@@ -428,6 +439,7 @@ gdn_status gdn_scan_fwd(const gdn_scan_fwd_args* args, void* stream) {
   if (!aligned(args->y, 16)) return fail(GDN_E_INVALID, "y must be 16-byte aligned");
   if (!aligned(args->hT, 4) || !aligned(args->h_save, 4)) return fail(GDN_E_INVALID, "hT or h_save misaligned");
   const ScanPlan pl = scan_plan(a, false, args->h_save == nullptr);
+  if (gdn_status st = check_grid(a, pl); st != GDN_OK) return st;
   if (gdn_status st = check_ws(a.workspace, a.workspace_bytes, pl.total); st != GDN_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   if (gdn_status st = scan_tables(a, pl, s); st != GDN_OK) return st;
@@ -459,6 +471,7 @@ gdn_status gdn_scan_bwd(const gdn_scan_bwd_args* args, void* stream) {
       !aligned(args->ddt_bias, 4) || !aligned(args->dh0, 4) || !aligned(args->dhT, 4) || !aligned(args->h_saved, 4))
     return fail(GDN_E_INVALID, "a gradient pointer is misaligned");
   const ScanPlan pl = scan_plan(a, true, args->h_saved == nullptr);
+  if (gdn_status st = check_grid(a, pl); st != GDN_OK) return st;
   if (gdn_status st = check_ws(a.workspace, a.workspace_bytes, pl.total); st != GDN_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   void* ws = a.workspace;
@@ -520,12 +533,12 @@ gdn_status gdn_scan_bwd(const gdn_scan_bwd_args* args, void* stream) {
   gdn::ScanGradParams g{};
   g.dt = a.dt; g.dt_stride = a.dt_stride; g.dt_f32 = a.dt_dtype == GDN_F32; g.softplus = a.dt_softplus;
   g.dt_bias = a.dt_bias; g.A = a.A; g.H = a.H; g.G = a.G; g.Dk = a.Dk; g.Dv = a.Dv; g.tokens = (int64_t)a.B * a.T;
-  g.seq = p.seq; g.segs = p.segs; g.seg_first = p.seg_first;
+  g.seq = p.seq; g.segs = p.segs; g.chunk_tab = at<int2>(ws, pl.o_chunk_tab);
   g.rt = at<float>(ws, pl.o_rt); g.ct = at<float>(ws, pl.o_ct); g.xd = at<float>(ws, pl.o_xd); g.cb = at<float>(ws, pl.o_cb);
   g.anchor = at<double>(ws, pl.o_anchor);
   g.anchor0 = a.h0 ? at<double>(ws, pl.o_anchor0) : nullptr;
   g.ddt = args->ddt; g.part = at<double>(ws, pl.o_sums); g.dA = args->dA; g.dD = args->dD; g.ddt_bias = args->ddt_bias;
-  e = timed("scan_ddt", s, [&] { return gdn::launch_scan_grad(g, pl.nseg, s); });
+  e = timed("scan_ddt", s, [&] { return gdn::launch_scan_grad(g, pl.nchunk, s); });
   return e == hipSuccess ? GDN_OK : hip_fail(e, "scan step gradient launch");
 }
 
@@ -540,7 +553,7 @@ gdn_status gdn_scan_step(const gdn_scan_step_args* args, void* stream) {
   if (!((a.Dk == 64 || a.Dk == 128) && (a.Dv == 64 || a.Dv == 128)))
     return fail(GDN_E_UNSUPPORTED, "unsupported head sizes Dk=%d Dv=%d", a.Dk, a.Dv);
   if (a.dt_softplus != 0 && a.dt_softplus != 1) return fail(GDN_E_INVALID, "dt_softplus must be 0 or 1");
-  if ((long long)a.N * a.H >= (1LL << 31)) return fail(GDN_E_INVALID, "problem too large");
+  if ((long long)a.N * a.H >= (1LL << 24)) return fail(GDN_E_INVALID, "problem too large");
   if (a.N == 0) return GDN_OK;
   if (!a.x || !a.dt || !a.b || !a.c || !a.A || !a.state || !a.y) return fail(GDN_E_INVALID, "null pointer");
   if (a.x_stride < (int64_t)a.H * a.Dv || a.b_stride < (int64_t)a.G * a.Dk || a.c_stride < (int64_t)a.G * a.Dk ||

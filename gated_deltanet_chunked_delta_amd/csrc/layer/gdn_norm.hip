@@ -80,7 +80,7 @@ __global__ __launch_bounds__(NORM_NT) void norm_fwd_kernel(NormParams p) {
   constexpr int RPB = NORM_NT / TPR;
   const int lane = threadIdx.x % TPR;
   const int64_t rows = p.R * p.G;
-  const int64_t r0 = blockIdx.x * (int64_t)(RPB * RW) + threadIdx.x / TPR;
+  const int64_t r0 = (blockIdx.y * (int64_t)gridDim.x + blockIdx.x) * (RPB * RW) + threadIdx.x / TPR;
   constexpr bool before = GATE == GATE_BEFORE, after = GATE == GATE_AFTER;
   const float inv = 1.f / p.D;
   NormRow<E, V, TPR, NV> x[RW], z[RW];
@@ -348,7 +348,8 @@ __device__ __forceinline__ LongRow<E> long_row(const NormParams& p, int64_t tok,
 template <class E>
 __global__ __launch_bounds__(NORM_NT) void norm_fwd_long_kernel(NormParams p) {
   __shared__ float red[NORM_NT / 64];
-  const int64_t r = blockIdx.x, tok = r / p.G;
+  const int64_t r = blockIdx.y * (int64_t)gridDim.x + blockIdx.x, tok = r / p.G;
+  if (r >= p.R * p.G) return;
   LongRow<E> a = long_row<E>(p, tok, (int)(r - tok * p.G));
   a.stats(p, red);
   E* y = static_cast<E*>(p.y) + r * p.D;
@@ -429,6 +430,12 @@ __global__ __launch_bounds__(32 * NDW_ROWS) void norm_dw_kernel(NormParams p) {
   }
 }
 
+// A launch has fewer than 2^32 threads in x: more workgroups go on in y.
+dim3 grid_2d(int64_t n) {
+  constexpr int64_t most = 1 << 23;
+  return n <= most ? dim3((uint32_t)n) : dim3((uint32_t)most, (uint32_t)((n + most - 1) / most));
+}
+
 template <class E, int V, int TPR, int NV, int GATE>
 hipError_t norm_run_gate(const NormParams& p, bool bwd, hipStream_t st) {
   const int64_t rows = p.R * p.G;
@@ -440,9 +447,9 @@ hipError_t norm_run_gate(const NormParams& p, bool bwd, hipStream_t st) {
     // four vectors a thread in flight, as long as the chip stays full of workgroups
     constexpr int RPB = NORM_NT / TPR, RW = V == 1 || NV >= 4 ? 1 : 4 / NV;
     if (rows >= (int64_t)RPB * RW * 1024)
-      hipLaunchKernelGGL((norm_fwd_kernel<E, V, TPR, NV, RW, GATE>), dim3((rows + RPB * RW - 1) / (RPB * RW)), dim3(NORM_NT), 0, st, p);
+      hipLaunchKernelGGL((norm_fwd_kernel<E, V, TPR, NV, RW, GATE>), grid_2d((rows + RPB * RW - 1) / (RPB * RW)), dim3(NORM_NT), 0, st, p);
     else
-      hipLaunchKernelGGL((norm_fwd_kernel<E, V, TPR, NV, 1, GATE>), dim3((rows + RPB - 1) / RPB), dim3(NORM_NT), 0, st, p);
+      hipLaunchKernelGGL((norm_fwd_kernel<E, V, TPR, NV, 1, GATE>), grid_2d((rows + RPB - 1) / RPB), dim3(NORM_NT), 0, st, p);
   }
   return hipGetLastError();
 }
@@ -470,7 +477,7 @@ hipError_t norm_pick(const NormParams& p, bool bwd, hipStream_t st) {
   if (bwd)
     hipLaunchKernelGGL((norm_bwd_long_kernel<E>), dim3(p.blocks * (p.shared ? 1 : p.G)), dim3(NORM_NT), 0, st, p);
   else
-    hipLaunchKernelGGL((norm_fwd_long_kernel<E>), dim3(p.R * p.G), dim3(NORM_NT), 0, st, p);
+    hipLaunchKernelGGL((norm_fwd_long_kernel<E>), grid_2d(p.R * p.G), dim3(NORM_NT), 0, st, p);
   return hipGetLastError();
 }
 

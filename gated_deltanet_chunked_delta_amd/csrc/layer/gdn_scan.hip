@@ -21,9 +21,9 @@
 //   rt_t = C_t . (exp(a_t) h_{t-1}) dy_t,   ct_t = B_t . (exp(a_{t+1}) dh_{t+1}) x_t
 // (the terms of a token with itself cancel and are left out, so under strong
 // decay both sides are as small as da itself).  The recursion is undamped, so
-// it restarts every AB chunks from <h, dh> there: the forward key sweep leaves
-// its state at those places and the backward one takes the product; what the
-// sums miss the next place's product by is spread over the tokens between.  Then
+// it restarts at every chunk's end from <h, dh> there: the forward key sweep
+// leaves its states and the backward one takes the products; what a chunk's sums
+// miss the product at its start by is spread over its tokens.  Then
 // dD_t = ct_t + (C_t . B_t)(x_t . dy_t) + A da_t.
 //
 // Precision.  Products of bf16 inputs are exact and summed in fp32.  An fp32
@@ -735,11 +735,12 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
   const int kcol = 32 * (nt >> 1) + 8 * (t16 >> 2) + 4 * (nt & 1) + (t16 & 3);
   const int krow = 32 * (nt >> 1) + 8 * g4 + 4 * (nt & 1);
 
-  const int nch = (r.len + CH - 1) / CH, nab = (p.seq.segc + AB - 1) / AB;
+  const int nch = (r.len + CH - 1) / CH;
   const int nsl = p.H * spv;  // slices of all heads
-  // the state at anchor block b of this segment: [tile of 16 keys][pt][lane] per slice
-  auto dump_of = [&](int b, int s) {
-    return reinterpret_cast<f32x4*>(p.dump) + ((((int64_t)j * nab + b) * nsl + slice_of(s)) * NW + nt) * 256 + l;
+  const int64_t chunk0 = p.seq.first_chunk(p.chunk_first, r.n) + r.c0;  // the segment's first, over all sequences
+  // the state at the end of the segment's chunk ci: [tile of 16 keys][pt][lane] per slice
+  auto dump_of = [&](int ci, int s) {
+    return reinterpret_cast<f32x4*>(p.dump) + (((chunk0 + ci) * nsl + slice_of(s)) * NW + nt) * 256 + l;
   };
   TileStage<E, DK, NTH, REV> tk, tq;
   TileStage<E, PS, NTH, REV> tv[HS], tw[HS];
@@ -808,15 +809,14 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
     const int ci = REV ? nch - 1 - i : i;  // chunk within the segment
     const float sg = sign_of(boundary<REV>(r, nch, i));
     // backwards: the state entering the chunk is the gradient of the state at its end
-    const bool anchor = REV && ((ci + 1) % AB == 0 || i == 0);
     f32x4 dump[4];  // of the next slice
     auto request_dump = [&](int s) {
-      const f32x4* d = dump_of(ci / AB, s);
+      const f32x4* d = dump_of(ci, s);
 #pragma unroll
       for (int pt = 0; pt < 4; ++pt) dump[pt] = __builtin_nontemporal_load(d + pt * 64);
     };
     float anc[4] = {0.f, 0.f, 0.f, 0.f};
-    if (anchor) request_dump(0);
+    if (REV) request_dump(0);
     __syncthreads();  // this chunk's tiles and decays are in place
     // the chunk's own part: tiles of (rows s, columns t), the diagonal ones, which
     // cost more, on the first four waves; of eight waves the others take the rest
@@ -891,7 +891,7 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
     for (int s = 0; s < HS; ++s) {
       if (s >= ns) break;
       sched_fence();
-      if (anchor) {  // <state at the chunk's end, its gradient>, this lane's part
+      if (REV) {  // <state at the chunk's end, its gradient>, this lane's part
 #pragma unroll
         for (int pt = 0; pt < 4; ++pt)
           anc[s] += (dump[pt][0] * T[s][pt][0] + dump[pt][1] * T[s][pt][1]) + (dump[pt][2] * T[s][pt][2] + dump[pt][3] * T[s][pt][3]);
@@ -952,7 +952,7 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
           for (int pt = 0; pt < 4; ++pt) mma(T[s][pt], vf[pt], kp[kb].p[q]);
       }
     }
-    if (anchor) {
+    if (REV) {
       const float a = sum_groups4(anc);  // slice g
       if (t16 == 0 && g4 < HS) lds_opaque(sh0)->anc[nt][g4] = a;
     }
@@ -970,20 +970,20 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
 #pragma unroll
       for (int tb = 0; tb < 4; ++tb) st16(out, oo + (REV ? -tb : tb) * 16 * DK * 4, o[tb]);
     }
-    if (!REV && ((ci + 1) % AB == 0 || ci + 1 == nch)) {
+    if (!REV) {
 #pragma unroll
       for (int s = 0; s < HS; ++s)
         if (s < ns) {
-          f32x4* d = dump_of(ci / AB, s);
+          f32x4* d = dump_of(ci, s);
 #pragma unroll
           for (int pt = 0; pt < 4; ++pt) __builtin_nontemporal_store(T[s][pt] * -sg, d + pt * 64);
         }
     }
     Lds& sh = *lds_opaque(sh0);
-    if (anchor && tid < ns) {
+    if (REV && tid < ns) {
       double a = 0.;
       for (int n = 0; n < NW; ++n) a += sh.anc[n][tid];
-      p.anchor[((int64_t)j * nab + ci / AB) * nsl + slice_of(tid)] = a;
+      p.anchor[(chunk0 + ci) * nsl + slice_of(tid)] = a;
     }
     for (int k = tid; k < ns * CH; k += NTH) {
       const int s = k / CH, row = k % CH;

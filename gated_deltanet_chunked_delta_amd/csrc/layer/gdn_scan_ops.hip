@@ -49,105 +49,76 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanJoinParams p) {
   }
 }
 
-// ddt of every token and each anchor block's sums for dA, dD and ddt_bias: a
-// wave per (anchor block of AB chunks, head), lane = token of a 64-token piece,
-// everything the block reads requested at once.  The recursion of da is a
-// suffix sum of v_t = rt_t - D_t ct_t, undamped (a rounding stays in it to the
-// block's start), so it and the sums over tokens are held in 64 bits, and what
-// the sums miss the next anchor by is spread evenly over the tokens.  Where a
+// ddt of every token and each chunk's sums for dA, dD and ddt_bias: a wave per
+// (chunk, head), lane = token.  The recursion of da is a suffix sum of
+// v_t = rt_t - D_t ct_t, undamped (a rounding stays in it to the chunk's start),
+// so it and the sums over tokens are held in 64 bits, and what the sums miss the
+// anchor at the chunk's start by is spread evenly over the tokens.  Where a
 // token's own decay is below fp32's unit round-off the recursion restarts with
 // v_t = rt_t (cut): what is left of da_{t+1} - D_t ct_t = <., exp(a_t) h_{t-1}>
 // there is below the rounding of its two parts, which |A| in ddt would multiply.
-__global__ __launch_bounds__(64) void scan_grad_kernel(ScanGradParams p, int nab) {
-  const int j = blockIdx.x / nab, blk = blockIdx.x % nab, h = blockIdx.y, l = lane_id();
+__global__ __launch_bounds__(64) void scan_grad_kernel(ScanGradParams p) {
+  const int h = blockIdx.y, l = lane_id();
+  const int64_t chunk = blockIdx.x;
   const int nsl = p.Dv / PS, g = h / (p.H / p.G);
-  SegRange r;
-  if (!seg_range(p.seq, p.segs, p.seg_first, j, r)) return;
-  double sA = 0., sD = 0., sb = 0.;
-  const int t0 = blk * AB * CH, t1 = min(r.len, t0 + AB * CH);
-  if (t0 < t1) {
-    const float A = p.A[h], bias = p.dt_bias ? p.dt_bias[h] : 0.f;
-    float raw[AB], d[AB], cb[AB];
-    double v[AB], ct[AB], xd[AB];
-    bool in[AB], cut[AB];
+  const int2 nc = p.seq.chunk_of(p.chunk_tab, (int)chunk);  // (sequence, chunk within it)
+  if (nc.x < 0) return;  // the device cu_seqlens disagrees with the plan: nothing is written
+  const int len = min(CH, p.seq.len(nc.x) - nc.y * CH);
+  const int64_t row = p.seq.start(nc.x) + nc.y * CH + min(l, len - 1);
+  const bool in = l < len;
+  const float A = p.A[h];
+  const float raw = scan_dt_raw(p.dt, p.dt_f32, row * p.dt_stride + h) + (p.dt_bias ? p.dt_bias[h] : 0.f);
+  const float cb = p.cb[(int64_t)g * p.tokens + row];
+  double v = 0., ct = 0., xd = 0.;
+  for (int s = 0; s < nsl; ++s) {
+    const int64_t at = ((int64_t)h * nsl + s) * p.tokens + row;
+    v += p.rt[at];
+    ct += p.ct[at];
+    xd += p.xd[at];
+  }
+  // <h, dh> at the chunk's end, and at its start (the end of the chunk before)
+  double carry = 0., start = 0.;
+  for (int s = 0; s < nsl; ++s) {
+    carry += p.anchor[(chunk * p.H + h) * nsl + s];
+    if (nc.y > 0) start += p.anchor[((chunk - 1) * p.H + h) * nsl + s];
+    else if (p.anchor0) start += p.anchor0[((int64_t)nc.x * p.H + h) * nsl + s];
+  }
+  const float d = p.softplus ? scan_softplus(raw) : raw;
+  const bool cut = in && d * A < LN_EPS;
+  if (!cut) v -= d * ct;
+  if (!in) v = 0.;
+  const double miss = __any(cut) ? 0. : (start - carry - wave_sum_d(v)) / len;
+  double suf = v + (in ? miss : 0.);
+  int ended = cut;  // a cut at or behind this token, within the chunk
 #pragma unroll
-    for (int k = 0; k < AB; ++k) {
-      const int t = t0 + k * CH + l;
-      in[k] = t < t1;
-      const int64_t row = r.row0 + min(t, t1 - 1);
-      raw[k] = scan_dt_raw(p.dt, p.dt_f32, row * p.dt_stride + h) + bias;
-      cb[k] = p.cb[(int64_t)g * p.tokens + row];
-      v[k] = ct[k] = xd[k] = 0.;
-      for (int s = 0; s < nsl; ++s) {
-        const int64_t at = ((int64_t)h * nsl + s) * p.tokens + row;
-        v[k] += p.rt[at];
-        ct[k] += p.ct[at];
-        xd[k] += p.xd[at];
-      }
-    }
-    // <h, dh> at the block's end, and at its start (the end of the block before)
-    double carry = 0., start = 0.;
-    for (int s = 0; s < nsl; ++s) {
-      carry += p.anchor[((int64_t)blockIdx.x * p.H + h) * nsl + s];
-      if (blk > 0) start += p.anchor[((int64_t)(blockIdx.x - 1) * p.H + h) * nsl + s];
-      else if (r.s > 0) start += p.anchor[((int64_t)(j * nab - nab + (p.seq.segc - 1) / AB) * p.H + h) * nsl + s];
-      else if (p.anchor0) start += p.anchor0[((int64_t)r.n * p.H + h) * nsl + s];
-    }
-    double sum = 0.;
-    bool any_cut = false;
-#pragma unroll
-    for (int k = 0; k < AB; ++k) {
-      d[k] = p.softplus ? scan_softplus(raw[k]) : raw[k];
-      cut[k] = in[k] && d[k] * A < LN_EPS;
-      if (!cut[k]) v[k] -= d[k] * ct[k];
-      if (!in[k]) v[k] = 0.;
-      any_cut |= cut[k];
-      sum += v[k];
-    }
-    const double miss = __any(any_cut) ? 0. : (start - carry - wave_sum_d(sum)) / (t1 - t0);
-#pragma unroll
-    for (int k = AB - 1; k >= 0; --k) {
-      double suf = v[k] + (in[k] ? miss : 0.);
-      int ended = cut[k];  // a cut at or behind this token, within the piece
-#pragma unroll
-      for (int o = 1; o < 64; o <<= 1) {
-        const double y = __shfl_down(suf, o, 64);
-        const int f = __shfl_down(ended, o, 64);
-        if (l + o < 64 && !ended) {
-          suf += y;
-          ended = f;
-        }
-      }
-      const double da = ended ? suf : carry + suf;
-      carry = __shfl(da, 0, 64);
-      double dd = ct[k] + cb[k] * xd[k] + A * da;
-      if (p.softplus) dd *= 1.f / (1.f + expf(-raw[k]));
-      if (in[k]) {
-        const int64_t row = r.row0 + t0 + k * CH + l;
-        if (p.dt_f32) static_cast<float*>(p.ddt)[row * p.H + h] = (float)dd;
-        else static_cast<bf16*>(p.ddt)[row * p.H + h] = to_e<bf16>((float)dd);
-        sA += d[k] * da;
-        sD += xd[k];
-        sb += dd;
-      }
+  for (int o = 1; o < 64; o <<= 1) {
+    const double y = __shfl_down(suf, o, 64);
+    const int f = __shfl_down(ended, o, 64);
+    if (l + o < 64 && !ended) {
+      suf += y;
+      ended = f;
     }
   }
-  sA = wave_sum_d(sA);
-  sD = wave_sum_d(sD);
-  sb = wave_sum_d(sb);
+  const double da = ended ? suf : carry + suf;
+  double dd = ct + cb * xd + A * da;
+  if (p.softplus) dd *= 1.f / (1.f + expf(-raw));
+  if (in) {
+    if (p.dt_f32) static_cast<float*>(p.ddt)[row * p.H + h] = (float)dd;
+    else static_cast<bf16*>(p.ddt)[row * p.H + h] = to_e<bf16>((float)dd);
+  }
+  const double sA = wave_sum_d(in ? d * da : 0.), sD = wave_sum_d(in ? xd : 0.), sb = wave_sum_d(in ? dd : 0.);
   if (l == 0) {
-    double* o = p.part + ((int64_t)blockIdx.x * p.H + h) * 3;
+    double* o = p.part + (chunk * p.H + h) * 3;
     o[0] = sA;
     o[1] = sD;
     o[2] = sb;
   }
 }
-__global__ __launch_bounds__(64) void scan_grad_sum_kernel(ScanGradParams p, int nblk) {
+__global__ __launch_bounds__(64) void scan_grad_sum_kernel(ScanGradParams p, int nchunk) {
   const int h = blockIdx.x, l = lane_id();
   if (plan_invalid(p.seq, p.segs)) return;
-  if (plan_invalid(p.seq, p.segs)) return;
   double s[3] = {0., 0., 0.};
-  for (int j = l; j < nblk; j += 64)
+  for (int j = l; j < nchunk; j += 64)
     for (int i = 0; i < 3; ++i) s[i] += p.part[((int64_t)j * p.H + h) * 3 + i];
 #pragma unroll
   for (int o = 32; o > 0; o >>= 1)
@@ -237,12 +208,13 @@ hipError_t launch_scan_join(const ScanJoinParams& p, hipStream_t st) {
   hipLaunchKernelGGL(scan_join_kernel, dim3(p.Dk * p.Dv / 1024, p.H, p.N), dim3(256), 0, st, p);
   return hipGetLastError();
 }
-hipError_t launch_scan_grad(const ScanGradParams& p, int nseg, hipStream_t st) {
-  const int nab = (p.seq.segc + AB - 1) / AB;
-  hipLaunchKernelGGL(scan_grad_kernel, dim3(nseg * nab, p.H), dim3(64), 0, st, p, nab);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(scan_grad_sum_kernel, dim3(p.H), dim3(64), 0, st, p, nseg * nab);
+hipError_t launch_scan_grad(const ScanGradParams& p, int nchunk, hipStream_t st) {
+  if (nchunk > 0) {
+    hipLaunchKernelGGL(scan_grad_kernel, dim3(nchunk, p.H), dim3(64), 0, st, p);
+    hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  hipLaunchKernelGGL(scan_grad_sum_kernel, dim3(p.H), dim3(64), 0, st, p, nchunk);
   return hipGetLastError();
 }
 hipError_t launch_scan_reduce(int dtype, const ScanReduceParams& p, hipStream_t st) {

@@ -188,6 +188,11 @@ def _seqs(cu, cu_host, B, T, dev, need_host):
     return cu, cu_host, cu.numel() - 1
 
 
+def _own_lengths(cu_host):
+    """A copy of the host lengths, kept for the backward pass: the caller may reuse its own."""
+    return None if cu_host is None else torch.as_tensor(cu_host, dtype=torch.int32).clone()
+
+
 def _workspace(nbytes, dev):
     if nbytes == 0:
         _check(1)
@@ -310,7 +315,7 @@ class _ShortConv(torch.autograd.Function):
     def forward(ctx, x, weight, bias, initial_state, silu, cu_seqlens, cu_seqlens_host, output_final_state):
         y, fin = gdn_conv_fwd(x, weight, bias, silu, initial_state, cu_seqlens, cu_seqlens_host, output_final_state)
         ctx.save_for_backward(x, weight, bias, initial_state, cu_seqlens)
-        ctx.silu, ctx.cu_host = silu, cu_seqlens_host
+        ctx.silu, ctx.cu_host = silu, _own_lengths(cu_seqlens_host)
         ctx.set_materialize_grads(False)
         return y, fin
 
@@ -409,8 +414,8 @@ def gdn_scan_bwd(x, dt, A, B, C, dy, D=None, dt_bias=None, dt_softplus: bool = F
     with _on(dev):
         if states is not None:
             _t("states", states, states.shape, torch.float32, dev)
-            if states.numel() * 4 < L.gdn_scan_states_bytes(ctypes.byref(a)):
-                raise GDNError("states is smaller than gdn_scan_states_bytes")
+            if states.numel() * 4 != max(16, L.gdn_scan_states_bytes(ctypes.byref(a))):
+                raise GDNError("states are not those of a forward pass with these arguments")
             args.h_saved = _ptr(states)
         ws = _workspace(L.gdn_scan_bwd_workspace_size(ctypes.byref(args)), dev)
     args.a.workspace, args.a.workspace_bytes = ws.data_ptr(), ws.numel()
@@ -456,8 +461,8 @@ def gdn_scan_step(x, dt, A, B, C, state, D=None, dt_bias=None, dt_softplus: bool
 class _SelectiveScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, dt, A, B, C, D, dt_bias, h0, dt_softplus, cu_seqlens, cu_seqlens_host, final, seg_mode):
-        if cu_seqlens is not None and cu_seqlens_host is None:
-            cu_seqlens_host = cu_seqlens.cpu()
+        cu_seqlens_host = _own_lengths(cu_seqlens_host if cu_seqlens_host is not None else
+                                       None if cu_seqlens is None else cu_seqlens.cpu())
         res = gdn_scan_fwd(x, dt, A, B, C, D, dt_bias, dt_softplus, h0, cu_seqlens, cu_seqlens_host, final,
                            save_states=True, seg_mode=seg_mode)
         ctx.save_for_backward(x, dt, A, B, C, D, dt_bias, h0, cu_seqlens, res[2])

@@ -672,3 +672,113 @@ def test_gradients_by_differences(dev):
         scale = max(abs(an), abs(fd), grads[k].double().norm().item() * v.norm().item() * 0.05)
         print(f"    {k} {fd:.6f} {an:.6f}", flush=True)
         assert abs(fd - an) <= 5e-3 * scale, k
+
+
+def test_ragged_packed_batch(dev):
+    """One long sequence among many short ones, the empty ones included: the right values, and
+    a workspace that goes as the tokens and not as sequences times the longest one."""
+    import ctypes
+    from gated_deltanet_chunked_delta_amd import layers, selective_scan
+    g, H = gen(31), 2
+    lens = [3, 0, 700] + [1, 70, 2] * 20
+    T, n = sum(lens), len(lens)
+    s = scan_inputs(g, (1, T), H, 1, 64, 64, torch.bfloat16, True, n, True, dev)
+    order = ["x", "dt", "A", "B", "C", "D", "bias", "h0"]
+    r = {k: d64(s[k]).requires_grad_(True) for k in order}
+    dy = rn(g, 1, T, H, 64, dt=torch.bfloat16)
+    ry, rh = ref_scan(r["x"], r["dt"], r["A"], r["B"], r["C"], r["D"], r["bias"], True, r["h0"], bounds_of(1, T, lens))
+    rg = ref_grads([ry], [d64(dy)], [r[k] for k in order])
+    chunks = sum((n_ + 63) // 64 for n_ in lens)
+    for seg in (0, -1, 2 ** 31 - 1):
+        leaves = [s[k].detach().requires_grad_(True) for k in order]
+        y, hT = selective_scan(*leaves[:7], dt_softplus=True, initial_state=leaves[7], output_final_state=True,
+                               seg_mode=seg, **cu_of(lens, dev))
+        grads = torch.autograd.grad(y, leaves, dy)
+        close("y", y, ry, 8 * U[torch.bfloat16])
+        close("hT", hT, rh, 2e-6)
+        for k, got, want in zip(order, grads, rg):
+            tol = {"h0": 2e-6, "A": 2e-5, "D": 4e-6, "bias": 2e-5}.get(k, 8 * U[torch.bfloat16])
+            close("d" + k, got, want, tol)
+        f = layers.ScanBwdArgs()
+        f.a, keep = layers._scan_args(*(s[k] for k in ("x", "dt", "A", "B", "C", "D", "bias")), True, s["h0"],
+                                      cu_of(lens, dev)["cu_seqlens"], cu_of(lens, dev)["cu_seqlens_host"], seg)
+        size = layers.lib().gdn_scan_bwd_workspace_size(ctypes.byref(f))
+        # a state a chunk, three a segment and sequence, and what goes with the tokens
+        assert size < 4 * H * 64 * 64 * (chunks + 3 * (chunks + n)) + 64 * T * H * 64 + (1 << 16), (seg, size)
+        del keep
+
+
+def test_lengths_reused_between_forward_and_backward(dev):
+    """A loader that writes the next batch's lengths into the same host buffer before the
+    backward pass does not change it."""
+    from gated_deltanet_chunked_delta_amd import selective_scan, short_conv
+    g, lens = gen(32), [70, 130, 20]
+    s = scan_inputs(g, (1, 220), 2, 1, 64, 64, torch.float32, False, 1, False, dev)
+    w, x = rn(g, 96, 4), rn(g, 1, 220, 96)
+    dy, dx = rn(g, 1, 220, 2, 64), rn(g, 1, 220, 96)
+    leaves = [s[k].requires_grad_(True) for k in ("x", "dt", "A", "B", "C")]
+    cl = [x.requires_grad_(True), w.requires_grad_(True)]
+    got = []
+    for reuse in (False, True):
+        kw = cu_of(lens, dev)
+        y, u = selective_scan(*leaves, **kw), short_conv(*cl, **kw)
+        if reuse:
+            kw["cu_seqlens_host"].copy_(torch.tensor([0, 5, 6, 7], dtype=torch.int32))
+        got.append(torch.autograd.grad(y, leaves, dy) + torch.autograd.grad(u, cl, dx))
+    assert all(torch.equal(a, b) for a, b in zip(*got))
+
+
+def test_states_of_another_forward_are_refused(dev):
+    from gated_deltanet_chunked_delta_amd import GDNError, layers
+    g = gen(33)
+    s = scan_inputs(g, (1, 300), 2, 1, 64, 64, torch.bfloat16, False, 1, False, dev)
+    a, dy = [s[k] for k in ("x", "dt", "A", "B", "C")], rn(g, 1, 300, 2, 64, dt=torch.bfloat16)
+    _, _, st = layers.gdn_scan_fwd(*a, seg_mode=1, save_states=True)
+    layers.gdn_scan_bwd(*a, dy, seg_mode=1, states=st)
+    for seg in (2, -1):
+        with pytest.raises(GDNError, match="states"):
+            layers.gdn_scan_bwd(*a, dy, seg_mode=seg, states=st)
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_bad_values_stay_in_their_sequence(dev, bad):
+    """A NaN or infinity anywhere in one packed sequence reaches no other one, nor their
+    states and gradients; what is summed over tokens becomes NaN."""
+    from gated_deltanet_chunked_delta_amd import gated_group_norm, selective_scan, short_conv
+    g, lens = gen(34), [65, 90, 40]
+    lo, hi = lens[0], lens[0] + lens[1]
+    kw = cu_of(lens, dev)
+    out = []
+    for where in (None, lo, hi - 1, lo + 70):
+        g = gen(34)
+        s = scan_inputs(g, (1, sum(lens)), 2, 1, 64, 64, torch.bfloat16, True, 3, True, dev)
+        x, w = rn(g, 1, sum(lens), 96, dt=torch.bfloat16), rn(g, 96, 4, dt=torch.bfloat16)
+        dy, dx = rn(g, *s["x"].shape, dt=torch.bfloat16), rn(g, *x.shape, dt=torch.bfloat16)
+        if where is not None:
+            for t in (s["x"], s["B"], s["C"], x):
+                t[0, where] = bad
+        leaves = [s[k].requires_grad_(True) for k in ("x", "dt", "B", "C", "h0")]
+        y, hT = selective_scan(s["x"], s["dt"], s["A"], s["B"], s["C"], dt_bias=s["bias"], dt_softplus=True,
+                               initial_state=s["h0"], output_final_state=True, seg_mode=1, **kw)
+        u, fin = short_conv(x.requires_grad_(True), w, output_final_state=True, **kw)
+        v = gated_group_norm(s["x"], torch.ones(64, dtype=torch.bfloat16, device=dev))
+        grads = torch.autograd.grad(y, leaves, dy) + torch.autograd.grad(u, x, dx)
+        rows = [t[0] for t in (y, u, v, *grads[:4], grads[5])]
+        out.append([torch.cat([t[:lo], t[hi:]]).detach() for t in rows] +
+                   [t[[0, 2]].detach() for t in (hT, fin, grads[4])])
+    for other in out[1:]:
+        assert all(torch.equal(a, b) for a, b in zip(out[0], other))
+
+
+def test_norm_of_more_rows_than_one_grid_row(dev):
+    """70 million short rows: more threads than one launch dimension takes."""
+    from gated_deltanet_chunked_delta_amd import gated_group_norm
+    R = 70_000_000
+    x = torch.randint(-3, 4, (R, 1, 3), device=dev, dtype=torch.int8).to(torch.bfloat16)
+    w = torch.tensor([1.0, 2.0, -0.5], device=dev, dtype=torch.bfloat16)
+    y = gated_group_norm(x, w, eps=1.0)
+    for lo in range(0, R, 10_000_000):
+        v = x[lo:lo + 10_000_000].double()
+        want = v / torch.sqrt((v * v).mean(-1, keepdim=True) + 1.0) * w.double()
+        e = (y[lo:lo + 10_000_000].double() - want).abs().max().item()
+        assert e <= want.abs().max().item() * (U[torch.bfloat16] + 1e-6), (lo, e)
