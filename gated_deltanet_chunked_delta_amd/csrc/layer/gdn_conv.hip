@@ -13,9 +13,9 @@
 // brings into cache as well.  Threads are numbered channels first over the
 // runs, so a wave stays full for any channel count.
 // Measured (bf16, W = 4): 8,192 x 6,144 in 38 us (201 MB, most of it from cache);
-// 40,828 x 2,304 in 92 us (377 MB, 4.1 TB/s), its gradient in 173 us + 8 us for the
-// weights' sums (565 MB; with some 35 vector instructions an element, two of them
-// transcendental, the arithmetic takes about 100 us beside the traffic's 115).
+// 49,828 x 2,304 in 92 us (459 MB, 5.0 TB/s), its gradient in 173 us + 8 us for the
+// weights' sums (689 MB; with some 35 vector instructions an element, two of them
+// transcendental, the arithmetic takes about 120 us beside the traffic's 141).
 // A token for each of 16 sequences of 6,144 channels: 6 us, all of it latency.
 #include "gdn_layer.h"
 
@@ -374,7 +374,7 @@ hipError_t conv_launch(const ConvParams& p, bool bwd, hipStream_t st) {
 
 // The gradient takes four channels a thread in either type: with eight its open
 // sums, taps and parts need 212 registers, which leaves two waves a SIMD (199 us
-// against 192 us for 40,828 x 2,304 bf16, W = 4, both before the streamed stores).
+// against 192 us for 49,828 x 2,304 bf16, W = 4, both before the streamed stores).
 template <class E, int W>
 hipError_t conv_launch_v(bool vec, const ConvParams& p, bool bwd, hipStream_t st) {
   if (!vec) return conv_launch<E, 1, W>(p, bwd, st);

@@ -61,7 +61,7 @@ __device__ __forceinline__ void store_vec(E* p, const float (&f)[V]) {
 // A store past the L2, for outputs that stream through memory and are not read
 // again by the kernel: the inputs' lines, which neighbouring workgroups do read
 // again, stay (norm of 32,768 x 16 x 128: 81 -> 70 us; convolution gradient of
-// 40,828 x 2,304: 180 -> 173 us).  The convolution's forward pass keeps ordinary
+// 49,828 x 2,304: 180 -> 173 us).  The convolution's forward pass keeps ordinary
 // stores: 92 us against 105 there.
 template <class E, int V>
 __device__ __forceinline__ void stream_vec(E* p, const float (&f)[V]) {

@@ -13,6 +13,10 @@ fallback.
 one token.  Inputs may be slices of a wider row (the output of one projection,
 say): every entry of a token has to be contiguous, the distance between tokens
 is free.  Tensors of a call share one device, whose current stream it uses.
+
+Calls can be captured into a graph, a backward pass too, provided that no eager
+graph of the same leaves is alive then: autograd would synchronise with the
+stream that one was made on, which a capture cannot.
 """
 from __future__ import annotations
 
@@ -210,16 +214,29 @@ def _on(dev):
     return _NO_SWITCH if torch.cuda.current_device() == dev.index else torch.cuda.device(dev)
 
 
+# The current stream's handle; without building a Stream object around it (1.7 us,
+# a fifth of a single-token call) where this PyTorch has the call for that.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
+    lambda index: torch.cuda.current_stream(index).cuda_stream)
+
+
 def _call(fn, args, dev):
-    with _on(dev):
-        status = fn(ctypes.byref(args), torch.cuda.current_stream(dev).cuda_stream)
+    if torch.cuda.current_device() == dev.index:
+        status = fn(ctypes.byref(args), _raw_stream(dev.index))
+    else:
+        with torch.cuda.device(dev):
+            status = fn(ctypes.byref(args), _raw_stream(dev.index))
     if status:
         _check(status)
 
 
 def _wants_grad(*tensors):
     """Whether a call has to go through autograd; one that has not calls the library directly."""
-    return torch.is_grad_enabled() and any(t is not None and t.requires_grad for t in tensors)
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                return True
+    return False
 
 
 # ------------------------------------------------------------------ short causal convolution
@@ -246,8 +263,7 @@ def _conv_args(x, weight, bias, silu, initial_state, cu_seqlens, cu_seqlens_host
 def _rows_like(x, packed_unchecked):
     """An output of x's shape: rows behind the last sequence (possible only where
     the lengths were not checked on the host) hold zeros."""
-    make = torch.zeros if packed_unchecked else torch.empty
-    return make(x.shape, dtype=x.dtype, device=x.device)
+    return x.new_zeros(x.shape) if packed_unchecked else x.new_empty(x.shape)
 
 
 def gdn_conv_fwd(x, weight, bias=None, silu: bool = True, initial_state=None, cu_seqlens=None, cu_seqlens_host=None,
@@ -302,8 +318,9 @@ def gdn_conv_step(x, state, weight, bias=None, silu: bool = True, state_idx=None
     _t("state_idx", state_idx, (N,), torch.int32, dev, optional=True)
     _on_gpu("x", x)
     if y is None:
-        y = torch.empty((N, D), dtype=dt, device=dev)
-    _t("y", y, (N, D), dt, dev)
+        y = weight.new_empty((N, D))
+    else:
+        _t("y", y, (N, D), dt, dev)
     a.N, a.D, a.W, a.num_slots, a.silu = N, D, W, state.shape[0], int(bool(silu))
     a.x, a.state, a.state_idx, a.w, a.bias, a.y = map(_ptr, (x, state, state_idx, weight, bias, y))
     _call(lib().gdn_conv_step, a, dev)
@@ -448,8 +465,9 @@ def gdn_scan_step(x, dt, A, B, C, state, D=None, dt_bias=None, dt_softplus: bool
     _t("state_idx", state_idx, (N,), torch.int32, dev, optional=True)
     _on_gpu("x", x)
     if y is None:
-        y = torch.empty((N, H, Dv), dtype=e, device=dev)
-    _t("y", y, (N, H, Dv), e, dev)
+        y = x.new_empty((N, H, Dv))
+    else:
+        _t("y", y, (N, H, Dv), e, dev)
     a.N, a.H, a.G, a.Dk, a.Dv = N, H, G, Dk, Dv
     a.dt_softplus, a.num_slots = int(bool(dt_softplus)), state.shape[0]
     a.x, a.dt, a.b, a.c, a.A, a.D, a.dt_bias, a.state, a.state_idx, a.y = map(
@@ -533,7 +551,7 @@ def gdn_norm_fwd(x, weight, z=None, bias=None, eps: float = 1e-5, center: bool =
     """y of the gated group norm (see gated_group_norm)."""
     args = NormFwdArgs()
     args.a = _norm_args(x, weight, z, bias, eps, center, gate_first)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = x.new_empty(x.shape)
     args.y = _ptr(y)
     _call(lib().gdn_norm_fwd, args, x.device)
     return y

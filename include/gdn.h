@@ -294,7 +294,8 @@ gdn_status gdn_decode_step(const gdn_decode_args* args, void* stream);
  * initial state (rows oldest first; zero when NULL); its final state is its
  * last W-1 inputs, initial state included when it is shorter.  cu_seqlens
  * (device, int32 [num_seqs + 1], B == 1) packs sequences; tokens at or past
- * cu_seqlens[N] belong to none: their y and dx are left as they were. */
+ * cu_seqlens[N] belong to none: their y and dx are left as they were.
+ * B * T stays below 2^31 - 1024 tokens. */
 typedef struct {
   int32_t dtype;
   int32_t B, T, D, W;
@@ -352,10 +353,14 @@ gdn_status gdn_conv_step(const gdn_conv_step_args* args, void* stream);
  * A <= 0 and d_t >= 0 in the intended domain (the decay never exceeds 1); a
  * token with d_t = 0 leaves the state as it is.  Dk in {64, 128}; Dv a
  * multiple of 64 up to 256; H a multiple of G.  x, B and C need 16-byte
- * aligned pointers and token strides of whole 16 bytes.
+ * aligned pointers and token strides of whole 16 bytes, below 2^22 elements; at
+ * most 65535 sequences.  A value that is not finite makes its sequence not finite
+ * from the start of its chunk of 64 tokens on, and no other sequence.
  * cu_seqlens / cu_seqlens_host as for the chunk calls.  seg_mode: sequences
  * are cut into segments that run side by side and are joined exactly
- * (0 = automatic, -1 = off, k > 0 = segments of k chunks of 64 tokens). */
+ * (0 = automatic, -1 = off, k > 0 = segments of k chunks of 64 tokens).  The
+ * gradient's workspace holds a state for every chunk: 4 Dk Dv H bytes for every
+ * 64 tokens. */
 typedef struct {
   int32_t dtype;               /* of x, B, C (and y, dy, dx, dB, dC) */
   int32_t dt_dtype;            /* of dt (and ddt): GDN_F32, or GDN_BF16 */
@@ -431,7 +436,8 @@ gdn_status gdn_scan_step(const gdn_scan_step_args* args, void* stream);
  *     v = x silu(z) with z and gate_first, else x
  *     n = (v - m) / sqrt(mean((v - m)^2) + eps),   m = mean(v) with center, else 0
  *     y = n w + bias,  times silu(z) with z and not gate_first
- * w and bias are [G, D], or [D] for all groups with shared. */
+ * w and bias are [G, D], or [D] for all groups with shared.  R * G stays below
+ * 2^31, G below 2^16. */
 typedef struct {
   int32_t dtype;
   int64_t R;
