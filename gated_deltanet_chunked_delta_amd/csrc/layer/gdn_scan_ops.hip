@@ -13,7 +13,10 @@ template <class E> __device__ __forceinline__ float ldE(const void* p, int64_t i
 // Per (sequence, head): end states of the segments, each from a zero start,
 // become the states entering them (in sweep order).  Four entries a thread; the
 // states of JOIN_AHEAD segments are requested together, since the chain through
-// them is only a multiply-add each.
+// them is only a multiply-add each.  Bound: the states, read and written (4 x 8
+// segments of 16 heads of 128 x 128, 67 MB in 12 us), or the chain (128 segments of
+// 4 heads, as many bytes, in 19; with one entry a thread, or the next eight requested
+// ahead, within 2 us of that either way).
 constexpr int JOIN_AHEAD = 8;
 __global__ __launch_bounds__(256) void scan_join_kernel(ScanJoinParams p) {
   const int n = blockIdx.z, h = blockIdx.y;
@@ -57,6 +60,7 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanJoinParams p) {
 // token's own decay is below fp32's unit round-off the recursion restarts with
 // v_t = rt_t (cut): what is left of da_{t+1} - D_t ct_t = <., exp(a_t) h_{t-1}>
 // there is below the rounding of its two parts, which |A| in ddt would multiply.
+// 16,384 tokens of 16 heads: 9 us, and 4 for the sums (latency).
 __global__ __launch_bounds__(64) void scan_grad_kernel(ScanGradParams p) {
   const int h = blockIdx.y, l = lane_id();
   const int64_t chunk = blockIdx.x;
@@ -130,7 +134,8 @@ __global__ __launch_bounds__(64) void scan_grad_sum_kernel(ScanGradParams p, int
   }
 }
 
-// dB or dC from the parts: four columns a thread.
+// dB or dC from the parts: four columns a thread.  Bound: the parts, read once
+// (eight of 16,384 x 128: 67 MB in 12 us, 5.8 TB/s).
 template <class E>
 __global__ __launch_bounds__(256) void scan_reduce_kernel(ScanReduceParams p) {
   const int64_t i = blockIdx.x * 256ll + threadIdx.x;
@@ -146,7 +151,8 @@ __global__ __launch_bounds__(256) void scan_reduce_kernel(ScanReduceParams p) {
 
 // Single-token step: a workgroup owns 32 columns of one (sequence, head) state,
 // its 256 threads 4 columns x Dk/32 rows each, as the delta rule's step does.
-// Bound: the fp32 state, read and written once, non-temporal.
+// Bound: the fp32 state, read and written once, non-temporal (64 sequences of 16
+// heads of 128 x 128: 135 MB in 26 us, 5.2 TB/s).
 constexpr int STEP_COLS = 32;
 template <class E, int DK, int DV>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanStepParams p) {
