@@ -253,7 +253,7 @@ struct ScanStepParams {
   const int32_t* state_idx;
   int num_slots;
   void* y;                   // [N][H][Dv]
-  int N, H, G;
+  int N, H, G, Dv;
 };
 
 // Outputs of a sweep.
@@ -262,7 +262,7 @@ hipError_t launch_sweep(int dtype, int rev, int mode, const SweepParams& p, int 
 hipError_t launch_scan_join(const ScanJoinParams& p, hipStream_t st);
 hipError_t launch_scan_grad(const ScanGradParams& p, int nchunk, hipStream_t st);
 hipError_t launch_scan_reduce(int dtype, const ScanReduceParams& p, hipStream_t st);
-hipError_t launch_scan_step(int dtype, int Dk, int Dv, const ScanStepParams& p, hipStream_t st);
+hipError_t launch_scan_step(int dtype, int Dk, const ScanStepParams& p, hipStream_t st);
 // Parts of out2 per group of heads that a key sweep writes.
 int sweep_parts_per_group(int dtype, int H, int G, int Dv);
 // Workgroups of a sweep per segment.

@@ -550,7 +550,7 @@ gdn_status gdn_scan_step(const gdn_scan_step_args* args, void* stream) {
   if (a.N < 0 || a.H < 1 || a.G < 1 || a.Dk < 1 || a.Dv < 1)
     return fail(GDN_E_INVALID, "bad sizes N=%d H=%d G=%d Dk=%d Dv=%d", a.N, a.H, a.G, a.Dk, a.Dv);
   if (a.H % a.G != 0) return fail(GDN_E_INVALID, "H = %d is not a multiple of G = %d", a.H, a.G);
-  if (!((a.Dk == 64 || a.Dk == 128) && (a.Dv == 64 || a.Dv == 128)))
+  if (!((a.Dk == 64 || a.Dk == 128) && a.Dv % gdn::PS == 0 && a.Dv <= 256))
     return fail(GDN_E_UNSUPPORTED, "unsupported head sizes Dk=%d Dv=%d", a.Dk, a.Dv);
   if (a.dt_softplus != 0 && a.dt_softplus != 1) return fail(GDN_E_INVALID, "dt_softplus must be 0 or 1");
   if ((long long)a.N * a.H >= (1LL << 24)) return fail(GDN_E_INVALID, "problem too large");
@@ -571,9 +571,9 @@ gdn_status gdn_scan_step(const gdn_scan_step_args* args, void* stream) {
   p.x = a.x; p.dt = a.dt; p.b = a.b; p.c = a.c;
   p.x_stride = a.x_stride; p.dt_stride = a.dt_stride; p.b_stride = a.b_stride; p.c_stride = a.c_stride;
   p.A = a.A; p.D = a.D; p.dt_bias = a.dt_bias; p.dt_f32 = a.dt_dtype == GDN_F32; p.softplus = a.dt_softplus;
-  p.state = a.state; p.state_idx = a.state_idx; p.num_slots = a.num_slots; p.y = a.y; p.N = a.N; p.H = a.H; p.G = a.G;
+  p.state = a.state; p.state_idx = a.state_idx; p.num_slots = a.num_slots; p.y = a.y; p.N = a.N; p.H = a.H; p.G = a.G; p.Dv = a.Dv;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  hipError_t e = timed("scan_step", s, [&] { return gdn::launch_scan_step(a.dtype, a.Dk, a.Dv, p, s); });
+  hipError_t e = timed("scan_step", s, [&] { return gdn::launch_scan_step(a.dtype, a.Dk, p, s); });
   return e == hipSuccess ? GDN_OK : hip_fail(e, "scan step launch");
 }
 

@@ -154,8 +154,9 @@ __global__ __launch_bounds__(256) void scan_reduce_kernel(ScanReduceParams p) {
 // Bound: the fp32 state, read and written once, non-temporal (64 sequences of 16
 // heads of 128 x 128: 135 MB in 26 us, 5.2 TB/s).
 constexpr int STEP_COLS = 32;
-template <class E, int DK, int DV>
+template <class E, int DK>
 __global__ __launch_bounds__(256) void scan_step_kernel(ScanStepParams p) {
+  const int DV = p.Dv;
   constexpr int RPT = DK / 32;
   __shared__ float red[32][STEP_COLS + 1];
   const int tid = threadIdx.x, tc = tid & 7, tr = tid >> 3;
@@ -198,12 +199,10 @@ __global__ __launch_bounds__(256) void scan_step_kernel(ScanStepParams p) {
 }
 
 template <class E>
-hipError_t step_any(int Dk, int Dv, const ScanStepParams& p, hipStream_t st) {
-  const dim3 g(p.N * p.H, Dv / STEP_COLS), b(256);
-  if (Dk == 128 && Dv == 128) hipLaunchKernelGGL((scan_step_kernel<E, 128, 128>), g, b, 0, st, p);
-  else if (Dk == 64 && Dv == 64) hipLaunchKernelGGL((scan_step_kernel<E, 64, 64>), g, b, 0, st, p);
-  else if (Dk == 64 && Dv == 128) hipLaunchKernelGGL((scan_step_kernel<E, 64, 128>), g, b, 0, st, p);
-  else if (Dk == 128 && Dv == 64) hipLaunchKernelGGL((scan_step_kernel<E, 128, 64>), g, b, 0, st, p);
+hipError_t step_any(int Dk, const ScanStepParams& p, hipStream_t st) {
+  const dim3 g(p.N * p.H, p.Dv / STEP_COLS), b(256);
+  if (Dk == 128) hipLaunchKernelGGL((scan_step_kernel<E, 128>), g, b, 0, st, p);
+  else if (Dk == 64) hipLaunchKernelGGL((scan_step_kernel<E, 64>), g, b, 0, st, p);
   else return hipErrorInvalidValue;
   return hipGetLastError();
 }
@@ -230,9 +229,9 @@ hipError_t launch_scan_reduce(int dtype, const ScanReduceParams& p, hipStream_t 
   else hipLaunchKernelGGL((scan_reduce_kernel<float>), dim3((n + 255) / 256), dim3(256), 0, st, p);
   return hipGetLastError();
 }
-hipError_t launch_scan_step(int dtype, int Dk, int Dv, const ScanStepParams& p, hipStream_t st) {
+hipError_t launch_scan_step(int dtype, int Dk, const ScanStepParams& p, hipStream_t st) {
   if (p.N * p.H == 0) return hipSuccess;
-  return dtype == GDN_BF16 ? step_any<bf16>(Dk, Dv, p, st) : step_any<float>(Dk, Dv, p, st);
+  return dtype == GDN_BF16 ? step_any<bf16>(Dk, p, st) : step_any<float>(Dk, p, st);
 }
 
 }  // namespace gdn

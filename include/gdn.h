@@ -408,7 +408,7 @@ typedef struct {
 
 typedef struct {               /* one token for each of N sequences */
   int32_t dtype, dt_dtype;
-  int32_t N, H, G, Dk, Dv;     /* Dk, Dv in {64, 128} */
+  int32_t N, H, G, Dk, Dv;     /* as for the scan */
   const void* x;               /* [N, H, Dv] */
   const void* dt;              /* [N, H] */
   const void* b;               /* [N, G, Dk] */

@@ -358,7 +358,8 @@ def test_scan_extreme_decays(dev, scale):
 
 
 @pytest.mark.parametrize("N,H,G,Dk,Dv,dtype", [(1, 1, 1, 64, 64, "bf16"), (5, 6, 2, 128, 64, "bf16"),
-                                               (3, 4, 1, 64, 128, "f32"), (9, 2, 2, 128, 128, "bf16")])
+                                               (3, 4, 1, 64, 128, "f32"), (9, 2, 2, 128, 128, "bf16"),
+                                               (2, 3, 1, 64, 192, "bf16"), (2, 2, 1, 128, 256, "f32")])
 def test_scan_steps_continue_a_prompt(dev, N, H, G, Dk, Dv, dtype):
     from gated_deltanet_chunked_delta_amd import layers
     g, dt, T, more = gen(N + Dk), DT[dtype], 70, 3
@@ -782,3 +783,84 @@ def test_norm_of_more_rows_than_one_grid_row(dev):
         want = v / torch.sqrt((v * v).mean(-1, keepdim=True) + 1.0) * w.double()
         e = (y[lo:lo + 10_000_000].double() - want).abs().max().item()
         assert e <= want.abs().max().item() * (U[torch.bfloat16] + 1e-6), (lo, e)
+
+
+def test_gradients_of_one_output_only(dev):
+    """Only the final states are used, or only y: the other output's gradient is zero."""
+    from gated_deltanet_chunked_delta_amd import selective_scan, short_conv
+    g = gen(35)
+    s = scan_inputs(g, (1, 150), 2, 1, 64, 64, torch.float32, False, 1, True, dev)
+    order = ["x", "dt", "A", "B", "C", "h0"]
+    leaves = [s[k].requires_grad_(True) for k in order]
+    x, w, init = (rn(g, 2, 9, 40).requires_grad_(True), rn(g, 40, 3).requires_grad_(True),
+                  rn(g, 2, 2, 40).requires_grad_(True))
+    dh, df = rn(g, 1, 2, 64, 64), rn(g, 2, 2, 40)
+    _, hT = selective_scan(*leaves[:5], initial_state=leaves[5], output_final_state=True, seg_mode=1)
+    got = torch.autograd.grad(hT, leaves, dh)
+    _, fin = short_conv(x, w, initial_state=init, output_final_state=True)
+    cgot = torch.autograd.grad(fin, [x, w, init], df)
+    r = {k: d64(s[k]).requires_grad_(True) for k in order}
+    _, rh = ref_scan(r["x"], r["dt"], r["A"], r["B"], r["C"], None, None, False, r["h0"], bounds_of(1, 150, None))
+    rg = ref_grads([rh], [d64(dh)], [r[k] for k in order])
+    for k, a, b in zip(order, got, rg):
+        if b is None:  # (hT does not depend on C)
+            assert not bool(a.any())
+        else:
+            close("d" + k, a, b, {"A": 2e-5, "dt": 1e-5}.get(k, 2e-6))
+    # the final state copies the last inputs: nothing else has a gradient
+    want = torch.zeros_like(x)
+    want[:, -2:] = df
+    assert torch.equal(cgot[0], want) and not bool(cgot[1].any()) and not bool(cgot[2].any())
+
+
+def test_empty_calls(dev):
+    """No tokens, no rows, no sequences: empty outputs, zero gradients of the weights."""
+    from gated_deltanet_chunked_delta_amd import gated_group_norm, layers, selective_scan, short_conv
+    bf = torch.bfloat16
+    z = lambda *s, dt=bf: torch.zeros(*s, dtype=dt, device=dev)
+    x, w, b = z(0, 3, 64).requires_grad_(True), (z(3, 64) + 1).requires_grad_(True), z(3, 64).requires_grad_(True)
+    y = gated_group_norm(x, w, z(0, 3, 64), b)
+    assert y.shape == (0, 3, 64)
+    dx, dw, db = torch.autograd.grad(y, [x, w, b], torch.zeros_like(y))
+    assert dx.shape == x.shape and not bool(dw.any()) and not bool(db.any())
+    x, w, init = z(2, 0, 48).requires_grad_(True), (z(48, 4) + 1).requires_grad_(True), (z(2, 3, 48) + 2).requires_grad_(True)
+    y, fin = short_conv(x, w, initial_state=init, output_final_state=True)
+    assert y.shape == (2, 0, 48) and torch.equal(fin, init)
+    dx, dw, di = torch.autograd.grad(fin, [x, w, init], torch.full_like(fin, 3.0))
+    assert dx.shape == x.shape and not bool(dw.any()) and bool((di == 3.0).all())
+    h0 = torch.randn(2, 2, 64, 64, device=dev).requires_grad_(True)
+    A = -torch.ones(2, device=dev).requires_grad_(True)
+    y, hT = selective_scan(z(2, 0, 2, 64), z(2, 0, 2), A, z(2, 0, 1, 64), z(2, 0, 1, 64), initial_state=h0,
+                           output_final_state=True)
+    assert y.shape == (2, 0, 2, 64) and torch.equal(hT, h0)
+    dA, dh0 = torch.autograd.grad(hT, [A, h0], torch.full_like(hT, 3.0))
+    assert not bool(dA.any()) and bool((dh0 == 3.0).all())
+    st = z(4, 3, 48)
+    assert layers.gdn_conv_step(z(0, 48), st, z(48, 4)).shape == (0, 48) and not bool(st.any())
+    hs = torch.ones(4, 2, 64, 64, device=dev)
+    y = layers.gdn_scan_step(z(0, 2, 64), z(0, 2), A.detach(), z(0, 1, 64), z(0, 1, 64), hs)
+    assert y.shape == (0, 2, 64) and bool((hs == 1).all())
+
+
+def test_two_streams_at_once(dev):
+    """The same operators on two streams side by side give what they give alone."""
+    from gated_deltanet_chunked_delta_amd import selective_scan, short_conv
+    g = gen(36)
+    s = scan_inputs(g, (2, 700), 4, 1, 64, 64, torch.bfloat16, True, 2, True, dev)
+    x, w = rn(g, 2, 700, 160, dt=torch.bfloat16), rn(g, 160, 4, dt=torch.bfloat16)
+    dy = rn(g, 2, 700, 4, 64, dt=torch.bfloat16)
+
+    def run():
+        leaves = [s[k].detach().requires_grad_(True) for k in ("x", "dt", "A", "B", "C")]
+        y = selective_scan(*leaves, dt_bias=s["bias"], dt_softplus=True, initial_state=s["h0"])
+        return [y, short_conv(x, w)] + list(torch.autograd.grad(y, leaves, dy))
+
+    want = run()
+    torch.cuda.synchronize()
+    streams, got = [torch.cuda.Stream(), torch.cuda.Stream()], []
+    for k in range(6):
+        with torch.cuda.stream(streams[k % 2]):
+            got.append(run())
+    torch.cuda.synchronize()
+    for o in got:
+        assert all(torch.equal(a, b) for a, b in zip(o, want))

@@ -117,7 +117,7 @@ def test_scan_sizes(L):
     assert L.gdn_scan_bwd_workspace_size(ctypes.byref(b)) > own
 
 
-@pytest.mark.parametrize("kw,status", [(dict(Dk=32), 2), (dict(Dv=256), 2), (dict(G=3), 1), (dict(b=None), 1),
+@pytest.mark.parametrize("kw,status", [(dict(Dk=32), 2), (dict(Dv=320), 2), (dict(G=3), 1), (dict(b=None), 1),
                                        (dict(state=FAKE + 4), 1), (dict(x_stride=100), 1), (dict(num_slots=2), 1),
                                        (dict(N=0, x=None, state=None), 0)])
 def test_scan_step_refusals(L, kw, status):
