@@ -864,3 +864,67 @@ def test_two_streams_at_once(dev):
     torch.cuda.synchronize()
     for o in got:
         assert all(torch.equal(a, b) for a, b in zip(o, want))
+
+
+def test_offsets_past_32_bits(dev):
+    """A short sequence packed behind more than 2^31 elements, and slots that far into a cache,
+    give bit for bit what they give alone."""
+    from gated_deltanet_chunked_delta_amd import gated_group_norm, layers, selective_scan, short_conv
+    bf, H, Dv, tail = torch.bfloat16, 64, 128, 150
+    T = (1 << 31) // (H * Dv) + 1000
+    x = torch.randn(1, T, H, Dv, device=dev, dtype=bf)
+    dt = torch.rand(1, T, H, device=dev) * 0.1
+    B, C = torch.randn(1, T, 1, 64, device=dev, dtype=bf), torch.randn(1, T, 1, 64, device=dev, dtype=bf)
+    A = -torch.rand(H, device=dev)
+    cu = torch.tensor([0, T - tail, T], dtype=torch.int32)
+    alone = [t[:, -tail:].contiguous() for t in (x, dt, B, C)]
+
+    def scan(x, dt, B, C, **kw):
+        leaves = [t.detach().requires_grad_(True) for t in (x, dt, B, C)]
+        y, hT = selective_scan(leaves[0], leaves[1], A, leaves[2], leaves[3], seg_mode=-1, output_final_state=True, **kw)
+        grads = torch.autograd.grad(y, leaves, y.detach())
+        return [t[:, -tail:].detach().clone() for t in (y, *grads)] + [hT[-1:].detach().clone()]
+
+    print("[offsets] scan", flush=True)
+    got = scan(x, dt, B, C, cu_seqlens=cu.to(dev), cu_seqlens_host=cu)
+    assert all(torch.equal(a, b) for a, b in zip(got, scan(*alone)))
+    del got, dt, B, C
+    x, xa = x.view(1, T, H * Dv), alone[0].view(1, tail, H * Dv)
+    w = torch.randn(H * Dv, 4, device=dev, dtype=bf)
+
+    def conv(x, **kw):
+        leaf = x.detach().requires_grad_(True)
+        u, fin = short_conv(leaf, w, output_final_state=True, **kw)
+        (dx,) = torch.autograd.grad(u, leaf, u.detach())
+        return [u[:, -tail:].detach().clone(), dx[:, -tail:].clone(), fin[-1:].detach().clone()]
+
+    print("[offsets] convolution", flush=True)
+    got = conv(x, cu_seqlens=cu.to(dev), cu_seqlens_host=cu)
+    assert all(torch.equal(a, b) for a, b in zip(got, conv(xa)))
+
+    def norm(x):
+        leaf = x.detach().view(1, -1, H, Dv).requires_grad_(True)
+        y = gated_group_norm(leaf, w[:Dv, 0].contiguous(), x.view(leaf.shape))
+        (dx,) = torch.autograd.grad(y, leaf, y.detach())
+        return [y[:, -tail:].detach().clone(), dx[:, -tail:].clone()]
+
+    print("[offsets] norm", flush=True)
+    assert all(torch.equal(a, b) for a, b in zip(norm(x), norm(xa)))
+    del x, got
+    print("[offsets] steps", flush=True)
+    slots = (1 << 31) // (H * 64 * Dv) + 9
+    state = torch.zeros(slots, H, 64, Dv, device=dev)
+    xs, dts, Bs, Cs = (t[0, :3].contiguous() for t in alone)
+    idx = torch.tensor([slots - 1, 5, slots - 3], dtype=torch.int32, device=dev)
+    y = layers.gdn_scan_step(xs, dts, A, Bs, Cs, state, state_idx=idx)
+    small = torch.zeros(3, H, 64, Dv, device=dev)
+    assert torch.equal(y, layers.gdn_scan_step(xs, dts, A, Bs, Cs, small))
+    assert torch.equal(state[idx.long()], small) and bool(small.any())
+    del state
+    slots = (1 << 31) // (3 * H * Dv) + 9
+    state = torch.zeros(slots, 3, H * Dv, device=dev, dtype=bf)
+    idx = torch.tensor([slots - 1, 5, slots - 3], dtype=torch.int32, device=dev)
+    u = layers.gdn_conv_step(xs.view(3, H * Dv), state, w, state_idx=idx)
+    small = torch.zeros(3, 3, H * Dv, device=dev, dtype=bf)
+    assert torch.equal(u, layers.gdn_conv_step(xs.view(3, H * Dv), small, w))
+    assert torch.equal(state[idx.long()], small) and bool(small.any())
