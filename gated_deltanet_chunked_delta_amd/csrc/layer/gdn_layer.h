@@ -182,7 +182,8 @@ struct SweepParams {
   float* s_loc;              // sweeps without output: each segment's own end state [nseg][H][Dk][Dv]
   float* s_dec;              // and its total decay [nseg][H]
   void* out1;                // [tokens][H][Dv]
-  float* out2;               // [parts][tokens][Dk]
+  float* out2;               // [G * parts][tokens][Dk], where a group has more than one part
+  void* out2_whole;          // [tokens][G][Dk], where it has one
   float* rt;                 // [H * Dv / PS][tokens]
   float* xd;                 // nullable [H * Dv / PS][tokens]: x_t . dy_t over the slice
   float* cb;                 // nullable [G][tokens]: C_t . B_t

@@ -172,7 +172,8 @@ ScanPlan scan_plan(const gdn_scan_args& a, bool bwd, bool own_states) {
     p.o_anchor0 = take(sizeof(double) * vh * a.num_seqs);
     p.o_dump = take(sizeof(float) * state_elems(a) * chunks);
     p.o_sums = take(sizeof(double) * 3 * a.H * chunks);
-    p.o_part = take(sizeof(float) * gdn::sweep_parts_per_group(a.dtype, a.H, a.G, a.Dv) * (size_t)a.G * tokens * a.Dk);
+    const int parts = gdn::sweep_parts_per_group(a.dtype, a.H, a.G, a.Dv);
+    if (parts > 1) p.o_part = take(sizeof(float) * parts * (size_t)a.G * tokens * a.Dk);
   }
   p.total = off;
   return p;
@@ -499,18 +500,20 @@ gdn_status gdn_scan_bwd(const gdn_scan_bwd_args* args, void* stream) {
   red.seq = p.seq; red.segs = p.segs;
   p.s_in = hs;
   p.out2 = at<float>(ws, pl.o_part);
+  p.out2_whole = args->dc;
   p.rt = at<float>(ws, pl.o_rt);
   p.dump = at<float>(ws, pl.o_dump);
   hipError_t e = timed("scan_dc", s, [&] { return gdn::launch_sweep(a.dtype, 0, gdn::SWEEP_KEY, p, pl.nseg, s); });
   if (e != hipSuccess) return hip_fail(e, "scan dC launch");
   red.out = args->dc;
-  e = timed("scan_reduce", s, [&] { return gdn::launch_scan_reduce(a.dtype, red, s); });
+  if (red.ppg > 1) e = timed("scan_reduce", s, [&] { return gdn::launch_scan_reduce(a.dtype, red, s); });
   if (e != hipSuccess) return hip_fail(e, "scan reduce launch");
   // dB, and the backward row terms
   p = sweep_base(a, pl);
   sweep_dir(p, a, true, args->dy);
   p.s_in = gs;
   p.out2 = at<float>(ws, pl.o_part);
+  p.out2_whole = args->db;
   p.rt = at<float>(ws, pl.o_ct);
   p.xd = at<float>(ws, pl.o_xd);
   p.cb = at<float>(ws, pl.o_cb);
@@ -521,7 +524,7 @@ gdn_status gdn_scan_bwd(const gdn_scan_bwd_args* args, void* stream) {
   e = timed("scan_db", s, [&] { return gdn::launch_sweep(a.dtype, 1, gdn::SWEEP_KEY, p, pl.nseg, s); });
   if (e != hipSuccess) return hip_fail(e, "scan dB launch");
   red.out = args->db;
-  e = timed("scan_reduce", s, [&] { return gdn::launch_scan_reduce(a.dtype, red, s); });
+  if (red.ppg > 1) e = timed("scan_reduce", s, [&] { return gdn::launch_scan_reduce(a.dtype, red, s); });
   if (e != hipSuccess) return hip_fail(e, "scan reduce launch");
   // dx, dh0
   p.xd = nullptr; p.cb = nullptr;
