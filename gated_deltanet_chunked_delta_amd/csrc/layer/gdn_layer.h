@@ -181,6 +181,7 @@ struct SweepParams {
   float* s_end;              // nullable: state leaving the last segment of each sequence in sweep order [N][H][Dk][Dv]
   float* s_loc;              // sweeps without output: each segment's own end state [nseg][H][Dk][Dv]
   float* s_dec;              // and its total decay [nseg][H]
+  int round_once;            // bf16 out1: the chunk matrix and the state in two parts
   void* out1;                // [tokens][H][Dv]
   float* out2;               // [G * parts][tokens][Dk], where a group has more than one part
   void* out2_whole;          // [tokens][G][Dk], where it has one

@@ -188,6 +188,7 @@ gdn_status check_scan(const gdn_scan_args& a) {
   if (!((a.Dk == 64 || a.Dk == 128) && a.Dv % gdn::PS == 0 && a.Dv <= 256))
     return fail(GDN_E_UNSUPPORTED, "unsupported head sizes Dk=%d Dv=%d", a.Dk, a.Dv);
   if (a.dt_softplus != 0 && a.dt_softplus != 1) return fail(GDN_E_INVALID, "dt_softplus must be 0 or 1");
+  if (a.round_once != 0 && a.round_once != 1) return fail(GDN_E_INVALID, "round_once must be 0 or 1");
   const long long tokens = (long long)a.B * a.T;
   if (tokens >= (1LL << 31) || tokens * a.H * std::max(a.Dk, a.Dv) >= (1LL << 40) || (long long)a.H * a.Dv / gdn::PS > 65535)
     return fail(GDN_E_INVALID, "problem too large");
@@ -251,6 +252,7 @@ gdn::SweepParams sweep_base(const gdn_scan_args& a, const ScanPlan& pl) {
   p.seg_first = at<int>(ws, pl.o_seg_first);
   p.chunk_first = at<int>(ws, pl.o_chunk_first);
   p.per_seg = pl.multi;
+  p.round_once = a.round_once;
   p.s_dec = at<float>(ws, pl.o_dec);
   return p;
 }

@@ -30,9 +30,15 @@
 // factor (the state, keys or values times their decay) enters a product as
 // three bf16 parts, 24 bits in all, wherever its rounding would reach an fp32
 // result: the states, and the row terms rt, ct behind dA and ddt.  Where only a
-// bf16 output depends on it, it is rounded to bf16 once in out1 (the chunk matrix
-// and the state: together an error like the output's own rounding) and enters
-// out2 in two parts (the chunk matrix; a few products a wave).  fp32 inputs take the fp32 matrix instructions throughout.
+// bf16 output depends on it it enters in two parts, each rounded (2^-18 of it): the
+// chunk matrix in out2, and the values' decays in a segment whose state does not
+// leave.  In out1 the chunk matrix and the state are rounded to bf16 once, together
+// an error like the output's own rounding, unless the caller asks for outputs that
+// are rounded only once (round_once): then they too enter in two parts.  Rms error of
+// y against 64 bits, 4,096 tokens of 2 heads of 128 x 128: 2.04e-3, with round_once
+// 1.65e-3, which is the final rounding's alone; time of the four bf16 passes of
+// 333 to 65,536 tokens with it: 3 to 8 % more.
+// fp32 inputs take the fp32 matrix instructions throughout.
 //
 // Decay factors are products of factors <= 1 over 16-row blocks (a power of a
 // sum inside a block, a factor for the blocks between), so that no difference
@@ -66,26 +72,32 @@ template <> struct Parts<float> {
   static constexpr int N = 1;
   Frag<float> p[1];
 };
-template <int NP = 3>
 __device__ __forceinline__ void split(Parts<float>& o, const f32x4& lo, const f32x4& hi) { pack_frag(o.p[0], lo, hi); }
-template <int NP = 3>
 __device__ __forceinline__ void split(Parts<bf16>& o, const f32x4& lo, const f32x4& hi) {
   typedef uint32_t u32x4 __attribute__((__vector_size__(16)));
   float x[8] = {lo[0], lo[1], lo[2], lo[3], hi[0], hi[1], hi[2], hi[3]};
 #pragma unroll
-  for (int part = 0; part < NP; ++part) {
+  for (int part = 0; part < 3; ++part) {
     u32x4 v;
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
       const uint32_t a = __builtin_bit_cast(uint32_t, x[2 * i]), b = __builtin_bit_cast(uint32_t, x[2 * i + 1]);
       v[i] = __builtin_amdgcn_perm(b, a, 0x07060302u);  // the two high halves
-      if (part < NP - 1) {
+      if (part < 2) {
         x[2 * i] -= __builtin_bit_cast(float, a & 0xFFFF0000u);
         x[2 * i + 1] -= __builtin_bit_cast(float, b & 0xFFFF0000u);
       }
     }
     o.p[part].v = __builtin_bit_cast(bf16x8, v);
   }
+}
+// The first two parts rounded instead of cut: off by at most 2^-18 of the
+// operand to either side (two cut ones fall short by up to 2^-16).
+__device__ __forceinline__ void split2(Parts<float>& o, const f32x4& lo, const f32x4& hi) { pack_frag(o.p[0], lo, hi); }
+__device__ __forceinline__ void split2(Parts<bf16>& o, const f32x4& lo, const f32x4& hi) {
+  const PFrag<bf16> f(Frag<float>{lo, hi});
+  o.p[0] = f.hi;
+  o.p[1] = f.lo;
 }
 
 // Fragment whose k-slots walk down a column of a row-major LDS matrix (rows
@@ -141,6 +153,10 @@ __device__ __forceinline__ void mma_hi_lo(f32x4& acc, const Frag<bf16>& a, const
   mma(acc, a, b.hi);
 }
 __device__ __forceinline__ void mma_hi_lo(f32x4& acc, const Frag<float>& a, const PFrag<float>& b) { mma(acc, a, b.f); }
+__device__ __forceinline__ void mma_hi_lo(f32x4& acc, const PFrag<bf16>& a, const Frag<bf16>& b) {
+  mma(acc, a.lo, b);
+  mma(acc, a.hi, b);
+}
 
 // Tile of the lower triangle, tile (tb, sb) at index tb (tb + 1) / 2 + sb.
 __device__ __forceinline__ void tri_tile(int idx, int& tb, int& sb) {
@@ -419,31 +435,38 @@ __device__ __forceinline__ void st_f32x4(float* p, const f32x4& v) { *reinterpre
 // stands between chunks; in fp32 LDS does not hold it.
 template <class E> constexpr int kKeyBufs = sizeof(E) == 2 ? 2 : 1;
 
-template <class E, int DK, int NW>
+// MP: parts of the chunk matrix and of the state in out1 (bf16; see above)
+template <class E, int DK, int NW, int MP>
 struct ValueLds {
   E k[kKeyBufs<E>][CH * row_ld<E>(DK)];
   E q[CH * row_ld<E>(DK)];
   E v[NW][CH * row_ld<E>(VC)];
-  E m[NW / 2][10][64][4];     // by team
-  ChunkDecay dec[2][NW / 2];  // of this chunk and the next
+  E m[NW / 2][10][MP][64][4];  // by team, tile, part
+  ChunkDecay dec[2][NW / 2];   // of this chunk and the next
 };
 
-// Tile IDX of the head's chunk matrix: Q K^T, then the decays.
-template <int IDX, class E, int DK, int NW>
-__device__ __forceinline__ void chunk_matrix_tile(ValueLds<E, DK, NW>& sh, const E* k, const ChunkDecay& dec, int team) {
+// Tile IDX of the head's chunk matrix: Q K^T, then the decays; in MP parts.
+template <int IDX, class E, int DK, int NW, int MP>
+__device__ __forceinline__ void chunk_matrix_tile(ValueLds<E, DK, NW, MP>& sh, const E* k, const ChunkDecay& dec, int team) {
   constexpr int tb = IDX >= 6 ? 3 : IDX >= 3 ? 2 : IDX >= 1 ? 1 : 0, sb = IDX - tb * (tb + 1) / 2, LDK = row_ld<E>(DK);
   const int l = lane_id(), t16 = l & 15;
   f32x4 a = zero4();
 #pragma unroll
   for (int kb = 0; kb < DK / 32; ++kb)
     mma(a, ld_frag8(k, LDK, 16 * sb + t16, 32 * kb), ld_frag8(sh.q, LDK, 16 * tb + t16, 32 * kb));
-  st4f<E>(sh.m[team][IDX][l], a * tile_decay<sizeof(E) == 4>(dec, tb, sb));
+  a *= tile_decay<sizeof(E) == 4>(dec, tb, sb);
+#pragma unroll
+  for (int q = 0; q < MP; ++q) {
+    st4f<E>(sh.m[team][IDX][q][l], a);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) a[i] -= to_f(to_e<E>(a[i]));
+  }
 }
 
-template <class E, int DK, int NW, bool REV, bool OUT>
+template <class E, int DK, int NW, bool REV, bool OUT, int MP>
 __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, int parts) {
   extern __shared__ __align__(16) char smem[];
-  typedef ValueLds<E, DK, NW> Lds;
+  typedef ValueLds<E, DK, NW, MP> Lds;
   Lds* const sh0 = reinterpret_cast<Lds*>(smem);
   constexpr int LDK = row_ld<E>(DK), LDV = row_ld<E>(VC), NT = DK / 16, NTH = NW * 64;
   const int tid = threadIdx.x, w = __builtin_amdgcn_readfirstlane(wave_id()), l = lane_id(), t16 = l & 15, g4 = l >> 4;
@@ -462,8 +485,8 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
   const float Dh = OUT && p.D ? p.D[h] : 0.f;
 
   // The state leaves as fp32 from the state sweep and from a sequence's last
-  // segment; elsewhere only bf16 outputs read it, and two parts (16 bits) of
-  // the values are enough.
+  // segment; elsewhere only bf16 outputs read it, and two parts of the values
+  // are enough.
   const int np = !OUT || (last && p.s_end) ? Parts<E>::N : min(Parts<E>::N, 2);
   const int nch = (r.len + CH - 1) / CH;
   TileStage<E, DK, NTH, REV> tk, tq;
@@ -583,14 +606,19 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
       for (int kb = 0; kb < DK / 32; ++kb) {
         sched_fence();
         Lds& sh = *lds_opaque(sh0);
-        Frag<E> sf[2];
+        PFrag<E> sf[2];
 #pragma unroll
-        for (int pt = 0; pt < 2; ++pt) pack_frag(sf[pt], S[2 * kb][pt], S[2 * kb + 1][pt]);
+        for (int pt = 0; pt < 2; ++pt) sf[pt] = PFrag<E>(Frag<float>{S[2 * kb][pt], S[2 * kb + 1][pt]});
 #pragma unroll
         for (int tb = 0; tb < 4; ++tb) {
           const Frag<E> q = ld_frag8(sh.q, LDK, 16 * tb + t16, 32 * kb);
-          mma(o[tb][0], sf[0], q);
-          mma(o[tb][1], sf[1], q);
+          if constexpr (MP == 2) {
+            mma_hi_lo(o[tb][0], sf[0], q);
+            mma_hi_lo(o[tb][1], sf[1], q);
+          } else {
+            mma(o[tb][0], e_part(sf[0]), q);
+            mma(o[tb][1], e_part(sf[1]), q);
+          }
         }
       }
 #pragma unroll
@@ -615,18 +643,21 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
 #pragma unroll
         for (int kb = 0; kb <= tb / 2; ++kb) {
           const int i0 = tb * (tb + 1) / 2 + 2 * kb;
-          Frag<E> m;
-          if constexpr (sizeof(E) == 2) {
-            const bf16x4 x = *reinterpret_cast<const bf16x4*>(sh.m[team][i0][l]);
-            bf16x4 y = bf16x4{};
-            if (2 * kb + 1 <= tb) y = *reinterpret_cast<const bf16x4*>(sh.m[team][i0 + (2 * kb + 1 <= tb)][l]);
-            m.v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
-          } else {
-            m.lo = *reinterpret_cast<const f32x4*>(sh.m[team][i0][l]);
-            m.hi = 2 * kb + 1 <= tb ? *reinterpret_cast<const f32x4*>(sh.m[team][i0 + (2 * kb + 1 <= tb)][l]) : zero4();
+#pragma unroll
+          for (int q = MP - 1; q >= 0; --q) {
+            Frag<E> m;
+            if constexpr (sizeof(E) == 2) {
+              const bf16x4 x = *reinterpret_cast<const bf16x4*>(sh.m[team][i0][q][l]);
+              bf16x4 y = bf16x4{};
+              if (2 * kb + 1 <= tb) y = *reinterpret_cast<const bf16x4*>(sh.m[team][i0 + (2 * kb + 1 <= tb)][q][l]);
+              m.v = __builtin_shufflevector(x, y, 0, 1, 2, 3, 4, 5, 6, 7);
+            } else {
+              m.lo = *reinterpret_cast<const f32x4*>(sh.m[team][i0][q][l]);
+              m.hi = 2 * kb + 1 <= tb ? *reinterpret_cast<const f32x4*>(sh.m[team][i0 + (2 * kb + 1 <= tb)][q][l]) : zero4();
+            }
+            mma(o[tb][0], vf[kb][0], m);
+            mma(o[tb][1], vf[kb][1], m);
           }
-          mma(o[tb][0], vf[kb][0], m);
-          mma(o[tb][1], vf[kb][1], m);
         }
         const int row = 16 * tb + t16;
         const E* vr = sh.v[w] + row * LDV + 8 * g4;
@@ -675,7 +706,7 @@ __global__ __launch_bounds__(NW * 64, 2) void sweep_value_kernel(SweepParams p, 
         f32x4 lo, hi;
         frag_f32(vf[kb][pt], lo, hi);
         if (np == Parts<E>::N) split(vp[kb][pt], lo * e0, hi * e1);
-        else split<2>(vp[kb][pt], lo * e0, hi * e1);
+        else split2(vp[kb][pt], lo * e0, hi * e1);
       }
     }
 #pragma unroll
@@ -1050,16 +1081,22 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
   }
 }
 
-template <class E, int DK, int NW, bool REV, bool OUT>
-hipError_t value_launch(const SweepParams& p, int nseg, hipStream_t st) {
+template <class E, int DK, int NW, bool REV, bool OUT, int MP>
+hipError_t value_launch_parts(const SweepParams& p, int nseg, hipStream_t st) {
   const int upg = p.H / p.G * (p.Dv / VC), parts = (upg + NW - 1) / NW;
-  constexpr size_t lds = sizeof(ValueLds<E, DK, NW>);
+  constexpr size_t lds = sizeof(ValueLds<E, DK, NW, MP>);
   static_assert(lds <= 160 * 1024, "LDS of a compute unit");
-  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&sweep_value_kernel<E, DK, NW, REV, OUT>),
+  hipError_t e = hipFuncSetAttribute(reinterpret_cast<const void*>(&sweep_value_kernel<E, DK, NW, REV, OUT, MP>),
                                      hipFuncAttributeMaxDynamicSharedMemorySize, lds);
   if (e != hipSuccess) return e;
-  hipLaunchKernelGGL((sweep_value_kernel<E, DK, NW, REV, OUT>), dim3(nseg * p.G * parts), dim3(NW * 64), lds, st, p, parts);
+  hipLaunchKernelGGL((sweep_value_kernel<E, DK, NW, REV, OUT, MP>), dim3(nseg * p.G * parts), dim3(NW * 64), lds, st, p, parts);
   return hipGetLastError();
+}
+template <class E, int DK, int NW, bool REV, bool OUT>
+hipError_t value_launch(const SweepParams& p, int nseg, hipStream_t st) {
+  if constexpr (OUT && sizeof(E) == 2)
+    if (p.round_once) return value_launch_parts<E, DK, NW, REV, OUT, 2>(p, nseg, st);
+  return value_launch_parts<E, DK, NW, REV, OUT, 1>(p, nseg, st);
 }
 // Waves of a value sweep's workgroup: as many units as the group has, up to
 // eight (fp32: four, by LDS).

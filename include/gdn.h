@@ -358,7 +358,12 @@ gdn_status gdn_conv_step(const gdn_conv_step_args* args, void* stream);
  * from the start of its chunk of 64 tokens on, and no other sequence.
  * cu_seqlens / cu_seqlens_host as for the chunk calls.  seg_mode: sequences
  * are cut into segments that run side by side and are joined exactly
- * (0 = automatic, -1 = off, k > 0 = segments of k chunks of 64 tokens).  The
+ * (0 = automatic, -1 = off, k > 0 = segments of k chunks of 64 tokens).
+ * Precision: fp32 results carry fp32's, and dB, dC and ddt are rounded once.  Inside
+ * a bf16 y and dx the 64 x 64 matrix of a chunk and the state entering it are
+ * rounded to bf16 as well (rms error 1.8e-3 to 2.1e-3 of the values, of which the
+ * output's rounding is 1.65e-3), unless round_once is 1: then y and dx too are the
+ * fp32 result rounded once (3 to 8 % more time).  The
  * gradient's workspace holds a state for every chunk: 4 Dk Dv H bytes for every
  * 64 tokens. */
 typedef struct {
@@ -374,6 +379,7 @@ typedef struct {
   const float* D;              /* nullable [H] */
   const float* dt_bias;        /* nullable [H] */
   int32_t dt_softplus;
+  int32_t round_once;          /* 0 or 1 (see above) */
   const float* h0;             /* nullable [N, H, Dk, Dv] */
   const int32_t* cu_seqlens;
   const int32_t* cu_seqlens_host;

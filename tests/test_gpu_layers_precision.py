@@ -1,0 +1,115 @@
+"""The layer operators' precision on the GPU, at lengths and sums where a lost
+bit shows: outputs against the nearest value of their type to the 64-bit result,
+and fp32 results of thousands of tokens against a chunked 64-bit form.
+"""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+import torch.nn.functional as F  # noqa: E402
+
+BF = torch.bfloat16
+
+
+@pytest.fixture(scope="module")
+def dev():
+    if not torch.cuda.is_available():
+        pytest.skip("no GPU")
+    return torch.device("cuda:0")
+
+
+def scan64(x, dt, A, B, C, D, bias, softplus, h0, lens, Q=64):
+    """The scan in 64 bits by chunks of Q tokens, differentiable; x [T, H, P], B, C [T, G, N],
+    states [n, H, N, P].  Returns y and the final states."""
+    H, G = x.shape[1], B.shape[1]
+    rep = H // G
+    d = dt + bias if bias is not None else dt
+    d = torch.logaddexp(d, torch.zeros_like(d)) if softplus else d
+    tri = torch.tril(torch.ones(Q, Q, dtype=torch.bool, device=x.device))
+    ys, hs, at = [], [], 0
+    for n, L in enumerate(lens):
+        nc = (L + Q - 1) // Q
+
+        def cut(a):  # [L, heads, k] -> [nc, heads, Q, k], zero rows behind the end
+            a = torch.cat([a[at:at + L], a.new_zeros(nc * Q - L, *a.shape[1:])], 0)
+            return a.reshape(nc, Q, *a.shape[1:]).transpose(1, 2)
+
+        h = h0[n] if h0 is not None else x.new_zeros(H, B.shape[2], x.shape[2])
+        X, K, O, dd = cut(x), cut(B).repeat_interleave(rep, 1), cut(C).repeat_interleave(rep, 1), cut(d[..., None])
+        cum = (dd * A[:, None, None]).cumsum(2)
+        Lm = torch.exp(torch.where(tri, cum - cum.transpose(2, 3), torch.full_like(cum[:1, :1, :1, :1], -torch.inf)))
+        V = dd * X
+        inner = ((O @ K.transpose(2, 3)) * Lm) @ V
+        tot = cum[:, :, -1:]
+        add = K.transpose(2, 3) @ (torch.exp(tot - cum) * V)
+        rows = []
+        for c in range(nc):
+            rows.append(inner[c] + torch.exp(cum[c]) * (O[c] @ h))
+            h = torch.exp(tot[c]) * h + add[c]
+        if L:
+            y = torch.stack(rows).transpose(1, 2).reshape(nc * Q, H, -1)[:L]
+            ys.append(y if D is None else y + D[:, None] * x[at:at + L])
+        hs.append(h)
+        at += L
+    return (torch.cat(ys) if ys else torch.zeros_like(x)), torch.stack(hs)
+
+
+def inputs(seed, T, H, G, Dk, Dv, n, dt=BF, dev="cuda:0"):
+    g = torch.Generator(device=dev).manual_seed(seed)
+    rn = lambda *s: torch.randn(*s, generator=g, device=dev)
+    return dict(x=F.silu(rn(1, T, H, Dv)).to(dt), dt=rn(1, T, H).to(dt), A=-(1 + 15 * torch.rand(H, generator=g, device=dev)),
+                B=F.silu(rn(1, T, G, Dk)).to(dt), C=F.silu(rn(1, T, G, Dk)).to(dt), D=rn(H), bias=rn(H) - 4,
+                h0=0.3 * rn(n, H, Dk, Dv)), rn(1, T, H, Dv).to(dt), 0.3 * rn(n, H, Dk, Dv)
+
+
+ORDER = ["x", "dt", "A", "B", "C", "D", "bias", "h0"]
+
+
+def both(seed, lens, H, G, Dk, Dv, dt=BF, **opts):
+    """{name: (got, 64-bit)} of the outputs and gradients of one packed batch."""
+    from gated_deltanet_chunked_delta_amd import selective_scan
+    T, n = sum(lens), len(lens)
+    s, dy, dhT = inputs(seed, T, H, G, Dk, Dv, n, dt)
+    cu = torch.tensor([0] + list(lens)).cumsum(0).to(torch.int32)
+    kw = dict(cu_seqlens=cu.to(dy.device), cu_seqlens_host=cu) if n > 1 else {}
+    leaves = [s[k].requires_grad_(True) for k in ORDER]
+    y, hT = selective_scan(s["x"], s["dt"], s["A"], s["B"], s["C"], D=s["D"], dt_bias=s["bias"], dt_softplus=True,
+                           initial_state=s["h0"], output_final_state=True, **opts, **kw)
+    grads = torch.autograd.grad([y, hT], leaves, [dy, dhT])
+    torch.cuda.synchronize()
+    r = {k: s[k].detach().double() for k in ORDER}
+    r = {k: (v[0] if k in ("x", "dt", "B", "C") else v).requires_grad_(True) for k, v in r.items()}
+    ry, rh = scan64(*(r[k] for k in ORDER[:7]), True, r["h0"], lens)
+    rg = torch.autograd.grad([ry, rh], [r[k] for k in ORDER], [dy[0].double(), dhT.double()])
+    out = dict(y=(y[0], ry), hT=(hT, rh))
+    for k, a, b in zip(ORDER, grads, rg):
+        out["d" + k] = (a[0] if k in ("x", "dt", "B", "C") else a, b)
+    return {k: (a.detach(), b.detach()) for k, (a, b) in out.items()}
+
+
+def rms(t):
+    return t.double().square().mean().sqrt().item()
+
+
+ROUNDED = [  # lens, H, G, Dk, Dv, seg_mode
+    ([4096], 2, 1, 128, 128, 0),
+    ([1000, 3, 900], 4, 2, 64, 64, 2),
+    ([777], 3, 1, 128, 64, -1),
+    ([500, 140], 1, 1, 64, 192, 1),
+]
+
+
+@pytest.mark.parametrize("lens,H,G,Dk,Dv,seg", ROUNDED)
+def test_scan_outputs_are_rounded_once(dev, lens, H, G, Dk, Dv, seg):
+    """With round_once bf16 outputs and gradients are the 64-bit result rounded once, but for what precedes the
+    rounding: factors of the products off by 2^-18 each, two a product, so 2^-16 of the rms
+    scale with room for their sums.  A pre-rounding error e turns the rounding over with
+    probability 2 e / step, by one step, step <= 2^-7 of the value: rms
+    sqrt(2 e step) = sqrt(2 2^-16 2^-7) = 2^-11 of the rms."""
+    for k, (got, want) in both(3, lens, H, G, Dk, Dv, seg_mode=seg, round_once=True).items():
+        if got.dtype != BF:
+            continue
+        e = rms(got.double() - want.to(BF).double()) / rms(want)
+        print(f"    {k} {e:.2e}", flush=True)
+        assert e <= 2.0 ** -11, k
