@@ -17,6 +17,9 @@ is free.  Tensors of a call share one device, whose current stream it uses.
 Calls can be captured into a graph, a backward pass too, provided that no eager
 graph of the same leaves is alive then: autograd would synchronise with the
 stream that one was made on, which a capture cannot.
+
+Reverse mode only: forward-mode derivatives are refused.  No derivative passes
+through the ``gdn_*`` calls; the two steps refuse inputs that ask for one.
 """
 from __future__ import annotations
 
@@ -25,6 +28,7 @@ import ctypes
 from typing import Optional
 
 import torch
+from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
 from .binding import GDNError, _check, _dtype_code, _ptr, _vp, lib as _load
@@ -230,13 +234,29 @@ def _call(fn, args, dev):
         _check(status)
 
 
+def _has_tangent(tensors):
+    return forward_ad._current_level >= 0 and any(
+        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+
+
 def _wants_grad(*tensors):
-    """Whether a call has to go through autograd; one that has not calls the library directly."""
+    """Whether a call has to go through its autograd function (which has no forward mode and
+    says so); one that has not calls the library directly."""
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
                 return True
-    return False
+    return _has_tangent(tensors)
+
+
+def _no_derivative(name, *tensors):
+    """Refuses a step whose derivative the caller expects: it advances its state in place and has none."""
+    if torch.is_grad_enabled():
+        for t in tensors:
+            if t is not None and t.requires_grad:
+                raise GDNError(f"{name} has no gradient: call it under torch.no_grad()")
+    if _has_tangent(tensors):
+        raise GDNError(f"{name} has no derivative")
 
 
 # ------------------------------------------------------------------ short causal convolution
@@ -307,6 +327,7 @@ def gdn_conv_step(x, state, weight, bias=None, silu: bool = True, state_idx=None
     left as it was).  Two sequences of one call must not share a slot.  Returns y [N, D]."""
     if x.dim() != 2 or weight.dim() != 2:
         raise GDNError("x must be [N, D] and weight [D, W]")
+    _no_derivative("gdn_conv_step", x, state, weight, bias)
     N, D = x.shape
     W, dt, dev = weight.shape[1], x.dtype, x.device
     a = ConvStepArgs()
@@ -451,6 +472,7 @@ def gdn_scan_step(x, dt, A, B, C, state, D=None, dt_bias=None, dt_softplus: bool
     [S, H, Dk, Dv] fp32 is advanced in place (slots as in gdn_decode_step).  Returns y."""
     if x.dim() != 3 or B.dim() != 3:
         raise GDNError("x must be [N, H, Dv] and B, C [N, G, Dk]")
+    _no_derivative("gdn_scan_step", x, dt, A, B, C, state, D, dt_bias)
     N, H, Dv = x.shape
     G, Dk = B.shape[1:]
     dev, e = x.device, x.dtype

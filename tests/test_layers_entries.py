@@ -4,6 +4,7 @@ import ctypes
 
 import pytest
 import torch
+import torch.autograd.forward_ad as fw
 
 from gated_deltanet_chunked_delta_amd import GDNError, layers
 from gated_deltanet_chunked_delta_amd import binding as B
@@ -37,3 +38,62 @@ def test_round_once_field(L):
         a = fill(layers.ScanFwdArgs(), a=scan(round_once=v), y=FAKE)
         assert L.gdn_scan_fwd(ctypes.byref(a), None) == 1 and b"round_once" in L.gdn_last_error()
         assert L.gdn_scan_fwd_workspace_size(ctypes.byref(a)) == 0
+
+
+# ------------------------------------------------------------------ derivatives
+@pytest.fixture
+def stub(monkeypatch):
+    """The entries on CPU tensors, the library's calls replaced by a record of their names."""
+    calls = []
+
+    class Lib:
+        def __getattr__(self, name):
+            if name.endswith("_size") or name.endswith("_bytes"):
+                return lambda args: 256
+            return lambda args, stream: calls.append(name)
+    monkeypatch.setattr(layers, "lib", Lib)
+    monkeypatch.setattr(layers, "_on_gpu", lambda name, t: t.device)
+    monkeypatch.setattr(layers, "_raw_stream", lambda index: None)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    return calls
+
+
+def operators():
+    """{name: (function of its first input, that input)}"""
+    g = torch.Generator().manual_seed(0)
+    r = lambda *s: torch.randn(*s, generator=g)
+    A, w, nw, dt, k = -torch.ones(2), r(8, 4), r(8), r(1, 6, 2), r(1, 6, 1, 64)
+    st, hs = torch.zeros(3, 3, 8), torch.zeros(3, 2, 64, 64)
+    return dict(short_conv=(lambda x: layers.short_conv(x, w), r(1, 5, 8)),
+                selective_scan=(lambda x: layers.selective_scan(x, dt, A, k, k), r(1, 6, 2, 64)),
+                gated_group_norm=(lambda x: layers.gated_group_norm(x, nw), r(4, 2, 8)),
+                gdn_conv_step=(lambda x: layers.gdn_conv_step(x, st, w), r(3, 8)),
+                gdn_scan_step=(lambda x: layers.gdn_scan_step(x, dt[0, :3], A, k[0, :3], k[0, :3], hs), r(3, 2, 64)))
+
+
+NAMES = ["short_conv", "selective_scan", "gated_group_norm", "gdn_conv_step", "gdn_scan_step"]
+
+
+@pytest.mark.parametrize("name", NAMES)
+def test_forward_mode_is_refused(stub, name):
+    """No result without its tangent, in grad mode and outside it."""
+    f, x = operators()[name]
+    f(x)
+    assert len(stub) == 1
+    for grad in (True, False):
+        with fw.dual_level(), torch.set_grad_enabled(grad), pytest.raises((NotImplementedError, GDNError)):
+            f(fw.make_dual(x, torch.ones_like(x)))
+    with fw.dual_level():                       # a level without a tangent changes nothing
+        assert torch.is_tensor(f(x))
+
+
+@pytest.mark.parametrize("name", ["gdn_conv_step", "gdn_scan_step"])
+def test_steps_refuse_a_gradient(stub, name):
+    """A step has no gradient; it does not return a detached result without saying so."""
+    f, x = operators()[name]
+    with pytest.raises(GDNError, match="no_grad"):
+        f(x.requires_grad_(True))
+    assert not stub
+    with torch.no_grad():
+        f(x)
+    assert len(stub) == 1
