@@ -20,6 +20,8 @@ stream that one was made on, which a capture cannot.
 
 Reverse mode only: forward-mode derivatives are refused.  No derivative passes
 through the ``gdn_*`` calls; the two steps refuse inputs that ask for one.
+Tracers that would record a call without its kernels are refused as well
+(``torch.jit.trace`` keeps the three operators as one operation each).
 """
 from __future__ import annotations
 
@@ -224,7 +226,37 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
     lambda index: torch.cuda.current_stream(index).cuda_stream)
 
 
+# The library's calls are invisible to tracers, which would keep the outputs' allocation
+# and drop what fills them: such a call is refused.  An autograd function is one
+# operation to torch.jit.trace, and its replay calls the library; what it runs inside
+# is not traced.
+_tracing_state = torch._C._get_tracing_state
+_MODES = [torch._C._TorchDispatchModeKey.PROXY, torch._C._TorchDispatchModeKey.FAKE]
+
+
+def _refuse_traced():
+    if _tracing_state() is not None or any(torch._C._get_dispatch_mode(m) is not None for m in _MODES):
+        raise GDNError("this call cannot be traced: the trace would not hold the library's kernels")
+
+
+@contextlib.contextmanager
+def _untraced():
+    state = _tracing_state()
+    torch._C._set_tracing_state(None)
+    try:
+        yield
+    finally:
+        torch._C._set_tracing_state(state)
+
+
+def _as_one_op():
+    """What the forward pass of an autograd function runs in."""
+    return _NO_SWITCH if _tracing_state() is None else _untraced()
+
+
 def _call(fn, args, dev):
+    if _tracing_state() is not None or torch._C._len_torch_dispatch_stack():
+        _refuse_traced()
     if torch.cuda.current_device() == dev.index:
         status = fn(ctypes.byref(args), _raw_stream(dev.index))
     else:
@@ -246,7 +278,7 @@ def _wants_grad(*tensors):
         for t in tensors:
             if t is not None and t.requires_grad:
                 return True
-    return _has_tangent(tensors)
+    return _tracing_state() is not None or _has_tangent(tensors)
 
 
 def _no_derivative(name, *tensors):
@@ -351,7 +383,9 @@ def gdn_conv_step(x, state, weight, bias=None, silu: bool = True, state_idx=None
 class _ShortConv(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, weight, bias, initial_state, silu, cu_seqlens, cu_seqlens_host, output_final_state):
-        y, fin = gdn_conv_fwd(x, weight, bias, silu, initial_state, cu_seqlens, cu_seqlens_host, output_final_state)
+        with _as_one_op():
+            y, fin = gdn_conv_fwd(x, weight, bias, silu, initial_state, cu_seqlens, cu_seqlens_host,
+                                  output_final_state)
         ctx.save_for_backward(x, weight, bias, initial_state, cu_seqlens)
         ctx.silu, ctx.cu_host = silu, _own_lengths(cu_seqlens_host)
         ctx.set_materialize_grads(False)
@@ -507,10 +541,11 @@ class _SelectiveScan(torch.autograd.Function):
     @staticmethod
     def forward(ctx, x, dt, A, B, C, D, dt_bias, h0, dt_softplus, cu_seqlens, cu_seqlens_host, final, seg_mode,
                 round_once):
-        cu_seqlens_host = _own_lengths(cu_seqlens_host if cu_seqlens_host is not None else
-                                       None if cu_seqlens is None else cu_seqlens.cpu())
-        res = gdn_scan_fwd(x, dt, A, B, C, D, dt_bias, dt_softplus, h0, cu_seqlens, cu_seqlens_host, final,
-                           save_states=True, seg_mode=seg_mode, round_once=round_once)
+        with _as_one_op():
+            cu_seqlens_host = _own_lengths(cu_seqlens_host if cu_seqlens_host is not None else
+                                           None if cu_seqlens is None else cu_seqlens.cpu())
+            res = gdn_scan_fwd(x, dt, A, B, C, D, dt_bias, dt_softplus, h0, cu_seqlens, cu_seqlens_host, final,
+                               save_states=True, seg_mode=seg_mode, round_once=round_once)
         ctx.save_for_backward(x, dt, A, B, C, D, dt_bias, h0, cu_seqlens, res[2])
         ctx.dt_softplus, ctx.cu_host, ctx.seg_mode, ctx.round_once = dt_softplus, cu_seqlens_host, seg_mode, round_once
         ctx.set_materialize_grads(False)
@@ -610,7 +645,8 @@ class _GatedGroupNorm(torch.autograd.Function):
     def forward(ctx, x, weight, z, bias, eps, center, gate_first):
         ctx.save_for_backward(x, weight, z, bias)
         ctx.opts = (eps, center, gate_first)
-        return gdn_norm_fwd(x, weight, z, bias, eps, center, gate_first)
+        with _as_one_op():
+            return gdn_norm_fwd(x, weight, z, bias, eps, center, gate_first)
 
     @staticmethod
     @once_differentiable

@@ -97,3 +97,41 @@ def test_steps_refuse_a_gradient(stub, name):
     with torch.no_grad():
         f(x)
     assert len(stub) == 1
+
+
+# ------------------------------------------------------------------ tracers
+@pytest.mark.parametrize("name", NAMES)
+def test_traces_hold_the_call_or_are_refused(stub, name):
+    f, x = operators()[name]
+    if name.startswith("gdn_"):
+        with pytest.raises(GDNError, match="traced"):
+            torch.jit.trace(f, (x,), check_trace=False)
+    else:
+        t = torch.jit.trace(f, (x,), check_trace=False)
+        for n in (1, 2):
+            del stub[:]
+            t(x)
+            assert len(stub) == 1               # the replay calls the library
+    from torch._subclasses.fake_tensor import FakeTensorMode
+    from torch.fx.experimental.proxy_tensor import make_fx
+    del stub[:]
+    with pytest.raises(GDNError, match="traced"):
+        make_fx(f)(x)
+    with pytest.raises((GDNError, RuntimeError)), FakeTensorMode(allow_non_fake_inputs=True) as m:
+        f(m.from_tensor(x))
+    assert not stub
+
+
+def test_traces_of_direct_calls_are_refused(stub):
+    x, w = torch.randn(1, 5, 8), torch.randn(8, 4)
+    with pytest.raises(GDNError, match="traced"):
+        torch.jit.trace(lambda a: layers.gdn_conv_fwd(a, w), (x,), check_trace=False)
+    assert not stub
+
+
+def test_modes_that_only_watch_are_no_tracers(stub):
+    from torch.utils.flop_counter import FlopCounterMode
+    f, x = operators()["short_conv"]
+    with FlopCounterMode(display=False):
+        f(x)
+    assert stub == ["gdn_conv_fwd"]
