@@ -198,6 +198,13 @@ def _seqs(cu, cu_host, B, T, dev, need_host):
     return cu, cu_host, cu.numel() - 1
 
 
+def _gradient(t):
+    """An incoming gradient as the scan's kernels take it.  Where autograd hands on a view (a
+    slice of a concatenation's gradient, say) it may be contiguous and still start anywhere."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _own_lengths(cu_host):
     """A copy of the host lengths, kept for the backward pass: the caller may reuse its own."""
     return None if cu_host is None else torch.as_tensor(cu_host, dtype=torch.int32).clone()
@@ -560,7 +567,7 @@ class _SelectiveScan(torch.autograd.Function):
                 return (None,) * 14
             dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
         dx, ddt, dA, dB, dC, dD, dbias, dh0 = gdn_scan_bwd(
-            x, dt, A, B, C, dy.contiguous(), D, dt_bias, ctx.dt_softplus, h0,
+            x, dt, A, B, C, _gradient(dy), D, dt_bias, ctx.dt_softplus, h0,
             None if dhT is None else dhT.contiguous(), cu, ctx.cu_host, states, ctx.seg_mode,
             ctx.round_once)
         return dx, ddt, dA, dB, dC, dD, dbias, dh0, None, None, None, None, None, None

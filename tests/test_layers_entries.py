@@ -44,13 +44,19 @@ def test_round_once_field(L):
 @pytest.fixture
 def stub(monkeypatch):
     """The entries on CPU tensors, the library's calls replaced by a record of their names."""
-    calls = []
+    class Calls(list):
+        args = None
+    calls = Calls()
 
     class Lib:
         def __getattr__(self, name):
             if name.endswith("_size") or name.endswith("_bytes"):
                 return lambda args: 256
-            return lambda args, stream: calls.append(name)
+
+            def call(args, stream):
+                calls.append(name)
+                calls.args = args._obj
+            return call
     monkeypatch.setattr(layers, "lib", Lib)
     monkeypatch.setattr(layers, "_on_gpu", lambda name, t: t.device)
     monkeypatch.setattr(layers, "_raw_stream", lambda index: None)
@@ -97,6 +103,35 @@ def test_steps_refuse_a_gradient(stub, name):
     with torch.no_grad():
         f(x)
     assert len(stub) == 1
+
+
+@pytest.mark.parametrize("dt", [torch.bfloat16, torch.float32])
+@pytest.mark.parametrize("lead", [1, 3, 8])
+def test_gradients_that_start_anywhere(stub, dt, lead):
+    """The gradient of y behind `lead` other entries of a concatenation is contiguous and starts
+    off 16 bytes; the library gets an aligned one with its values."""
+    x = torch.randn(1, 6, 2, 64).to(dt).requires_grad_(True)
+    A, d, k = -torch.ones(2), torch.randn(1, 6, 2), torch.randn(1, 6, 1, 64).to(dt)
+    seen = []
+
+    class Watch(torch.autograd.Function):
+        @staticmethod
+        def forward(ctx, y):
+            return y.view_as(y)
+
+        @staticmethod
+        def backward(ctx, g):
+            seen.append(g)
+            return g
+
+    y = Watch.apply(layers.selective_scan(x, d, A, k, k))
+    both = torch.cat([torch.zeros(lead, dtype=dt), y.flatten()])
+    both.backward(torch.arange(both.numel()).to(dt))
+    g = seen[0]
+    assert g.is_contiguous() and g.data_ptr() % 16 == lead * dt.itemsize % 16
+    at = stub.args.dy
+    assert stub[-1] == "gdn_scan_bwd" and at % 16 == 0 and (at == g.data_ptr()) == (lead * dt.itemsize % 16 == 0)
+    assert torch.equal(layers._gradient(g), g)
 
 
 # ------------------------------------------------------------------ tracers
