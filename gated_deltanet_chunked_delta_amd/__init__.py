@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import torch
 
-from .binding import GDNError, gdn_chunk_bwd, gdn_chunk_fwd, gdn_decode_step, lib  # noqa: F401
+from .binding import GDNError, _gradient, gdn_chunk_bwd, gdn_chunk_fwd, gdn_decode_step, lib  # noqa: F401
 from .layers import (gated_group_norm, gdn_conv_bwd, gdn_conv_fwd, gdn_conv_step, gdn_norm_bwd,  # noqa: F401
                      gdn_norm_fwd, gdn_scan_bwd, gdn_scan_fwd, gdn_scan_step, selective_scan, short_conv)
 
@@ -39,7 +39,7 @@ class _ChunkGatedDeltaRule(torch.autograd.Function):
     def backward(ctx, do, dhT):
         q, k, v, g, beta, h0, cu, states, chunk_t, gate_scale = ctx.saved_tensors
         dq, dk, dv, dg, dbeta, dh0 = gdn_chunk_bwd(
-            q, k, v, g, beta, ctx.scale, do.contiguous(), h0=h0,
+            q, k, v, g, beta, ctx.scale, _gradient(do), h0=h0,
             dhT=None if dhT is None else dhT.contiguous(), cu_seqlens=cu,
             cu_seqlens_host=ctx.cu_host, cp_mode=ctx.cp_mode, need_dh0=h0 is not None, states=states,
             chunk_t=chunk_t, qk_norm=ctx.qk_norm, gate_act=ctx.gate_act, gate_scale=gate_scale)

@@ -125,6 +125,13 @@ def _contig(name, t, dtype=None, device=None):
     return t
 
 
+def _gradient(t):
+    """An incoming gradient as the kernels take it.  Where autograd hands on a view (a
+    slice of a concatenation's gradient, say) it may be contiguous and still start anywhere."""
+    t = t.contiguous()
+    return t if t.data_ptr() % 16 == 0 else t.clone()
+
+
 def _prep(a, q, qk_norm, gate_act, gate_scale):
     """Fill the pre-processing fields of an argument struct."""
     a.qk_norm, a.gate_act = int(bool(qk_norm)), int(bool(gate_act))

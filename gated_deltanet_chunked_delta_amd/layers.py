@@ -33,7 +33,7 @@ import torch
 from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
-from .binding import GDNError, _check, _dtype_code, _ptr, _vp, lib as _load
+from .binding import GDNError, _check, _dtype_code, _gradient, _ptr, _vp, lib as _load
 
 __all__ = ["short_conv", "selective_scan", "gated_group_norm", "gdn_conv_fwd", "gdn_conv_bwd", "gdn_conv_step",
            "gdn_scan_fwd", "gdn_scan_bwd", "gdn_scan_step", "gdn_norm_fwd", "gdn_norm_bwd"]
@@ -196,13 +196,6 @@ def _seqs(cu, cu_host, B, T, dev, need_host):
         if int(cu_host[0]) != 0 or int(cu_host[-1]) != T or bool((cu_host[1:] < cu_host[:-1]).any()):
             raise GDNError(f"cu_seqlens must rise from 0 to {T}")
     return cu, cu_host, cu.numel() - 1
-
-
-def _gradient(t):
-    """An incoming gradient as the scan's kernels take it.  Where autograd hands on a view (a
-    slice of a concatenation's gradient, say) it may be contiguous and still start anywhere."""
-    t = t.contiguous()
-    return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
 def _own_lengths(cu_host):

@@ -49,3 +49,17 @@ def test_gradients_that_start_anywhere(dev, dt):
             else:
                 e = (a.double() - b.double()).abs().max() / b.double().abs().max()
                 assert e <= 2 * ((16 + 2 * 48 ** 0.5) * 2.0 ** -24 + (2.0 ** -8 if dt == BF else 0.0))
+
+
+def test_chunk_rule_gradients_that_start_anywhere(dev):
+    from gated_deltanet_chunked_delta_amd import chunk_gated_delta_rule
+    g = torch.Generator(device=dev).manual_seed(2)
+    rn = lambda *s: torch.randn(*s, generator=g, device=dev)
+    into = [t.requires_grad_(True) for t in (
+        rn(1, 130, 2, 64).to(BF), rn(1, 130, 2, 64).to(BF), rn(1, 130, 2, 64).to(BF), -rn(1, 130, 2).abs(), rn(1, 130, 2).to(BF))]
+    f = lambda: chunk_gated_delta_rule(*into, qk_norm=True)
+    dy = rn(1, 130, 2, 64).to(BF)
+    want = torch.autograd.grad(f(), into, dy)
+    z = torch.zeros(3, dtype=BF, device=dev)
+    got = torch.autograd.grad(torch.cat([z, f().flatten()]), into, torch.cat([z, dy.flatten()]))
+    assert all(torch.equal(a, b) for a, b in zip(got, want))

@@ -134,6 +134,27 @@ def test_gradients_that_start_anywhere(stub, dt, lead):
     assert torch.equal(layers._gradient(g), g)
 
 
+def test_chunk_rule_gradients_that_start_anywhere(monkeypatch):
+    """The same for the delta rule's own gradient."""
+    import gated_deltanet_chunked_delta_amd as pkg
+    seen = []
+
+    def fwd(q, k, v, *a, **kw):
+        return torch.zeros_like(v), torch.zeros(1), torch.zeros(1), torch.zeros(1)
+
+    def bwd(q, k, v, g, beta, scale, do, **kw):
+        seen.append(do)
+        return tuple(torch.zeros_like(t) for t in (q, k, v, g, beta)) + (None,)
+    monkeypatch.setattr(pkg, "gdn_chunk_fwd", fwd)
+    monkeypatch.setattr(pkg, "gdn_chunk_bwd", bwd)
+    q = torch.randn(1, 6, 2, 64).bfloat16().requires_grad_(True)
+    o = pkg.chunk_gated_delta_rule(q, q, q, torch.zeros(1, 6, 2), torch.zeros(1, 6, 2).bfloat16())
+    both = torch.cat([torch.zeros(3).bfloat16(), o.flatten()])
+    w = torch.arange(both.numel()).bfloat16()
+    both.backward(w)
+    assert seen[0].data_ptr() % 16 == 0 and torch.equal(seen[0].flatten(), w[3:])
+
+
 # ------------------------------------------------------------------ tracers
 @pytest.mark.parametrize("name", NAMES)
 def test_traces_hold_the_call_or_are_refused(stub, name):
