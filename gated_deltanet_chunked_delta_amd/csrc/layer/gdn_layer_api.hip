@@ -14,6 +14,9 @@ using namespace gdn_host;
 bool known_dtype(int d) { return d == GDN_F32 || d == GDN_BF16; }
 size_t esize(int d) { return d == GDN_BF16 ? 2 : 4; }
 
+// A launch has fewer than 2^32 threads (in x; blocks of up to 512).
+bool launchable(double threads) { return threads < 4294967296. - 512.; }
+
 // ---------------------------------------------------------------- convolution
 gdn_status check_conv(const gdn_conv_args& a) {
   if (!known_dtype(a.dtype)) return fail(GDN_E_UNSUPPORTED, "unknown dtype %d", a.dtype);
@@ -67,6 +70,12 @@ bool conv_vec(const gdn_conv_args& a) {
          aligned(a.bias, 16);
 }
 int64_t runs_of(const gdn_conv_args& a, int run) { return ((int64_t)a.B * a.T + run - 1) / run; }
+
+// The threads of a pass with V channels each: the runs, and W-1 rows of each
+// sequence's state where those are written.
+bool conv_launchable(const gdn_conv_args& a, int run, int V, bool states) {
+  return launchable((double)(runs_of(a, run) + (states ? (int64_t)a.num_seqs * (a.W - 1) : 0)) * (a.D / V));
+}
 
 // The gradient's run length does not depend on pointers, so that the workspace
 // size is known before they are.
@@ -226,9 +235,8 @@ gdn_status check_scan(const gdn_scan_args& a) {
   return GDN_OK;
 }
 
-// A launch has fewer than 2^32 threads.
 gdn_status check_grid(const gdn_scan_args& a, const ScanPlan& pl) {
-  if ((long long)pl.nseg * gdn::sweep_workgroups(a.dtype, a.H, a.G, a.Dv) >= (1LL << 32) / 512)
+  if (!launchable(512. * pl.nseg * gdn::sweep_workgroups(a.dtype, a.H, a.G, a.Dv)))
     return fail(GDN_E_INVALID, "problem too large: %d segments", pl.nseg);
   return GDN_OK;
 }
@@ -299,7 +307,8 @@ gdn_status check_norm(const gdn_norm_args& a) {
   if (!known_dtype(a.dtype)) return fail(GDN_E_UNSUPPORTED, "unknown dtype %d", a.dtype);
   if (a.R < 0 || a.G < 1 || a.D < 1)
     return fail(GDN_E_INVALID, "bad sizes R=%lld G=%d D=%d", (long long)a.R, a.G, a.D);
-  if (a.R >= (1LL << 40) / a.G / a.D || a.R * a.G >= (1LL << 31) || a.G > 65535)
+  if (a.R >= (1LL << 40) / a.G / a.D || a.R * a.G >= (1LL << 31) || a.G > 65535 ||
+      a.D >= INT_MAX - 1024)
     return fail(GDN_E_INVALID, "problem too large");
   if ((a.shared | a.center | a.gate_first) & ~1) return fail(GDN_E_INVALID, "shared, center and gate_first must be 0 or 1");
   if (!(a.eps > 0.f) || !std::isfinite(a.eps)) return fail(GDN_E_INVALID, "eps must be positive and finite");
@@ -353,6 +362,7 @@ gdn_status gdn_conv_fwd(const gdn_conv_fwd_args* args, void* stream) {
   const bool vec = conv_vec(a) && aligned(p.y, 16) && aligned(p.fin, 16);
   p.run = conv_run(a, vec, 4, 32, 16);
   p.nruns = runs_of(a, p.run);
+  if (!conv_launchable(a, p.run, vec ? 16 / (int)esize(a.dtype) : 1, p.fin)) return fail(GDN_E_INVALID, "problem too large");
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = timed("conv_fwd", s, [&] { return gdn::launch_conv_fwd(a.dtype, a.W, vec, p, s); });
   return e == hipSuccess ? GDN_OK : hip_fail(e, "convolution launch");
@@ -383,6 +393,8 @@ gdn_status gdn_conv_bwd(const gdn_conv_bwd_args* args, void* stream) {
   p.run = conv_bwd_run(a);
   p.nruns = runs_of(a, p.run);
   const bool vec = conv_vec(a) && aligned(p.dy, 16) && aligned(p.dx, 16) && aligned(p.dfin, 16) && aligned(p.dinit, 16);
+  if (!conv_launchable(a, p.run, vec ? 4 : 1, p.dinit) || !launchable(16. * (a.W + 1) * a.D))
+    return fail(GDN_E_INVALID, "problem too large");
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = timed("conv_bwd", s, [&] { return gdn::launch_conv_bwd(a.dtype, a.W, vec, p, s); });
   if (e != hipSuccess) return hip_fail(e, "convolution gradient launch");
@@ -609,6 +621,7 @@ gdn_status gdn_norm_bwd(const gdn_norm_bwd_args* args, void* stream) {
   if (gdn_status st = check_norm(a); st != GDN_OK) return st;
   if (a.R > 0 && (!args->dy || !args->dx || (a.z && !args->dz))) return fail(GDN_E_INVALID, "null gradient pointer");
   if (!args->dw || (a.bias && !args->dbias)) return fail(GDN_E_INVALID, "null gradient pointer");
+  if (!launchable((a.bias ? 32. : 16.) * a.D)) return fail(GDN_E_INVALID, "problem too large");
   const size_t es = esize(a.dtype);
   if (!aligned(args->dy, es) || !aligned(args->dx, es) || !aligned(args->dz, es) || !aligned(args->dw, es) ||
       !aligned(args->dbias, es))

@@ -176,6 +176,11 @@ def _rows(name, t, shape, inner, dtype, dev):
     return width if stride is None else stride
 
 
+def _past_32_bits():
+    """The library's sizes are 32 bits; a larger one would be cut to its low half."""
+    raise GDNError("problem too large: a size of 2^31 or more")
+
+
 def _seqs(cu, cu_host, B, T, dev, need_host):
     """(device pointer, host tensor or None, number of sequences)."""
     if cu is None:
@@ -299,6 +304,8 @@ def _conv_args(x, weight, bias, silu, initial_state, cu_seqlens, cu_seqlens_host
         raise GDNError("weight must be [D, W]")
     B, T, D = x.shape
     W, dt, dev = weight.shape[1], x.dtype, x.device
+    if (B | T | D | W) >> 31:
+        _past_32_bits()
     a = ConvArgs()
     a.dtype = _dtype_code(x)
     a.x_stride = _rows("x", x, (B, T, D), 1, dt, dev)
@@ -362,6 +369,8 @@ def gdn_conv_step(x, state, weight, bias=None, silu: bool = True, state_idx=None
     _no_derivative("gdn_conv_step", x, state, weight, bias)
     N, D = x.shape
     W, dt, dev = weight.shape[1], x.dtype, x.device
+    if (N | D | W | state.shape[0]) >> 31:
+        _past_32_bits()
     a = ConvStepArgs()
     a.dtype = _dtype_code(x)
     a.x_stride = _rows("x", x, (N, D), 1, dt, dev)
@@ -425,6 +434,8 @@ def _scan_args(x, dt, A, B, C, D, dt_bias, dt_softplus, h0, cu_seqlens, cu_seqle
         raise GDNError("x must be [B, T, H, Dv] and B, C [B, T, G, Dk]")
     nb, T, H, Dv = x.shape
     G, Dk = B.shape[2:]
+    if (nb | T | H | Dv | G | Dk) >> 31:
+        _past_32_bits()
     dev, e = x.device, x.dtype
     a = ScanArgs()
     a.dtype = _dtype_code(x)
@@ -509,6 +520,8 @@ def gdn_scan_step(x, dt, A, B, C, state, D=None, dt_bias=None, dt_softplus: bool
     _no_derivative("gdn_scan_step", x, dt, A, B, C, state, D, dt_bias)
     N, H, Dv = x.shape
     G, Dk = B.shape[1:]
+    if (N | H | Dv | G | Dk | state.shape[0]) >> 31:
+        _past_32_bits()
     dev, e = x.device, x.dtype
     a = ScanStepArgs()
     a.dtype = _dtype_code(x)
@@ -594,6 +607,8 @@ def _norm_args(x, weight, z, bias, eps, center, gate_first):
     if x.dim() < 2:
         raise GDNError("x must be [..., G, D]")
     G, D = x.shape[-2:]
+    if (G | D) >> 31:
+        _past_32_bits()
     dt, dev = x.dtype, x.device
     a = NormArgs()
     a.dtype = _dtype_code(x)

@@ -40,6 +40,37 @@ def test_round_once_field(L):
         assert L.gdn_scan_fwd_workspace_size(ctypes.byref(a)) == 0
 
 
+def test_sizes_past_32_bits_are_refused():
+    """A size of 2^32 + 5 is not taken for 5."""
+    m = lambda *s, dt=torch.bfloat16: torch.empty(*s, dtype=dt, device="meta")
+    n = 2 ** 32 + 5
+    for f in (lambda: layers.short_conv(m(1, n, 1), m(1, 4)), lambda: layers.gdn_conv_fwd(m(1, 8, 1), m(1, n)),
+              lambda: layers.gdn_conv_bwd(m(1, n, 1), m(1, 4), m(1, n, 1)),
+              lambda: layers.gdn_conv_step(m(1, n), m(1, 3, n), m(n, 4)),
+              lambda: layers.gdn_conv_step(m(5, 1), m(n, 3, 1), m(1, 4)),
+              lambda: layers.selective_scan(m(1, n, 1, 64), m(1, n, 1), m(1, dt=torch.float32), m(1, n, 1, 64), m(1, n, 1, 64)),
+              lambda: layers.gated_group_norm(m(3, 2, n), m(n)), lambda: layers.gated_group_norm(m(3, n, 1), m(1))):
+        with pytest.raises(GDNError, match="too large"):
+            f()
+
+
+def test_launches_of_2_32_threads_are_refused(L):
+    """Before anything is enqueued: many sequences' states, many channels' weight gradients."""
+    conv = dict(dtype=B.GDN_BF16, B=1, T=1 << 21, D=1001, W=4, x=FAKE, x_stride=1001, w=FAKE, cu_seqlens=FAKE,
+                num_seqs=1 << 21, silu=1)
+    f = fill(layers.ConvFwdArgs(), a=fill(layers.ConvArgs(), **conv), y=FAKE, final_state=FAKE)
+    assert L.gdn_conv_fwd(ctypes.byref(f), None) == 1 and b"too large" in L.gdn_last_error()
+    grad = dict(dy=FAKE, dx=FAKE, dw=FAKE, workspace=FAKE, workspace_bytes=1 << 60)
+    b = fill(layers.ConvBwdArgs(), a=fill(layers.ConvArgs(), **conv), dinit=FAKE, **grad)
+    assert L.gdn_conv_bwd(ctypes.byref(b), None) == 1 and b"too large" in L.gdn_last_error()
+    wide = dict(conv, T=2, D=1 << 27, x_stride=1 << 27, cu_seqlens=None, num_seqs=1)
+    b = fill(layers.ConvBwdArgs(), a=fill(layers.ConvArgs(), **wide), **grad)
+    assert L.gdn_conv_bwd(ctypes.byref(b), None) == 1 and b"too large" in L.gdn_last_error()
+    n = fill(layers.NormArgs(), dtype=B.GDN_BF16, R=2, G=1, D=1 << 28, x=FAKE, x_stride=1 << 28, w=FAKE, eps=1e-5)
+    b = fill(layers.NormBwdArgs(), a=n, dy=FAKE, dx=FAKE, dw=FAKE, workspace=FAKE, workspace_bytes=1 << 60)
+    assert L.gdn_norm_bwd(ctypes.byref(b), None) == 1 and b"too large" in L.gdn_last_error()
+
+
 # ------------------------------------------------------------------ derivatives
 @pytest.fixture
 def stub(monkeypatch):
