@@ -163,7 +163,7 @@ __global__ __launch_bounds__(CONV_NT) void conv_fwd_kernel(ConvParams p, int64_t
         float u = tap.b[e];
 #pragma unroll
         for (int k = 0; k < W; ++k) u += tap.w[k][e] * win[k][e];
-        y[e] = p.silu ? silu_gate(u) : u;
+        y[e] = p.silu ? silu_gate<E>(u) : u;
       }
       store_vec<E, V>(yp, y);
       yp += p.D;
@@ -259,7 +259,7 @@ __global__ __launch_bounds__(CONV_NT) void conv_bwd_kernel(ConvParams p, int64_t
           float u = tap.b[e];
 #pragma unroll
           for (int k = 0; k < W; ++k) u += tap.w[k][e] * win[k][e];
-          const float du = p.silu ? g[e] * dsilu_gate(u, fast_sigmoid(u)) : g[e];
+          const float du = p.silu ? g[e] * dsilu_gate(u, fast_sigmoid<E>(u)) : g[e];
 #pragma unroll
           for (int k = 0; k < W; ++k) acc[k][e] += tap.w[k][e] * du;
           if (mine) {
@@ -355,7 +355,7 @@ __global__ __launch_bounds__(64) void conv_step_kernel(ConvStepParams p) {
   }
   if (p.silu) {
 #pragma unroll
-    for (int e = 0; e < V; ++e) y[e] = silu_gate(y[e]);
+    for (int e = 0; e < V; ++e) y[e] = silu_gate<E>(y[e]);
   }
   store_vec<E, V>(static_cast<E*>(p.y) + (int64_t)n * p.D + c0, y);
 }

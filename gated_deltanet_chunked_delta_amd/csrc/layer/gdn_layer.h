@@ -71,14 +71,28 @@ __device__ __forceinline__ void stream_vec(E* p, const float (&f)[V]) {
 // Elements of one 16-byte access.
 template <class E> constexpr int kVec = 16 / (int)sizeof(E);
 
-// sigmoid(x) and the SiLU gate with the hardware's exponential and reciprocal
-// (each within about one unit in the last place of fp32): the exact division of
-// sigmoid_f takes ten instructions, a third of what these memory-bound kernels
-// spend on an element.  exp overflow gives 1 / inf = 0.
+// sigmoid(x) and the SiLU gate with the hardware's exponential and reciprocal,
+// each within a unit in the last place: the exact division of sigmoid_f takes ten
+// instructions, a third of what these memory-bound kernels spend on an element.
+// exp overflow gives 1 / inf = 0.  The exponent -x log2(e) rounded to fp32 alone is
+// off by |x| 2^-24, which is far below a bf16 result's step; for fp32 tensors
+// what that product misses (log2(e)'s own tail too) enters as a first-order
+// factor: silu within 3.7 fp32 roundings (2^-24) of its value for x in -80 .. 80, 62
+// without it.
+template <class E>
 __device__ __forceinline__ float fast_sigmoid(float x) {
-  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * x));
+  const float h = -1.44269504f * x;
+  float e = __builtin_amdgcn_exp2f(h);
+  if constexpr (sizeof(E) == 4) {
+    // (finite for every x; past +-128 the exponential is 0 or inf)
+    const float c = __builtin_amdgcn_fmed3f(x, -128.f, 128.f);
+    const float miss = fmaf(-1.44269504f, c, 1.44269504f * c) - 1.92596299e-8f * c;
+    e *= fmaf(miss, 0.69314718f, 1.f);
+  }
+  return __builtin_amdgcn_rcpf(1.f + e);
 }
-__device__ __forceinline__ float silu_gate(float x) { return x * fast_sigmoid(x); }
+template <class E>
+__device__ __forceinline__ float silu_gate(float x) { return x * fast_sigmoid<E>(x); }
 // its derivative, from x and sigmoid(x)
 __device__ __forceinline__ float dsilu_gate(float x, float s) { return s + x * (s - s * s); }
 

@@ -103,7 +103,7 @@ __global__ __launch_bounds__(NORM_NT) void norm_fwd_kernel(NormParams p) {
       if (GATE) {
         IO::get(z[k].v[i], act[i]);
 #pragma unroll
-        for (int e = 0; e < V; ++e) act[i][e] = silu_gate(act[i][e]);
+        for (int e = 0; e < V; ++e) act[i][e] = silu_gate<E>(act[i][e]);
       }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -195,7 +195,7 @@ __global__ __launch_bounds__(NORM_NT) void norm_bwd_kernel(NormParams p) {
         float t[V];
         IO::get(z.v[i], t);
 #pragma unroll
-        for (int e = 0; e < V; ++e) n[i][e] *= silu_gate(t[e]);
+        for (int e = 0; e < V; ++e) n[i][e] *= silu_gate<E>(t[e]);
       }
 #pragma unroll
       for (int e = 0; e < V; ++e) s += n[i][e];
@@ -225,7 +225,7 @@ __global__ __launch_bounds__(NORM_NT) void norm_bwd_kernel(NormParams p) {
         float t[V];
         IO::get(z.v[i], t);
 #pragma unroll
-        for (int e = 0; e < V; ++e) d[e] *= silu_gate(t[e]);
+        for (int e = 0; e < V; ++e) d[e] *= silu_gate<E>(t[e]);
       }
 #pragma unroll
       for (int e = 0; e < V; ++e) {
@@ -260,7 +260,7 @@ __global__ __launch_bounds__(NORM_NT) void norm_bwd_kernel(NormParams p) {
         else if (BIAS) IO::get(IO::load(static_cast<const E*>(p.bias) + (int64_t)wg * p.D + c), b);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float sg = fast_sigmoid(t[e]), act = t[e] * sg;
+          const float sg = fast_sigmoid<E>(t[e]), act = t[e] * sg;
           const float dv = ((after ? d[e] * act : d[e]) * w[e] - n[i][e] * c1 - c2) * rstd;
           dx[e] = before ? dv * act : dv;
           dz[e] = (before ? dv * xv[e] : d[e] * (n[i][e] * w[e] + b[e])) * dsilu_gate(t[e], sg);
@@ -313,7 +313,7 @@ struct LongRow {
   float mean, rstd;
   __device__ __forceinline__ float gated(int c) const {
     const float v = to_f(x[c]);
-    return before ? v * silu_gate(to_f(z[c])) : v;
+    return before ? v * silu_gate<E>(to_f(z[c])) : v;
   }
   __device__ __forceinline__ void stats(const NormParams& p, float* red) {
     const float inv = 1.f / p.D;
@@ -356,7 +356,7 @@ __global__ __launch_bounds__(NORM_NT) void norm_fwd_long_kernel(NormParams p) {
   for (int c = threadIdx.x; c < p.D; c += NORM_NT) {
     float o = (a.gated(c) - a.mean) * a.rstd * to_f(a.w[c]);
     if (a.b) o += to_f(a.b[c]);
-    if (a.after) o *= silu_gate(to_f(a.z[c]));
+    if (a.after) o *= silu_gate<E>(to_f(a.z[c]));
     y[c] = to_e<E>(o);
   }
 }
@@ -378,7 +378,7 @@ __global__ __launch_bounds__(NORM_NT) void norm_bwd_long_kernel(NormParams p) {
     a.stats(p, red);
     float c1 = 0.f, c2 = 0.f;
     for (int c = threadIdx.x; c < p.D; c += NORM_NT) {
-      const float gd = to_f(a.dy[c]) * (a.after ? silu_gate(to_f(a.z[c])) : 1.f);
+      const float gd = to_f(a.dy[c]) * (a.after ? silu_gate<E>(to_f(a.z[c])) : 1.f);
       const float n = (a.gated(c) - a.mean) * a.rstd, dn = gd * to_f(a.w[c]);
       c1 += dn * n;
       c2 += dn;
@@ -390,7 +390,7 @@ __global__ __launch_bounds__(NORM_NT) void norm_bwd_long_kernel(NormParams p) {
     E* dx = static_cast<E*>(p.dx) + (tok * p.G + g) * p.D;
     E* dz = p.z ? static_cast<E*>(p.dz) + (tok * p.G + g) * p.D : nullptr;
     for (int c = threadIdx.x; c < p.D; c += NORM_NT) {
-      const float z = p.z ? to_f(a.z[c]) : 0.f, sg = fast_sigmoid(z), act = z * sg, dy = to_f(a.dy[c]);
+      const float z = p.z ? to_f(a.z[c]) : 0.f, sg = fast_sigmoid<E>(z), act = z * sg, dy = to_f(a.dy[c]);
       const float n = (a.gated(c) - a.mean) * a.rstd;
       const float dn = (a.after ? dy * act : dy) * to_f(a.w[c]);
       const float dv = (dn - n * c1 - c2) * a.rstd;

@@ -113,3 +113,41 @@ def test_scan_outputs_are_rounded_once(dev, lens, H, G, Dk, Dv, seg):
         e = rms(got.double() - want.to(BF).double()) / rms(want)
         print(f"    {k} {e:.2e}", flush=True)
         assert e <= 2.0 ** -11, k
+
+
+def test_gates_of_fp32_tensors(dev):
+    """silu(x) of fp32 tensors over the exponential's range, relative to every value: the
+    exponential and the reciprocal off by 2^-23 each, and three roundings: 7 fp32 roundings,
+    and one more for the norm's product.  Its derivative s + x (s - s s) likewise, relative to
+    the size of its terms (s one rounding finer than 1 where x is large)."""
+    from gated_deltanet_chunked_delta_amd import gated_group_norm, layers, short_conv
+    x = torch.linspace(-80, 80, 64 * 1024, device=dev).view(1, -1, 64)
+    x = torch.cat([x, x / 16], 1).contiguous()
+    w = torch.zeros(64, 2, device=dev)
+    w[:, 1] = 1                                                  # u = x
+    want = x.double() * torch.sigmoid(x.double())
+    live = x.abs() > 1e-3
+    def worst(name, got, ref, size):
+        e = ((got.double() - ref).abs() / size)[live].max().item() * 2 ** 24
+        print(f"    {name} {e:.1f} roundings", flush=True)
+        return e
+    n = torch.ones_like(x)
+    w1 = torch.ones(64, device=dev)
+    conv = short_conv(x, w)
+    step = layers.gdn_conv_step(x[0].contiguous(), torch.zeros(x.shape[1], 1, 64, device=dev), w)
+    norm = gated_group_norm(n, w1, x, eps=1e-30)                 # n / sqrt(1) = 1
+    long = gated_group_norm(torch.ones(23, 1, 5501, device=dev), torch.ones(5501, device=dev),
+                            x.flatten()[:23 * 5501].view(23, 1, 5501), eps=1e-30)
+    assert worst("convolution", conv, want, want.abs()) <= 8
+    assert torch.equal(step[None], conv)
+    assert worst("norm", norm, want, want.abs()) <= 8
+    lw = want.flatten()[:23 * 5501].view(23, 1, 5501)
+    assert ((long.double() - lw).abs() <= 8 * 2.0 ** -24 * lw.abs() + 1e-30).all()
+    leaf = x.clone().requires_grad_(True)
+    (dx,) = torch.autograd.grad(short_conv(leaf, w), leaf, torch.ones_like(x))
+    s = torch.sigmoid(x.double())
+    size = s + x.double().abs() * s * torch.clamp(1 - s, min=2.0 ** -24)
+    assert worst("derivative", dx, s + x.double() * s * (1 - s), size) <= 24
+    inf = float("inf")
+    e = short_conv(torch.tensor([inf, 200.0, -200.0, float("nan")], device=dev).view(1, 1, 4), w[:4])
+    assert e[0, 0, 0] == inf and e[0, 0, 1] == 200 and e[0, 0, 2] == 0 and e[0, 0, 3].isnan()
