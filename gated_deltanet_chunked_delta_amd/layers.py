@@ -235,18 +235,18 @@ _raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None) or (
 # and drop what fills them: such a call is refused.  An autograd function is one
 # operation to torch.jit.trace, and its replay calls the library; what it runs inside
 # is not traced.
-_tracing_state = torch._C._get_tracing_state
+_is_tracing, _dispatch_modes = torch._C._is_tracing, torch._C._len_torch_dispatch_stack
 _MODES = [torch._C._TorchDispatchModeKey.PROXY, torch._C._TorchDispatchModeKey.FAKE]
 
 
 def _refuse_traced():
-    if _tracing_state() is not None or any(torch._C._get_dispatch_mode(m) is not None for m in _MODES):
+    if _is_tracing() or any(torch._C._get_dispatch_mode(m) is not None for m in _MODES):
         raise GDNError("this call cannot be traced: the trace would not hold the library's kernels")
 
 
 @contextlib.contextmanager
 def _untraced():
-    state = _tracing_state()
+    state = torch._C._get_tracing_state()
     torch._C._set_tracing_state(None)
     try:
         yield
@@ -256,24 +256,24 @@ def _untraced():
 
 def _as_one_op():
     """What the forward pass of an autograd function runs in."""
-    return _NO_SWITCH if _tracing_state() is None else _untraced()
+    return _untraced() if _is_tracing() else _NO_SWITCH
 
 
 def _call(fn, args, dev):
-    if _tracing_state() is not None or torch._C._len_torch_dispatch_stack():
+    if _dispatch_modes() or _is_tracing():
         _refuse_traced()
-    if torch.cuda.current_device() == dev.index:
-        status = fn(ctypes.byref(args), _raw_stream(dev.index))
+    index = dev.index
+    if torch.cuda.current_device() == index:
+        status = fn(ctypes.byref(args), _raw_stream(index))
     else:
         with torch.cuda.device(dev):
-            status = fn(ctypes.byref(args), _raw_stream(dev.index))
+            status = fn(ctypes.byref(args), _raw_stream(index))
     if status:
         _check(status)
 
 
 def _has_tangent(tensors):
-    return forward_ad._current_level >= 0 and any(
-        t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
+    return any(t is not None and forward_ad.unpack_dual(t).tangent is not None for t in tensors)
 
 
 def _wants_grad(*tensors):
@@ -283,16 +283,16 @@ def _wants_grad(*tensors):
         for t in tensors:
             if t is not None and t.requires_grad:
                 return True
-    return _tracing_state() is not None or _has_tangent(tensors)
+    return _is_tracing() or forward_ad._current_level >= 0 and _has_tangent(tensors)
 
 
-def _no_derivative(name, *tensors):
+def _no_derivative(name, tensors):
     """Refuses a step whose derivative the caller expects: it advances its state in place and has none."""
     if torch.is_grad_enabled():
         for t in tensors:
             if t is not None and t.requires_grad:
                 raise GDNError(f"{name} has no gradient: call it under torch.no_grad()")
-    if _has_tangent(tensors):
+    if forward_ad._current_level >= 0 and _has_tangent(tensors):
         raise GDNError(f"{name} has no derivative")
 
 
@@ -366,25 +366,24 @@ def gdn_conv_step(x, state, weight, bias=None, silu: bool = True, state_idx=None
     left as it was).  Two sequences of one call must not share a slot.  Returns y [N, D]."""
     if x.dim() != 2 or weight.dim() != 2:
         raise GDNError("x must be [N, D] and weight [D, W]")
-    _no_derivative("gdn_conv_step", x, state, weight, bias)
+    _no_derivative("gdn_conv_step", (x, state, weight, bias))
     N, D = x.shape
     W, dt, dev = weight.shape[1], x.dtype, x.device
-    if (N | D | W | state.shape[0]) >> 31:
+    slots = state.shape[0]
+    if (N | D | W | slots) >> 31:
         _past_32_bits()
-    a = ConvStepArgs()
-    a.dtype = _dtype_code(x)
-    a.x_stride = _rows("x", x, (N, D), 1, dt, dev)
+    stride = _rows("x", x, (N, D), 1, dt, dev)
     _t("weight", weight, (D, W), dt, dev)
     _t("bias", bias, (D,), dt, dev, optional=True)
-    _t("state", state, (state.shape[0], W - 1, D), dt, dev)
+    _t("state", state, (slots, W - 1, D), dt, dev)
     _t("state_idx", state_idx, (N,), torch.int32, dev, optional=True)
     _on_gpu("x", x)
     if y is None:
         y = weight.new_empty((N, D))
     else:
         _t("y", y, (N, D), dt, dev)
-    a.N, a.D, a.W, a.num_slots, a.silu = N, D, W, state.shape[0], int(bool(silu))
-    a.x, a.state, a.state_idx, a.w, a.bias, a.y = map(_ptr, (x, state, state_idx, weight, bias, y))
+    a = ConvStepArgs(_dtype_code(x), N, D, W, x.data_ptr(), stride, state.data_ptr(), _ptr(state_idx), slots,
+                     weight.data_ptr(), _ptr(bias), bool(silu), y.data_ptr())
     _call(lib().gdn_conv_step, a, dev)
     return y
 
@@ -517,35 +516,33 @@ def gdn_scan_step(x, dt, A, B, C, state, D=None, dt_bias=None, dt_softplus: bool
     [S, H, Dk, Dv] fp32 is advanced in place (slots as in gdn_decode_step).  Returns y."""
     if x.dim() != 3 or B.dim() != 3:
         raise GDNError("x must be [N, H, Dv] and B, C [N, G, Dk]")
-    _no_derivative("gdn_scan_step", x, dt, A, B, C, state, D, dt_bias)
+    _no_derivative("gdn_scan_step", (x, dt, A, B, C, state, D, dt_bias))
     N, H, Dv = x.shape
     G, Dk = B.shape[1:]
-    if (N | H | Dv | G | Dk | state.shape[0]) >> 31:
+    slots = state.shape[0]
+    if (N | H | Dv | G | Dk | slots) >> 31:
         _past_32_bits()
     dev, e = x.device, x.dtype
-    a = ScanStepArgs()
-    a.dtype = _dtype_code(x)
-    a.x_stride = _rows("x", x, (N, H, Dv), 2, e, dev)
-    a.b_stride = _rows("B", B, (N, G, Dk), 2, e, dev)
-    a.c_stride = _rows("C", C, (N, G, Dk), 2, e, dev)
+    code = _dtype_code(x)
+    xs = _rows("x", x, (N, H, Dv), 2, e, dev)
+    bs = _rows("B", B, (N, G, Dk), 2, e, dev)
+    cs = _rows("C", C, (N, G, Dk), 2, e, dev)
     if dt.dtype not in (e, torch.float32):
         raise GDNError(f"dt must be {e} or float32, got {dt.dtype}")
-    a.dt_dtype = _dtype_code(dt)
-    a.dt_stride = _rows("dt", dt, (N, H), 1, dt.dtype, dev)
+    ds = _rows("dt", dt, (N, H), 1, dt.dtype, dev)
     _t("A", A, (H,), torch.float32, dev)
     _t("D", D, (H,), torch.float32, dev, optional=True)
     _t("dt_bias", dt_bias, (H,), torch.float32, dev, optional=True)
-    _t("state", state, (state.shape[0], H, Dk, Dv), torch.float32, dev)
+    _t("state", state, (slots, H, Dk, Dv), torch.float32, dev)
     _t("state_idx", state_idx, (N,), torch.int32, dev, optional=True)
     _on_gpu("x", x)
     if y is None:
         y = x.new_empty((N, H, Dv))
     else:
         _t("y", y, (N, H, Dv), e, dev)
-    a.N, a.H, a.G, a.Dk, a.Dv = N, H, G, Dk, Dv
-    a.dt_softplus, a.num_slots = int(bool(dt_softplus)), state.shape[0]
-    a.x, a.dt, a.b, a.c, a.A, a.D, a.dt_bias, a.state, a.state_idx, a.y = map(
-        _ptr, (x, dt, B, C, A, D, dt_bias, state, state_idx, y))
+    a = ScanStepArgs(code, _dtype_code(dt), N, H, G, Dk, Dv, x.data_ptr(), dt.data_ptr(), B.data_ptr(), C.data_ptr(),
+                     xs, ds, bs, cs, A.data_ptr(), _ptr(D), _ptr(dt_bias), bool(dt_softplus), state.data_ptr(),
+                     _ptr(state_idx), slots, y.data_ptr())
     _call(lib().gdn_scan_step, a, dev)
     return y
 
@@ -610,23 +607,21 @@ def _norm_args(x, weight, z, bias, eps, center, gate_first):
     if (G | D) >> 31:
         _past_32_bits()
     dt, dev = x.dtype, x.device
-    a = NormArgs()
-    a.dtype = _dtype_code(x)
-    a.x_stride = _rows("x", x, x.shape, 2, dt, dev)
-    a.z_stride = 0 if z is None else _rows("z", z, x.shape, 2, dt, dev)
-    a.shared = int(weight.dim() == 1)
-    shape = (D,) if a.shared else (G, D)
+    code = _dtype_code(x)
+    x_stride = _rows("x", x, x.shape, 2, dt, dev)
+    z_stride = 0 if z is None else _rows("z", z, x.shape, 2, dt, dev)
+    shared = weight.dim() == 1
+    shape = (D,) if shared else (G, D)
     _t("weight", weight, shape, dt, dev)
     _t("bias", bias, shape, dt, dev, optional=True)
-    a.R = 1
+    R = 1
     for n in x.shape[:-2]:
-        a.R *= n
-    a.G, a.D, a.center, a.gate_first, a.eps = G, D, int(bool(center)), int(bool(gate_first)), float(eps)
+        R *= n
     if gate_first and z is None:
         raise GDNError("gate_first needs z")
-    a.x, a.z, a.w, a.bias = map(_ptr, (x, z, weight, bias))
     _on_gpu("x", x)
-    return a
+    return NormArgs(code, R, G, D, x.data_ptr(), x_stride, _ptr(z), z_stride, weight.data_ptr(), _ptr(bias), shared,
+                    bool(center), bool(gate_first), eps)
 
 
 def gdn_norm_fwd(x, weight, z=None, bias=None, eps: float = 1e-5, center: bool = False, gate_first: bool = False):
