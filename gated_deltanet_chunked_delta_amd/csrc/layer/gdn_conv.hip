@@ -259,7 +259,11 @@ __global__ __launch_bounds__(CONV_NT) void conv_bwd_kernel(ConvParams p, int64_t
           float u = tap.b[e];
 #pragma unroll
           for (int k = 0; k < W; ++k) u += tap.w[k][e] * win[k][e];
-          const float du = p.silu ? g[e] * dsilu_gate(u, fast_sigmoid<E>(u)) : g[e];
+          // computed either way and chosen (fp32's longer gate would become a branch, which
+          // waits for every load: 8,192 x 1,001 in 44 us instead of 36)
+          float gated = g[e] * dsilu_gate(u, fast_sigmoid<E>(u));
+          if constexpr (sizeof(E) == 4) pin(gated);
+          const float du = p.silu ? gated : g[e];
 #pragma unroll
           for (int k = 0; k < W; ++k) acc[k][e] += tap.w[k][e] * du;
           if (mine) {

@@ -75,21 +75,20 @@ template <class E> constexpr int kVec = 16 / (int)sizeof(E);
 // each within a unit in the last place: the exact division of sigmoid_f takes ten
 // instructions, a third of what these memory-bound kernels spend on an element.
 // exp overflow gives 1 / inf = 0.  The exponent -x log2(e) rounded to fp32 alone is
-// off by |x| 2^-24, which is far below a bf16 result's step; for fp32 tensors
-// what that product misses (log2(e)'s own tail too) enters as a first-order
-// factor: silu within 3.7 fp32 roundings (2^-24) of its value for x in -80 .. 80, 62
-// without it.
+// off by |x| 2^-24, which is far below a bf16 result's step.  For fp32 tensors
+// what 2^h misses exp(-x) by enters as a first-order factor, 1 + (-x - h ln 2) with ln 2
+// in two parts: silu within 4 fp32 roundings (2^-24) of its value for x in -80 .. 80,
+// 62 without it.  (x held to +-88 there, where the gate is 0 or 1; a NaN comes back in
+// through the products with x itself.)
 template <class E>
 __device__ __forceinline__ float fast_sigmoid(float x) {
-  const float h = -1.44269504f * x;
-  float e = __builtin_amdgcn_exp2f(h);
   if constexpr (sizeof(E) == 4) {
-    // (finite for every x; past +-128 the exponential is 0 or inf)
-    const float c = __builtin_amdgcn_fmed3f(x, -128.f, 128.f);
-    const float miss = fmaf(-1.44269504f, c, 1.44269504f * c) - 1.92596299e-8f * c;
-    e *= fmaf(miss, 0.69314718f, 1.f);
+    const float c = __builtin_amdgcn_fmed3f(x, -88.f, 88.f), h = -1.44269504f * c;
+    const float e = __builtin_amdgcn_exp2f(h);
+    const float miss = fmaf(h, 1.90465430e-9f, fmaf(h, -0.69314718f, -c));
+    return __builtin_amdgcn_rcpf(1.f + fmaf(e, miss, e));
   }
-  return __builtin_amdgcn_rcpf(1.f + e);
+  return __builtin_amdgcn_rcpf(1.f + __builtin_amdgcn_exp2f(-1.44269504f * x));
 }
 template <class E>
 __device__ __forceinline__ float silu_gate(float x) { return x * fast_sigmoid<E>(x); }
