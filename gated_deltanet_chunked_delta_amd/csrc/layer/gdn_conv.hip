@@ -303,15 +303,16 @@ __global__ __launch_bounds__(CONV_NT) void conv_bwd_kernel(ConvParams p, int64_t
     for (int e = 0; e < V; ++e) part[(int64_t)k * p.D + e] = k < W ? dw[k < W ? k : 0][e] : db[e];
 }
 
-// dw and dbias: column sums of the runs' parts, 64 columns a workgroup, sixteen
-// threads a column, each over every sixteenth run.
+// dw and dbias: column sums of the runs' parts in 64 bits (an fp32 sum has at most a
+// run's terms), 32 columns a workgroup, sixteen threads a column, each over every
+// sixteenth run.
 constexpr int DW_COLS = 32, DW_ROWS = 16;
 template <class E, int W>
 __global__ __launch_bounds__(DW_COLS * DW_ROWS) void conv_dw_kernel(ConvParams p) {
-  __shared__ float red[DW_ROWS][DW_COLS + 1];
+  __shared__ double red[DW_ROWS][DW_COLS + 1];
   const int cl = threadIdx.x % DW_COLS, rl = threadIdx.x / DW_COLS;
   const int64_t cols = (int64_t)(W + 1) * p.D, col = blockIdx.x * (int64_t)DW_COLS + cl;
-  float s = 0.f;
+  double s = 0.;
   if (col < cols) {
 #pragma unroll 8
     for (int64_t r = rl; r < p.nruns; r += DW_ROWS) s += p.part[r * cols + col];
@@ -319,12 +320,12 @@ __global__ __launch_bounds__(DW_COLS * DW_ROWS) void conv_dw_kernel(ConvParams p
   red[rl][cl] = s;
   __syncthreads();
   if (rl == 0 && col < cols) {
-    s = 0.f;
+    s = 0.;
 #pragma unroll
     for (int r = 0; r < DW_ROWS; ++r) s += red[r][cl];
     const int k = (int)(col / p.D), d = (int)(col % p.D);
-    if (k < W) static_cast<E*>(p.dw)[(int64_t)d * W + k] = to_e<E>(s);
-    else if (p.dbias) static_cast<E*>(p.dbias)[d] = to_e<E>(s);
+    if (k < W) static_cast<E*>(p.dw)[(int64_t)d * W + k] = to_e<E>((float)s);
+    else if (p.dbias) static_cast<E*>(p.dbias)[d] = to_e<E>((float)s);
   }
 }
 

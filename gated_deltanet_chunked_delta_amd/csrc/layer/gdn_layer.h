@@ -154,8 +154,9 @@ struct NormParams {
   void* dw;
   void* dbias;               // nullable
   float* part;               // [weight groups][blocks][1 or 2][D]
-  int blocks;                // workgroups per weight group (backward)
+  int blocks;                // workgroups per weight group (backward); the launcher may take more
 };
+constexpr int NORM_ROWS = 64;  // rows whose weight gradients one fp32 sum takes, at most
 hipError_t launch_norm_fwd(int dtype, bool vec, const NormParams& p, hipStream_t st);
 hipError_t launch_norm_bwd(int dtype, bool vec, const NormParams& p, hipStream_t st);
 

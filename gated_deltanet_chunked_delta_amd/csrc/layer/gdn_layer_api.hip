@@ -341,8 +341,12 @@ int norm_blocks(const gdn_norm_args& a) {
   const int64_t per_cu = a.D * (int64_t)esize(a.dtype) <= 64 * 16 ? 4 : 2;
   return (int)std::max<int64_t>(1, std::min<int64_t>(rows, per_cu * cu_count() / groups));
 }
+// Parts for the most workgroups: those that take one row at a time (how many they
+// take depends on the pointers' alignment).
 size_t norm_part_bytes(const gdn_norm_args& a) {
-  return sizeof(float) * (a.shared ? 1 : a.G) * (size_t)norm_blocks(a) * (a.bias ? 2 : 1) * a.D;
+  const int64_t rows = a.shared ? a.R * a.G : a.R;
+  const int64_t blocks = std::max<int64_t>(norm_blocks(a), (rows + gdn::NORM_ROWS - 1) / gdn::NORM_ROWS);
+  return sizeof(float) * (a.shared ? 1 : a.G) * (size_t)blocks * (a.bias ? 2 : 1) * a.D;
 }
 
 }  // namespace

@@ -151,7 +151,7 @@ __global__ __launch_bounds__(NORM_NT) void norm_fwd_kernel(NormParams p) {
 //   dz = silu'(z) (dv x  with the gate before,  dy o  after it)
 // p.blocks workgroups per weight group walk that group's rows, each thread
 // always on the same columns, and keep dw and dbias in registers; their parts
-// are joined by norm_dw_kernel in a fixed order.  Rows of one vector a
+// are joined by norm_dw_kernel in 64 bits and a fixed order.  Rows of one vector a
 // thread are requested one ahead; a row is held as loaded (16 bytes a vector) and
 // converted where it is used, which leaves registers for four vectors a thread.
 template <class E, int V, int TPR, int NV, bool BIAS, int GATE>
@@ -403,17 +403,17 @@ __global__ __launch_bounds__(NORM_NT) void norm_bwd_long_kernel(NormParams p) {
   }
 }
 
-// dw and dbias: sums of the workgroups' parts, 32 columns a workgroup, sixteen
-// threads a column.
+// dw and dbias: sums of the workgroups' parts in 64 bits, 32 columns a workgroup,
+// sixteen threads a column.
 constexpr int NDW_ROWS = 16;
 template <class E>
 __global__ __launch_bounds__(32 * NDW_ROWS) void norm_dw_kernel(NormParams p) {
-  __shared__ float red[NDW_ROWS][33];
+  __shared__ double red[NDW_ROWS][33];
   const int kinds = p.dbias ? 2 : 1;
   const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
   const int64_t cols = (int64_t)kinds * p.D, col = blockIdx.x * 32ll + cl;
   const int wg = blockIdx.y;
-  float s = 0.f;
+  double s = 0.;
   if (col < cols) {
     const float* q = p.part + (int64_t)wg * p.blocks * cols + col;
 #pragma unroll 8
@@ -422,11 +422,11 @@ __global__ __launch_bounds__(32 * NDW_ROWS) void norm_dw_kernel(NormParams p) {
   red[rl][cl] = s;
   __syncthreads();
   if (rl == 0 && col < cols) {
-    s = 0.f;
+    s = 0.;
 #pragma unroll
     for (int r = 0; r < NDW_ROWS; ++r) s += red[r][cl];
-    if (col < p.D) static_cast<E*>(p.dw)[(int64_t)wg * p.D + col] = to_e<E>(s);
-    else static_cast<E*>(p.dbias)[(int64_t)wg * p.D + col - p.D] = to_e<E>(s);
+    if (col < p.D) static_cast<E*>(p.dw)[(int64_t)wg * p.D + col] = to_e<E>((float)s);
+    else static_cast<E*>(p.dbias)[(int64_t)wg * p.D + col - p.D] = to_e<E>((float)s);
   }
 }
 
@@ -436,10 +436,18 @@ dim3 grid_2d(int64_t n) {
   return n <= most ? dim3((uint32_t)n) : dim3((uint32_t)most, (uint32_t)((n + most - 1) / most));
 }
 
+// Enough workgroups of rpb rows at a time for NORM_ROWS rows a thread (as far as one
+// launch goes: 2^24 workgroups in all).
+void norm_grad_blocks(NormParams& p, int rpb) {
+  const int64_t rows = p.shared ? p.R * p.G : p.R, most = ((1 << 24) - 1) / (p.shared ? 1 : p.G);
+  p.blocks = max(p.blocks, (int)min((rows + rpb * NORM_ROWS - 1) / (rpb * NORM_ROWS), most));
+}
+
 template <class E, int V, int TPR, int NV, int GATE>
-hipError_t norm_run_gate(const NormParams& p, bool bwd, hipStream_t st) {
+hipError_t norm_run_gate(NormParams& p, bool bwd, hipStream_t st) {
   const int64_t rows = p.R * p.G;
   if (bwd) {
+    norm_grad_blocks(p, NORM_NT / TPR);
     const dim3 grid(p.blocks * (p.shared ? 1 : p.G));
     if (p.dbias) hipLaunchKernelGGL((norm_bwd_kernel<E, V, TPR, NV, true, GATE>), grid, dim3(NORM_NT), 0, st, p);
     else hipLaunchKernelGGL((norm_bwd_kernel<E, V, TPR, NV, false, GATE>), grid, dim3(NORM_NT), 0, st, p);
@@ -454,13 +462,13 @@ hipError_t norm_run_gate(const NormParams& p, bool bwd, hipStream_t st) {
   return hipGetLastError();
 }
 template <class E, int V, int TPR, int NV>
-hipError_t norm_run(const NormParams& p, bool bwd, hipStream_t st) {
+hipError_t norm_run(NormParams& p, bool bwd, hipStream_t st) {
   if (!p.z) return norm_run_gate<E, V, TPR, NV, GATE_NONE>(p, bwd, st);
   return p.gate_first ? norm_run_gate<E, V, TPR, NV, GATE_BEFORE>(p, bwd, st) : norm_run_gate<E, V, TPR, NV, GATE_AFTER>(p, bwd, st);
 }
 
 template <class E, int V>
-hipError_t norm_pick(const NormParams& p, bool bwd, hipStream_t st) {
+hipError_t norm_pick(NormParams& p, bool bwd, hipStream_t st) {
   const int nv = (p.D + V - 1) / V;  // vectors in a row
   if constexpr (V > 1) {
     if (nv <= 8) return norm_run<E, V, 8, 1>(p, bwd, st);
@@ -474,6 +482,7 @@ hipError_t norm_pick(const NormParams& p, bool bwd, hipStream_t st) {
   if constexpr (V > 1)
     if (nv <= 512) return norm_run<E, V, 256, 2>(p, bwd, st);
   if (nv <= 1024) return norm_run<E, V, 256, 4>(p, bwd, st);
+  if (bwd) norm_grad_blocks(p, 1);
   if (bwd)
     hipLaunchKernelGGL((norm_bwd_long_kernel<E>), dim3(p.blocks * (p.shared ? 1 : p.G)), dim3(NORM_NT), 0, st, p);
   else
@@ -482,7 +491,7 @@ hipError_t norm_pick(const NormParams& p, bool bwd, hipStream_t st) {
 }
 
 template <class E>
-hipError_t norm_any(bool vec, const NormParams& p, bool bwd, hipStream_t st) {
+hipError_t norm_any(bool vec, NormParams p, bool bwd, hipStream_t st) {
   hipError_t e = vec ? norm_pick<E, kVec<E>>(p, bwd, st) : norm_pick<E, 1>(p, bwd, st);
   if (e != hipSuccess || !bwd) return e;
   const int kinds = p.dbias ? 2 : 1;

@@ -151,3 +151,39 @@ def test_gates_of_fp32_tensors(dev):
     inf = float("inf")
     e = short_conv(torch.tensor([inf, 200.0, -200.0, float("nan")], device=dev).view(1, 1, 4), w[:4])
     assert e[0, 0, 0] == inf and e[0, 0, 1] == 200 and e[0, 0, 2] == 0 and e[0, 0, 3].isnan()
+
+
+@pytest.mark.parametrize("rows,G,D", [(1 << 20, 1, 8), (300_000, 2, 24), (40_000, 1, 5501), (1 << 25, 1, 3)])
+@pytest.mark.parametrize("shared", [False, True])
+def test_weight_gradients_over_many_rows(dev, rows, G, D, shared):
+    """Sums of many like terms, where an fp32 sum of n terms is off by up to n / 2 roundings: a
+    thread's has at most 64 terms, a workgroup's 32 of those, the rest is summed in 64 bits."""
+    from gated_deltanet_chunked_delta_amd import gated_group_norm
+    x = torch.full((rows, G, D), 1.5, device=dev)
+    x[..., 1::2] = -0.75
+    ws = (D,) if shared else (G, D)
+    w, b = torch.ones(*ws, device=dev, requires_grad=True), torch.zeros(*ws, device=dev, requires_grad=True)
+    dy = torch.full((rows, G, D), 0.1, device=dev)
+    dw, db = torch.autograd.grad(gated_group_norm(x, w, bias=b), [w, b], dy)
+    n = rows * (G if shared else 1)
+    v = x[0, 0].double()
+    want = 0.1 * n * v / torch.sqrt((v * v).mean() + 1e-5)
+    for name, got, ref in (("dw", dw, want), ("db", db, torch.full_like(v, n * 0.1))):
+        e = ((got.double() - ref) / ref).abs().max().item() * 2 ** 24
+        print(f"    {name} {e:.1f} roundings", flush=True)
+        assert e <= 32 + 16 + 8, name         # and a row's statistics, 0.1 and the result
+
+
+def test_convolution_weight_gradients_over_many_tokens(dev):
+    """The same: a thread's sum has at most 128 terms."""
+    from gated_deltanet_chunked_delta_amd import short_conv
+    T, D = 1 << 20, 8
+    x = torch.full((1, T, D), 1.5, device=dev)
+    w, b = torch.zeros(D, 4, device=dev, requires_grad=True), torch.zeros(D, device=dev, requires_grad=True)
+    dy = torch.full_like(x, 0.1)
+    dw, db = torch.autograd.grad(short_conv(x, w, b, silu=False), [w, b], dy)
+    lag = torch.tensor([3.0, 2.0, 1.0, 0.0], device=dev, dtype=torch.float64)
+    for name, got, ref in (("dw", dw, (0.15 * (T - lag)).expand(D, 4)), ("db", db, torch.full_like(db, 0.1 * T).double())):
+        e = ((got.double() - ref) / ref).abs().max().item() * 2 ** 24
+        print(f"    {name} {e:.1f} roundings", flush=True)
+        assert e <= 64 + 4, name
