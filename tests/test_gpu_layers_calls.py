@@ -63,3 +63,85 @@ def test_chunk_rule_gradients_that_start_anywhere(dev):
     z = torch.zeros(3, dtype=BF, device=dev)
     got = torch.autograd.grad(torch.cat([z, f().flatten()]), into, torch.cat([z, dy.flatten()]))
     assert all(torch.equal(a, b) for a, b in zip(got, want))
+
+
+@pytest.mark.parametrize("lens", [None, [70, 0, 129]])
+def test_captured_autograd_training(dev, lens):
+    """The three operators with autograd, forward and backward captured together; every replay,
+    with eager work between, gives what an eager pass of other leaves gives."""
+    from gated_deltanet_chunked_delta_amd import gated_group_norm, selective_scan, short_conv
+    H, Dk, Dv, T = 2, 64, 64, 199
+    kw = {}
+    if lens:
+        cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+        kw = dict(cu_seqlens=cu.to(dev), cu_seqlens_host=cu)
+    g = torch.Generator(device=dev).manual_seed(5)
+    rn = lambda *s: torch.randn(*s, generator=g, device=dev)
+    values = [rn(1, T, H * Dv).to(BF), rn(H * Dv, 4).to(BF), rn(1, T, H).to(BF), -1 - rn(H).abs(), rn(1, T, 1, Dk).to(BF),
+              rn(1, T, 1, Dk).to(BF), rn(H), rn(Dv).to(BF), rn(1, T, H, Dv).to(BF)]
+    dy = rn(1, T, H, Dv).to(BF)
+
+    def train(leaves):
+        x, w, dt, A, B, C, bias, nw, z = leaves
+        c = short_conv(x, w, **kw).view(1, T, H, Dv)
+        y = gated_group_norm(selective_scan(c, dt, A, B, C, dt_bias=bias, dt_softplus=True, seg_mode=1, **kw), nw, z)
+        return [y.detach(), *torch.autograd.grad(y, leaves, dy)]
+
+    fresh = lambda: [v.clone().requires_grad_(True) for v in values]
+    side = torch.cuda.Stream()
+    static = fresh()
+    side.wait_stream(torch.cuda.current_stream())
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.stream(side):
+        train(static)                       # (its eager graph is gone when the capture begins)
+        side.synchronize()
+        with torch.cuda.graph(graph, stream=side):
+            got = train(static)
+    torch.cuda.synchronize()
+    for k in range(3):
+        values[0] = rn(1, T, H * Dv).to(BF)
+        with torch.no_grad():
+            static[0].copy_(values[0])
+        graph.replay()
+        torch.cuda.synchronize()
+        want = train(fresh())
+        torch.cuda.synchronize()
+        assert all(torch.equal(a, b) for a, b in zip(got, want)), k
+
+
+@pytest.mark.parametrize("bad", [float("nan"), float("inf")])
+def test_bad_values_are_not_lost(dev, bad):
+    """A value that is not finite makes its sequence not finite from its chunk of 64 tokens on,
+    leaves the chunks before it as they are, and shows in every gradient summed over tokens."""
+    from gated_deltanet_chunked_delta_amd import gated_group_norm, selective_scan, short_conv
+    lens, at = [30, 200, 10], 30 + 70
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    kw = dict(cu_seqlens=cu.to(dev), cu_seqlens_host=cu)
+    out = []
+    for poison in (False, True):
+        g = torch.Generator(device=dev).manual_seed(6)
+        rn = lambda *s: torch.randn(*s, generator=g, device=dev)
+        x, B, C, u = rn(1, 240, 2, 64).to(BF), rn(1, 240, 1, 64).to(BF), rn(1, 240, 1, 64).to(BF), rn(1, 240, 48).to(BF)
+        dt, A, D, bias, w = rn(1, 240, 2) - 2, -1 - rn(2).abs(), rn(2), rn(2), rn(48, 4).to(BF)
+        nw, cb = rn(64).to(BF), rn(48).to(BF)
+        if poison:
+            for t in (x, u):
+                t[0, at] = bad
+        leaves = [t.requires_grad_(True) for t in (A, D, bias)]
+        y, hT = selective_scan(x, dt, A, B, C, D=D, dt_bias=bias, dt_softplus=True, output_final_state=True, **kw)
+        sums = list(torch.autograd.grad(y, leaves, torch.ones_like(y)))
+        c = short_conv(u, w.requires_grad_(True), cb.requires_grad_(True), **kw)
+        sums += torch.autograd.grad(c, [w, cb], torch.ones_like(c))
+        n = gated_group_norm(x, nw.requires_grad_(True))
+        sums += torch.autograd.grad(n, [nw], torch.ones_like(n))
+        out.append(([t.detach() for t in (y, hT, c, n)], sums))
+    (y0, h0, c0, n0), clean = out[0]
+    (y1, h1, c1, n1), dirty = out[1]
+    assert all(t.isfinite().all() for t in out[0][0] + clean)
+    assert torch.equal(y1[:, :94], y0[:, :94]) and torch.equal(y1[:, 230:], y0[:, 230:])
+    assert not y1[:, 94:230].isfinite().any()
+    assert not h1[1].isfinite().any() and torch.equal(h1[[0, 2]], h0[[0, 2]])
+    assert not c1[:, at:at + 4].isfinite().any() and torch.equal(c1[:, :at], c0[:, :at]) and torch.equal(c1[:, at + 4:], c0[:, at + 4:])
+    assert not n1[:, at].isfinite().any() and torch.equal(n1[:, at + 1:], n0[:, at + 1:])
+    for k, t in enumerate(dirty):
+        assert not t.isfinite().any(), k

@@ -19,13 +19,17 @@ def dev():
     return torch.device("cuda:0")
 
 
-def scan64(x, dt, A, B, C, D, bias, softplus, h0, lens, Q=64):
+def scan64(x, dt, A, B, C, D, bias, softplus, h0, lens, Q=64, keep=None):
     """The scan in 64 bits by chunks of Q tokens, differentiable; x [T, H, P], B, C [T, G, N],
-    states [n, H, N, P].  Returns y and the final states."""
+    states [n, H, N, P].  Returns y and the final states; keep receives the steps and the log
+    decays."""
     H, G = x.shape[1], B.shape[1]
     rep = H // G
     d = dt + bias if bias is not None else dt
     d = torch.logaddexp(d, torch.zeros_like(d)) if softplus else d
+    a = d * A
+    if keep is not None:
+        keep.update(d=d, a=a)
     tri = torch.tril(torch.ones(Q, Q, dtype=torch.bool, device=x.device))
     ys, hs, at = [], [], 0
     for n, L in enumerate(lens):
@@ -37,7 +41,7 @@ def scan64(x, dt, A, B, C, D, bias, softplus, h0, lens, Q=64):
 
         h = h0[n] if h0 is not None else x.new_zeros(H, B.shape[2], x.shape[2])
         X, K, O, dd = cut(x), cut(B).repeat_interleave(rep, 1), cut(C).repeat_interleave(rep, 1), cut(d[..., None])
-        cum = (dd * A[:, None, None]).cumsum(2)
+        cum = cut(a[..., None]).cumsum(2)
         Lm = torch.exp(torch.where(tri, cum - cum.transpose(2, 3), torch.full_like(cum[:1, :1, :1, :1], -torch.inf)))
         V = dd * X
         inner = ((O @ K.transpose(2, 3)) * Lm) @ V
@@ -67,7 +71,8 @@ ORDER = ["x", "dt", "A", "B", "C", "D", "bias", "h0"]
 
 
 def both(seed, lens, H, G, Dk, Dv, dt=BF, **opts):
-    """{name: (got, 64-bit)} of the outputs and gradients of one packed batch."""
+    """{name: (got, 64-bit)} of the outputs and gradients of one packed batch; under "sums" the
+    64-bit gradients of the steps and log decays, the steps and dt + bias."""
     from gated_deltanet_chunked_delta_amd import selective_scan
     T, n = sum(lens), len(lens)
     s, dy, dhT = inputs(seed, T, H, G, Dk, Dv, n, dt)
@@ -80,12 +85,16 @@ def both(seed, lens, H, G, Dk, Dv, dt=BF, **opts):
     torch.cuda.synchronize()
     r = {k: s[k].detach().double() for k in ORDER}
     r = {k: (v[0] if k in ("x", "dt", "B", "C") else v).requires_grad_(True) for k, v in r.items()}
-    ry, rh = scan64(*(r[k] for k in ORDER[:7]), True, r["h0"], lens)
-    rg = torch.autograd.grad([ry, rh], [r[k] for k in ORDER], [dy[0].double(), dhT.double()])
+    keep = {}
+    ry, rh = scan64(*(r[k] for k in ORDER[:7]), True, r["h0"], lens, keep=keep)
+    *rg, gd, ga = torch.autograd.grad([ry, rh], [r[k] for k in ORDER] + [keep["d"], keep["a"]],
+                                      [dy[0].double(), dhT.double()])
     out = dict(y=(y[0], ry), hT=(hT, rh))
     for k, a, b in zip(ORDER, grads, rg):
         out["d" + k] = (a[0] if k in ("x", "dt", "B", "C") else a, b)
-    return {k: (a.detach(), b.detach()) for k, (a, b) in out.items()}
+    out = {k: (a.detach(), b.detach()) for k, (a, b) in out.items()}
+    out["sums"] = (gd, ga, keep["d"].detach(), (r["dt"] + r["bias"]).detach())
+    return out
 
 
 def rms(t):
@@ -107,12 +116,97 @@ def test_scan_outputs_are_rounded_once(dev, lens, H, G, Dk, Dv, seg):
     scale with room for their sums.  A pre-rounding error e turns the rounding over with
     probability 2 e / step, by one step, step <= 2^-7 of the value: rms
     sqrt(2 e step) = sqrt(2 2^-16 2^-7) = 2^-11 of the rms."""
-    for k, (got, want) in both(3, lens, H, G, Dk, Dv, seg_mode=seg, round_once=True).items():
+    r = both(3, lens, H, G, Dk, Dv, seg_mode=seg, round_once=True)
+    del r["sums"]
+    for k, (got, want) in r.items():
         if got.dtype != BF:
             continue
         e = rms(got.double() - want.to(BF).double()) / rms(want)
         print(f"    {k} {e:.2e}", flush=True)
         assert e <= 2.0 ** -11, k
+
+
+
+@pytest.mark.parametrize("lens,H,G,Dk,Dv,seg", ROUNDED)
+def test_scan_outputs_by_default(dev, lens, H, G, Dk, Dv, seg):
+    """Without round_once y and dx pass two more bf16 roundings, of a chunk's matrix and of the
+    state, which enter through sums: each adds at most an error like the output's own, sqrt(3) of
+    it in all.  dB, dC and ddt are rounded once as with round_once."""
+    r = both(3, lens, H, G, Dk, Dv, seg_mode=seg)
+    del r["sums"]
+    for k, (got, want) in r.items():
+        if got.dtype != BF:
+            continue
+        own = rms(want.to(BF).double() - want)
+        e = rms(got.double() - want)
+        print(f"    {k} {e / rms(want):.3e} (rounding alone {own / rms(want):.3e})", flush=True)
+        if k in ("y", "dx"):
+            assert e <= 3 ** 0.5 * own, k
+        else:
+            assert rms(got.double() - want.to(BF).double()) <= 2.0 ** -11 * rms(want), k
+
+
+def chunk_scale(t, lens):
+    """sqrt of the sum over chunks of 64 tokens of (the chunk's sum)^2, by head: what an error
+    that goes with a chunk's terms, of either sign from chunk to chunk, adds up to."""
+    at, tot = 0, 0.0
+    for n in lens:
+        for c in range(at, at + n, 64):
+            tot = tot + t[c:min(c + 64, at + n)].sum(0).square()
+        at += n
+    return tot.sqrt()
+
+
+@pytest.mark.parametrize("seed", [1, 2])
+@pytest.mark.parametrize("lens,H,G,Dk,Dv", [([8192], 2, 1, 128, 128), ([5000, 3192], 4, 2, 64, 64)])
+def test_scan_fp32_results_of_long_sequences(dev, lens, H, G, Dk, Dv, seed):
+    """fp32 results of bf16 inputs over thousands of tokens.  An entry of a state is a sum of 64
+    products a chunk: off by sqrt(64) = 8 fp32 roundings of its size (one standard deviation),
+    and the decay forgets within a few chunks: 1e-6 of the largest entry, 17 roundings, has room.
+    da_t is a product of two such states, so off by 8 sqrt(2) roundings of its size; as d da
+    added up over the chunks that is the standard deviation of dA = sum d da (which may
+    cancel far below its terms), and the same of the two parts of ddt = A da + (dh B) x that of the
+    bias's gradient.  Four of them, 4 8 sqrt(2) = 45 roundings, hold for the 12 heads here.  A
+    drift of one sign adds up as the plain sum, sqrt(128 chunks) = 11 times as fast: 1e-6 of dA
+    (states kept without alternating sign) is 190 of these roundings, operands cut to 16 bits 1,400."""
+    r = both(seed, lens, H, G, Dk, Dv)
+    gd, ga, d, v = r.pop("sums")
+    for k in ("hT", "dh0"):
+        got, want = r[k]
+        e = ((got.double() - want).abs().max() / want.abs().max()).item()
+        print(f"    {k} {e:.2e}", flush=True)
+        assert e <= 1e-6, k
+    A = inputs(seed, sum(lens), H, G, Dk, Dv, len(lens))[0]["A"].double()
+    u = 2.0 ** -24
+    terms = dict(dA=(d * ga).abs(), dbias=((A * ga).abs() + (gd - A * ga).abs()) * torch.sigmoid(v))
+    for k, t in terms.items():
+        got, want = r[k]
+        tol = 45 * u * chunk_scale(t, lens) + u * want.abs()
+        e = ((got.double() - want).abs() / tol).max().item()
+        print(f"    {k} {e:.3f} of the bound ({((got.double() - want).abs().max() / want.abs().max()).item():.2e} of the largest)", flush=True)
+        assert e <= 1, k
+
+
+MANY = {"65": [(3 * i) % 7 for i in range(64)] + [130], "1100": [(5 * i) % 4 for i in range(1099)] + [70]}
+SHAPES = [("65", 2, 1, 64, 64), ("1100", 1, 1, 64, 64), ([200], 64, 1, 128, 64), ([70, 60], 128, 1, 128, 64)]
+
+
+@pytest.mark.parametrize("lens,H,G,Dk,Dv", SHAPES)
+@pytest.mark.parametrize("dt", [BF, torch.float32])
+def test_scan_of_many_sequences_and_heads(dev, lens, H, G, Dk, Dv, dt):
+    """More sequences than one wave and than one workgroup plans, and many heads on one B and C.
+    Tolerances as for the other shapes: bf16 outputs rounded once, fp32 results 2e-6 of the
+    largest entry, the sums over all tokens 2e-5."""
+    r = both(4, MANY.get(str(lens), lens), H, G, Dk, Dv, dt, round_once=True)
+    del r["sums"]
+    for k, (got, want) in r.items():
+        if got.dtype == BF:
+            e, tol = rms(got.double() - want.to(BF).double()) / rms(want), 2.0 ** -11
+        else:
+            e = ((got.double() - want).abs().max() / want.abs().max()).item()
+            tol = {"dA": 2e-5, "dbias": 2e-5, "ddt": 1e-5, "dD": 4e-6}.get(k, 2e-6)
+        print(f"    {k} {e:.2e} (<= {tol:.1e})", flush=True)
+        assert e <= tol, k
 
 
 def test_gates_of_fp32_tensors(dev):
