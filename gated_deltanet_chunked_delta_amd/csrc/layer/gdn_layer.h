@@ -200,6 +200,7 @@ struct SweepParams {
   float* out2;               // [G * parts][tokens][Dk], where a group has more than one part
   void* out2_whole;          // [tokens][G][Dk], where it has one
   float* rt;                 // [H * Dv / PS][tokens]
+  float* rt2;                // the same: of the chunk's own pairs, by source token (forwards); rt's part from the state (backwards)
   float* xd;                 // nullable [H * Dv / PS][tokens]: x_t . dy_t over the slice
   float* cb;                 // nullable [G][tokens]: C_t . B_t
   // anchors of the decay gradient: the forward key sweep leaves its state at the
@@ -207,8 +208,6 @@ struct SweepParams {
   const int* chunk_first;    // first chunk of each sequence
   float* dump;               // [chunks][H * Dv / PS][Dk * PS] in the key sweep's own order
   double* anchor;            // [chunks][H * Dv / PS]
-  const float* h0;           // nullable: the backward key sweep also writes <h0, its gradient>
-  double* anchor0;           // [N][H * Dv / PS]
 };
 
 struct ScanJoinParams {      // end states of the segments -> states entering them
@@ -233,12 +232,14 @@ struct ScanGradParams {      // ddt, dA, dD, ddt_bias from the row terms
   SeqInfo seq;
   const SegDesc* segs;
   const float* rt;           // forward sweep's row terms [slices][tokens]
+  const float* rt2;
   const float* ct;           // backward sweep's
+  const float* ct2;
   const float* xd;
   const float* cb;
   const int2* chunk_tab;
   const double* anchor;      // [chunks][H * Dv / PS]
-  const double* anchor0;     // nullable (no h0) [N][H * Dv / PS]
+  int has_h0;
   void* ddt;                 // [tokens][H], dtype of dt
   double* part;              // [chunks][H][3]
   float* dA;

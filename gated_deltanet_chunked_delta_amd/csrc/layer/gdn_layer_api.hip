@@ -86,7 +86,7 @@ struct ScanPlan {
   int nseg = 0, nchunk = 0, segc = 1;
   bool multi = false;  // some sequence has more than one segment
   size_t o_chunk_first = 0, o_seg_first = 0, o_segs = 0, o_chunk_tab = 0;
-  size_t o_state = 0, o_dec = 0, o_grad = 0, o_rt = 0, o_ct = 0, o_xd = 0, o_cb = 0, o_anchor = 0, o_anchor0 = 0, o_dump = 0, o_sums = 0,
+  size_t o_state = 0, o_dec = 0, o_grad = 0, o_rt = 0, o_rt2 = 0, o_ct = 0, o_ct2 = 0, o_xd = 0, o_cb = 0, o_anchor = 0, o_dump = 0, o_sums = 0,
          o_part = 0, total = 0;
 };
 
@@ -173,12 +173,13 @@ ScanPlan scan_plan(const gdn_scan_args& a, bool bwd, bool own_states) {
     const size_t tokens = (size_t)a.B * a.T, vh = (size_t)a.H * (a.Dv / gdn::PS);
     p.o_grad = take(st);
     p.o_rt = take(sizeof(float) * vh * tokens);
+    p.o_rt2 = take(sizeof(float) * vh * tokens);
     p.o_ct = take(sizeof(float) * vh * tokens);
+    p.o_ct2 = take(sizeof(float) * vh * tokens);
     p.o_xd = take(sizeof(float) * vh * tokens);
     p.o_cb = take(sizeof(float) * a.G * tokens);
     const size_t chunks = (size_t)p.nchunk;
     p.o_anchor = take(sizeof(double) * vh * chunks);
-    p.o_anchor0 = take(sizeof(double) * vh * a.num_seqs);
     p.o_dump = take(sizeof(float) * state_elems(a) * chunks);
     p.o_sums = take(sizeof(double) * 3 * a.H * chunks);
     const int parts = gdn::sweep_parts_per_group(a.dtype, a.H, a.G, a.Dv);
@@ -520,6 +521,7 @@ gdn_status gdn_scan_bwd(const gdn_scan_bwd_args* args, void* stream) {
   p.out2 = at<float>(ws, pl.o_part);
   p.out2_whole = args->dc;
   p.rt = at<float>(ws, pl.o_rt);
+  p.rt2 = at<float>(ws, pl.o_rt2);
   p.dump = at<float>(ws, pl.o_dump);
   hipError_t e = timed("scan_dc", s, [&] { return gdn::launch_sweep(a.dtype, 0, gdn::SWEEP_KEY, p, pl.nseg, s); });
   if (e != hipSuccess) return hip_fail(e, "scan dC launch");
@@ -533,12 +535,11 @@ gdn_status gdn_scan_bwd(const gdn_scan_bwd_args* args, void* stream) {
   p.out2 = at<float>(ws, pl.o_part);
   p.out2_whole = args->db;
   p.rt = at<float>(ws, pl.o_ct);
+  p.rt2 = at<float>(ws, pl.o_ct2);
   p.xd = at<float>(ws, pl.o_xd);
   p.cb = at<float>(ws, pl.o_cb);
   p.dump = at<float>(ws, pl.o_dump);
   p.anchor = at<double>(ws, pl.o_anchor);
-  p.h0 = a.h0;
-  p.anchor0 = at<double>(ws, pl.o_anchor0);
   e = timed("scan_db", s, [&] { return gdn::launch_sweep(a.dtype, 1, gdn::SWEEP_KEY, p, pl.nseg, s); });
   if (e != hipSuccess) return hip_fail(e, "scan dB launch");
   red.out = args->db;
@@ -555,9 +556,9 @@ gdn_status gdn_scan_bwd(const gdn_scan_bwd_args* args, void* stream) {
   g.dt = a.dt; g.dt_stride = a.dt_stride; g.dt_f32 = a.dt_dtype == GDN_F32; g.softplus = a.dt_softplus;
   g.dt_bias = a.dt_bias; g.A = a.A; g.H = a.H; g.G = a.G; g.Dk = a.Dk; g.Dv = a.Dv; g.tokens = (int64_t)a.B * a.T;
   g.seq = p.seq; g.segs = p.segs; g.chunk_tab = at<int2>(ws, pl.o_chunk_tab);
-  g.rt = at<float>(ws, pl.o_rt); g.ct = at<float>(ws, pl.o_ct); g.xd = at<float>(ws, pl.o_xd); g.cb = at<float>(ws, pl.o_cb);
+  g.rt = at<float>(ws, pl.o_rt); g.rt2 = at<float>(ws, pl.o_rt2); g.ct = at<float>(ws, pl.o_ct); g.ct2 = at<float>(ws, pl.o_ct2); g.xd = at<float>(ws, pl.o_xd); g.cb = at<float>(ws, pl.o_cb);
   g.anchor = at<double>(ws, pl.o_anchor);
-  g.anchor0 = a.h0 ? at<double>(ws, pl.o_anchor0) : nullptr;
+  g.has_h0 = a.h0 != nullptr;
   g.ddt = args->ddt; g.part = at<double>(ws, pl.o_sums); g.dA = args->dA; g.dD = args->dD; g.ddt_bias = args->ddt_bias;
   e = timed("scan_ddt", s, [&] { return gdn::launch_scan_grad(g, pl.nchunk, s); });
   return e == hipSuccess ? GDN_OK : hip_fail(e, "scan step gradient launch");

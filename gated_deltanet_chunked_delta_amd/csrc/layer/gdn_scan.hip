@@ -22,8 +22,16 @@
 // (the terms of a token with itself cancel and are left out, so under strong
 // decay both sides are as small as da itself).  The recursion is undamped, so
 // it restarts at every chunk's end from <h, dh> there: the forward key sweep
-// leaves its states and the backward one takes the products; what a chunk's sums
-// miss the product at its start by is spread over its tokens.  Then
+// leaves its states and the backward one takes the products, in 64 bits; what a chunk's
+// sums miss the product at its start by is spread over its tokens (but in a first
+// chunk with an h0, where <h0, dh0> is of larger terms than those sums).  A pair of
+// tokens of one chunk enters rt_t of the later and D_t ct_t of the earlier one and
+// cancels before both: so the forward key sweep takes both sums from the same
+// products (rt; rt2 by the earlier token), and of the backward one's ct only the part
+// that comes from the state (rt2) enters the recursion.  Error of dA in fp32 roundings of
+// its terms (16 heads of 128 x 128, 4,096 tokens fp32 and 8,192 bf16; 4 of 64 x 64, 3,392
+// fp32 with h0): 5.2, 3.9, 5.5; with the pairs from two sweeps, products in 32 bits and
+// the spread in every chunk 8.0, 7.1, 8.7 (and 2 % less time of a training pass).  Then
 // dD_t = ct_t + (C_t . B_t)(x_t . dy_t) + A da_t.
 //
 // Precision.  Products of bf16 inputs are exact and summed in fp32.  An fp32
@@ -137,10 +145,11 @@ __device__ __forceinline__ void frag_f32(const Frag<float>& f, f32x4& lo, f32x4&
 
 // The matrix cores' sums come out low by a fraction of a unit in the last place
 // on average, whatever their sign.  A state gathers such errors chunk by chunk,
-// and dA and the bias's gradient add products of two states over all tokens: 1e-6
-// of dA at 16,384 tokens, of one sign in every head.  So a state is kept with its
-// sign turned over from chunk to chunk of its sequence (sign_of chunk boundary b)
-// and the errors of neighbouring chunks cancel: 3e-7, the fp32 terms' own noise.
+// and dA and the bias's gradient add products of two states over all tokens.  So a
+// state is kept with its sign turned over from chunk to chunk of its sequence
+// (sign_of chunk boundary b) and the errors of neighbouring chunks cancel: over 48 heads
+// of 16,384 tokens the error of dA has a mean of 0.5 fp32 roundings of its terms, and
+// of -12 with states of one sign.
 __device__ __forceinline__ float sign_of(int b) { return b & 1 ? -1.f : 1.f; }
 
 // Keeps the instruction scheduler from moving work across: without it the reads
@@ -217,6 +226,24 @@ __device__ __forceinline__ double readlane_d(double x, int lane) {
   v[0] = __builtin_amdgcn_readlane(v[0], lane);
   v[1] = __builtin_amdgcn_readlane(v[1], lane);
   return __builtin_bit_cast(double, v);
+}
+// Sum over the 16 lanes of each row, in every lane.
+__device__ __forceinline__ double row16_sum_d(double x) {
+  x += dpp_mov_d<0xB1>(x);   // lane ^ 1
+  x += dpp_mov_d<0x4E>(x);   // lane ^ 2
+  x += dpp_mov_d<0x141>(x);  // half-row mirror
+  x += dpp_mov_d<0x140>(x);  // row mirror
+  return x;
+}
+// Sums over the 16 lanes of each row of four values at once: lane t gets that of
+// x[t % 4].
+__device__ __forceinline__ float row16_sum4(const f32x4& x) {
+  const bool odd = threadIdx.x & 1, high = threadIdx.x & 2;
+  const float a = (odd ? x[1] : x[0]) + quad_xor<1>(odd ? x[0] : x[1]);
+  const float b = (odd ? x[3] : x[2]) + quad_xor<1>(odd ? x[2] : x[3]);
+  float c = (high ? b : a) + quad_xor<2>(high ? a : b);
+  c += dpp_mov<0x128>(c);  // row rotated by 8
+  return c + dpp_mov<0x124>(c);
 }
 // Sums over the four 16-lane groups of four values at once: lane 16 g + t gets
 // the sum of x[g] over lanes t, 16 + t, 32 + t, 48 + t.  Exchanging odd with even
@@ -760,9 +787,10 @@ struct KeyLds {
   E v[HS][CH * row_ld<E>(PS)];
   E w[HS][CH * row_ld<E>(PS)];
   f32x4 z[10][64];               // sum over slices of the decayed chunk matrix, by tile and lane
-  float rti[4][HS][CH];          // row terms of the chunk itself, by source block
+  float rti[10][HS][16];         // row terms of the chunk itself, by tile and target row
+  float cti[10][HS][16];         // forwards: the same pairs' sums by source row
   float rtx[DK / 16][HS][CH];    // row terms of the state, by key tile
-  float anc[DK / 16][HS];
+  double anc[DK / 16][4][HS];    // <state, its gradient>, by key tile and lane group
   ChunkDecay dec[2][HS];         // of this chunk and the next
 };
 
@@ -866,7 +894,6 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
 #pragma unroll
       for (int pt = 0; pt < 4; ++pt) dump[pt] = __builtin_nontemporal_load(d + pt * 64);
     };
-    float anc[4] = {0.f, 0.f, 0.f, 0.f};
     if (REV) request_dump(0);
     __syncthreads();  // this chunk's tiles and decays are in place
     // the chunk's own part: tiles of (rows s, columns t), the diagonal ones, which
@@ -905,15 +932,20 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
         }
         if (s == 0 || slice_of(s) % spv == 0) f = tile_decay<true>(sh.dec[i & 1][head_of(s)], tb, sb);
         const f32x4 z = x * f;
-        float rt = 0.f;
+        f32x4 pair = z * cb;  // of source row 4g + e and target row t16, other than itself
+        if (sb == tb) {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-          if (sb < tb || 4 * g4 + e < t16) rt += z[e] * cb[e];
-        rts[s] = rt;
+          for (int e = 0; e < 4; ++e) pair[e] = 4 * g4 + e < t16 ? pair[e] : 0.f;
+        }
+        rts[s] = (pair[0] + pair[1]) + (pair[2] + pair[3]);
+        if (!REV) {
+          const float own = row16_sum4(pair);  // source row 4g + t16 % 4
+          if (t16 < 4) sh.cti[idx][s][4 * g4 + t16] = own;
+        }
         if (s < ns) zs += z * sh.dec[i & 1][head_of(s)].tw[row];
       }
       const float rt = sum_groups4(rts);  // slice g
-      if (g4 < HS) sh.rti[sb][g4][row] = rt;
+      if (g4 < HS) sh.rti[idx][g4][t16] = rt;
       sh.z[idx][l] = zs;
     }
     if (ds >= 0 && i + 1 < nch)
@@ -943,10 +975,13 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
       if (s >= ns) break;
       sched_fence();
       if (REV) {  // <state at the chunk's end, its gradient>, this lane's part
+        double a = 0.;
 #pragma unroll
         for (int pt = 0; pt < 4; ++pt)
-          anc[s] += (dump[pt][0] * T[s][pt][0] + dump[pt][1] * T[s][pt][1]) + (dump[pt][2] * T[s][pt][2] + dump[pt][3] * T[s][pt][3]);
-        anc[s] = sg * row16_sum(anc[s]);
+#pragma unroll
+          for (int e = 0; e < 4; ++e) a += (double)dump[pt][e] * T[s][pt][e];
+        a = row16_sum_d(a);
+        if (t16 == 0) lds_opaque(sh0)->anc[nt][g4][s] = sg * a;
         if (s + 1 < ns) request_dump(s + 1);
       }
       // u = W T^T of the state before the chunk, four row blocks side by side
@@ -1003,10 +1038,6 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
           for (int pt = 0; pt < 4; ++pt) mma(T[s][pt], vf[pt], kp[kb].p[q]);
       }
     }
-    if (REV) {
-      const float a = sum_groups4(anc);  // slice g
-      if (t16 == 0 && g4 < HS) lds_opaque(sh0)->anc[nt][g4] = a;
-    }
     __syncthreads();  // the chunk's tiles are read, its row terms are in place
     // The next chunk's tiles into LDS and the requests of the one after it come
     // before this chunk's stores: the wait for a requested tile covers every
@@ -1038,45 +1069,35 @@ __global__ __launch_bounds__(DK * 4) void sweep_key_kernel(SweepParams p, int pa
     Lds& sh = *lds_opaque(sh0);
     if (REV && tid < ns) {
       double a = 0.;
-      for (int n = 0; n < NW; ++n) a += sh.anc[n][tid];
+      for (int n = 0; n < NW; ++n)
+        for (int g = 0; g < 4; ++g) a += sh.anc[n][g][tid];
       p.anchor[(chunk0 + ci) * nsl + slice_of(tid)] = a;
     }
     for (int k = tid; k < ns * CH; k += NTH) {
       const int s = k / CH, row = k % CH;
-      float a = sh.rti[0][s][row];
+      const int blk = row / 16, r16 = row % 16;
+      double own = 0., state = 0.;
 #pragma unroll
-      for (int sb = 1; sb < 4; ++sb) {
-        const float v = sh.rti[sb][s][row];  // (left from another chunk above the diagonal)
-        a += sb <= row / 16 ? v : 0.f;
+      for (int sb = 0; sb < 4; ++sb) {
+        const float v = sh.rti[blk * (blk + 1) / 2 + min(sb, blk)][s][r16];
+        own += sb <= blk ? v : 0.f;
       }
 #pragma unroll
-      for (int n = 0; n < NW; ++n) a += sh.rtx[n][s][row];
-      if (row < c.nt) p.rt[(int64_t)slice_of(s) * p.tokens + row_of<REV>(c, row)] = a;
-    }
-  }
-  if (REV && p.h0 && r.s == 0) {
-    Lds& sh = *sh0;
-    // <h0, its gradient>: the anchor at the sequence's start
-    float anc[4] = {0.f, 0.f, 0.f, 0.f};
+      for (int n = 0; n < NW; ++n) state += sh.rtx[n][s][row];
+      if (row < c.nt) {
+        const int64_t at = (int64_t)slice_of(s) * p.tokens + row_of<REV>(c, row);
+        p.rt[at] = (float)(own + state);
+        if (!REV) {
+          state = 0.;
 #pragma unroll
-    for (int s = 0; s < HS; ++s)
-      if (s < ns) {
-        const int sl = slice_of(s);
-        const float* s0 = p.h0 + ((int64_t)r.n * p.H + sl / spv) * st_off + (int64_t)kcol * p.Dv + sl % spv * PS;
-#pragma unroll
-        for (int pt = 0; pt < 4; ++pt)
-#pragma unroll
-          for (int i = 0; i < 4; ++i) anc[s] += T[s][pt][i] * s0[32 * (pt >> 1) + 8 * g4 + 4 * (pt & 1) + i];
-        anc[s] = sign_of(boundary<REV>(r, nch, nch)) * row16_sum(anc[s]);
+          for (int tb = 0; tb < 4; ++tb) {
+            const int hi = max(tb, blk);
+            const float v = sh.cti[hi * (hi + 1) / 2 + blk][s][r16];
+            state += tb >= blk ? v : 0.f;
+          }
+        }
+        p.rt2[at] = (float)state;
       }
-    __syncthreads();
-    const float part_sum = sum_groups4(anc);
-    if (t16 == 0 && g4 < HS) sh.anc[nt][g4] = part_sum;
-    __syncthreads();
-    if (tid < ns) {
-      double a = 0.;
-      for (int n = 0; n < NW; ++n) a += sh.anc[n][tid];
-      p.anchor0[(int64_t)r.n * nsl + slice_of(tid)] = a;
     }
   }
 }

@@ -56,7 +56,8 @@ __global__ __launch_bounds__(256) void scan_join_kernel(ScanJoinParams p) {
 // (chunk, head), lane = token.  The recursion of da is a suffix sum of
 // v_t = rt_t - D_t ct_t, undamped (a rounding stays in it to the chunk's start),
 // so it and the sums over tokens are held in 64 bits, and what the sums miss the
-// anchor at the chunk's start by is spread evenly over the tokens.  Where a
+// anchor at the chunk's start by is spread evenly over the tokens (a sequence's first
+// chunk: zero without an h0; with one its product is not used).  Where a
 // token's own decay is below fp32's unit round-off the recursion restarts with
 // v_t = rt_t (cut): what is left of da_{t+1} - D_t ct_t = <., exp(a_t) h_{t-1}>
 // there is below the rounding of its two parts, which |A| in ddt would multiply.
@@ -73,25 +74,26 @@ __global__ __launch_bounds__(64) void scan_grad_kernel(ScanGradParams p) {
   const float A = p.A[h];
   const float raw = scan_dt_raw(p.dt, p.dt_f32, row * p.dt_stride + h) + (p.dt_bias ? p.dt_bias[h] : 0.f);
   const float cb = p.cb[(int64_t)g * p.tokens + row];
-  double v = 0., ct = 0., xd = 0.;
+  double v = 0., own = 0., ct = 0., cs = 0., xd = 0.;
   for (int s = 0; s < nsl; ++s) {
     const int64_t at = ((int64_t)h * nsl + s) * p.tokens + row;
     v += p.rt[at];
+    own += p.rt2[at];  // of D_t ct_t the chunk's own pairs, and the rest
+    cs += p.ct2[at];
     ct += p.ct[at];
     xd += p.xd[at];
   }
-  // <h, dh> at the chunk's end, and at its start (the end of the chunk before)
+  // <h, dh> at the chunk's end, and at its start (the end of the chunk before; h = 0 before the first)
   double carry = 0., start = 0.;
   for (int s = 0; s < nsl; ++s) {
     carry += p.anchor[(chunk * p.H + h) * nsl + s];
     if (nc.y > 0) start += p.anchor[((chunk - 1) * p.H + h) * nsl + s];
-    else if (p.anchor0) start += p.anchor0[((int64_t)nc.x * p.H + h) * nsl + s];
   }
   const float d = p.softplus ? scan_softplus(raw) : raw;
   const bool cut = in && d * A < LN_EPS;
-  if (!cut) v -= d * ct;
+  if (!cut) v -= own + d * cs;
   if (!in) v = 0.;
-  const double miss = __any(cut) ? 0. : (start - carry - wave_sum_d(v)) / len;
+  const double miss = __any(cut) || (nc.y == 0 && p.has_h0) ? 0. : (start - carry - wave_sum_d(v)) / len;
   double suf = v + (in ? miss : 0.);
   int ended = cut;  // a cut at or behind this token, within the chunk
 #pragma unroll
