@@ -7,15 +7,19 @@
 // W-1 inputs, oldest first.
 //
 // Bound: memory -- one read of x and one write of y (2 W flops an element).  A
-// thread owns 16 bytes of channels (8 bf16 or 4 fp32) and walks `run`
+// thread owns 16 bytes of channels (8 bf16 or 4 fp32; in the gradient four of
+// either type; one where widths or pointers do not allow that) and walks `run`
 // consecutive tokens with the last W-1 inputs in registers, so that x is
 // fetched once but for W-1 rows per run, which the neighbouring run's thread
 // brings into cache as well.  Threads are numbered channels first over the
 // runs, so a wave stays full for any channel count.
 // Measured (bf16, W = 4): 8,192 x 6,144 in 38 us (201 MB, most of it from cache);
-// 49,828 x 2,304 in 92 us (459 MB, 5.0 TB/s), its gradient in 173 us + 8 us for the
+// 49,828 x 2,304 in 92 us (459 MB, 5.0 TB/s), its gradient in 175 us + 7 us for the
 // weights' sums (689 MB; with some 35 vector instructions an element, two of them
 // transcendental, the arithmetic takes about 120 us beside the traffic's 141).
+// fp32: 8,192 x 6,144 in 83 us (403 MB, 4.8 TB/s), its gradient in 170.  One channel a
+// thread: 8,192 x 1,001 bf16 in 12.3 us (2.7 TB/s) and 45 us (1.1), by the two-byte
+// accesses' instructions.
 // A token for each of 16 sequences of 6,144 channels: 6 us, all of it latency.
 #include "gdn_layer.h"
 

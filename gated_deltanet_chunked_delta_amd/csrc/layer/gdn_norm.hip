@@ -14,7 +14,9 @@
 // share a wave.  Rows too long for that are re-read by a whole workgroup.
 // Measured (bf16, gated): 32,768 x 16 heads of 128 in 70 us (403 MB, 5.8 TB/s);
 // 16,384 rows of 2,000 in 37 us (197 MB) and the gradient in 76 us (328 MB,
-// 4.3 TB/s); 64 x 16 heads of 128 in 7 us, all of it latency.
+// 4.3 TB/s); 64 x 16 heads of 128 in 7 us, all of it latency.  Widths off 16 bytes take
+// one element a thread and access, and past 1,024 of them the re-reading kernels:
+// 16,384 x 999 bf16 in 41 us (2.4 TB/s) and 115 us (1.4), x 1,999 in 91 us and 565 us.
 #include "gdn_layer.h"
 
 namespace gdn {

@@ -44,8 +44,9 @@
 // an error like the output's own rounding, unless the caller asks for outputs that
 // are rounded only once (round_once): then they too enter in two parts.  Rms error of
 // y against 64 bits, 4,096 tokens of 2 heads of 128 x 128: 2.04e-3, with round_once
-// 1.65e-3, which is the final rounding's alone; time of the four bf16 passes of
-// 333 to 65,536 tokens with it: 3 to 8 % more.
+// 1.65e-3, which is the final rounding's alone; time with it: 333
+// tokens 24.0 us instead of 23.5, 8,192 81.9 (79.2), 65,536 132 (120), a training
+// pass of 4 x 4,096 609 (589).
 // fp32 inputs take the fp32 matrix instructions throughout.
 //
 // Decay factors are products of factors <= 1 over 16-row blocks (a power of a
@@ -55,12 +56,18 @@
 // Bound: neither memory nor the matrix cores alone.  A workgroup fills a compute
 // unit (tiles and states: LDS, and up to 256 registers a lane at two waves a SIMD),
 // and a chunk's phases wait for each other.  Measured, bf16, 16 heads of 128 x 128
-// with one B and C: 8,192 tokens forward, states 30 us, join 15, outputs 43 (74 MB:
-// 15 us at the memory's rate); 4 x 4,096 tokens, states 43, y 70, dx 66, dC 163, dB
-// 147 us.  A value sweep's chunk takes about 14,000 cycles, a key sweep's about
-// 35,000 for four slices, of which its matrix instructions would fill 8,000; its
+// with one B and C: 8,192 tokens forward, states 29 us, join 14, outputs 44 (74 MB:
+// 15 us at the memory's rate); 4 x 4,096 tokens, states 43, y 71, dx 69, dC 171, dB
+// 157 us.  A value sweep's chunk takes about 14,000 cycles, a key sweep's about
+// 36,000 for four slices, of which its matrix instructions would fill 8,000; its
 // share of a chunk's state out (or in) and its parts of dC (dB) are 60 MB over the
-// chip, 12 us at the memory's rate.
+// chip, 12 us at the memory's rate.  fp32 (tiles of twice the bytes wait in registers):
+// 8,192 tokens of 16 heads of 128 x 128 forward 268 us, backward 666 us.
+// Registers: value sweeps with outputs spill in fp32 (bytes a lane: Dk = 64, two waves 128
+// forwards and 28 backwards; Dk = 128, four waves 248 and 148, two waves 564 and 412)
+// and in bf16 where a group has one head of 64 columns and Dk = 128 (104 and 44);
+// the dC sweep <bf16, 128, 4> spills 8.  Key sweeps of Dk = 64 with four slices, with two in
+// fp32, and with two backwards in bf16 hold 266 to 343 registers: one wave a SIMD.
 #include "gdn_layer.h"
 #include "gdn_scan_device.h"
 

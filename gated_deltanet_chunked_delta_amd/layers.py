@@ -12,7 +12,8 @@ fallback.
 ``gdn_conv_step`` and ``gdn_scan_step`` advance a serving loop's state slots by
 one token.  Inputs may be slices of a wider row (the output of one projection,
 say): every entry of a token has to be contiguous, the distance between tokens
-is free.  Tensors of a call share one device, whose current stream it uses.
+is free; for the scan's x, B and C, and the scan step's x, both start and distance
+have to be whole 16 bytes (``.contiguous()`` makes them so).  Tensors of a call share one device, whose current stream it uses.
 
 Calls can be captured into a graph, a backward pass too, provided that no eager
 graph of the same leaves is alive then: autograd would synchronise with the
@@ -589,7 +590,7 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus: bool = Fal
     (y, hT).  cu_seqlens (int32, B = 1) packs sequences; without its host copy
     cu_seqlens_host it is read back once (a device synchronisation).  round_once: bf16 y and
     dx are the fp32 result rounded once; without it a chunk's matrix and state are rounded
-    inside as well (rms error up to a quarter above the output rounding's, 3 to 8 % less time)."""
+    inside as well (rms error up to a quarter above the output rounding's, 2 to 10 % less time)."""
     if _wants_grad(x, dt, A, B, C, D, dt_bias, initial_state):
         y, hT = _SelectiveScan.apply(x, dt, A, B, C, D, dt_bias, initial_state, bool(dt_softplus), cu_seqlens,
                                      cu_seqlens_host, bool(output_final_state), int(seg_mode), bool(round_once))

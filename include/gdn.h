@@ -363,7 +363,7 @@ gdn_status gdn_conv_step(const gdn_conv_step_args* args, void* stream);
  * a bf16 y and dx the 64 x 64 matrix of a chunk and the state entering it are
  * rounded to bf16 as well (rms error 1.8e-3 to 2.1e-3 of the values, of which the
  * output's rounding is 1.65e-3), unless round_once is 1: then y and dx too are the
- * fp32 result rounded once (3 to 8 % more time).  The
+ * fp32 result rounded once (2 to 10 % more time).  The
  * gradient's workspace holds a state for every chunk: 4 Dk Dv H bytes for every
  * 64 tokens. */
 typedef struct {
