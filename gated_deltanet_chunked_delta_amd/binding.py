@@ -132,6 +132,16 @@ def _gradient(t):
     return t if t.data_ptr() % 16 == 0 else t.clone()
 
 
+# torch.compile cannot follow what fills a C structure in: read back, a field is not its
+# value, and later writes are lost.  So a compiled function's graph ends at the calls,
+# which run as they are; only where _compiling() was traced does _outside run.
+_compiling = torch.compiler.is_dynamo_compiling
+
+
+def _outside(fn, *args):
+    return torch._dynamo.disable(fn)(*args)
+
+
 def _prep(a, q, qk_norm, gate_act, gate_scale):
     """Fill the pre-processing fields of an argument struct."""
     a.qk_norm, a.gate_act = int(bool(qk_norm)), int(bool(gate_act))

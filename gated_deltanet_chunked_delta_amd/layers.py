@@ -22,7 +22,8 @@ stream that one was made on, which a capture cannot.
 Reverse mode only: forward-mode derivatives are refused.  No derivative passes
 through the ``gdn_*`` calls; the two steps refuse inputs that ask for one.
 Tracers that would record a call without its kernels are refused as well
-(``torch.jit.trace`` keeps the three operators as one operation each).
+(``torch.jit.trace`` keeps the three operators as one operation each, and a
+function compiled by ``torch.compile`` leaves its graph for a call).
 """
 from __future__ import annotations
 
@@ -34,7 +35,7 @@ import torch
 from torch.autograd import forward_ad
 from torch.autograd.function import once_differentiable
 
-from .binding import GDNError, _check, _dtype_code, _gradient, _ptr, _vp, lib as _load
+from .binding import GDNError, _check, _compiling, _dtype_code, _gradient, _outside, _ptr, _vp, lib as _load
 
 __all__ = ["short_conv", "selective_scan", "gated_group_norm", "gdn_conv_fwd", "gdn_conv_bwd", "gdn_conv_step",
            "gdn_scan_fwd", "gdn_scan_bwd", "gdn_scan_step", "gdn_norm_fwd", "gdn_norm_bwd"]
@@ -331,6 +332,9 @@ def gdn_conv_fwd(x, weight, bias=None, silu: bool = True, initial_state=None, cu
     """y, final_state (None unless output_final_state) of the short causal convolution:
     x [B, T, D], weight [D, W], bias [D], states [N, W-1, D] (the inputs before a
     sequence's start, oldest first), all of one dtype."""
+    if _compiling():
+        return _outside(gdn_conv_fwd, x, weight, bias, silu, initial_state, cu_seqlens, cu_seqlens_host,
+                        output_final_state)
     a, host = _conv_args(x, weight, bias, silu, initial_state, cu_seqlens, cu_seqlens_host)
     y = _rows_like(x, cu_seqlens is not None and host is None)
     fin = torch.empty((a.num_seqs, a.W - 1, a.D), dtype=x.dtype, device=x.device) if output_final_state else None
@@ -343,6 +347,8 @@ def gdn_conv_fwd(x, weight, bias=None, silu: bool = True, initial_state=None, cu
 def gdn_conv_bwd(x, weight, dy, bias=None, silu: bool = True, initial_state=None, cu_seqlens=None,
                  cu_seqlens_host=None, dfinal=None):
     """(dx, dweight, dbias, dinitial_state), the last two None without bias / initial_state."""
+    if _compiling():
+        return _outside(gdn_conv_bwd, x, weight, dy, bias, silu, initial_state, cu_seqlens, cu_seqlens_host, dfinal)
     a, host = _conv_args(x, weight, bias, silu, initial_state, cu_seqlens, cu_seqlens_host)
     dev, dt = x.device, x.dtype
     _t("dy", dy, x.shape, dt, dev)
@@ -365,6 +371,8 @@ def gdn_conv_step(x, state, weight, bias=None, silu: bool = True, state_idx=None
     """One token for each of N sequences: x [N, D], state [S, W-1, D] (advanced in place;
     sequence n uses slot n, or state_idx[n]; out-of-range indices mark padding, whose y is
     left as it was).  Two sequences of one call must not share a slot.  Returns y [N, D]."""
+    if _compiling():
+        return _outside(gdn_conv_step, x, state, weight, bias, silu, state_idx, y)
     if x.dim() != 2 or weight.dim() != 2:
         raise GDNError("x must be [N, D] and weight [D, W]")
     _no_derivative("gdn_conv_step", (x, state, weight, bias))
@@ -419,6 +427,9 @@ def short_conv(x, weight, bias=None, silu: bool = True, initial_state=None, outp
     optional bias [D] and SiLU, differentiable in x, weight, bias and initial_state.
     Returns y, or (y, final_state [N, W-1, D]).  cu_seqlens (int32, B = 1) packs
     sequences; cu_seqlens_host, when given, is checked against T."""
+    if _compiling():
+        return _outside(short_conv, x, weight, bias, silu, initial_state, output_final_state, cu_seqlens,
+                        cu_seqlens_host)
     if _wants_grad(x, weight, bias, initial_state):
         y, fin = _ShortConv.apply(x, weight, bias, initial_state, bool(silu), cu_seqlens, cu_seqlens_host,
                                   bool(output_final_state))
@@ -465,6 +476,9 @@ def gdn_scan_fwd(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus: bool = False
                  round_once: bool = False):
     """(y, hT) with hT None unless output_final_state, followed by the saved segment
     states if save_states (a flat fp32 tensor for gdn_scan_bwd)."""
+    if _compiling():
+        return _outside(gdn_scan_fwd, x, dt, A, B, C, D, dt_bias, dt_softplus, h0, cu_seqlens, cu_seqlens_host,
+                        output_final_state, save_states, seg_mode, round_once)
     a, host = _scan_args(x, dt, A, B, C, D, dt_bias, dt_softplus, h0, cu_seqlens, cu_seqlens_host, seg_mode,
                          round_once)
     dev, L = x.device, lib()
@@ -488,6 +502,9 @@ def gdn_scan_bwd(x, dt, A, B, C, dy, D=None, dt_bias=None, dt_softplus: bool = F
                  cu_seqlens=None, cu_seqlens_host=None, states=None, seg_mode: int = 0, round_once: bool = False):
     """(dx, ddt, dA, dB, dC, dD, ddt_bias, dh0); dD, ddt_bias and dh0 are None where their
     inputs are.  states: gdn_scan_fwd(..., save_states=True) on the same inputs."""
+    if _compiling():
+        return _outside(gdn_scan_bwd, x, dt, A, B, C, dy, D, dt_bias, dt_softplus, h0, dhT, cu_seqlens,
+                        cu_seqlens_host, states, seg_mode, round_once)
     a, host = _scan_args(x, dt, A, B, C, D, dt_bias, dt_softplus, h0, cu_seqlens, cu_seqlens_host, seg_mode,
                          round_once)
     dev, L = x.device, lib()
@@ -515,6 +532,8 @@ def gdn_scan_bwd(x, dt, A, B, C, dy, D=None, dt_bias=None, dt_softplus: bool = F
 def gdn_scan_step(x, dt, A, B, C, state, D=None, dt_bias=None, dt_softplus: bool = False, state_idx=None, y=None):
     """One token for each of N sequences: x [N, H, Dv], dt [N, H], B, C [N, G, Dk]; state
     [S, H, Dk, Dv] fp32 is advanced in place (slots as in gdn_decode_step).  Returns y."""
+    if _compiling():
+        return _outside(gdn_scan_step, x, dt, A, B, C, state, D, dt_bias, dt_softplus, state_idx, y)
     if x.dim() != 3 or B.dim() != 3:
         raise GDNError("x must be [N, H, Dv] and B, C [N, G, Dk]")
     _no_derivative("gdn_scan_step", (x, dt, A, B, C, state, D, dt_bias))
@@ -591,6 +610,9 @@ def selective_scan(x, dt, A, B, C, D=None, dt_bias=None, dt_softplus: bool = Fal
     cu_seqlens_host it is read back once (a device synchronisation).  round_once: bf16 y and
     dx are the fp32 result rounded once; without it a chunk's matrix and state are rounded
     inside as well (rms error up to a quarter above the output rounding's, 2 to 10 % less time)."""
+    if _compiling():
+        return _outside(selective_scan, x, dt, A, B, C, D, dt_bias, dt_softplus, initial_state, output_final_state,
+                        cu_seqlens, cu_seqlens_host, seg_mode, round_once)
     if _wants_grad(x, dt, A, B, C, D, dt_bias, initial_state):
         y, hT = _SelectiveScan.apply(x, dt, A, B, C, D, dt_bias, initial_state, bool(dt_softplus), cu_seqlens,
                                      cu_seqlens_host, bool(output_final_state), int(seg_mode), bool(round_once))
@@ -627,6 +649,8 @@ def _norm_args(x, weight, z, bias, eps, center, gate_first):
 
 def gdn_norm_fwd(x, weight, z=None, bias=None, eps: float = 1e-5, center: bool = False, gate_first: bool = False):
     """y of the gated group norm (see gated_group_norm)."""
+    if _compiling():
+        return _outside(gdn_norm_fwd, x, weight, z, bias, eps, center, gate_first)
     args = NormFwdArgs()
     args.a = _norm_args(x, weight, z, bias, eps, center, gate_first)
     y = x.new_empty(x.shape)
@@ -637,6 +661,8 @@ def gdn_norm_fwd(x, weight, z=None, bias=None, eps: float = 1e-5, center: bool =
 
 def gdn_norm_bwd(x, weight, dy, z=None, bias=None, eps: float = 1e-5, center: bool = False, gate_first: bool = False):
     """(dx, dweight, dz, dbias), the last two None without z / bias."""
+    if _compiling():
+        return _outside(gdn_norm_bwd, x, weight, dy, z, bias, eps, center, gate_first)
     args = NormBwdArgs()
     args.a = _norm_args(x, weight, z, bias, eps, center, gate_first)
     dev = x.device
@@ -677,6 +703,8 @@ def gated_group_norm(x, weight, z: Optional[torch.Tensor] = None, bias=None, eps
         y = y silu(z) with a gate and not gate_first
 
     weight and bias are [G, D], or [D] shared by all groups."""
+    if _compiling():
+        return _outside(gated_group_norm, x, weight, z, bias, eps, center, gate_first)
     if not _wants_grad(x, weight, z, bias):
         return gdn_norm_fwd(x, weight, z, bias, eps, center, gate_first)
     return _GatedGroupNorm.apply(x, weight, z, bias, float(eps), bool(center), bool(gate_first))

@@ -145,3 +145,41 @@ def test_bad_values_are_not_lost(dev, bad):
     assert not n1[:, at].isfinite().any() and torch.equal(n1[:, at + 1:], n0[:, at + 1:])
     for k, t in enumerate(dirty):
         assert not t.isfinite().any(), k
+
+
+@pytest.mark.parametrize("name", ["conv", "scan", "norm", "conv_step", "scan_step", "library"])
+def test_inside_a_compiled_function(dev, name):
+    """A function compiled by torch.compile leaves its graph for the calls: results and gradients
+    are those of the function itself, bit for bit, in its first call and in later ones of
+    another length."""
+    from gated_deltanet_chunked_delta_amd import (gated_group_norm, gdn_conv_fwd, gdn_conv_step, gdn_norm_fwd,
+                                                  gdn_scan_fwd, gdn_scan_step, selective_scan, short_conv)
+    g = torch.Generator(device=dev).manual_seed(8)
+    rn = lambda *s: torch.randn(*s, generator=g, device=dev)
+    A = -1 - rn(2).abs()
+    scan = lambda T: (rn(1, T, 2, 64), rn(1, T, 2), A, rn(1, T, 1, 64), rn(1, T, 1, 64))
+
+    def library(x, dt, A, B, C):
+        y, hT = gdn_scan_fwd(2 * x, dt, A, B, C, dt_softplus=True)
+        z, fin = gdn_conv_fwd(y.flatten(2), torch.ones(128, 4, device=dev))
+        return gdn_norm_fwd(z.view(x.shape), torch.ones(64, device=dev)), hT, fin
+
+    f, inputs = {
+        "conv": (lambda x, w: short_conv(2 * x, w, output_final_state=True), lambda T: (rn(1, T, 48), rn(48, 4))),
+        "scan": (lambda *a: selective_scan(2 * a[0], *a[1:], dt_softplus=True, output_final_state=True), scan),
+        "norm": (lambda x, w: (gated_group_norm(2 * x, w),), lambda T: (rn(T, 2, 64), rn(64))),
+        "conv_step": (lambda x, w, state: (gdn_conv_step(2 * x, state, w), state), lambda T: (rn(T, 48), rn(48, 4), rn(T, 3, 48))),
+        "scan_step": (lambda x, dt, A, B, C, state: (gdn_scan_step(2 * x, dt, A, B, C, state, dt_softplus=True), state),
+                      lambda T: (rn(T, 2, 64), rn(T, 2), A, rn(T, 1, 64), rn(T, 1, 64), rn(T, 2, 64, 64))),
+        "library": (library, scan),
+    }[name]
+    torch._dynamo.reset()
+    compiled = torch.compile(f, backend="eager")
+    trained = name in ("conv", "scan", "norm")
+    for T in (70, 70, 5, 133):
+        at, results = inputs(T), []
+        for call in (f, compiled):
+            leaves = [t.clone().requires_grad_(trained) for t in at]
+            out = list(call(*leaves))
+            results.append(out + (list(torch.autograd.grad(out, leaves, [torch.ones_like(t) for t in out])) if trained else []))
+        assert all(torch.equal(a, b) for a, b in zip(*results))

@@ -222,3 +222,28 @@ def test_modes_that_only_watch_are_no_tracers(stub):
     with FlopCounterMode(display=False):
         f(x)
     assert stub == ["gdn_conv_fwd"]
+
+
+@pytest.mark.parametrize("final", [False, True])
+@pytest.mark.parametrize("grad", [False, True])
+def test_compiled_functions_leave_their_graph_for_a_call(stub, final, grad):
+    """torch.compile cannot follow what fills a C structure in; the library gets it whole:
+    outputs of the right shapes, and the fields that are written after nesting."""
+    f = {"short_conv": lambda x: layers.short_conv(x, torch.ones(8, 4), output_final_state=final),
+         "selective_scan": lambda x: layers.selective_scan(
+             x, torch.ones(1, 6, 2), -torch.ones(2), torch.ones(1, 6, 1, 64), torch.ones(1, 6, 1, 64),
+             output_final_state=final, round_once=True)}
+    for name, call in f.items():
+        torch._dynamo.reset()
+        for T in (6, 6, 9) if name == "short_conv" else (6, 6):
+            x = torch.zeros(1, T, 8) if name == "short_conv" else torch.zeros(1, T, 2, 64)
+            out = torch.compile(lambda x: call(x.requires_grad_(grad)), backend="eager")(x)
+            y, state = out if final else (out, None)
+            a = stub.args.a
+            assert y.shape == x.shape and y.requires_grad == grad and stub.args.y
+            assert (a.B, a.T, a.num_seqs) == (1, T, 1) and a.x == x.data_ptr()
+            if name == "short_conv":
+                assert not final or (state.shape == (1, 3, 8) and stub.args.final_state)
+            else:
+                assert a.workspace and a.workspace_bytes == 256 and a.round_once == 1
+                assert not final or (state.shape == (1, 2, 64, 64) and stub.args.hT)
