@@ -10,7 +10,7 @@ from __future__ import annotations
 
 import torch
 
-from .binding import GDNError, _gradient, gdn_chunk_bwd, gdn_chunk_fwd, gdn_decode_step, lib  # noqa: F401
+from .binding import GDNError, _compiling, _gradient, _outside, gdn_chunk_bwd, gdn_chunk_fwd, gdn_decode_step, lib  # noqa: F401
 from .layers import (gated_group_norm, gdn_conv_bwd, gdn_conv_fwd, gdn_conv_step, gdn_norm_bwd,  # noqa: F401
                      gdn_norm_fwd, gdn_scan_bwd, gdn_scan_fwd, gdn_scan_step, selective_scan, short_conv)
 
@@ -61,6 +61,9 @@ def chunk_gated_delta_rule(q, k, v, g, beta, scale=None, initial_state=None, out
     softplus(g), beta = sigmoid(beta) inside the kernels (gate_scale is not
     differentiated).
     """
+    if _compiling():
+        return _outside(chunk_gated_delta_rule, q, k, v, g, beta, scale, initial_state, output_final_state,
+                        cu_seqlens, cu_seqlens_host, cp_mode, save_states, qk_norm, gate_act, gate_scale)
     if scale is None:
         scale = q.shape[-1] ** -0.5
     o, hT = _ChunkGatedDeltaRule.apply(q, k, v, g, beta, initial_state, float(scale), cu_seqlens,

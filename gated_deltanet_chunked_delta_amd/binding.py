@@ -206,6 +206,9 @@ def gdn_chunk_fwd(q, k, v, g, beta, scale: float, h0=None, cu_seqlens=None, cu_s
     k; gate and beta logits, see include/gdn.h).  o / hT: optional output tensors
     to write into (else allocated).  noalloc: call gdn_chunk_fwd_noalloc, which
     takes no workspace (the library's own scratch; see include/gdn.h)."""
+    if _compiling():
+        return _outside(gdn_chunk_fwd, q, k, v, g, beta, scale, h0, cu_seqlens, cu_seqlens_host, output_final_state,
+                        cp_mode, save_states, save_t, qk_norm, gate_act, gate_scale, o, hT, noalloc)
     a, keep = _common(q, k, v, g, beta, scale, h0, cu_seqlens, cu_seqlens_host, cp_mode,
                       qk_norm, gate_act, gate_scale)
     L = lib()
@@ -253,6 +256,9 @@ def gdn_chunk_bwd(q, k, v, g, beta, scale: float, do, h0=None, dhT=None, cu_seql
     (gdn_chunk_fwd(..., save_states=True / save_t=True)); what is given is not
     recomputed.  With qk_norm / gate_act the gradients are with respect to the raw
     inputs."""
+    if _compiling():
+        return _outside(gdn_chunk_bwd, q, k, v, g, beta, scale, do, h0, dhT, cu_seqlens, cu_seqlens_host, cp_mode,
+                        need_dh0, states, chunk_t, qk_norm, gate_act, gate_scale)
     a, keep = _common(q, k, v, g, beta, scale, h0, cu_seqlens, cu_seqlens_host, cp_mode,
                       qk_norm, gate_act, gate_scale)
     _contig("do", do, q.dtype, q.device)
@@ -290,6 +296,8 @@ def gdn_decode_step(q, k, v, g, beta, scale: float, state, state_idx=None, o=Non
     """One recurrent step for N sequences: q, k [N, H, Dk], v [N, H, Dv], g, beta [N, H];
     state [S, H, Dk, Dv] fp32 is updated in place (sequence n uses slot n, or state_idx[n]
     when given; out-of-range indices mark padding).  Returns o [N, H, Dv]."""
+    if _compiling():
+        return _outside(gdn_decode_step, q, k, v, g, beta, scale, state, state_idx, o, qk_norm, gate_act, gate_scale)
     dev = q.device
     dt = q.dtype
     for name, t, d in (("q", q, dt), ("k", k, dt), ("v", v, dt), ("beta", beta, dt),

@@ -183,3 +183,26 @@ def test_inside_a_compiled_function(dev, name):
             out = list(call(*leaves))
             results.append(out + (list(torch.autograd.grad(out, leaves, [torch.ones_like(t) for t in out])) if trained else []))
         assert all(torch.equal(a, b) for a, b in zip(*results))
+
+
+def test_chunk_rule_inside_a_compiled_function(dev):
+    from gated_deltanet_chunked_delta_amd import chunk_gated_delta_rule, gdn_decode_step
+    g = torch.Generator(device=dev).manual_seed(9)
+    rn = lambda *s: torch.randn(*s, generator=g, device=dev)
+
+    def f(q, k, v, g, beta):
+        with torch.no_grad():
+            state = torch.zeros(1, 2, 64, 64, device=dev)
+            step = gdn_decode_step(*(t[:, 0].contiguous() for t in (q, k, v, g, beta)), 0.125, state)
+        return chunk_gated_delta_rule(q, 2 * k, v, g, beta, qk_norm=True, output_final_state=True) + (step, state)
+
+    torch._dynamo.reset()
+    compiled = torch.compile(f, backend="eager")
+    for T in (70, 70, 5, 133):
+        inputs = (rn(1, T, 2, 64).to(BF), rn(1, T, 2, 64).to(BF), rn(1, T, 2, 64).to(BF), -rn(1, T, 2).abs(), rn(1, T, 2).to(BF))
+        results = []
+        for call in (f, compiled):
+            leaves = [t.clone().requires_grad_(True) for t in inputs]
+            out = list(call(*leaves))
+            results.append(out + list(torch.autograd.grad(out[:2], leaves, [torch.ones_like(t) for t in out[:2]])))
+        assert all(torch.equal(a, b) for a, b in zip(*results))
