@@ -1,0 +1,116 @@
+// gdn_block.h -- parameter blocks and launchers of a block's operators: residual
+// norm, rows in 8 bits, projections, gated linear recurrence (not part of the ABI).
+#pragma once
+#include <hip/hip_runtime.h>
+#include <stdint.h>
+
+#include <algorithm>
+
+#include "gdn.h"
+#include "gdn_device.h"
+#include "gdn_internal.h"
+#include "layer/gdn_layer.h"
+
+namespace gdn {
+
+// ---------------------------------------------------------------- rows of any width
+// Vectors aligned to an element only: rows of odd widths and slices start anywhere.
+// The memory takes such accesses (a line more for some of them), so one path of full
+// width serves every width, with single elements at a row's end alone.
+typedef bf16x8 bf16x8_any __attribute__((aligned(2)));
+typedef bf16x4 bf16x4_any __attribute__((aligned(2)));
+typedef f32x4 f32x4_any __attribute__((aligned(4)));
+
+template <int V> __device__ __forceinline__ void ld_full(const bf16* p, float (&f)[V]) {
+  if constexpr (V == 8) {
+    const bf16x8 v = *reinterpret_cast<const bf16x8_any*>(p);
+#pragma unroll
+    for (int i = 0; i < 8; ++i) f[i] = (float)v[i];
+  } else {
+    const bf16x4 v = *reinterpret_cast<const bf16x4_any*>(p);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = (float)v[i];
+  }
+}
+template <int V> __device__ __forceinline__ void ld_full(const float* p, float (&f)[V]) {
+#pragma unroll
+  for (int j = 0; j < V / 4; ++j) {
+    const f32x4 v = reinterpret_cast<const f32x4_any*>(p)[j];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[4 * j + i] = v[i];
+  }
+}
+// V elements at p of which n belong to the row (the rest: 0).
+template <int V, class E>
+__device__ __forceinline__ void ld_part(const E* p, int n, float (&f)[V]) {
+  if (n >= V) {
+    ld_full<V>(p, f);
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i) f[i] = i < n ? to_f(p[i]) : 0.f;
+  }
+}
+template <int V, class E>
+__device__ __forceinline__ void st_part(E* p, int n, const float (&f)[V]) {
+  if (n >= V) {
+    if constexpr (sizeof(E) == 2) {
+      if constexpr (V == 8)
+        __builtin_nontemporal_store(VecIO<bf16, 8>::pack(f), reinterpret_cast<bf16x8_any*>(p));
+      else
+        __builtin_nontemporal_store(VecIO<bf16, 4>::pack(f), reinterpret_cast<bf16x4_any*>(p));
+    } else {
+#pragma unroll
+      for (int j = 0; j < V / 4; ++j)
+        __builtin_nontemporal_store(f32x4{f[4 * j], f[4 * j + 1], f[4 * j + 2], f[4 * j + 3]},
+                                    reinterpret_cast<f32x4_any*>(p) + j);
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < V; ++i)
+      if (i < n) p[i] = to_e<E>(f[i]);
+  }
+}
+
+// A launch has fewer than 2^32 threads in x: more workgroups go on in y.
+inline dim3 blocks_2d(int64_t n) {
+  constexpr int64_t most = 1 << 22;
+  return n <= most ? dim3((uint32_t)n) : dim3((uint32_t)most, (uint32_t)((n + most - 1) / most));
+}
+__device__ __forceinline__ int64_t block_2d() { return blockIdx.y * (int64_t)gridDim.x + blockIdx.x; }
+
+// ---------------------------------------------------------------- residual norm, rows in 8 bits
+struct AddNormParams {
+  const void* x;             // [R][D], x_stride elements between rows
+  int64_t x_stride;
+  const void* r;             // nullable, r_stride
+  int64_t r_stride;
+  const void* w;             // [D]
+  void* s;                   // [R][D], with r
+  void* y;                   // nullable [R][D]
+  uint8_t* q;                // nullable [R][D]
+  float* q_scale;            // [R]
+  int64_t R;
+  int D;
+  float eps;
+  // backward
+  const void* dy;
+  const void* ds;            // nullable
+  void* dx;                  // nullable
+  void* dr;                  // nullable
+  void* dw;                  // nullable
+  float* part;               // [blocks][D]
+  int blocks;
+};
+// One fp32 sum takes at most these many rows' terms of the weight's gradient.
+constexpr int ADDNORM_ROWS = 64;
+// Workgroups (rows of parts) of the gradient.
+int addnorm_blocks(int64_t R, int D, int esize, int cus);
+hipError_t launch_addnorm_fwd(int dtype, int res_dtype, const AddNormParams& p, hipStream_t st);
+hipError_t launch_addnorm_bwd(int dtype, int res_dtype, const AddNormParams& p, hipStream_t st);
+hipError_t launch_quant_rows(int dtype, const AddNormParams& p, hipStream_t st);
+
+// ---------------------------------------------------------------- sums of parts
+// out[c] = sum over rows of part[row][c], in 64 bits and a fixed order, rounded once.
+hipError_t launch_join_parts(int dtype, const float* part, int64_t rows, int64_t cols, void* out, hipStream_t st);
+
+}  // namespace gdn

@@ -478,6 +478,73 @@ gdn_status gdn_norm_fwd(const gdn_norm_fwd_args* args, void* stream);
 size_t gdn_norm_bwd_workspace_size(const gdn_norm_bwd_args* args);
 gdn_status gdn_norm_bwd(const gdn_norm_bwd_args* args, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Operators of a block around its mixer: the residual norm in front of it, the
+ * projections into and out of it (bf16, fp32, or 8 bits with scales), and the
+ * channelwise member of the recurrences' family.  The rules of the operators
+ * around the recurrence hold here too (dtype, ownership, streams, errors, token
+ * strides); these operators need no alignment beyond an element's own.
+ *
+ * 8 bits: e4m3 (OCP, largest value 448) with one fp32 scale a row.  Of a row v
+ * with top = max(max |v|, 2^-100):  scale = top / 448,  q = e4m3(448 v / top), rounded
+ * once, ties to even; the row stands for q * scale.  A row that holds an infinity or a
+ * NaN holds NaN in q (all of it, or where the NaN is). */
+
+/* Residual norm over rows of D channels:
+ *     s = x + r  (rounded to r's type; x itself without r),   y = s / sqrt(mean(s^2) + eps) w
+ * The norm reads s as it is stored, so that the backward pass and whatever reads
+ * the stream later see the same values.  r is in x's type or fp32.  Either y or
+ * (q, q_scale) is written.  R below 2^31. */
+typedef struct {
+  int32_t dtype;               /* of x, w, y (dy, dx, dw) */
+  int32_t res_dtype;           /* of r and s (ds, dr): GDN_F32 or dtype; dtype without r */
+  int64_t R;
+  int32_t D;
+  float eps;                   /* > 0 */
+  const void* x;               /* [R, D] */
+  int64_t x_stride;
+  const void* r;               /* nullable [R, D] */
+  int64_t r_stride;
+  const void* w;               /* [D] */
+  void* s;                     /* [R, D], written; needed with r */
+  void* y;                     /* nullable [R, D], written */
+  void* q;                     /* nullable [R, D] e4m3, written */
+  float* q_scale;              /* [R], written; needed with q */
+} gdn_addnorm_fwd_args;
+
+/* Gradient of x and r alike: dv = (dy w - n mean(dy w n)) / sqrt(mean(s^2) + eps) + ds, n = s / sqrt(...) */
+typedef struct {
+  int32_t dtype, res_dtype;
+  int64_t R;
+  int32_t D;
+  float eps;
+  const void* s;               /* [R, D] of res_dtype: the sum, or x (then res_dtype is dtype) */
+  int64_t s_stride;
+  const void* w;
+  const void* dy;              /* [R, D] */
+  const void* ds;              /* nullable [R, D] of res_dtype */
+  void* dx;                    /* nullable [R, D] of dtype, written */
+  void* dr;                    /* nullable [R, D] of res_dtype, written */
+  void* dw;                    /* nullable [D], written */
+  void* workspace;             /* gdn_addnorm_bwd_workspace_size bytes, 16-byte aligned */
+  size_t workspace_bytes;
+} gdn_addnorm_bwd_args;
+
+typedef struct {
+  int32_t dtype;               /* of x */
+  int64_t R;
+  int32_t D;
+  const void* x;               /* [R, D] */
+  int64_t x_stride;
+  void* q;                     /* [R, D] e4m3, written */
+  float* q_scale;              /* [R], written */
+} gdn_quant_args;
+
+gdn_status gdn_addnorm_fwd(const gdn_addnorm_fwd_args* args, void* stream);
+size_t gdn_addnorm_bwd_workspace_size(const gdn_addnorm_bwd_args* args);
+gdn_status gdn_addnorm_bwd(const gdn_addnorm_bwd_args* args, void* stream);
+gdn_status gdn_quant_rows(const gdn_quant_args* args, void* stream);
+
 /* Per-kernel timing, for benchmarks (off by default).  While enabled, every
  * kernel the library launches is bracketed by a pair of HIP events recorded on
  * the call's stream.  gdn_profile_read waits for the recorded events, adds
