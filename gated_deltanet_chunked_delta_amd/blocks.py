@@ -19,9 +19,9 @@ from torch.autograd.function import once_differentiable
 
 from . import layers as _layers
 from .binding import GDNError, _compiling, _dtype_code, _outside, _ptr, _vp, lib as _load
-from .layers import (_as_one_op, _call, _no_derivative, _on, _past_32_bits, _rows, _t, _wants_grad, _workspace)
+from .layers import (_as_one_op, _call, _no_derivative, _on, _own_lengths, _past_32_bits, _rows, _rows_like, _seqs, _t, _wants_grad, _workspace)
 
-__all__ = ["add_rms_norm", "add_rms_norm_8bit", "quantize_rows"]
+__all__ = ["add_rms_norm", "add_rms_norm_8bit", "quantize_rows", "gated_recurrence", "gdn_rec_step"]
 
 _i32, _i64, _sz, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 
@@ -42,8 +42,31 @@ class QuantArgs(ctypes.Structure):
     _fields_ = [("dtype", _i32), ("R", _i64), ("D", _i32), ("x", _vp), ("x_stride", _i64), ("q", _vp), ("q_scale", _vp)]
 
 
-_SIGNATURES = [("gdn_addnorm_fwd", AddNormFwdArgs), ("gdn_addnorm_bwd", AddNormBwdArgs), ("gdn_quant_rows", QuantArgs)]
-_SIZES = [("gdn_addnorm_bwd_workspace_size", AddNormBwdArgs)]
+class RecArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("g_dtype", _i32), ("B", _i32), ("T", _i32), ("D", _i32), ("x", _vp), ("x_stride", _i64),
+                ("g", _vp), ("g_stride", _i64), ("i", _vp), ("i_stride", _i64), ("scale", _vp), ("h0", _vp),
+                ("cu_seqlens", _vp), ("num_seqs", _i32), ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class RecFwdArgs(ctypes.Structure):
+    _fields_ = [("a", RecArgs), ("y", _vp), ("hT", _vp), ("h_save", _vp)]
+
+
+class RecBwdArgs(ctypes.Structure):
+    _fields_ = [("a", RecArgs), ("h_saved", _vp), ("dy", _vp), ("dhT", _vp), ("dx", _vp), ("dg", _vp), ("di", _vp),
+                ("dscale", _vp), ("dh0", _vp)]
+
+
+class RecStepArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("g_dtype", _i32), ("N", _i32), ("D", _i32), ("x", _vp), ("x_stride", _i64), ("g", _vp),
+                ("g_stride", _i64), ("i", _vp), ("i_stride", _i64), ("scale", _vp), ("state", _vp), ("state_idx", _vp),
+                ("num_slots", _i32), ("y", _vp)]
+
+
+_SIGNATURES = [("gdn_addnorm_fwd", AddNormFwdArgs), ("gdn_addnorm_bwd", AddNormBwdArgs), ("gdn_quant_rows", QuantArgs),
+               ("gdn_rec_fwd", RecFwdArgs), ("gdn_rec_bwd", RecBwdArgs), ("gdn_rec_step", RecStepArgs)]
+_SIZES = [("gdn_addnorm_bwd_workspace_size", AddNormBwdArgs), ("gdn_rec_fwd_workspace_size", RecFwdArgs),
+          ("gdn_rec_bwd_workspace_size", RecBwdArgs), ("gdn_rec_states_bytes", RecArgs)]
 _lib = None
 
 
@@ -220,3 +243,159 @@ def quantize_rows(x):
     a.q, a.q_scale = q.data_ptr(), scale.data_ptr()
     _call(lib().gdn_quant_rows, a, x.device)
     return q, scale
+
+
+# ------------------------------------------------------------------ gated linear recurrence
+def _gate_dtype(x, g):
+    if g.dtype not in (x.dtype, torch.float32):
+        raise GDNError(f"g must be {x.dtype} or float32, got {g.dtype}")
+    return g.dtype
+
+
+def _rec_args(x, g, i, scale, h0, cu_seqlens, cu_seqlens_host):
+    if x.dim() != 3:
+        raise GDNError("x must be [B, T, D]")
+    B, T, D = x.shape
+    if (B | T | D) >> 31:
+        _past_32_bits()
+    dt, dev = x.dtype, x.device
+    a = RecArgs()
+    a.dtype, a.x_stride = _dtype_code(x), _rows("x", x, (B, T, D), 1, dt, dev)
+    gdt = _gate_dtype(x, g)
+    a.g_dtype, a.g_stride = _dtype_code(g), _rows("g", g, (B, T, D), 1, gdt, dev)
+    a.i_stride = 0 if i is None else _rows("i", i, (B, T, D), 1, dt, dev)
+    _t("scale", scale, (D,), torch.float32, dev, optional=True)
+    cu, host, n = _seqs(cu_seqlens, cu_seqlens_host, B, T, dev, need_host=False)
+    _t("initial_state", h0, (n, D), torch.float32, dev, optional=True)
+    a.B, a.T, a.D, a.num_seqs = B, T, D, n
+    a.x, a.g, a.i, a.scale, a.h0, a.cu_seqlens = map(_ptr, (x, g, i, scale, h0, cu))
+    _on_gpu("x", x)
+    return a, cu is not None and host is None
+
+
+def gdn_rec_fwd(x, g, i=None, scale=None, h0=None, cu_seqlens=None, cu_seqlens_host=None,
+                output_final_state: bool = True, save_states: bool = False):
+    """(y, hT) with hT None unless output_final_state, followed by the chunks' states if
+    save_states (a flat fp32 tensor for gdn_rec_bwd)."""
+    if _compiling():
+        return _outside(gdn_rec_fwd, x, g, i, scale, h0, cu_seqlens, cu_seqlens_host, output_final_state, save_states)
+    a, unchecked = _rec_args(x, g, i, scale, h0, cu_seqlens, cu_seqlens_host)
+    dev, L = x.device, lib()
+    args = RecFwdArgs()
+    y = _rows_like(x, unchecked)
+    hT = torch.empty((a.num_seqs, a.D), dtype=torch.float32, device=dev) if output_final_state else None
+    args.a, args.y, args.hT = a, y.data_ptr(), _ptr(hT)
+    states = None
+    with _on(dev):
+        if save_states:
+            states = torch.empty(L.gdn_rec_states_bytes(ctypes.byref(a)) // 4, dtype=torch.float32, device=dev)
+            args.h_save = states.data_ptr()
+        ws = _workspace(L.gdn_rec_fwd_workspace_size(ctypes.byref(args)), dev)
+    args.a.workspace, args.a.workspace_bytes = ws.data_ptr(), ws.numel()
+    _call(L.gdn_rec_fwd, args, dev)
+    return (y, hT, states) if save_states else (y, hT)
+
+
+def gdn_rec_bwd(x, g, dy, i=None, scale=None, h0=None, dhT=None, cu_seqlens=None, cu_seqlens_host=None, states=None):
+    """(dx, dg, di, dscale, dh0); the last three are None where their inputs are.  states:
+    gdn_rec_fwd(..., save_states=True) on the same inputs."""
+    if _compiling():
+        return _outside(gdn_rec_bwd, x, g, dy, i, scale, h0, dhT, cu_seqlens, cu_seqlens_host, states)
+    a, unchecked = _rec_args(x, g, i, scale, h0, cu_seqlens, cu_seqlens_host)
+    dev, L = x.device, lib()
+    _t("dy", dy, x.shape, x.dtype, dev)
+    _t("dhT", dhT, (a.num_seqs, a.D), torch.float32, dev, optional=True)
+    args = RecBwdArgs()
+    dx, dg = _rows_like(x, unchecked), _rows_like(g, unchecked)
+    di = None if i is None else _rows_like(i, unchecked)
+    ds, dh0 = (None if t is None else torch.empty_like(t) for t in (scale, h0))
+    args.a = a
+    args.dy, args.dhT, args.dx, args.dg, args.di, args.dscale, args.dh0 = map(_ptr, (dy, dhT, dx, dg, di, ds, dh0))
+    with _on(dev):
+        if states is not None:
+            _t("states", states, states.shape, torch.float32, dev)
+            if states.numel() * 4 != L.gdn_rec_states_bytes(ctypes.byref(a)):
+                raise GDNError("states are not those of a forward pass with these arguments")
+            args.h_saved = states.data_ptr()
+        ws = _workspace(L.gdn_rec_bwd_workspace_size(ctypes.byref(args)), dev)
+    args.a.workspace, args.a.workspace_bytes = ws.data_ptr(), ws.numel()
+    _call(L.gdn_rec_bwd, args, dev)
+    return dx, dg, di, ds, dh0
+
+
+class _GatedRecurrence(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, g, i, scale, h0, cu_seqlens, cu_seqlens_host, final):
+        with _as_one_op():
+            y, hT, states = gdn_rec_fwd(x, g, i, scale, h0, cu_seqlens, cu_seqlens_host, final, save_states=True)
+        ctx.save_for_backward(x, g, i, scale, h0, cu_seqlens, states)
+        ctx.cu_host = _own_lengths(cu_seqlens_host)
+        ctx.set_materialize_grads(False)
+        return y, hT
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy, dhT):
+        x, g, i, scale, h0, cu, states = ctx.saved_tensors
+        if dy is None:
+            if dhT is None:
+                return (None,) * 8
+            dy = torch.zeros(x.shape, dtype=x.dtype, device=x.device)
+        dx, dg, di, ds, dh0 = gdn_rec_bwd(x, g, dy.contiguous(), i, scale, h0,
+                                          None if dhT is None else dhT.contiguous(), cu, ctx.cu_host, states)
+        return dx, dg, di, ds, dh0, None, None, None
+
+
+def gated_recurrence(x, g, i=None, scale=None, initial_state=None, output_final_state: bool = False, cu_seqlens=None,
+                     cu_seqlens_host=None):
+    """Gated linear recurrence over x [B, T, D], channel by channel, differentiable in every
+    tensor argument:
+
+        h_t = exp(L_t) h_{t-1} + m_t sigmoid(i_t) x_t,   y_t = h_t
+        L_t = g_t, m_t = 1;   with scale:  L_t = -scale sigmoid(g_t), m_t = sqrt(1 - exp(2 L_t))
+
+    g [B, T, D] is in x's dtype or fp32: log decays (<= 0), or logits with scale [D] (fp32, >= 0);
+    i [B, T, D], when given, are logits of the input's gate.  States [N, D] are fp32.  Returns y, or
+    (y, hT).  cu_seqlens (int32, B = 1) packs sequences; cu_seqlens_host, when given, is checked
+    against T."""
+    if _compiling():
+        return _outside(gated_recurrence, x, g, i, scale, initial_state, output_final_state, cu_seqlens, cu_seqlens_host)
+    if _wants_grad(x, g, i, scale, initial_state):
+        y, hT = _GatedRecurrence.apply(x, g, i, scale, initial_state, cu_seqlens, cu_seqlens_host,
+                                       bool(output_final_state))
+    else:
+        y, hT = gdn_rec_fwd(x, g, i, scale, initial_state, cu_seqlens, cu_seqlens_host, output_final_state)
+    return (y, hT) if output_final_state else y
+
+
+def gdn_rec_step(x, g, state, i=None, scale=None, state_idx=None, y=None):
+    """One token for each of N sequences: x, g, i [N, D] (as gated_recurrence); state [S, D] fp32 is
+    advanced in place (slots as in gdn_decode_step: sequence n uses slot n, or state_idx[n];
+    out-of-range indices mark padding, whose y is left as it was; no two sequences of a call
+    share a slot).  Returns y [N, D]."""
+    if _compiling():
+        return _outside(gdn_rec_step, x, g, state, i, scale, state_idx, y)
+    if x.dim() != 2:
+        raise GDNError("x must be [N, D]")
+    _no_derivative("gdn_rec_step", (x, g, state, i, scale))
+    N, D = x.shape
+    slots = state.shape[0]
+    if (N | D | slots) >> 31:
+        _past_32_bits()
+    dt, dev = x.dtype, x.device
+    code = _dtype_code(x)
+    xs = _rows("x", x, (N, D), 1, dt, dev)
+    gs = _rows("g", g, (N, D), 1, _gate_dtype(x, g), dev)
+    ist = 0 if i is None else _rows("i", i, (N, D), 1, dt, dev)
+    _t("scale", scale, (D,), torch.float32, dev, optional=True)
+    _t("state", state, (slots, D), torch.float32, dev)
+    _t("state_idx", state_idx, (N,), torch.int32, dev, optional=True)
+    _on_gpu("x", x)
+    if y is None:
+        y = x.new_empty((N, D))
+    else:
+        _t("y", y, (N, D), dt, dev)
+    a = RecStepArgs(code, _dtype_code(g), N, D, x.data_ptr(), xs, g.data_ptr(), gs, _ptr(i), ist, _ptr(scale),
+                    state.data_ptr(), _ptr(state_idx), slots, y.data_ptr())
+    _call(lib().gdn_rec_step, a, dev)
+    return y

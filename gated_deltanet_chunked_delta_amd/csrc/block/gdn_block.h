@@ -21,6 +21,11 @@ typedef bf16x8 bf16x8_any __attribute__((aligned(2)));
 typedef bf16x4 bf16x4_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
+typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
+typedef bf16x2 bf16x2_any __attribute__((aligned(2)));
+typedef __attribute__((__vector_size__(2 * sizeof(float)))) float f32x2;
+typedef f32x2 f32x2_any __attribute__((aligned(4)));
+
 template <int V> __device__ __forceinline__ void ld_full(const bf16* p, float (&f)[V]) {
   if constexpr (V == 8) {
     const bf16x8 v = *reinterpret_cast<const bf16x8_any*>(p);
@@ -108,6 +113,52 @@ int addnorm_blocks(int64_t R, int D, int esize, int cus);
 hipError_t launch_addnorm_fwd(int dtype, int res_dtype, const AddNormParams& p, hipStream_t st);
 hipError_t launch_addnorm_bwd(int dtype, int res_dtype, const AddNormParams& p, hipStream_t st);
 hipError_t launch_quant_rows(int dtype, const AddNormParams& p, hipStream_t st);
+
+// ---------------------------------------------------------------- gated linear recurrence
+struct RecParams {
+  const void* x;             // [tokens][D], *_stride elements between tokens
+  const void* g;
+  const void* i;             // nullable
+  int64_t x_stride, g_stride, i_stride;
+  int g_f32;
+  const float* scale;        // nullable [D]
+  const float* h0;           // nullable [N][D]
+  const int32_t* cu;         // nullable [N+1]
+  int T, D, N, tokens;
+  int chunk, nchunk;         // tokens of a chunk (REC_SUB times 1, 2, 4 or 8)
+  float2* sum;               // [nchunk][D]: what a chunk makes of the state entering it
+  float* enter;              // [nchunk][D]: that state
+  // forward
+  void* y;
+  float* hT;                 // nullable [N][D]
+  // backward
+  const void* dy;
+  const float* dhT;          // nullable
+  float* carry;              // [nchunk][D]: gradient of the state leaving a chunk, from the tokens behind it
+  void* dx;
+  void* dg;
+  void* di;                  // nullable
+  float* dh0;                // nullable
+  float* part;               // nullable [nchunk][D]: dscale's parts
+};
+struct RecStepParams {
+  const void* x;
+  const void* g;
+  const void* i;
+  int64_t x_stride, g_stride, i_stride;
+  int g_f32;
+  const float* scale;
+  float* state;
+  const int32_t* state_idx;
+  int num_slots, N, D;
+  void* y;
+};
+constexpr int REC_SUB = 16;  // tokens that a thread of the gradient holds
+hipError_t launch_rec_sum(int dtype, const RecParams& p, bool rev, hipStream_t st);   // chunks -> sum
+hipError_t launch_rec_join(const RecParams& p, bool rev, hipStream_t st);             // sum -> enter or carry
+hipError_t launch_rec_fwd(int dtype, const RecParams& p, hipStream_t st);
+hipError_t launch_rec_bwd(int dtype, const RecParams& p, hipStream_t st);
+hipError_t launch_rec_step(int dtype, const RecStepParams& p, hipStream_t st);
 
 // ---------------------------------------------------------------- sums of parts
 // out[c] = sum over rows of part[row][c], in 64 bits and a fixed order, rounded once.

@@ -40,6 +40,83 @@ gdn_status check_addnorm_bwd(const gdn_addnorm_bwd_args& a) {
 }
 int norm_blocks(const gdn_addnorm_bwd_args& a) { return gdn::addnorm_blocks(a.R, a.D, (int)esize(a.dtype), cu_count()); }
 
+// ---------------------------------------------------------------- gated linear recurrence
+bool launchable(double threads) { return threads < 4294967296. - 512.; }
+
+gdn_status check_rec(const gdn_rec_args& a) {
+  if (!known_dtype(a.dtype)) return fail(GDN_E_UNSUPPORTED, "unknown dtype %d", a.dtype);
+  if (a.g_dtype != a.dtype && a.g_dtype != GDN_F32)
+    return fail(GDN_E_UNSUPPORTED, "g_dtype %d: g is in x's type or fp32", a.g_dtype);
+  if (a.B < 1 || a.T < 0 || a.D < 1) return fail(GDN_E_INVALID, "bad sizes B=%d T=%d D=%d", a.B, a.T, a.D);
+  const long long tokens = (long long)a.B * a.T;
+  if (tokens >= std::min((1LL << 40) / a.D, (1LL << 31) - 1024) || a.D >= (1 << 24)) return fail(GDN_E_INVALID, "problem too large");
+  if (a.cu_seqlens) {
+    if (a.B != 1) return fail(GDN_E_INVALID, "cu_seqlens requires B == 1 (got %d)", a.B);
+    if (a.num_seqs < 1) return fail(GDN_E_INVALID, "num_seqs must be >= 1 with cu_seqlens");
+    if (!aligned(a.cu_seqlens, 4)) return fail(GDN_E_INVALID, "cu_seqlens misaligned");
+  } else if (a.num_seqs != a.B) {
+    return fail(GDN_E_INVALID, "num_seqs (%d) must equal B (%d) without cu_seqlens", a.num_seqs, a.B);
+  }
+  if (tokens > 0 && (!a.x || !a.g)) return fail(GDN_E_INVALID, "null input pointer");
+  if (a.x_stride < a.D || a.g_stride < a.D || (a.i && a.i_stride < a.D))
+    return fail(GDN_E_INVALID, "a token stride is below D = %d", a.D);
+  const size_t es = esize(a.dtype);
+  if (!aligned(a.x, es) || !aligned(a.i, es) || !aligned(a.g, esize(a.g_dtype)) || !aligned(a.scale, 4) || !aligned(a.h0, 4))
+    return fail(GDN_E_INVALID, "a pointer is misaligned");
+  return GDN_OK;
+}
+// Tokens of a chunk: long chunks leave fewer states, short ones more waves.  The
+// longest that still gives every compute unit sixteen waves.
+int rec_chunk(const gdn_rec_args& a) {
+  const int64_t tokens = (int64_t)a.B * a.T, per = 64 * 4 / (int64_t)esize(a.dtype), wide = (a.D + per - 1) / per;
+  int c = gdn::REC_SUB;
+  while (c < 8 * gdn::REC_SUB && (tokens + 2 * c - 1) / (2 * c) * wide >= 16ll * cu_count()) c *= 2;
+  return c;
+}
+struct RecPlan {
+  int chunk, nchunk;
+  size_t o_sum = 0, o_enter = 0, o_carry = 0, o_part = 0, total = 0;
+};
+RecPlan rec_plan(const gdn_rec_args& a, bool bwd, bool own_states) {
+  RecPlan p;
+  p.chunk = rec_chunk(a);
+  p.nchunk = (int)(((int64_t)a.B * a.T + p.chunk - 1) / p.chunk);
+  size_t off = 0;
+  auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes); return o; };
+  const size_t rows = (size_t)p.nchunk * a.D;
+  p.o_sum = take(8 * rows);
+  if (own_states) p.o_enter = take(4 * rows);
+  if (bwd) {
+    p.o_carry = take(4 * rows);
+    if (a.scale) p.o_part = take(4 * rows);
+  }
+  p.total = std::max<size_t>(off, 16);
+  return p;
+}
+gdn_status check_rec_grid(const gdn_rec_args& a, const RecPlan& pl) {
+  const double per = 64. * 4 / esize(a.dtype);
+  if (!launchable(((double)pl.nchunk + a.num_seqs) * std::ceil(a.D / per) * 4 * pl.chunk))
+    return fail(GDN_E_INVALID, "problem too large: %d chunks and %d sequences of %d channels", pl.nchunk, a.num_seqs, a.D);
+  return GDN_OK;
+}
+gdn::RecParams rec_params(const gdn_rec_args& a, const RecPlan& pl) {
+  gdn::RecParams p{};
+  p.x = a.x; p.g = a.g; p.i = a.i; p.x_stride = a.x_stride; p.g_stride = a.g_stride; p.i_stride = a.i_stride;
+  p.g_f32 = a.g_dtype == GDN_F32; p.scale = a.scale; p.h0 = a.h0; p.cu = a.cu_seqlens;
+  p.T = a.T; p.D = a.D; p.N = a.num_seqs; p.tokens = a.B * a.T; p.chunk = pl.chunk; p.nchunk = pl.nchunk;
+  p.sum = at<float2>(a.workspace, pl.o_sum);
+  return p;
+}
+// States entering the chunks (rev: gradients leaving them).  One chunk starts with its
+// sequences: nothing enters it.
+gdn_status rec_states(const gdn_rec_args& a, const gdn::RecParams& p, bool rev, hipStream_t s) {
+  if (p.nchunk <= 1) return GDN_OK;
+  hipError_t e = timed(rev ? "rec_rev_sum" : "rec_sum", s, [&] { return gdn::launch_rec_sum(a.dtype, p, rev, s); });
+  if (e != hipSuccess) return hip_fail(e, "recurrence chunk launch");
+  e = timed("rec_join", s, [&] { return gdn::launch_rec_join(p, rev, s); });
+  return e == hipSuccess ? GDN_OK : hip_fail(e, "recurrence join launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -111,6 +188,102 @@ gdn_status gdn_quant_rows(const gdn_quant_args* args, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = timed("quant_rows", s, [&] { return gdn::launch_quant_rows(a.dtype, p, s); });
   return e == hipSuccess ? GDN_OK : hip_fail(e, "row quantisation launch");
+}
+
+size_t gdn_rec_fwd_workspace_size(const gdn_rec_fwd_args* args) {
+  if (!args) { fail(GDN_E_INVALID, "null args"); return 0; }
+  if (check_rec(args->a) != GDN_OK) return 0;
+  return rec_plan(args->a, false, !args->h_save).total;
+}
+size_t gdn_rec_bwd_workspace_size(const gdn_rec_bwd_args* args) {
+  if (!args) { fail(GDN_E_INVALID, "null args"); return 0; }
+  if (check_rec(args->a) != GDN_OK) return 0;
+  return rec_plan(args->a, true, !args->h_saved).total;
+}
+size_t gdn_rec_states_bytes(const gdn_rec_args* a) {
+  if (!a) { fail(GDN_E_INVALID, "null args"); return 0; }
+  if (check_rec(*a) != GDN_OK) return 0;
+  return std::max<size_t>(16, 4 * (size_t)rec_plan(*a, false, false).nchunk * a->D);
+}
+
+gdn_status gdn_rec_fwd(const gdn_rec_fwd_args* args, void* stream) {
+  if (!args) return fail(GDN_E_INVALID, "null args");
+  const gdn_rec_args& a = args->a;
+  if (gdn_status st = check_rec(a); st != GDN_OK) return st;
+  if ((long long)a.B * a.T > 0 && !args->y) return fail(GDN_E_INVALID, "null output y");
+  if (!aligned(args->y, esize(a.dtype)) || !aligned(args->hT, 4) || !aligned(args->h_save, 4))
+    return fail(GDN_E_INVALID, "a pointer is misaligned");
+  const RecPlan pl = rec_plan(a, false, !args->h_save);
+  if (gdn_status st = check_rec_grid(a, pl); st != GDN_OK) return st;
+  if (gdn_status st = check_ws(a.workspace, a.workspace_bytes, pl.total); st != GDN_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  gdn::RecParams p = rec_params(a, pl);
+  p.enter = args->h_save ? args->h_save : at<float>(a.workspace, pl.o_enter);
+  p.y = args->y;
+  p.hT = args->hT;
+  if (gdn_status st = rec_states(a, p, false, s); st != GDN_OK) return st;
+  hipError_t e = timed("rec_fwd", s, [&] { return gdn::launch_rec_fwd(a.dtype, p, s); });
+  return e == hipSuccess ? GDN_OK : hip_fail(e, "recurrence launch");
+}
+
+gdn_status gdn_rec_bwd(const gdn_rec_bwd_args* args, void* stream) {
+  if (!args) return fail(GDN_E_INVALID, "null args");
+  const gdn_rec_args& a = args->a;
+  if (gdn_status st = check_rec(a); st != GDN_OK) return st;
+  if ((long long)a.B * a.T > 0 && (!args->dy || !args->dx || !args->dg || (a.i && !args->di)))
+    return fail(GDN_E_INVALID, "null gradient pointer");
+  if (a.scale && !args->dscale) return fail(GDN_E_INVALID, "null gradient pointer");
+  const size_t es = esize(a.dtype);
+  if (!aligned(args->dy, es) || !aligned(args->dx, es) || !aligned(args->di, es) || !aligned(args->dg, esize(a.g_dtype)) ||
+      !aligned(args->dscale, 4) || !aligned(args->dh0, 4) || !aligned(args->dhT, 4) || !aligned(args->h_saved, 4))
+    return fail(GDN_E_INVALID, "a gradient pointer is misaligned");
+  const RecPlan pl = rec_plan(a, true, !args->h_saved);
+  if (gdn_status st = check_rec_grid(a, pl); st != GDN_OK) return st;
+  if (gdn_status st = check_ws(a.workspace, a.workspace_bytes, pl.total); st != GDN_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  gdn::RecParams p = rec_params(a, pl);
+  p.dy = args->dy; p.dhT = args->dhT; p.dx = args->dx; p.dg = args->dg; p.di = args->di; p.dh0 = args->dh0;
+  p.carry = at<float>(a.workspace, pl.o_carry);
+  p.part = a.scale ? at<float>(a.workspace, pl.o_part) : nullptr;
+  if (args->h_saved) {
+    p.enter = const_cast<float*>(args->h_saved);
+  } else {
+    p.enter = at<float>(a.workspace, pl.o_enter);
+    if (gdn_status st = rec_states(a, p, false, s); st != GDN_OK) return st;
+  }
+  if (gdn_status st = rec_states(a, p, true, s); st != GDN_OK) return st;
+  hipError_t e = timed("rec_bwd", s, [&] { return gdn::launch_rec_bwd(a.dtype, p, s); });
+  if (e != hipSuccess) return hip_fail(e, "recurrence gradient launch");
+  if (!a.scale) return GDN_OK;
+  e = timed("rec_dscale", s, [&] { return gdn::launch_join_parts(GDN_F32, p.part, pl.nchunk, a.D, args->dscale, s); });
+  return e == hipSuccess ? GDN_OK : hip_fail(e, "scale gradient launch");
+}
+
+gdn_status gdn_rec_step(const gdn_rec_step_args* args, void* stream) {
+  if (!args) return fail(GDN_E_INVALID, "null args");
+  const gdn_rec_step_args& a = *args;
+  if (!known_dtype(a.dtype)) return fail(GDN_E_UNSUPPORTED, "unknown dtype %d", a.dtype);
+  if (a.g_dtype != a.dtype && a.g_dtype != GDN_F32)
+    return fail(GDN_E_UNSUPPORTED, "g_dtype %d: g is in x's type or fp32", a.g_dtype);
+  if (a.N < 0 || a.D < 1) return fail(GDN_E_INVALID, "bad sizes N=%d D=%d", a.N, a.D);
+  if (a.D >= (1 << 24) || !launchable((a.D + 128.) * a.N)) return fail(GDN_E_INVALID, "problem too large");
+  if (a.N == 0) return GDN_OK;
+  if (!a.x || !a.g || !a.state || !a.y) return fail(GDN_E_INVALID, "null pointer");
+  if (a.x_stride < a.D || a.g_stride < a.D || (a.i && a.i_stride < a.D))
+    return fail(GDN_E_INVALID, "a token stride is below D = %d", a.D);
+  const size_t es = esize(a.dtype);
+  if (!aligned(a.x, es) || !aligned(a.i, es) || !aligned(a.y, es) || !aligned(a.g, esize(a.g_dtype)) || !aligned(a.scale, 4) ||
+      !aligned(a.state, 4) || !aligned(a.state_idx, 4))
+    return fail(GDN_E_INVALID, "misaligned pointer");
+  if (a.num_slots < (a.state_idx ? 0 : a.N))
+    return fail(GDN_E_INVALID, "num_slots (%d) must be >= N (%d) without state_idx", a.num_slots, a.N);
+  gdn::RecStepParams p{};
+  p.x = a.x; p.g = a.g; p.i = a.i; p.x_stride = a.x_stride; p.g_stride = a.g_stride; p.i_stride = a.i_stride;
+  p.g_f32 = a.g_dtype == GDN_F32; p.scale = a.scale; p.state = a.state; p.state_idx = a.state_idx; p.num_slots = a.num_slots;
+  p.N = a.N; p.D = a.D; p.y = a.y;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  hipError_t e = timed("rec_step", s, [&] { return gdn::launch_rec_step(a.dtype, p, s); });
+  return e == hipSuccess ? GDN_OK : hip_fail(e, "recurrence step launch");
 }
 
 }  // extern "C"

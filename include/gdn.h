@@ -545,6 +545,75 @@ size_t gdn_addnorm_bwd_workspace_size(const gdn_addnorm_bwd_args* args);
 gdn_status gdn_addnorm_bwd(const gdn_addnorm_bwd_args* args, void* stream);
 gdn_status gdn_quant_rows(const gdn_quant_args* args, void* stream);
 
+/* Gated linear recurrence over [B, T, D], channels last: per sequence and channel
+ *     L_t = g_t,  m_t = 1;   or with scale:  L_t = -scale sigmoid(g_t),  m_t = sqrt(1 - exp(2 L_t))
+ *     h_t = exp(L_t) h_{t-1} + m_t sigmoid(i_t) x_t   (sigmoid(i_t) = 1 without i),   h_0 = h0
+ *     y_t = h_t,   hT = the last h_t
+ * L <= 0 in the intended domain (scale >= 0); where m_t = 0 (scale 0, or a sigmoid that
+ * vanishes) its derivative counts as 0.  cu_seqlens as for the convolution: no host copy is
+ * needed, tokens at or past cu_seqlens[N] belong to no sequence and are left as they were.
+ * States are fp32.  B * T below 2^31 - 1024. */
+typedef struct {
+  int32_t dtype;               /* of x, i, y (dy, dx, di) */
+  int32_t g_dtype;             /* of g (dg): dtype, or GDN_F32 */
+  int32_t B, T, D;
+  const void* x;               /* [B, T, D] */
+  int64_t x_stride;
+  const void* g;               /* [B, T, D] */
+  int64_t g_stride;
+  const void* i;               /* nullable [B, T, D] */
+  int64_t i_stride;
+  const float* scale;          /* nullable [D] */
+  const float* h0;             /* nullable [N, D] */
+  const int32_t* cu_seqlens;   /* nullable */
+  int32_t num_seqs;            /* N; B when cu_seqlens is NULL */
+  void* workspace;
+  size_t workspace_bytes;
+} gdn_rec_args;
+
+typedef struct {
+  gdn_rec_args a;
+  void* y;                     /* [B, T, D], written */
+  float* hT;                   /* nullable [N, D], written */
+  float* h_save;               /* nullable, gdn_rec_states_bytes(&a) bytes: the state entering every chunk
+                                  of tokens, for gdn_rec_bwd */
+} gdn_rec_fwd_args;
+
+typedef struct {
+  gdn_rec_args a;
+  const float* h_saved;        /* nullable: h_save of the forward on the same inputs (else recomputed) */
+  const void* dy;              /* [B, T, D] */
+  const float* dhT;            /* nullable [N, D] */
+  void* dx;                    /* [B, T, D], written */
+  void* dg;                    /* [B, T, D] of g_dtype, written */
+  void* di;                    /* [B, T, D], written; needed with i */
+  float* dscale;               /* [D], written; needed with scale */
+  float* dh0;                  /* nullable [N, D], written */
+} gdn_rec_bwd_args;
+
+typedef struct {               /* one token for each of N sequences */
+  int32_t dtype, g_dtype;
+  int32_t N, D;
+  const void* x;               /* [N, D] */
+  int64_t x_stride;
+  const void* g;               /* [N, D] */
+  int64_t g_stride;
+  const void* i;               /* nullable [N, D] */
+  int64_t i_stride;
+  const float* scale;          /* nullable [D] */
+  float* state;                /* [num_slots, D], advanced in place */
+  const int32_t* state_idx;    /* nullable [N], as gdn_decode_step */
+  int32_t num_slots;
+  void* y;                     /* [N, D], written */
+} gdn_rec_step_args;
+
+size_t gdn_rec_fwd_workspace_size(const gdn_rec_fwd_args* args);
+size_t gdn_rec_bwd_workspace_size(const gdn_rec_bwd_args* args);
+size_t gdn_rec_states_bytes(const gdn_rec_args* a);
+gdn_status gdn_rec_fwd(const gdn_rec_fwd_args* args, void* stream);
+gdn_status gdn_rec_bwd(const gdn_rec_bwd_args* args, void* stream);
+gdn_status gdn_rec_step(const gdn_rec_step_args* args, void* stream);
+
 /* Per-kernel timing, for benchmarks (off by default).  While enabled, every
  * kernel the library launches is bracketed by a pair of HIP events recorded on
  * the call's stream.  gdn_profile_read waits for the recorded events, adds
