@@ -14,7 +14,7 @@ import torch
 
 from .binding import GDNError, _compiling, _gradient, _outside, gdn_chunk_bwd, gdn_chunk_fwd, gdn_decode_step, lib  # noqa: F401
 from .blocks import (add_rms_norm, add_rms_norm_8bit, gated_recurrence, gdn_addnorm_bwd, gdn_addnorm_fwd,  # noqa: F401
-                     gdn_rec_bwd, gdn_rec_fwd, gdn_rec_step, quantize_rows)  # noqa: F401
+                     gdn_linear_bwd, gdn_linear_fwd, linear, linear_8bit, gdn_rec_bwd, gdn_rec_fwd, gdn_rec_step, quantize_rows)  # noqa: F401
 from .layers import (gated_group_norm, gdn_conv_bwd, gdn_conv_fwd, gdn_conv_step, gdn_norm_bwd,  # noqa: F401
                      gdn_norm_fwd, gdn_scan_bwd, gdn_scan_fwd, gdn_scan_step, selective_scan, short_conv)
 
@@ -22,6 +22,7 @@ __all__ = ["gdn_chunk_fwd", "gdn_chunk_bwd", "gdn_decode_step", "chunk_gated_del
            "short_conv", "selective_scan", "gated_group_norm", "gdn_conv_fwd", "gdn_conv_bwd", "gdn_conv_step",
            "gdn_scan_fwd", "gdn_scan_bwd", "gdn_scan_step", "gdn_norm_fwd", "gdn_norm_bwd",
            "add_rms_norm", "add_rms_norm_8bit", "quantize_rows", "gdn_addnorm_fwd", "gdn_addnorm_bwd",
+           "linear", "linear_8bit", "gdn_linear_fwd", "gdn_linear_bwd",
            "gated_recurrence", "gdn_rec_fwd", "gdn_rec_bwd", "gdn_rec_step"]
 
 

@@ -21,7 +21,7 @@ from . import layers as _layers
 from .binding import GDNError, _compiling, _dtype_code, _outside, _ptr, _vp, lib as _load
 from .layers import (_as_one_op, _call, _no_derivative, _on, _own_lengths, _past_32_bits, _rows, _rows_like, _seqs, _t, _wants_grad, _workspace)
 
-__all__ = ["add_rms_norm", "add_rms_norm_8bit", "quantize_rows", "gated_recurrence", "gdn_rec_step"]
+__all__ = ["add_rms_norm", "add_rms_norm_8bit", "quantize_rows", "linear", "linear_8bit", "gated_recurrence", "gdn_rec_step"]
 
 _i32, _i64, _sz, _f32 = ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t, ctypes.c_float
 
@@ -63,10 +63,26 @@ class RecStepArgs(ctypes.Structure):
                 ("num_slots", _i32), ("y", _vp)]
 
 
+class LinearArgs(ctypes.Structure):
+    _fields_ = [("dtype", _i32), ("out_dtype", _i32), ("M", _i64), ("N", _i32), ("K", _i32), ("x", _vp), ("x_stride", _i64),
+                ("w", _vp), ("x_scale", _vp), ("w_scale", _vp), ("bias", _vp), ("r", _vp), ("r_stride", _i64), ("act", _i32),
+                ("workspace", _vp), ("workspace_bytes", _sz)]
+
+
+class LinearFwdArgs(ctypes.Structure):
+    _fields_ = [("a", LinearArgs), ("y", _vp), ("v_save", _vp)]
+
+
+class LinearBwdArgs(ctypes.Structure):
+    _fields_ = [("a", LinearArgs), ("v_saved", _vp), ("dy", _vp), ("dx", _vp), ("dw", _vp), ("dbias", _vp)]
+
+
 _SIGNATURES = [("gdn_addnorm_fwd", AddNormFwdArgs), ("gdn_addnorm_bwd", AddNormBwdArgs), ("gdn_quant_rows", QuantArgs),
+               ("gdn_linear_fwd", LinearFwdArgs), ("gdn_linear_bwd", LinearBwdArgs),
                ("gdn_rec_fwd", RecFwdArgs), ("gdn_rec_bwd", RecBwdArgs), ("gdn_rec_step", RecStepArgs)]
 _SIZES = [("gdn_addnorm_bwd_workspace_size", AddNormBwdArgs), ("gdn_rec_fwd_workspace_size", RecFwdArgs),
-          ("gdn_rec_bwd_workspace_size", RecBwdArgs), ("gdn_rec_states_bytes", RecArgs)]
+          ("gdn_rec_bwd_workspace_size", RecBwdArgs), ("gdn_linear_fwd_workspace_size", LinearFwdArgs),
+          ("gdn_linear_bwd_workspace_size", LinearBwdArgs), ("gdn_rec_states_bytes", RecArgs)]
 _lib = None
 
 
@@ -243,6 +259,134 @@ def quantize_rows(x):
     a.q, a.q_scale = q.data_ptr(), scale.data_ptr()
     _call(lib().gdn_quant_rows, a, x.device)
     return q, scale
+
+
+# ------------------------------------------------------------------ projections
+GDN_E4M3 = 2
+_ACTS = {None: 0, "silu": 1, "gelu": 2}
+
+
+def _linear_args(x, weight, bias, activation, residual, out_dtype):
+    if weight.dim() != 2:
+        raise GDNError("weight must be [N, K]")
+    K = _row_input("x", x)
+    N, dev = weight.shape[0], x.device
+    if N >> 31:
+        _past_32_bits()
+    if activation not in _ACTS:
+        raise GDNError(f"unknown activation {activation!r} (None, 'silu' or 'gelu')")
+    a = LinearArgs()
+    a.M, a.N, a.K, a.act = _flat(x), N, K, _ACTS[activation]
+    a.x, a.x_stride = x.data_ptr(), _rows("x", x, x.shape, 1, x.dtype, dev)
+    _t("weight", weight, (N, K), x.dtype, dev)
+    _t("bias", bias, (N,), out_dtype, dev, optional=True)
+    shape = (*x.shape[:-1], N)
+    if residual is not None:
+        a.r, a.r_stride = residual.data_ptr(), _rows("residual", residual, shape, 1, out_dtype, dev)
+    a.w, a.bias = weight.data_ptr(), _ptr(bias)
+    _on_gpu("x", x)
+    return a, shape
+
+
+def _linear_run(a, shape, out_dtype, dev, save):
+    args = LinearFwdArgs()
+    y = torch.empty(shape, dtype=out_dtype, device=dev)
+    v = torch.empty(shape, dtype=torch.float32, device=dev) if save else None
+    args.a, args.y, args.v_save = a, y.data_ptr(), _ptr(v)
+    with _on(dev):
+        ws = _workspace(lib().gdn_linear_fwd_workspace_size(ctypes.byref(args)), dev)
+    args.a.workspace, args.a.workspace_bytes = ws.data_ptr(), ws.numel()
+    _call(lib().gdn_linear_fwd, args, dev)
+    return y, v
+
+
+def gdn_linear_fwd(x, weight, bias=None, activation=None, residual=None, save: bool = False):
+    """(y, v) of the projection (see linear): v [..., N] fp32 is the value before the activation,
+    for gdn_linear_bwd, with an activation and save; else None."""
+    if _compiling():
+        return _outside(gdn_linear_fwd, x, weight, bias, activation, residual, save)
+    code = _dtype_code(x)
+    a, shape = _linear_args(x, weight, bias, activation, residual, x.dtype)
+    a.dtype = a.out_dtype = code
+    return _linear_run(a, shape, x.dtype, x.device, save and activation is not None)
+
+
+def gdn_linear_bwd(x, weight, dy, activation=None, v=None, need=(True, True, True)):
+    """(dx, dweight, dbias) of the projection; a gradient that is not in `need` is None.  v:
+    gdn_linear_fwd(..., save=True) on the same inputs, with an activation."""
+    if _compiling():
+        return _outside(gdn_linear_bwd, x, weight, dy, activation, v, need)
+    code = _dtype_code(x)
+    a, shape = _linear_args(x, weight, None, activation, None, x.dtype)
+    dt, dev = x.dtype, x.device
+    a.dtype = a.out_dtype = code
+    _t("dy", dy, shape, dt, dev)
+    _t("v", v, shape, torch.float32, dev, optional=activation is None)
+    if not any(need):
+        return None, None, None
+    args = LinearBwdArgs()
+    dx = torch.empty(x.shape, dtype=dt, device=dev) if need[0] else None
+    dw = torch.empty_like(weight) if need[1] else None
+    db = torch.empty(a.N, dtype=dt, device=dev) if need[2] else None
+    args.a, args.v_saved, args.dy, args.dx, args.dw, args.dbias = a, _ptr(v), dy.data_ptr(), *map(_ptr, (dx, dw, db))
+    with _on(dev):
+        ws = _workspace(lib().gdn_linear_bwd_workspace_size(ctypes.byref(args)), dev)
+    args.a.workspace, args.a.workspace_bytes = ws.data_ptr(), ws.numel()
+    _call(lib().gdn_linear_bwd, args, dev)
+    return dx, dw, db
+
+
+class _Linear(torch.autograd.Function):
+    @staticmethod
+    def forward(ctx, x, weight, bias, residual, activation):
+        need = ctx.needs_input_grad
+        with _as_one_op():
+            y, v = gdn_linear_fwd(x, weight, bias, activation, residual, save=any(need[:3]))
+        ctx.save_for_backward(x, weight, v)
+        ctx.act = activation
+        return y
+
+    @staticmethod
+    @once_differentiable
+    def backward(ctx, dy):
+        x, weight, v = ctx.saved_tensors
+        need = ctx.needs_input_grad
+        dx, dw, db = gdn_linear_bwd(x, weight, dy.contiguous(), ctx.act, v, need[:3]) if any(need[:3]) else (None,) * 3
+        return dx, dw, db, dy if need[3] else None, None
+
+
+def linear(x, weight, bias=None, activation=None, residual=None):
+    """Projection with its epilogue, differentiable in x, weight, bias and residual:
+
+        y = act(x weight^T + bias) + residual
+
+    x [..., K], weight [N, K], bias [N], residual [..., N], all of one dtype (bf16 or fp32);
+    activation None, "silu" or "gelu" (its tanh form).  Sums are fp32 and y is rounded once.  With
+    an activation a training pass keeps the value before it in fp32 (4 bytes an output)."""
+    if _compiling():
+        return _outside(linear, x, weight, bias, activation, residual)
+    if not _wants_grad(x, weight, bias, residual):
+        return gdn_linear_fwd(x, weight, bias, activation, residual)[0]
+    return _Linear.apply(x, weight, bias, residual, activation)
+
+
+def linear_8bit(x, x_scale, weight, weight_scale, bias=None, activation=None, residual=None, out_dtype=torch.bfloat16):
+    """linear of 8-bit rows: x [..., K] e4m3 with x_scale [...] (add_rms_norm_8bit, quantize_rows),
+    weight [N, K] e4m3 with weight_scale [N] (quantize_rows); bias, residual and y in out_dtype (bf16
+    or fp32).  No derivative."""
+    if _compiling():
+        return _outside(linear_8bit, x, x_scale, weight, weight_scale, bias, activation, residual, out_dtype)
+    _no_derivative("linear_8bit", (bias, residual, x_scale, weight_scale))
+    if x.dtype is not torch.float8_e4m3fn:
+        raise GDNError(f"x must be {torch.float8_e4m3fn}, got {x.dtype}")
+    if out_dtype not in (torch.bfloat16, torch.float32):
+        raise GDNError(f"unsupported out_dtype {out_dtype}")
+    a, shape = _linear_args(x, weight, bias, activation, residual, out_dtype)
+    _t("x_scale", x_scale, x.shape[:-1], torch.float32, x.device)
+    _t("weight_scale", weight_scale, (a.N,), torch.float32, x.device)
+    a.dtype, a.out_dtype = GDN_E4M3, 1 if out_dtype is torch.bfloat16 else 0
+    a.x_scale, a.w_scale = x_scale.data_ptr(), weight_scale.data_ptr()
+    return _linear_run(a, shape, out_dtype, x.device, False)[0]
 
 
 # ------------------------------------------------------------------ gated linear recurrence

@@ -160,6 +160,63 @@ hipError_t launch_rec_fwd(int dtype, const RecParams& p, hipStream_t st);
 hipError_t launch_rec_bwd(int dtype, const RecParams& p, hipStream_t st);
 hipError_t launch_rec_step(int dtype, const RecStepParams& p, hipStream_t st);
 
+// ---------------------------------------------------------------- products
+// What a product's sums go through on their way out: v = sum (x_scale[m] w_scale[n]) +
+// bias[n], out = act(v) + r.
+struct Epilogue {
+  const float* x_scale;      // nullable [M]
+  const float* w_scale;      // nullable [N]
+  const void* bias;          // nullable [N]
+  const void* r;             // nullable [M][N], r_stride
+  int64_t r_stride;
+  int act;
+  void* out;                 // [M][N]
+  float* v_save;             // nullable [M][N]
+};
+// out[m][n] = sum over k of a[m][k] b[n][k]: both operands' rows contiguous along k, in
+// 16-byte units (pointers, strides; zeros fill the last unit of a row).
+struct GemmParams {
+  const void* a;
+  const void* b;
+  int64_t lda, ldb;          // bytes between rows
+  int64_t M;
+  int N, kbytes;             // bytes of a row that take part
+  int splits, steps;         // the sum over k in `splits` parts of `steps` steps of 128 bytes
+  float* part;               // [splits][M][N], with splits > 1
+  Epilogue e;
+};
+// How a product is divided: tiles of 256 x 256 or 128 x 128, splits along k.
+struct GemmPlan { int tile, splits, steps; };
+GemmPlan gemm_plan(int64_t M, int N, int64_t kbytes, int cus);
+inline size_t gemm_part_bytes(const GemmPlan& g, int64_t M, int N) { return g.splits > 1 ? 4ull * g.splits * M * N : 0; }
+hipError_t launch_gemm(int dtype, int out_dtype, const GemmParams& p, const GemmPlan& g, hipStream_t st);
+// Few rows: a workgroup to 16 outputs, its waves along k.  Any strides and alignment.
+constexpr int SKINNY_M = 64;
+struct SkinnyParams {
+  const void* x;
+  const void* w;
+  int64_t x_stride, w_stride;  // bytes
+  int M, N, kbytes;
+  Epilogue e;
+};
+hipError_t launch_skinny(int dtype, int out_dtype, const SkinnyParams& p, hipStream_t st);
+// Rows re-laid for a product: in [R][C] (times act'(v) where v is given) to `rows`
+// [R][ldo] and turned to `cols` [C][ldt], zeros behind the ends; sums[row / 64][C].
+struct PackParams {
+  const void* in;
+  int64_t ld;                // elements
+  int64_t R;
+  int C;
+  const float* v;            // nullable [R][C]
+  int act;
+  void* rows;                // nullable
+  int64_t ldo;
+  void* cols;                // nullable
+  int64_t ldt;
+  float* sums;               // nullable
+};
+hipError_t launch_pack(int dtype, const PackParams& p, hipStream_t st);
+
 // ---------------------------------------------------------------- sums of parts
 // out[c] = sum over rows of part[row][c], in 64 bits and a fixed order, rounded once.
 hipError_t launch_join_parts(int dtype, const float* part, int64_t rows, int64_t cols, void* out, hipStream_t st);

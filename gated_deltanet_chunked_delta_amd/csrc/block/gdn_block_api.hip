@@ -117,6 +117,108 @@ gdn_status rec_states(const gdn_rec_args& a, const gdn::RecParams& p, bool rev, 
   return e == hipSuccess ? GDN_OK : hip_fail(e, "recurrence join launch");
 }
 
+// ---------------------------------------------------------------- products
+size_t bytes_of(int d) { return d == GDN_E4M3 ? 1 : esize(d); }
+constexpr int64_t ROW_BYTES = 1 << 23;  // of an operand's row: 256 of them stay within a buffer's 2^31
+int64_t row16(int64_t n, int dtype) { return (n * (int64_t)bytes_of(dtype) + 15) / 16 * 16; }
+
+gdn_status check_linear(const gdn_linear_args& a, bool bwd) {
+  const bool q = a.dtype == GDN_E4M3 && !bwd;
+  if (!known_dtype(a.dtype) && !q) return fail(GDN_E_UNSUPPORTED, "unsupported dtype %d", a.dtype);
+  if (!known_dtype(a.out_dtype) || (!q && a.out_dtype != a.dtype))
+    return fail(GDN_E_UNSUPPORTED, "out_dtype %d does not go with dtype %d", a.out_dtype, a.dtype);
+  if (a.M < 0 || a.N < 1 || a.K < 1) return fail(GDN_E_INVALID, "bad sizes M=%lld N=%d K=%d", (long long)a.M, a.N, a.K);
+  if (a.act < GDN_ACT_NONE || a.act > GDN_ACT_GELU) return fail(GDN_E_UNSUPPORTED, "unknown activation %d", a.act);
+  if (a.M >= (1LL << 31) || row16(a.K, a.dtype) >= ROW_BYTES || a.M >= (1LL << 40) / std::max(a.N, a.K) ||
+      (bwd && (row16(a.N, a.dtype) >= ROW_BYTES || row16(a.M, a.dtype) >= ROW_BYTES)))
+    return fail(GDN_E_INVALID, "problem too large");
+  if (!a.w) return fail(GDN_E_INVALID, "null weight");
+  if (a.M > 0 && !a.x) return fail(GDN_E_INVALID, "null input x");
+  if (q && (!a.x_scale || !a.w_scale)) return fail(GDN_E_INVALID, "8-bit rows need x_scale and w_scale");
+  if (!q && (a.x_scale || a.w_scale)) return fail(GDN_E_INVALID, "scales belong to 8-bit rows");
+  if (a.x_stride < a.K || (a.r && a.r_stride < a.N)) return fail(GDN_E_INVALID, "a row stride is below its row's width");
+  const size_t es = bytes_of(a.dtype), os = esize(a.out_dtype);
+  if (!aligned(a.x, es) || !aligned(a.w, es) || !aligned(a.bias, os) || !aligned(a.r, os) || !aligned(a.x_scale, 4) ||
+      !aligned(a.w_scale, 4))
+    return fail(GDN_E_INVALID, "a pointer is misaligned");
+  const double tiles = ((a.M + 127) / 128. + 1) * ((a.N + 127) / 128. + 1);
+  if (!launchable(256. * 16 * tiles)) return fail(GDN_E_INVALID, "problem too large");
+  return GDN_OK;
+}
+// Whether a product can read these rows as they lie.
+bool rows_fit(const void* p, int64_t stride, int64_t n, int dtype) {
+  const int64_t es = (int64_t)bytes_of(dtype);
+  return aligned(p, 16) && stride * es % 16 == 0 && n * es % 16 == 0 && stride * es < ROW_BYTES;
+}
+struct LinearPlan {
+  gdn::GemmPlan g;
+  bool skinny = false;
+  size_t o_x = 0, o_w = 0, o_part = 0, total = 0;
+};
+LinearPlan linear_plan(const gdn_linear_args& a) {
+  LinearPlan p;
+  size_t off = 0;
+  auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes); return o; };
+  p.skinny = a.M <= gdn::SKINNY_M;
+  if (!p.skinny) {
+    const int64_t row = row16(a.K, a.dtype);
+    if (!rows_fit(a.x, a.x_stride, a.K, a.dtype)) p.o_x = take((size_t)a.M * row);
+    if (!rows_fit(a.w, a.K, a.K, a.dtype)) p.o_w = take((size_t)a.N * row);
+    p.g = gdn::gemm_plan(a.M, a.N, row, cu_count());
+    p.o_part = take(gdn::gemm_part_bytes(p.g, a.M, a.N));
+  }
+  p.total = std::max<size_t>(off, 16);
+  return p;
+}
+struct LinearBwdPlan {
+  gdn::GemmPlan gx, gw;
+  bool pre = false;  // dy act'(v), or dy re-laid, is written out
+  size_t o_pre = 0, o_pre_t = 0, o_w_t = 0, o_x_t = 0, o_sums = 0, o_part = 0, total = 0;
+};
+LinearBwdPlan linear_bwd_plan(const gdn_linear_bwd_args& b) {
+  const gdn_linear_args& a = b.a;
+  LinearBwdPlan p;
+  size_t off = 0;
+  auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes); return o; };
+  const int64_t rn = row16(a.N, a.dtype), rm = row16(a.M, a.dtype);
+  p.pre = b.dx && (a.act || !rows_fit(b.dy, a.N, a.N, a.dtype));
+  if (p.pre) p.o_pre = take((size_t)a.M * rn);
+  size_t part = 0;
+  if (b.dx) {
+    p.o_w_t = take((size_t)a.K * rn);
+    p.gx = gdn::gemm_plan(a.M, a.K, rn, cu_count());
+    part = gdn::gemm_part_bytes(p.gx, a.M, a.K);
+  }
+  if (b.dw) {
+    p.o_pre_t = take((size_t)a.N * rm);
+    p.o_x_t = take((size_t)a.K * rm);
+    p.gw = gdn::gemm_plan(a.N, a.K, rm, cu_count());
+    part = std::max(part, gdn::gemm_part_bytes(p.gw, a.N, a.K));
+  }
+  if (b.dbias) p.o_sums = take(4 * (size_t)((a.M + 63) / 64) * a.N);
+  p.o_part = take(part);
+  p.total = std::max<size_t>(off, 16);
+  return p;
+}
+gdn::Epilogue epilogue(const gdn_linear_fwd_args& f) {
+  const gdn_linear_args& a = f.a;
+  gdn::Epilogue e{};
+  e.x_scale = a.x_scale; e.w_scale = a.w_scale; e.bias = a.bias; e.r = a.r; e.r_stride = a.r_stride; e.act = a.act;
+  e.out = f.y; e.v_save = f.v_save;
+  return e;
+}
+gdn_status run_pack(int dtype, const gdn::PackParams& p, hipStream_t s) {
+  if (p.R == 0) return GDN_OK;
+  hipError_t e = timed("linear_pack", s, [&] { return gdn::launch_pack(dtype, p, s); });
+  return e == hipSuccess ? GDN_OK : hip_fail(e, "row copy launch");
+}
+gdn_status run_gemm(const char* name, int dtype, int out_dtype, gdn::GemmParams p, const gdn::GemmPlan& g, hipStream_t s) {
+  p.splits = g.splits;
+  p.steps = g.steps;
+  hipError_t e = timed(name, s, [&] { return gdn::launch_gemm(dtype, out_dtype, p, g, s); });
+  return e == hipSuccess ? GDN_OK : hip_fail(e, "product launch");
+}
+
 }  // namespace
 
 extern "C" {
@@ -284,6 +386,112 @@ gdn_status gdn_rec_step(const gdn_rec_step_args* args, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   hipError_t e = timed("rec_step", s, [&] { return gdn::launch_rec_step(a.dtype, p, s); });
   return e == hipSuccess ? GDN_OK : hip_fail(e, "recurrence step launch");
+}
+
+size_t gdn_linear_fwd_workspace_size(const gdn_linear_fwd_args* args) {
+  if (!args) { fail(GDN_E_INVALID, "null args"); return 0; }
+  if (check_linear(args->a, false) != GDN_OK) return 0;
+  return linear_plan(args->a).total;
+}
+size_t gdn_linear_bwd_workspace_size(const gdn_linear_bwd_args* args) {
+  if (!args) { fail(GDN_E_INVALID, "null args"); return 0; }
+  if (check_linear(args->a, true) != GDN_OK) return 0;
+  return linear_bwd_plan(*args).total;
+}
+
+gdn_status gdn_linear_fwd(const gdn_linear_fwd_args* args, void* stream) {
+  if (!args) return fail(GDN_E_INVALID, "null args");
+  const gdn_linear_args& a = args->a;
+  if (gdn_status st = check_linear(a, false); st != GDN_OK) return st;
+  if (a.M == 0) return GDN_OK;
+  if (!args->y) return fail(GDN_E_INVALID, "null output y");
+  if (!aligned(args->y, esize(a.out_dtype)) || !aligned(args->v_save, 4)) return fail(GDN_E_INVALID, "a pointer is misaligned");
+  const LinearPlan pl = linear_plan(a);
+  if (gdn_status st = check_ws(a.workspace, a.workspace_bytes, pl.total); st != GDN_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  const int64_t es = (int64_t)bytes_of(a.dtype), row = row16(a.K, a.dtype);
+  if (pl.skinny) {
+    gdn::SkinnyParams p{};
+    p.x = a.x; p.w = a.w; p.x_stride = a.x_stride * es; p.w_stride = a.K * es; p.M = (int)a.M; p.N = a.N;
+    p.kbytes = (int)(a.K * es);
+    p.e = epilogue(*args);
+    hipError_t e = timed("linear_few", s, [&] { return gdn::launch_skinny(a.dtype, a.out_dtype, p, s); });
+    return e == hipSuccess ? GDN_OK : hip_fail(e, "product launch");
+  }
+  gdn::GemmParams p{};
+  p.a = a.x; p.lda = a.x_stride * es; p.b = a.w; p.ldb = a.K * es; p.M = a.M; p.N = a.N; p.kbytes = (int)row;
+  p.part = at<float>(a.workspace, pl.o_part);
+  p.e = epilogue(*args);
+  auto relay = [&](const void* in, int64_t stride, int64_t R, size_t off) {
+    gdn::PackParams k{};
+    k.in = in; k.ld = stride; k.R = R; k.C = a.K; k.rows = at<char>(a.workspace, off); k.ldo = row / es;
+    return run_pack(a.dtype, k, s);
+  };
+  if (!rows_fit(a.x, a.x_stride, a.K, a.dtype)) {
+    if (gdn_status st = relay(a.x, a.x_stride, a.M, pl.o_x); st != GDN_OK) return st;
+    p.a = at<char>(a.workspace, pl.o_x);
+    p.lda = row;
+  }
+  if (!rows_fit(a.w, a.K, a.K, a.dtype)) {
+    if (gdn_status st = relay(a.w, a.K, a.N, pl.o_w); st != GDN_OK) return st;
+    p.b = at<char>(a.workspace, pl.o_w);
+    p.ldb = row;
+  }
+  return run_gemm("linear_fwd", a.dtype, a.out_dtype, p, pl.g, s);
+}
+
+gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* args, void* stream) {
+  if (!args) return fail(GDN_E_INVALID, "null args");
+  const gdn_linear_args& a = args->a;
+  if (gdn_status st = check_linear(a, true); st != GDN_OK) return st;
+  if (a.M > 0 && !args->dy) return fail(GDN_E_INVALID, "null gradient pointer");
+  if (!args->dx && !args->dw && !args->dbias) return fail(GDN_E_INVALID, "no gradient asked for");
+  if (a.act && a.M > 0 && !args->v_saved) return fail(GDN_E_INVALID, "an activation's gradient needs v_saved");
+  const size_t es = esize(a.dtype);
+  if (!aligned(args->dy, es) || !aligned(args->dx, es) || !aligned(args->dw, es) || !aligned(args->dbias, es) ||
+      !aligned(args->v_saved, 4))
+    return fail(GDN_E_INVALID, "a pointer is misaligned");
+  const LinearBwdPlan pl = linear_bwd_plan(*args);
+  if (gdn_status st = check_ws(a.workspace, a.workspace_bytes, pl.total); st != GDN_OK) return st;
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  void* ws = a.workspace;
+  const int64_t rn = row16(a.N, a.dtype), rm = row16(a.M, a.dtype);
+  // dy act'(v): as it lies, turned, and its column sums
+  gdn::PackParams k{};
+  k.in = args->dy; k.ld = a.N; k.R = a.M; k.C = a.N;
+  k.v = a.act ? args->v_saved : nullptr; k.act = a.act;
+  if (pl.pre) { k.rows = at<char>(ws, pl.o_pre); k.ldo = rn / es; }
+  if (args->dw) { k.cols = at<char>(ws, pl.o_pre_t); k.ldt = rm / es; }
+  if (args->dbias) k.sums = at<float>(ws, pl.o_sums);
+  if (k.rows || k.cols || k.sums)
+    if (gdn_status st = run_pack(a.dtype, k, s); st != GDN_OK) return st;
+  if (args->dbias) {
+    hipError_t e = timed("linear_dbias", s, [&] { return gdn::launch_join_parts(a.dtype, k.sums, (a.M + 63) / 64, a.N, args->dbias, s); });
+    if (e != hipSuccess) return hip_fail(e, "bias gradient launch");
+  }
+  gdn::GemmParams p{};
+  p.part = at<float>(ws, pl.o_part);
+  if (args->dx && a.M > 0) {
+    gdn::PackParams t{};
+    t.in = a.w; t.ld = a.K; t.R = a.N; t.C = a.K; t.cols = at<char>(ws, pl.o_w_t); t.ldt = rn / es;
+    if (gdn_status st = run_pack(a.dtype, t, s); st != GDN_OK) return st;
+    p.a = pl.pre ? k.rows : args->dy; p.lda = rn; p.b = t.cols; p.ldb = rn;
+    p.M = a.M; p.N = a.K; p.kbytes = (int)rn;
+    p.e = gdn::Epilogue{};
+    p.e.out = args->dx;
+    if (gdn_status st = run_gemm("linear_dx", a.dtype, a.dtype, p, pl.gx, s); st != GDN_OK) return st;
+  }
+  if (args->dw) {
+    gdn::PackParams t{};
+    t.in = a.x; t.ld = a.x_stride; t.R = a.M; t.C = a.K; t.cols = at<char>(ws, pl.o_x_t); t.ldt = rm / es;
+    if (gdn_status st = run_pack(a.dtype, t, s); st != GDN_OK) return st;
+    p.a = k.cols; p.lda = rm; p.b = t.cols; p.ldb = rm;
+    p.M = a.N; p.N = a.K; p.kbytes = (int)rm;
+    p.e = gdn::Epilogue{};
+    p.e.out = args->dw;
+    if (gdn_status st = run_gemm("linear_dw", a.dtype, a.dtype, p, pl.gw, s); st != GDN_OK) return st;
+  }
+  return GDN_OK;
 }
 
 }  // extern "C"

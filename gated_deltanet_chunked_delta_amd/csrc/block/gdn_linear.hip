@@ -1,0 +1,434 @@
+// gdn_linear.hip -- products with an epilogue: out = act(a b^T scales + bias) + r.
+//
+// Both operands' rows run along k.  A step of the main loop takes 128 bytes of every
+// row of a tile -- 64 bf16, 32 fp32 or 128 8-bit values -- so one layout serves all types:
+// a row's 128 bytes are eight pieces of 16, a lane's operand for one 16-row block is two of
+// them.  Which k a piece stands for is the same for both operands, which is all that the
+// sum asks for.
+//
+// The tiles are loaded straight into LDS (buffer loads with the lds bit), two buffers deep,
+// one step ahead.  Such a load puts 64 lanes' pieces side by side, so the layout is made by
+// which piece a lane asks for: piece j of row r lies in slot j ^ s(r), with s such that the
+// 16 rows that a fragment read takes at once fall on all 64 banks.
+//
+// The products are formed turned (b's rows are the matrix core's rows), and the four 16-row
+// blocks of a wave's 64 outputs take rows 16 q + 4 j + i of b for block j: a lane then
+// holds 16 outputs side by side, and four lanes a whole line of a row.
+#include "gdn_block.h"
+
+namespace gdn {
+
+namespace {
+
+typedef uint32_t u32x4 __attribute__((__vector_size__(16)));
+typedef int i32x8 __attribute__((__vector_size__(32)));
+
+template <int T> struct ElemOf;
+template <> struct ElemOf<GDN_F32> { typedef float type; };
+template <> struct ElemOf<GDN_BF16> { typedef bf16 type; };
+
+// One lane's two pieces of a row, and the product of two 16-row blocks over one step.
+struct Pieces { u32x4 lo, hi; };
+template <int T>
+__device__ __forceinline__ void mma_step(f32x4& acc, const Pieces& a, const Pieces& b) {
+  if constexpr (T == GDN_BF16) {
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.lo), __builtin_bit_cast(bf16x8, b.lo), acc, 0, 0, 0);
+    acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.hi), __builtin_bit_cast(bf16x8, b.hi), acc, 0, 0, 0);
+  } else if constexpr (T == GDN_F32) {
+    const f32x4 al = __builtin_bit_cast(f32x4, a.lo), bl = __builtin_bit_cast(f32x4, b.lo);
+    const f32x4 ah = __builtin_bit_cast(f32x4, a.hi), bh = __builtin_bit_cast(f32x4, b.hi);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(al[j], bl[j], acc, 0, 0, 0);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(ah[j], bh[j], acc, 0, 0, 0);
+  } else {  // e4m3: 128 values of k at the full 8-bit rate, block scales of 1 (2^(127 - 127))
+    const i32x8 av = {(int)a.lo[0], (int)a.lo[1], (int)a.lo[2], (int)a.lo[3], (int)a.hi[0], (int)a.hi[1], (int)a.hi[2], (int)a.hi[3]};
+    const i32x8 bv = {(int)b.lo[0], (int)b.lo[1], (int)b.lo[2], (int)b.lo[3], (int)b.hi[0], (int)b.hi[1], (int)b.hi[2], (int)b.hi[3]};
+    acc = __builtin_amdgcn_mfma_scale_f32_16x16x128_f8f6f4(av, bv, acc, 0, 0, 0, 0x7f7f7f7f, 0, 0x7f7f7f7f);
+  }
+}
+
+// act(v); derivative in d
+template <bool D>
+__device__ __forceinline__ float act_of(int act, float v, float& d) {
+  if (act == GDN_ACT_SILU) {
+    const float s = fast_sigmoid<float>(v);
+    if (D) d = dsilu_gate(v, s);
+    return v * s;
+  }
+  if (act == GDN_ACT_GELU) {
+    constexpr float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
+    const float s = fast_sigmoid<float>(c * fmaf(0.044715f * v * v, v, v));
+    if (D) d = fmaf(v * (s - s * s), c * fmaf(3.f * 0.044715f * v, v, 1.f), s);
+    return v * s;
+  }
+  d = 1.f;
+  return v;
+}
+
+// Four outputs side by side of row m, from column n on (c of them exist).
+template <class O>
+__device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int N, int n, f32x4 v) {
+  const int c = N - n;
+  if (c <= 0) return;
+  float f[4] = {v[0], v[1], v[2], v[3]}, t[4];
+  if (e.x_scale) {
+    const float xs = e.x_scale[m];
+    ld_part<4>(e.w_scale + n, c, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] *= xs * t[i];
+  }
+  if (e.bias) {
+    ld_part<4>(static_cast<const O*>(e.bias) + n, c, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] += t[i];
+  }
+  if (e.v_save) {
+    float* p = e.v_save + m * N + n;
+    if (c >= 4) *reinterpret_cast<f32x4_any*>(p) = f32x4{f[0], f[1], f[2], f[3]};
+    else
+      for (int i = 0; i < c; ++i) p[i] = f[i];
+  }
+  if (e.act) {
+    float d;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] = act_of<false>(e.act, f[i], d);
+  }
+  if (e.r) {
+    ld_part<4>(static_cast<const O*>(e.r) + m * e.r_stride + n, c, t);
+#pragma unroll
+    for (int i = 0; i < 4; ++i) f[i] += t[i];
+  }
+  O* p = static_cast<O*>(e.out) + m * N + n;
+  if (c >= 4) {
+    if constexpr (sizeof(O) == 2) *reinterpret_cast<bf16x4_any*>(p) = bf16x4{(bf16)f[0], (bf16)f[1], (bf16)f[2], (bf16)f[3]};
+    else *reinterpret_cast<f32x4_any*>(p) = f32x4{f[0], f[1], f[2], f[3]};
+  } else {
+    for (int i = 0; i < c; ++i) p[i] = to_e<O>(f[i]);
+  }
+}
+
+// A tile's operand: where its rows start, how far they reach (below 2^31 bytes).
+constexpr uint32_t PAST_END = 0x80000000u;
+__device__ __forceinline__ u32x4 make_rsrc(const void* base, uint32_t bytes) {
+  const uint64_t p = reinterpret_cast<uint64_t>(base);
+  return u32x4{(uint32_t)p, (uint32_t)(p >> 32) & 0xffffu, bytes, 0x00027000u};
+}
+// 16 bytes a lane from rsrc + off to LDS at `lds` + 16 * lane; past the buffer's end: zeros.
+// The compiler does not see these loads: what reads their target waits by hand (lds_wait).
+__device__ __forceinline__ void load_lds(u32x4 rsrc, uint32_t off, uint32_t lds) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
+               :: "s"(lds), "v"(off), "s"(rsrc) : "memory", "m0");
+}
+__device__ __forceinline__ void lds_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
+
+__device__ __forceinline__ int swz_a(int row) { return (row >> 1) & 7; }
+__device__ __forceinline__ int swz_b(int row) { return ((row >> 1) & 1) | ((row >> 4) & 3) << 1; }
+
+// BM x BN tile, WM x WN waves, each TM 16-row blocks of a and 64 rows of b.
+template <int T, class O, int BM, int BN, int WM, int WN>
+__global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmParams p) {
+  constexpr int W = WM * WN, TM = BM / WM / 16, TN = 4;
+  static_assert(BN / WN == 64, "a wave takes 64 rows of b");
+  constexpr int NA = BM / 8 / W, NB = BN / 8 / W;  // loads of a wave and step
+  constexpr int BUF = (BM + BN) * 128;
+  __shared__ __attribute__((aligned(1024))) char smem[2 * BUF];
+  const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
+  // Workgroups go round the eight dies: each die takes a run of tiles of its own, in
+  // groups of eight tile rows, so that its L2 sees the same rows of a and b again.
+  const int tn_n = (p.N + BN - 1) / BN;
+  const int64_t tm_n = (p.M + BM - 1) / BM, tiles = tm_n * tn_n;
+  int64_t id = blockIdx.x;
+  const int split = (int)(id / tiles);
+  id -= split * tiles;
+  {
+    const int64_t per = tiles / 8, more = tiles % 8, die = id % 8;
+    id = id / 8 + die * per + min(die, more);
+  }
+  constexpr int GROUP = 8;
+  const int64_t g0 = id / (GROUP * (int64_t)tn_n) * GROUP, rows_g = min((int64_t)GROUP, tm_n - g0), in_g = id - g0 * tn_n;
+  const int64_t m0 = (g0 + in_g % rows_g) * BM;
+  const int n0 = (int)(in_g / rows_g) * BN;
+
+  const int64_t am = min((int64_t)BM, p.M - m0);
+  const int bn = min(BN, p.N - n0);
+  const u32x4 ra = make_rsrc(static_cast<const char*>(p.a) + m0 * p.lda, (uint32_t)((am - 1) * p.lda + p.kbytes));
+  const u32x4 rb = make_rsrc(static_cast<const char*>(p.b) + (int64_t)n0 * p.ldb, (uint32_t)((bn - 1) * p.ldb + p.kbytes));
+  const int k0 = split * p.steps * 128, k1 = min(p.kbytes, k0 + p.steps * 128);
+  const uint32_t base = __builtin_amdgcn_readfirstlane((uint32_t)(uintptr_t)(__attribute__((address_space(3))) char*)smem);
+  uint32_t oa[NA], ob[NB], ca[NA], cb[NB];  // byte offsets of the lane's pieces; their place along k
+#pragma unroll
+  for (int j = 0; j < NA; ++j) {
+    const int row = (w * NA + j) * 8 + (lane >> 3);
+    ca[j] = ((lane & 7) ^ swz_a(row)) * 16;
+    oa[j] = (uint32_t)(row * p.lda) + k0 + ca[j];
+  }
+#pragma unroll
+  for (int j = 0; j < NB; ++j) {
+    const int row = (w * NB + j) * 8 + (lane >> 3);
+    cb[j] = ((lane & 7) ^ swz_b(row)) * 16;
+    ob[j] = (uint32_t)(row * p.ldb) + k0 + cb[j];
+  }
+  auto request = [&](int k, int buf) {
+    const uint32_t at = base + buf * BUF + w * (NA * 1024);
+    const uint32_t left = k1 - k;  // pieces past the end of k ask past the buffer's end
+#pragma unroll
+    for (int j = 0; j < NA; ++j) load_lds(ra, ca[j] < left ? oa[j] : PAST_END, at + j * 1024);
+    const uint32_t bt = base + buf * BUF + BM * 128 + w * (NB * 1024);
+#pragma unroll
+    for (int j = 0; j < NB; ++j) load_lds(rb, cb[j] < left ? ob[j] : PAST_END, bt + j * 1024);
+#pragma unroll
+    for (int j = 0; j < NA; ++j) oa[j] += 128;
+#pragma unroll
+    for (int j = 0; j < NB; ++j) ob[j] += 128;
+  };
+  const int wm = w / WN, wn = w % WN, q = lane >> 4, r16 = lane & 15;
+  // fragment addresses: a's block i, row 16 i + r16; b's block j, row 16 (r16 / 4) + 4 j + r16 % 4
+  const char* fa = smem + (wm * TM * 16 + r16) * 128;
+  const int sa = swz_a(r16);  // (the same for every block: they lie 16 rows apart)
+  const int rb0 = 16 * (r16 >> 2) + (r16 & 3);
+  const char* fb = smem + BM * 128 + (wn * 64 + rb0) * 128;
+  const int sb = swz_b(rb0);  // (4 j leaves it as it is)
+  f32x4 acc[TM][TN];
+#pragma unroll
+  for (int i = 0; i < TM; ++i)
+#pragma unroll
+    for (int j = 0; j < TN; ++j) acc[i][j] = zero4();
+  if (k0 < k1) request(k0, 0);
+  lds_wait();
+  __syncthreads();
+  int buf = 0;
+  for (int k = k0; k < k1; k += 128) {
+    if (k + 128 < k1) request(k + 128, buf ^ 1);
+    const char *pa = fa + buf * BUF, *pb = fb + buf * BUF;
+    Pieces b[TN];
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      b[j].lo = *reinterpret_cast<const u32x4*>(pb + j * 512 + ((q ^ sb) << 4));
+      b[j].hi = *reinterpret_cast<const u32x4*>(pb + j * 512 + (((q + 4) ^ sb) << 4));
+    }
+#pragma unroll
+    for (int i = 0; i < TM; ++i) {
+      Pieces a;
+      a.lo = *reinterpret_cast<const u32x4*>(pa + i * 2048 + ((q ^ sa) << 4));
+      a.hi = *reinterpret_cast<const u32x4*>(pa + i * 2048 + (((q + 4) ^ sa) << 4));
+#pragma unroll
+      for (int j = 0; j < TN; ++j) mma_step<T>(acc[i][j], b[j], a);
+    }
+    lds_wait();
+    __syncthreads();
+    buf ^= 1;
+  }
+  const int n = n0 + wn * 64 + 16 * q;
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t m = m0 + (wm * TM + i) * 16 + r16;
+    if (m >= p.M) continue;
+#pragma unroll
+    for (int j = 0; j < TN; ++j) {
+      if (p.splits > 1) {
+        float* t = p.part + (split * p.M + m) * p.N + n + 4 * j;
+        const int c = p.N - n - 4 * j;
+        if (c >= 4) *reinterpret_cast<f32x4_any*>(t) = acc[i][j];
+        else
+          for (int x = 0; x < c; ++x) t[x] = acc[i][j][x];
+      } else {
+        finish4<O>(p.e, m, p.N, n + 4 * j, acc[i][j]);
+      }
+    }
+  }
+}
+
+// The splits' sums, in order, and the epilogue: four outputs a thread.
+template <class O>
+__global__ __launch_bounds__(256) void gemm_join_kernel(GemmParams p) {
+  const int per = (p.N + 3) / 4;
+  const int64_t i = block_2d() * 256 + threadIdx.x, m = i / per;
+  if (m >= p.M) return;
+  const int n = (int)(i - m * per) * 4, c = p.N - n;
+  f32x4 s = zero4();
+  for (int k = 0; k < p.splits; ++k) {
+    float f[4];
+    ld_part<4>(p.part + (k * p.M + m) * p.N + n, c, f);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) s[e] += f[e];
+  }
+  finish4<O>(p.e, m, p.N, n, s);
+}
+
+// Up to 16 MT rows of x by 16 outputs: eight waves take every eighth 128 bytes of k.
+// Bound: the weight's bytes (latency where there are few).
+__device__ __forceinline__ u32x4 ld_piece(const char* row, int k, int kbytes) {
+  typedef u32x4 u32x4_any __attribute__((aligned(1)));
+  if (k + 16 <= kbytes) return *reinterpret_cast<const u32x4_any*>(row + k);
+  u32x4 v = {};
+  for (int i = 0; i < 16 && k + i < kbytes; ++i) v[i / 4] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i % 4));
+  return v;
+}
+template <int T, class O, int MT>
+__global__ __launch_bounds__(512) void skinny_kernel(SkinnyParams p) {
+  constexpr int W = 8;
+  __shared__ f32x4 red[W][MT][64];
+  const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), q = lane >> 4, r16 = lane & 15;
+  const int n0 = blockIdx.x * 16;
+  const char* wr = static_cast<const char*>(p.w) + (int64_t)min(n0 + r16, p.N - 1) * p.w_stride;
+  const char* xr[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) xr[i] = static_cast<const char*>(p.x) + (int64_t)min(i * 16 + r16, p.M - 1) * p.x_stride;
+  f32x4 acc[MT];
+#pragma unroll
+  for (int i = 0; i < MT; ++i) acc[i] = zero4();
+  constexpr int U = MT <= 2 ? 4 : 2;  // steps requested together
+  for (int k = w * 128; k < p.kbytes; k += U * W * 128) {
+    Pieces b[U], a[U][MT];
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
+      const int ku = k + u * W * 128 + q * 16;
+      b[u].lo = ld_piece(wr, ku, p.kbytes);
+      b[u].hi = ld_piece(wr, ku + 64, p.kbytes);
+#pragma unroll
+      for (int i = 0; i < MT; ++i) {
+        a[u][i].lo = ld_piece(xr[i], ku, p.kbytes);
+        a[u][i].hi = ld_piece(xr[i], ku + 64, p.kbytes);
+      }
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u)
+#pragma unroll
+      for (int i = 0; i < MT; ++i) mma_step<T>(acc[i], b[u], a[u][i]);
+  }
+#pragma unroll
+  for (int i = 0; i < MT; ++i) red[w][i][lane] = acc[i];
+  __syncthreads();
+  // four outputs of a row a thread: entry (i, lane) holds rows n 4 (lane / 16) of column m = lane % 16
+  for (int t = threadIdx.x; t < MT * 64; t += 512) {
+    const int i = t / 64, l = t % 64;
+    f32x4 s = red[0][i][l];
+#pragma unroll
+    for (int v = 1; v < W; ++v) s += red[v][i][l];
+    const int m = i * 16 + (l & 15);
+    if (m < p.M) finish4<O>(p.e, m, p.N, n0 + 4 * (l >> 4), s);
+  }
+}
+
+// 64 x 64 elements a workgroup.
+template <class E>
+__global__ __launch_bounds__(256) void pack_kernel(PackParams p) {
+  __shared__ float tile[64][65];
+  const int cols_n = (p.C + 63) / 64;
+  const int64_t blk = block_2d(), br = blk / cols_n;
+  const int64_t r0 = br * 64;
+  const int c0 = (int)(blk - br * cols_n) * 64;
+  // (rows up to the end of the turned copy's padding)
+  if (r0 >= (p.R + 63) / 64 * 64) return;
+  const int tr = threadIdx.x / 4, tc = threadIdx.x % 4 * 16;
+  const int64_t r = r0 + tr;
+  float f[4][4];
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    const int c = c0 + tc + 4 * h;
+#pragma unroll
+    for (int e = 0; e < 4; ++e) f[h][e] = 0.f;
+    if (r < p.R && c < p.C) {
+      ld_part<4>(static_cast<const E*>(p.in) + r * p.ld + c, p.C - c, f[h]);
+      if (p.v) {
+        float v[4];
+        ld_part<4>(p.v + r * p.C + c, p.C - c, v);
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float d;
+          act_of<true>(p.act, v[e], d);
+          f[h][e] *= d;
+        }
+      }
+    }
+    if (p.rows && r < p.R && c < p.ldo) st_part<4>(static_cast<E*>(p.rows) + r * p.ldo + c, (int)(p.ldo - c), f[h]);
+#pragma unroll
+    for (int e = 0; e < 4; ++e) tile[tr][tc + 4 * h + e] = f[h][e];
+  }
+  if (!p.cols && !p.sums) return;
+  __syncthreads();
+  const int c = c0 + tr;  // a column a thread now, 16 rows of it
+  float s = 0.f;
+#pragma unroll
+  for (int h = 0; h < 4; ++h) {
+    float g[4];
+#pragma unroll
+    for (int e = 0; e < 4; ++e) {
+      g[e] = tile[tc + 4 * h + e][tr];
+      s += g[e];
+    }
+    const int64_t rr = r0 + tc + 4 * h;
+    if (p.cols && c < p.C && rr < p.ldt) st_part<4>(static_cast<E*>(p.cols) + c * p.ldt + rr, (int)min((int64_t)4, p.ldt - rr), g);
+  }
+  s += quad_xor<1>(s);
+  s += quad_xor<2>(s);
+  if (p.sums && c < p.C && threadIdx.x % 4 == 0) p.sums[br * p.C + c] = s;
+}
+// Bytes copied row by row (8-bit rows).
+__global__ __launch_bounds__(256) void pack_bytes_kernel(PackParams p) {
+  const int64_t i = block_2d() * 256 + threadIdx.x, per = p.ldo / 16, r = i / per;
+  if (r >= p.R) return;
+  const int c = (int)(i - r * per) * 16;
+  const u32x4 v = ld_piece(static_cast<const char*>(p.in) + r * p.ld, c, p.C);
+  *reinterpret_cast<u32x4*>(static_cast<char*>(p.rows) + r * p.ldo + c) = v;
+}
+
+template <int T, class O>
+hipError_t gemm_any(const GemmParams& p, const GemmPlan& g, hipStream_t st) {
+  const int64_t tiles = (p.M + g.tile - 1) / g.tile * ((p.N + g.tile - 1) / g.tile);
+  const dim3 grid((uint32_t)(tiles * g.splits));
+  if (g.tile == 256) hipLaunchKernelGGL((gemm_kernel<T, O, 256, 256, 2, 4>), grid, dim3(512), 0, st, p);
+  else hipLaunchKernelGGL((gemm_kernel<T, O, 128, 128, 2, 2>), grid, dim3(256), 0, st, p);
+  if (hipError_t e = hipGetLastError(); e != hipSuccess || g.splits == 1) return e;
+  hipLaunchKernelGGL((gemm_join_kernel<O>), blocks_2d((p.M * ((p.N + 3) / 4) + 255) / 256), dim3(256), 0, st, p);
+  return hipGetLastError();
+}
+template <int T, class O>
+hipError_t skinny_any(const SkinnyParams& p, hipStream_t st) {
+  const dim3 grid((p.N + 15) / 16);
+  if (p.M <= 16) hipLaunchKernelGGL((skinny_kernel<T, O, 1>), grid, dim3(512), 0, st, p);
+  else if (p.M <= 32) hipLaunchKernelGGL((skinny_kernel<T, O, 2>), grid, dim3(512), 0, st, p);
+  else hipLaunchKernelGGL((skinny_kernel<T, O, 4>), grid, dim3(512), 0, st, p);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+// Tiles of 256 x 256 where they fill the chip, else of 128 x 128; k is split where even
+// those leave compute units without work and the parts stay long.
+GemmPlan gemm_plan(int64_t M, int N, int64_t kbytes, int cus) {
+  GemmPlan g{256, 1, (int)((kbytes + 127) / 128)};
+  auto tiles = [&](int t) { return (M + t - 1) / t * ((N + t - 1) / t); };
+  if (tiles(256) < cus * 3 / 4) g.tile = 128;
+  const int64_t t = tiles(g.tile);
+  if (t < cus) {
+    const int most = (int)std::max<int64_t>(1, std::min<int64_t>({2 * cus / t, g.steps / 8, 16}));
+    g.steps = (g.steps + most - 1) / most;
+    g.splits = (int)(((kbytes + 127) / 128 + g.steps - 1) / std::max(g.steps, 1));
+    g.splits = std::max(g.splits, 1);
+  }
+  return g;
+}
+hipError_t launch_gemm(int dtype, int out_dtype, const GemmParams& p, const GemmPlan& g, hipStream_t st) {
+  if (dtype == GDN_BF16) return gemm_any<GDN_BF16, bf16>(p, g, st);
+  if (dtype == GDN_F32) return gemm_any<GDN_F32, float>(p, g, st);
+  return out_dtype == GDN_BF16 ? gemm_any<GDN_E4M3, bf16>(p, g, st) : gemm_any<GDN_E4M3, float>(p, g, st);
+}
+hipError_t launch_skinny(int dtype, int out_dtype, const SkinnyParams& p, hipStream_t st) {
+  if (dtype == GDN_BF16) return skinny_any<GDN_BF16, bf16>(p, st);
+  if (dtype == GDN_F32) return skinny_any<GDN_F32, float>(p, st);
+  return out_dtype == GDN_BF16 ? skinny_any<GDN_E4M3, bf16>(p, st) : skinny_any<GDN_E4M3, float>(p, st);
+}
+hipError_t launch_pack(int dtype, const PackParams& p, hipStream_t st) {
+  if (dtype == GDN_E4M3) {
+    hipLaunchKernelGGL(pack_bytes_kernel, blocks_2d((p.R * (p.ldo / 16) + 255) / 256), dim3(256), 0, st, p);
+  } else {
+    const dim3 grid = blocks_2d((p.R + 63) / 64 * ((p.C + 63) / 64));
+    if (dtype == GDN_BF16) hipLaunchKernelGGL((pack_kernel<bf16>), grid, dim3(256), 0, st, p);
+    else hipLaunchKernelGGL((pack_kernel<float>), grid, dim3(256), 0, st, p);
+  }
+  return hipGetLastError();
+}
+
+}  // namespace gdn

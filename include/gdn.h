@@ -71,7 +71,8 @@ typedef enum {
   GDN_E_HIP = 4          /* a HIP launch or query failed */
 } gdn_status;
 
-typedef enum { GDN_F32 = 0, GDN_BF16 = 1 } gdn_dtype;
+/* GDN_E4M3: the 8-bit rows of gdn_linear_fwd alone. */
+typedef enum { GDN_F32 = 0, GDN_BF16 = 1, GDN_E4M3 = 2 } gdn_dtype;
 
 /* Arguments shared by forward and backward. */
 typedef struct {
@@ -544,6 +545,53 @@ gdn_status gdn_addnorm_fwd(const gdn_addnorm_fwd_args* args, void* stream);
 size_t gdn_addnorm_bwd_workspace_size(const gdn_addnorm_bwd_args* args);
 gdn_status gdn_addnorm_bwd(const gdn_addnorm_bwd_args* args, void* stream);
 gdn_status gdn_quant_rows(const gdn_quant_args* args, void* stream);
+
+/* Projection with its epilogue, rows of K to rows of N:
+ *     v = x w^T + bias,   y = act(v) + r
+ * act: none, SiLU, or GELU in its tanh form, v sigmoid(2 sqrt(2 / pi) (v + 0.044715 v^3)).
+ * With GDN_E4M3, x and w are 8-bit rows as gdn_quant_rows makes them (a scale a token,
+ * a scale an output), bias, r and y in out_dtype, and no gradient exists.  Sums are fp32
+ * (products of bf16 and 8 bits are exact), rounded once into y.  The gradient's dy act'(v)
+ * is rounded to dtype before its products (bf16: it is their operand); dbias sums it unrounded.
+ * M below 2^31; rows of x and w below 2^23 bytes. */
+typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_GELU = 2 } gdn_act;
+typedef struct {
+  int32_t dtype;               /* of x and w (dx, dw): GDN_BF16, GDN_F32, or GDN_E4M3 */
+  int32_t out_dtype;           /* of bias, r and y (dy, dbias): dtype, or with GDN_E4M3 either */
+  int64_t M;
+  int32_t N, K;
+  const void* x;               /* [M, K] */
+  int64_t x_stride;
+  const void* w;               /* [N, K], contiguous */
+  const float* x_scale;        /* [M], with GDN_E4M3 */
+  const float* w_scale;        /* [N], with GDN_E4M3 */
+  const void* bias;            /* nullable [N] */
+  const void* r;               /* nullable [M, N] */
+  int64_t r_stride;
+  int32_t act;                 /* gdn_act */
+  void* workspace;
+  size_t workspace_bytes;
+} gdn_linear_args;
+
+typedef struct {
+  gdn_linear_args a;
+  void* y;                     /* [M, N], written */
+  float* v_save;               /* nullable [M, N], written: v in fp32, for gdn_linear_bwd with an activation */
+} gdn_linear_fwd_args;
+
+typedef struct {
+  gdn_linear_args a;           /* bias and r are not read */
+  const float* v_saved;        /* v_save of the forward; needed with an activation */
+  const void* dy;              /* [M, N] */
+  void* dx;                    /* nullable [M, K], written */
+  void* dw;                    /* nullable [N, K], written */
+  void* dbias;                 /* nullable [N], written */
+} gdn_linear_bwd_args;
+
+size_t gdn_linear_fwd_workspace_size(const gdn_linear_fwd_args* args);
+size_t gdn_linear_bwd_workspace_size(const gdn_linear_bwd_args* args);
+gdn_status gdn_linear_fwd(const gdn_linear_fwd_args* args, void* stream);
+gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* args, void* stream);
 
 /* Gated linear recurrence over [B, T, D], channels last: per sequence and channel
  *     L_t = g_t,  m_t = 1;   or with scale:  L_t = -scale sigmoid(g_t),  m_t = sqrt(1 - exp(2 L_t))
