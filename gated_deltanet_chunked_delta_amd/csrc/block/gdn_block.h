@@ -187,7 +187,7 @@ struct GemmParams {
 };
 // How a product is divided: tiles of 256 x 256 or 128 x 128, splits along k.
 struct GemmPlan { int tile, splits, steps; };
-GemmPlan gemm_plan(int64_t M, int N, int64_t kbytes, int cus);
+GemmPlan gemm_plan(int64_t M, int N, int64_t kbytes, int esize, int cus);
 inline size_t gemm_part_bytes(const GemmPlan& g, int64_t M, int N) { return g.splits > 1 ? 4ull * g.splits * M * N : 0; }
 hipError_t launch_gemm(int dtype, int out_dtype, const GemmParams& p, const GemmPlan& g, hipStream_t st);
 // Few rows: a workgroup to 16 outputs, its waves along k.  Any strides and alignment.

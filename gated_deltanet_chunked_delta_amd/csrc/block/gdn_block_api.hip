@@ -164,7 +164,7 @@ LinearPlan linear_plan(const gdn_linear_args& a) {
     const int64_t row = row16(a.K, a.dtype);
     if (!rows_fit(a.x, a.x_stride, a.K, a.dtype)) p.o_x = take((size_t)a.M * row);
     if (!rows_fit(a.w, a.K, a.K, a.dtype)) p.o_w = take((size_t)a.N * row);
-    p.g = gdn::gemm_plan(a.M, a.N, row, cu_count());
+    p.g = gdn::gemm_plan(a.M, a.N, row, (int)bytes_of(a.dtype), cu_count());
     p.o_part = take(gdn::gemm_part_bytes(p.g, a.M, a.N));
   }
   p.total = std::max<size_t>(off, 16);
@@ -186,13 +186,13 @@ LinearBwdPlan linear_bwd_plan(const gdn_linear_bwd_args& b) {
   size_t part = 0;
   if (b.dx) {
     p.o_w_t = take((size_t)a.K * rn);
-    p.gx = gdn::gemm_plan(a.M, a.K, rn, cu_count());
+    p.gx = gdn::gemm_plan(a.M, a.K, rn, (int)bytes_of(a.dtype), cu_count());
     part = gdn::gemm_part_bytes(p.gx, a.M, a.K);
   }
   if (b.dw) {
     p.o_pre_t = take((size_t)a.N * rm);
     p.o_x_t = take((size_t)a.K * rm);
-    p.gw = gdn::gemm_plan(a.N, a.K, rm, cu_count());
+    p.gw = gdn::gemm_plan(a.N, a.K, rm, (int)bytes_of(a.dtype), cu_count());
     part = std::max(part, gdn::gemm_part_bytes(p.gw, a.N, a.K));
   }
   if (b.dbias) p.o_sums = take(4 * (size_t)((a.M + 63) / 64) * a.N);

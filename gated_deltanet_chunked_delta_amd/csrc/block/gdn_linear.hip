@@ -29,7 +29,22 @@ template <> struct ElemOf<GDN_BF16> { typedef bf16 type; };
 
 // One lane's two pieces of a row, and the product of two 16-row blocks over one step.
 struct Pieces { u32x4 lo, hi; };
-template <int T>
+// Sixteen 8-bit values as bf16, which holds each of them.
+__device__ __forceinline__ void widen(u32x4 v, bf16x8& lo, bf16x8& hi) {
+  typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 pair;
+  pair t[8];
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    t[2 * j] = __builtin_bit_cast(pair, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[j], 1.f, false));
+    t[2 * j + 1] = __builtin_bit_cast(pair, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp8(v[j], 1.f, true));
+  }
+  lo = bf16x8{t[0][0], t[0][1], t[1][0], t[1][1], t[2][0], t[2][1], t[3][0], t[3][1]};
+  hi = bf16x8{t[4][0], t[4][1], t[5][0], t[5][1], t[6][0], t[6][1], t[7][0], t[7][1]};
+}
+// EXACT (8-bit rows with fp32 outputs): the 8-bit matrix instructions' sums carry about 17
+// bits (measured 1.3e-5 of the result against 64 bits, of either instruction), enough for a
+// bf16 result and not for an fp32 one; there the values are widened to bf16.
+template <int T, bool EXACT = false>
 __device__ __forceinline__ void mma_step(f32x4& acc, const Pieces& a, const Pieces& b) {
   if constexpr (T == GDN_BF16) {
     acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a.lo), __builtin_bit_cast(bf16x8, b.lo), acc, 0, 0, 0);
@@ -41,6 +56,14 @@ __device__ __forceinline__ void mma_step(f32x4& acc, const Pieces& a, const Piec
     for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(al[j], bl[j], acc, 0, 0, 0);
 #pragma unroll
     for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x4f32(ah[j], bh[j], acc, 0, 0, 0);
+  } else if constexpr (EXACT) {
+    bf16x8 al[4], bl[4];
+    widen(a.lo, al[0], al[1]);
+    widen(a.hi, al[2], al[3]);
+    widen(b.lo, bl[0], bl[1]);
+    widen(b.hi, bl[2], bl[3]);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_f32_16x16x32_bf16(al[j], bl[j], acc, 0, 0, 0);
   } else {  // e4m3: 128 values of k at the full 8-bit rate, block scales of 1 (2^(127 - 127))
     const i32x8 av = {(int)a.lo[0], (int)a.lo[1], (int)a.lo[2], (int)a.lo[3], (int)a.hi[0], (int)a.hi[1], (int)a.hi[2], (int)a.hi[3]};
     const i32x8 bv = {(int)b.lo[0], (int)b.lo[1], (int)b.lo[2], (int)b.lo[3], (int)b.hi[0], (int)b.hi[1], (int)b.hi[2], (int)b.hi[3]};
@@ -48,17 +71,17 @@ __device__ __forceinline__ void mma_step(f32x4& acc, const Pieces& a, const Piec
   }
 }
 
-// act(v); derivative in d
-template <bool D>
+// act(v); derivative in d.  E: the type that the result is rounded to
+template <class E, bool D>
 __device__ __forceinline__ float act_of(int act, float v, float& d) {
   if (act == GDN_ACT_SILU) {
-    const float s = fast_sigmoid<float>(v);
+    const float s = fast_sigmoid<E>(v);
     if (D) d = dsilu_gate(v, s);
     return v * s;
   }
   if (act == GDN_ACT_GELU) {
     constexpr float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-    const float s = fast_sigmoid<float>(c * fmaf(0.044715f * v * v, v, v));
+    const float s = fast_sigmoid<E>(c * fmaf(0.044715f * v * v, v, v));
     if (D) d = fmaf(v * (s - s * s), c * fmaf(3.f * 0.044715f * v, v, 1.f), s);
     return v * s;
   }
@@ -92,7 +115,7 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int N, int
   if (e.act) {
     float d;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] = act_of<false>(e.act, f[i], d);
+    for (int i = 0; i < 4; ++i) f[i] = act_of<O, false>(e.act, f[i], d);
   }
   if (e.r) {
     ld_part<4>(static_cast<const O*>(e.r) + m * e.r_stride + n, c, t);
@@ -107,6 +130,81 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int N, int
     for (int i = 0; i < c; ++i) p[i] = to_e<O>(f[i]);
   }
 }
+
+// Sixteen outputs side by side of each of a lane's rows: what belongs to the columns is
+// loaded once, and one branch decides for all sixteen (a tile's epilogue runs while its
+// compute unit's matrix cores wait).
+template <class O>
+struct Columns {
+  float b[16], ws[16];
+  int n, c;
+  __device__ __forceinline__ Columns(const Epilogue& e, int N, int n_) : n(n_), c(N - n_) {
+    if (c < 16) return;
+#pragma unroll
+    for (int j = 0; j < 16; j += 4) {
+      float t[4] = {};
+      if (e.bias) ld_full<4>(static_cast<const O*>(e.bias) + n + j, t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) b[j + i] = t[i];
+      if (e.w_scale) ld_full<4>(e.w_scale + n + j, t);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) ws[j + i] = t[i];
+    }
+  }
+  __device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int N, const f32x4 (&v)[4]) const {
+    if (c < 16) {
+#pragma unroll
+      for (int j = 0; j < 4; ++j) finish4<O>(e, m, N, n + 4 * j, v[j]);
+      return;
+    }
+    float f[16];
+#pragma unroll
+    for (int j = 0; j < 16; ++j) f[j] = v[j / 4][j % 4];
+    if (e.x_scale) {
+      const float xs = e.x_scale[m];
+#pragma unroll
+      for (int j = 0; j < 16; ++j) f[j] *= xs * ws[j];
+    }
+    if (e.bias) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) f[j] += b[j];
+    }
+    const int64_t at = m * N + n;
+    if (e.v_save) {
+#pragma unroll
+      for (int j = 0; j < 16; j += 4)
+        reinterpret_cast<f32x4_any*>(e.v_save + at)[j / 4] = f32x4{f[j], f[j + 1], f[j + 2], f[j + 3]};
+    }
+    float d;
+    if (e.act == GDN_ACT_SILU) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) f[j] = act_of<O, false>(GDN_ACT_SILU, f[j], d);
+    } else if (e.act == GDN_ACT_GELU) {
+#pragma unroll
+      for (int j = 0; j < 16; ++j) f[j] = act_of<O, false>(GDN_ACT_GELU, f[j], d);
+    }
+    constexpr int V = 16 / (int)sizeof(O);
+    if (e.r) {
+#pragma unroll
+      for (int j = 0; j < 16; j += V) {
+        float t[V];
+        ld_full<V>(static_cast<const O*>(e.r) + m * e.r_stride + n + j, t);
+#pragma unroll
+        for (int i = 0; i < V; ++i) f[j + i] += t[i];
+      }
+    }
+    O* p = static_cast<O*>(e.out) + at;
+#pragma unroll
+    for (int j = 0; j < 16; j += V) {
+      if constexpr (V == 8) {
+        const float t[8] = {f[j], f[j + 1], f[j + 2], f[j + 3], f[j + 4], f[j + 5], f[j + 6], f[j + 7]};
+        *reinterpret_cast<bf16x8_any*>(p + j) = VecIO<bf16, 8>::pack(t);
+      } else {
+        *reinterpret_cast<f32x4_any*>(p + j) = f32x4{f[j], f[j + 1], f[j + 2], f[j + 3]};
+      }
+    }
+  }
+};
 
 // A tile's operand: where its rows start, how far they reach (below 2^31 bytes).
 constexpr uint32_t PAST_END = 0x80000000u;
@@ -213,29 +311,36 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmParams p) {
       a.lo = *reinterpret_cast<const u32x4*>(pa + i * 2048 + ((q ^ sa) << 4));
       a.hi = *reinterpret_cast<const u32x4*>(pa + i * 2048 + (((q + 4) ^ sa) << 4));
 #pragma unroll
-      for (int j = 0; j < TN; ++j) mma_step<T>(acc[i][j], b[j], a);
+      for (int j = 0; j < TN; ++j) mma_step<T, sizeof(O) == 4>(acc[i][j], b[j], a);
     }
     lds_wait();
     __syncthreads();
     buf ^= 1;
   }
   const int n = n0 + wn * 64 + 16 * q;
+  if (n >= p.N) return;
+  if (p.splits > 1) {
 #pragma unroll
-  for (int i = 0; i < TM; ++i) {
-    const int64_t m = m0 + (wm * TM + i) * 16 + r16;
-    if (m >= p.M) continue;
+    for (int i = 0; i < TM; ++i) {
+      const int64_t m = m0 + (wm * TM + i) * 16 + r16;
+      if (m >= p.M) break;
 #pragma unroll
-    for (int j = 0; j < TN; ++j) {
-      if (p.splits > 1) {
+      for (int j = 0; j < TN; ++j) {
         float* t = p.part + (split * p.M + m) * p.N + n + 4 * j;
         const int c = p.N - n - 4 * j;
         if (c >= 4) *reinterpret_cast<f32x4_any*>(t) = acc[i][j];
         else
           for (int x = 0; x < c; ++x) t[x] = acc[i][j][x];
-      } else {
-        finish4<O>(p.e, m, p.N, n + 4 * j, acc[i][j]);
       }
     }
+    return;
+  }
+  const Columns<O> cols(p.e, p.N, n);
+#pragma unroll
+  for (int i = 0; i < TM; ++i) {
+    const int64_t m = m0 + (wm * TM + i) * 16 + r16;
+    if (m >= p.M) break;
+    cols.finish(p.e, m, p.N, acc[i]);
   }
 }
 
@@ -295,7 +400,7 @@ __global__ __launch_bounds__(512) void skinny_kernel(SkinnyParams p) {
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < MT; ++i) mma_step<T>(acc[i], b[u], a[u][i]);
+      for (int i = 0; i < MT; ++i) mma_step<T, sizeof(O) == 4>(acc[i], b[u], a[u][i]);
   }
 #pragma unroll
   for (int i = 0; i < MT; ++i) red[w][i][lane] = acc[i];
@@ -311,7 +416,17 @@ __global__ __launch_bounds__(512) void skinny_kernel(SkinnyParams p) {
   }
 }
 
-// 64 x 64 elements a workgroup.
+// Eight elements at p, which is aligned to four of them or more; rows of copies hold whole
+// 16 bytes, so only fp32's may end after four.
+__device__ __forceinline__ void put8(float* p, const float (&f)[8], bool both) {
+  *reinterpret_cast<f32x4*>(p) = f32x4{f[0], f[1], f[2], f[3]};
+  if (both) *reinterpret_cast<f32x4*>(p + 4) = f32x4{f[4], f[5], f[6], f[7]};
+}
+__device__ __forceinline__ void put8(bf16* p, const float (&f)[8], bool) { store_vec<bf16, 8>(p, f); }
+
+// 64 x 64 elements a workgroup, eight side by side a thread and access in either
+// direction: eight threads fill 128 bytes of a row, and of a turned row.  Stride 65 puts
+// the 64 values that a wave touches at once on 64 banks both ways.
 template <class E>
 __global__ __launch_bounds__(256) void pack_kernel(PackParams p) {
   __shared__ float tile[64][65];
@@ -319,51 +434,48 @@ __global__ __launch_bounds__(256) void pack_kernel(PackParams p) {
   const int64_t blk = block_2d(), br = blk / cols_n;
   const int64_t r0 = br * 64;
   const int c0 = (int)(blk - br * cols_n) * 64;
-  // (rows up to the end of the turned copy's padding)
-  if (r0 >= (p.R + 63) / 64 * 64) return;
-  const int tr = threadIdx.x / 4, tc = threadIdx.x % 4 * 16;
-  const int64_t r = r0 + tr;
-  float f[4][4];
+  if (r0 >= p.R) return;
+  const int ti = threadIdx.x / 8, tj = threadIdx.x % 8 * 8;
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    const int c = c0 + tc + 4 * h;
-#pragma unroll
-    for (int e = 0; e < 4; ++e) f[h][e] = 0.f;
+  for (int h = 0; h < 2; ++h) {
+    const int64_t r = r0 + ti + 32 * h;
+    const int c = c0 + tj;
+    float f[8] = {};
     if (r < p.R && c < p.C) {
-      ld_part<4>(static_cast<const E*>(p.in) + r * p.ld + c, p.C - c, f[h]);
+      ld_part<8>(static_cast<const E*>(p.in) + r * p.ld + c, p.C - c, f);
       if (p.v) {
-        float v[4];
-        ld_part<4>(p.v + r * p.C + c, p.C - c, v);
+        float v[8];
+        ld_part<8>(p.v + r * p.C + c, p.C - c, v);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
+        for (int e = 0; e < 8; ++e) {
           float d;
-          act_of<true>(p.act, v[e], d);
-          f[h][e] *= d;
+          act_of<E, true>(p.act, v[e], d);
+          f[e] *= d;
         }
       }
     }
-    if (p.rows && r < p.R && c < p.ldo) st_part<4>(static_cast<E*>(p.rows) + r * p.ldo + c, (int)(p.ldo - c), f[h]);
+    if (p.rows && r < p.R && c < p.ldo) put8(static_cast<E*>(p.rows) + r * p.ldo + c, f, c + 8 <= p.ldo);
 #pragma unroll
-    for (int e = 0; e < 4; ++e) tile[tr][tc + 4 * h + e] = f[h][e];
+    for (int e = 0; e < 8; ++e) tile[ti + 32 * h][tj + e] = f[e];
   }
   if (!p.cols && !p.sums) return;
   __syncthreads();
-  const int c = c0 + tr;  // a column a thread now, 16 rows of it
-  float s = 0.f;
 #pragma unroll
-  for (int h = 0; h < 4; ++h) {
-    float g[4];
+  for (int h = 0; h < 2; ++h) {
+    const int c = c0 + ti + 32 * h;
+    float g[8], s = 0.f;
 #pragma unroll
-    for (int e = 0; e < 4; ++e) {
-      g[e] = tile[tc + 4 * h + e][tr];
+    for (int e = 0; e < 8; ++e) {
+      g[e] = tile[tj + e][ti + 32 * h];
       s += g[e];
     }
-    const int64_t rr = r0 + tc + 4 * h;
-    if (p.cols && c < p.C && rr < p.ldt) st_part<4>(static_cast<E*>(p.cols) + c * p.ldt + rr, (int)min((int64_t)4, p.ldt - rr), g);
+    if (p.cols && c < p.C && r0 + tj < p.ldt) put8(static_cast<E*>(p.cols) + c * p.ldt + r0 + tj, g, r0 + tj + 8 <= p.ldt);
+    if (p.sums) {
+#pragma unroll
+      for (int o = 1; o < 8; o <<= 1) s += __shfl_xor(s, o, 64);
+      if (c < p.C && tj == 0) p.sums[br * p.C + c] = s;
+    }
   }
-  s += quad_xor<1>(s);
-  s += quad_xor<2>(s);
-  if (p.sums && c < p.C && threadIdx.x % 4 == 0) p.sums[br * p.C + c] = s;
 }
 // Bytes copied row by row (8-bit rows).
 __global__ __launch_bounds__(256) void pack_bytes_kernel(PackParams p) {
@@ -395,20 +507,39 @@ hipError_t skinny_any(const SkinnyParams& p, hipStream_t st) {
 
 }  // namespace
 
-// Tiles of 256 x 256 where they fill the chip, else of 128 x 128; k is split where even
-// those leave compute units without work and the parts stay long.
-GemmPlan gemm_plan(int64_t M, int N, int64_t kbytes, int cus) {
-  GemmPlan g{256, 1, (int)((kbytes + 127) / 128)};
-  auto tiles = [&](int t) { return (M + t - 1) / t * ((N + t - 1) / t); };
-  if (tiles(256) < cus * 3 / 4) g.tile = 128;
-  const int64_t t = tiles(g.tile);
-  if (t < cus) {
-    const int most = (int)std::max<int64_t>(1, std::min<int64_t>({2 * cus / t, g.steps / 8, 16}));
-    g.steps = (g.steps + most - 1) / most;
-    g.splits = (int)(((kbytes + 127) / 128 + g.steps - 1) / std::max(g.steps, 1));
-    g.splits = std::max(g.splits, 1);
+// The cheapest of both tiles and a few splits of k, by a model of their times in us that
+// was fitted to bf16 products of 64 to 16,384 rows (a step: 128 bytes of k).  A round of
+// 256 x 256 tiles, one a compute unit, takes 1.8 a step and 8 to start and end; 128 x 128
+// tiles take 0.69 and 5 one a compute unit, 1.1 and 6 two.  Splits add a join: its bytes,
+// and a launch.  Measured against the other choice: 4,096 x 2,048 -> 2,048 in tiles of 128
+// 37 us, of 256 60; 8,192 rows 73 and 67; 128 rows -> 6,144 in 4 parts 20, whole 25; a sum
+// over 32,768 to 2,048 x 2,048 of 256 in 4 parts 276, whole 652, of 128 in 2 parts 310.
+GemmPlan gemm_plan(int64_t M, int N, int64_t kbytes, int esize, int cus) {
+  const int steps = (int)((kbytes + 127) / 128);
+  const double slow = esize == 4 ? 8. : 1.;  // fp32's matrix instructions against bf16's
+  GemmPlan best{256, 1, steps};
+  double least = 0.;
+  for (int tile : {256, 128}) {
+    const int64_t tiles = (M + tile - 1) / tile * ((N + tile - 1) / tile);
+    for (int s = 1; s <= 16 && (s == 1 || (s <= steps / 8 && tiles * s <= 4 * (int64_t)cus)); s *= 2) {
+      const double k = (steps + s - 1) / s * slow;
+      const int64_t n = tiles * s;
+      double t;
+      if (tile == 256) {
+        t = (double)((n + cus - 1) / cus) * (1.8 * k + 8.);
+      } else {
+        const int64_t rest = n % (2 * cus);
+        t = (double)(n / (2 * cus)) * (1.1 * k + 6.) + (rest == 0 ? 0. : rest <= cus ? 0.69 * k + 5. : 1.1 * k + 6.);
+      }
+      if (s > 1) t += 4. + (double)M * N * (8. * s + 2.) / 4e6;
+      if (least == 0. || t < least) {
+        least = t;
+        best = GemmPlan{tile, s, (steps + s - 1) / s};
+      }
+    }
   }
-  return g;
+  if (best.steps > 0) best.splits = std::max(1, (steps + best.steps - 1) / best.steps);  // none of them empty
+  return best;
 }
 hipError_t launch_gemm(int dtype, int out_dtype, const GemmParams& p, const GemmPlan& g, hipStream_t st) {
   if (dtype == GDN_BF16) return gemm_any<GDN_BF16, bf16>(p, g, st);
