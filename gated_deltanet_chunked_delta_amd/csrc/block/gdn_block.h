@@ -125,16 +125,15 @@ struct RecParams {
   const float* h0;           // nullable [N][D]
   const int32_t* cu;         // nullable [N+1]
   int T, D, N, tokens;
-  int chunk, nchunk;         // tokens of a chunk (REC_SUB times 1, 2, 4 or 8)
-  float2* sum;               // [nchunk][D]: what a chunk makes of the state entering it
-  float* enter;              // [nchunk][D]: that state
+  int nchunk;                // chunks of REC_W REC_FS tokens (backward: REC_W REC_BS)
+  uint64_t* words;           // rec_words(nchunk, D): counters, the chunks' pairs, the groups' ends; null for one chunk
+  float* enter;              // [ceil(tokens / REC_STATE)][D]: the state before every REC_STATE tokens; nullable forwards
   // forward
-  void* y;
+  void* y;                   // nullable
   float* hT;                 // nullable [N][D]
   // backward
   const void* dy;
   const float* dhT;          // nullable
-  float* carry;              // [nchunk][D]: gradient of the state leaving a chunk, from the tokens behind it
   void* dx;
   void* dg;
   void* di;                  // nullable
@@ -153,9 +152,12 @@ struct RecStepParams {
   int num_slots, N, D;
   void* y;
 };
-constexpr int REC_SUB = 16;  // tokens that a thread of the gradient holds
-hipError_t launch_rec_sum(int dtype, const RecParams& p, bool rev, hipStream_t st);   // chunks -> sum
-hipError_t launch_rec_join(const RecParams& p, bool rev, hipStream_t st);             // sum -> enter or carry
+constexpr int REC_W = 8;                    // waves of a chunk
+constexpr int REC_BYTES = 4;               // of a token's row that a thread takes
+constexpr int REC_FS = 16, REC_BS = 8;      // tokens that a thread holds, forwards and backwards
+constexpr int REC_STATE = REC_W * REC_BS;   // tokens between saved states: one a chunk backwards
+static_assert(REC_STATE % REC_FS == 0 && REC_W * REC_FS % REC_STATE == 0, "a wave's first token is before a saved state or not");
+int64_t rec_words(int nchunk, int D);
 hipError_t launch_rec_fwd(int dtype, const RecParams& p, hipStream_t st);
 hipError_t launch_rec_bwd(int dtype, const RecParams& p, hipStream_t st);
 hipError_t launch_rec_step(int dtype, const RecStepParams& p, hipStream_t st);

@@ -65,56 +65,43 @@ gdn_status check_rec(const gdn_rec_args& a) {
     return fail(GDN_E_INVALID, "a pointer is misaligned");
   return GDN_OK;
 }
-// Tokens of a chunk: long chunks leave fewer states, short ones more waves.  The
-// longest that still gives every compute unit sixteen waves.
-int rec_chunk(const gdn_rec_args& a) {
-  const int64_t tokens = (int64_t)a.B * a.T, per = 64 * 4 / (int64_t)esize(a.dtype), wide = (a.D + per - 1) / per;
-  int c = gdn::REC_SUB;
-  while (c < 8 * gdn::REC_SUB && (tokens + 2 * c - 1) / (2 * c) * wide >= 16ll * cu_count()) c *= 2;
-  return c;
-}
+int64_t rec_chunks(const gdn_rec_args& a, int tokens) { return ((int64_t)a.B * a.T + tokens - 1) / tokens; }
 struct RecPlan {
-  int chunk, nchunk;
-  size_t o_sum = 0, o_enter = 0, o_carry = 0, o_part = 0, total = 0;
+  int fwd, bwd;  // chunks
+  size_t o_words = 0, o_enter = 0, o_part = 0, total = 0;
 };
 RecPlan rec_plan(const gdn_rec_args& a, bool bwd, bool own_states) {
   RecPlan p;
-  p.chunk = rec_chunk(a);
-  p.nchunk = (int)(((int64_t)a.B * a.T + p.chunk - 1) / p.chunk);
+  p.fwd = (int)rec_chunks(a, gdn::REC_W * gdn::REC_FS);
+  p.bwd = (int)rec_chunks(a, gdn::REC_W * gdn::REC_BS);
   size_t off = 0;
   auto take = [&](size_t bytes) { size_t o = off; off += align_up(bytes); return o; };
-  const size_t rows = (size_t)p.nchunk * a.D;
-  p.o_sum = take(8 * rows);
-  if (own_states) p.o_enter = take(4 * rows);
+  p.o_words = take(8 * (size_t)gdn::rec_words(bwd ? p.bwd : p.fwd, a.D));
   if (bwd) {
-    p.o_carry = take(4 * rows);
-    if (a.scale) p.o_part = take(4 * rows);
+    const size_t rows = 4 * (size_t)p.bwd * a.D;
+    if (own_states) p.o_enter = take(rows);
+    if (a.scale) p.o_part = take(rows);
   }
-  p.total = std::max<size_t>(off, 16);
+  p.total = off;
   return p;
 }
 gdn_status check_rec_grid(const gdn_rec_args& a, const RecPlan& pl) {
-  const double per = 64. * 4 / esize(a.dtype);
-  if (!launchable(((double)pl.nchunk + a.num_seqs) * std::ceil(a.D / per) * 4 * pl.chunk))
-    return fail(GDN_E_INVALID, "problem too large: %d chunks and %d sequences of %d channels", pl.nchunk, a.num_seqs, a.D);
+  const double per = 64. * gdn::REC_BYTES / esize(a.dtype);
+  if (!launchable(((double)pl.bwd + a.num_seqs) * std::ceil(a.D / per) * 64 * gdn::REC_W))
+    return fail(GDN_E_INVALID, "problem too large: %d chunks and %d sequences of %d channels", pl.bwd, a.num_seqs, a.D);
   return GDN_OK;
 }
-gdn::RecParams rec_params(const gdn_rec_args& a, const RecPlan& pl) {
+gdn::RecParams rec_params(const gdn_rec_args& a, const RecPlan& pl, int nchunk) {
   gdn::RecParams p{};
   p.x = a.x; p.g = a.g; p.i = a.i; p.x_stride = a.x_stride; p.g_stride = a.g_stride; p.i_stride = a.i_stride;
   p.g_f32 = a.g_dtype == GDN_F32; p.scale = a.scale; p.h0 = a.h0; p.cu = a.cu_seqlens;
-  p.T = a.T; p.D = a.D; p.N = a.num_seqs; p.tokens = a.B * a.T; p.chunk = pl.chunk; p.nchunk = pl.nchunk;
-  p.sum = at<float2>(a.workspace, pl.o_sum);
+  p.T = a.T; p.D = a.D; p.N = a.num_seqs; p.tokens = a.B * a.T; p.nchunk = nchunk;
+  p.words = nchunk > 1 ? at<uint64_t>(a.workspace, pl.o_words) : nullptr;
   return p;
 }
-// States entering the chunks (rev: gradients leaving them).  One chunk starts with its
-// sequences: nothing enters it.
-gdn_status rec_states(const gdn_rec_args& a, const gdn::RecParams& p, bool rev, hipStream_t s) {
-  if (p.nchunk <= 1) return GDN_OK;
-  hipError_t e = timed(rev ? "rec_rev_sum" : "rec_sum", s, [&] { return gdn::launch_rec_sum(a.dtype, p, rev, s); });
-  if (e != hipSuccess) return hip_fail(e, "recurrence chunk launch");
-  e = timed("rec_join", s, [&] { return gdn::launch_rec_join(p, rev, s); });
-  return e == hipSuccess ? GDN_OK : hip_fail(e, "recurrence join launch");
+gdn_status run_rec_fwd(const gdn_rec_args& a, const gdn::RecParams& p, hipStream_t s) {
+  hipError_t e = timed("rec_fwd", s, [&] { return gdn::launch_rec_fwd(a.dtype, p, s); });
+  return e == hipSuccess ? GDN_OK : hip_fail(e, "recurrence launch");
 }
 
 // ---------------------------------------------------------------- products
@@ -305,7 +292,7 @@ size_t gdn_rec_bwd_workspace_size(const gdn_rec_bwd_args* args) {
 size_t gdn_rec_states_bytes(const gdn_rec_args* a) {
   if (!a) { fail(GDN_E_INVALID, "null args"); return 0; }
   if (check_rec(*a) != GDN_OK) return 0;
-  return std::max<size_t>(16, 4 * (size_t)rec_plan(*a, false, false).nchunk * a->D);
+  return std::max<size_t>(16, 4 * (size_t)rec_plan(*a, false, false).bwd * a->D);
 }
 
 gdn_status gdn_rec_fwd(const gdn_rec_fwd_args* args, void* stream) {
@@ -319,13 +306,11 @@ gdn_status gdn_rec_fwd(const gdn_rec_fwd_args* args, void* stream) {
   if (gdn_status st = check_rec_grid(a, pl); st != GDN_OK) return st;
   if (gdn_status st = check_ws(a.workspace, a.workspace_bytes, pl.total); st != GDN_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  gdn::RecParams p = rec_params(a, pl);
-  p.enter = args->h_save ? args->h_save : at<float>(a.workspace, pl.o_enter);
+  gdn::RecParams p = rec_params(a, pl, pl.fwd);
+  p.enter = args->h_save;
   p.y = args->y;
   p.hT = args->hT;
-  if (gdn_status st = rec_states(a, p, false, s); st != GDN_OK) return st;
-  hipError_t e = timed("rec_fwd", s, [&] { return gdn::launch_rec_fwd(a.dtype, p, s); });
-  return e == hipSuccess ? GDN_OK : hip_fail(e, "recurrence launch");
+  return run_rec_fwd(a, p, s);
 }
 
 gdn_status gdn_rec_bwd(const gdn_rec_bwd_args* args, void* stream) {
@@ -343,21 +328,20 @@ gdn_status gdn_rec_bwd(const gdn_rec_bwd_args* args, void* stream) {
   if (gdn_status st = check_rec_grid(a, pl); st != GDN_OK) return st;
   if (gdn_status st = check_ws(a.workspace, a.workspace_bytes, pl.total); st != GDN_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
-  gdn::RecParams p = rec_params(a, pl);
-  p.dy = args->dy; p.dhT = args->dhT; p.dx = args->dx; p.dg = args->dg; p.di = args->di; p.dh0 = args->dh0;
-  p.carry = at<float>(a.workspace, pl.o_carry);
-  p.part = a.scale ? at<float>(a.workspace, pl.o_part) : nullptr;
-  if (args->h_saved) {
-    p.enter = const_cast<float*>(args->h_saved);
-  } else {
+  gdn::RecParams p = rec_params(a, pl, pl.bwd);
+  p.enter = const_cast<float*>(args->h_saved);
+  if (!args->h_saved) {  // the forward pass's states alone; its words lie where the gradient's will
     p.enter = at<float>(a.workspace, pl.o_enter);
-    if (gdn_status st = rec_states(a, p, false, s); st != GDN_OK) return st;
+    gdn::RecParams f = rec_params(a, pl, pl.fwd);
+    f.enter = p.enter;
+    if (gdn_status st = run_rec_fwd(a, f, s); st != GDN_OK) return st;
   }
-  if (gdn_status st = rec_states(a, p, true, s); st != GDN_OK) return st;
+  p.dy = args->dy; p.dhT = args->dhT; p.dx = args->dx; p.dg = args->dg; p.di = args->di; p.dh0 = args->dh0;
+  p.part = a.scale ? at<float>(a.workspace, pl.o_part) : nullptr;
   hipError_t e = timed("rec_bwd", s, [&] { return gdn::launch_rec_bwd(a.dtype, p, s); });
   if (e != hipSuccess) return hip_fail(e, "recurrence gradient launch");
   if (!a.scale) return GDN_OK;
-  e = timed("rec_dscale", s, [&] { return gdn::launch_join_parts(GDN_F32, p.part, pl.nchunk, a.D, args->dscale, s); });
+  e = timed("rec_dscale", s, [&] { return gdn::launch_join_parts(GDN_F32, p.part, pl.bwd, a.D, args->dscale, s); });
   return e == hipSuccess ? GDN_OK : hip_fail(e, "scale gradient launch");
 }
 

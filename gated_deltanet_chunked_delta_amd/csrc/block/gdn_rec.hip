@@ -6,21 +6,39 @@
 //   dx = dh m s,  di = dh m x s (1 - s),
 //   dL = a dh h_{t-1} - [with scale] dh s x a^2 / m,   dg = dL  or  -dL scale sigmoid'(g)
 //
-// Bound: memory.  All sequences of a call lie along one axis of tokens, which is cut
-// into chunks whatever the sequences' lengths.  What a chunk makes of the state that
-// enters it is one pair per channel, (A, U): A h + U -- or U alone where a sequence
-// starts inside, marked by A = -1 (a product of decays is never negative), so that a
-// value that is not finite reaches no other sequence.  One kernel forms the pairs, one
-// joins them to the states entering the chunks, one walks every chunk again from there.
-// The gradient's chain runs the other way with pairs of its own: in token order its
-// U is the sum of dy_t times the decays up to t, cut off at the first sequence's end.
+// Bound: memory, with nearly as much arithmetic (some 60 instructions an element, four
+// or five of them transcendental).  So every input is read once and every gate formed
+// once: a workgroup takes a chunk of tokens of 64 lanes' channels, a wave to every S
+// tokens, and holds decays and inputs in registers while it waits for the state that
+// enters its chunk.  All sequences of a call lie along one axis of tokens, whatever their
+// lengths.  What a chunk (or a wave's part) makes of the state entering it is one pair per
+// channel, (A, U): A h + U -- or U alone where a sequence starts inside, marked by A = -1
+// (a product of decays is never negative), so that a value that is not finite reaches no
+// other sequence.
+//
+// Chunks hand their pairs on through global words of 64 bits, written and read whole by
+// relaxed atomics past the dies' caches; a word of zeros is not written yet.  Chunks lie
+// in groups: a chunk composes the pairs of its group's chunks before it, in order, and
+// applies them to the state that leaves the group before, which that group's last chunk
+// writes.  Which words are read does not depend on time, so results do not either.  Every
+// wait ends: workgroups of the same channels number themselves by a counter when they
+// start, and wait only for words of lower numbers, whose workgroups run already and wait for
+// none above theirs.
+// The gradient's chain runs the other way with pairs of its own: in token order its U is
+// the sum of dy_t times the decays up to t, cut off at the first sequence's end.
+//
+// Measured (bf16, scale and i): 65,536 tokens of 2,048 channels in 326 us (1.07 GB, 3.3
+// TB/s; three kernels that read the inputs twice: 950), its gradient in 697 (1.88 GB, 2.7
+// TB/s); 16,384 of 2,304 in 95 and 197 us.  Four bytes of a row a thread and 16 (gradient: 8)
+// tokens: with eight bytes and half the tokens 413 and 1,075 us, by spilled registers in the
+// gradient; 8 tokens forwards 342 us; 16 waves of half the tokens and eight bytes 433 and 803.
 #include "gdn_block.h"
 
 namespace gdn {
 
 namespace {
 
-template <class E> constexpr int kRV = 4 / (int)sizeof(E);  // channels of a thread: 4 bytes a token
+template <class E> constexpr int kRV = REC_BYTES / (int)sizeof(E);  // channels of a thread
 
 // The sequence of a token, among the non-empty ones.
 struct RecSeq {
@@ -65,83 +83,88 @@ struct RecSeq {
   }
 };
 
-// exp(L) - 1 for L <= 0 within two roundings of its value: the series near 0 (the
+// exp(L) - 1 for L <= 0 within a few roundings of its value: the series near 0 (the
 // first term left out is below 2^-25 of the sum), the difference elsewhere.
 __device__ __forceinline__ float expm1_neg(float L, float a) {
-  float s = fmaf(L, 1.f / 5040, 1.f / 720);
-  s = fmaf(L, s, 1.f / 120);
-  s = fmaf(L, s, 1.f / 24);
+  float s = fmaf(L, 1.f / 120, 1.f / 24);
   s = fmaf(L, s, 1.f / 6);
   s = fmaf(L, s, 0.5f);
   s = fmaf(L, s, 1.f) * L;
-  return L > -0.35f ? s : a - 1.f;
+  return L > -0.1f ? s : a - 1.f;
 }
 
-// Decay and input of one token and channel.
-template <bool SC, bool IN>
+// Decay, input and what the gradient needs of them, of one token and channel.
+template <class E, class GT, bool SC, bool IN>
 struct RecGate {
-  float a, u, sg, m, im, si;  // im = 1 / m, 0 where m is
+  float a, u, sg, m, si;
   __device__ __forceinline__ RecGate(float x, float g, float i, float scale) {
     float L = g;
     if (SC) {
-      sg = fast_sigmoid<float>(g);
+      sg = fast_sigmoid<GT>(g);
       L = -scale * sg;
     }
     a = __builtin_amdgcn_exp2f(1.44269504f * L);
-    m = im = si = 1.f;
-    if (SC) {
-      const float e = expm1_neg(L, a), m2 = -e * (2.f + e);
-      const float r = __builtin_amdgcn_rsqf(m2);
-      im = m2 == 0.f ? 0.f : r;
-      m = m2 == 0.f ? 0.f : m2 * r;
-    }
-    if (IN) si = fast_sigmoid<float>(i);
+    m = si = 1.f;
     u = x;
-    if (SC) u *= m;
-    if (IN) u *= si;
+    if (SC) {  // 1 - a^2 without the cancellation where a is near 1
+      const float e = expm1_neg(L, a);
+      m = __builtin_amdgcn_sqrtf(fmaf(-e, e, -2.f * e));
+      u *= m;
+    }
+    if (IN) {
+      si = fast_sigmoid<E>(i);
+      u *= si;
+    }
   }
 };
 
-// The V channels at c of a token's row, as loaded; n of them exist.
-template <class E, int V> struct RecRaw { E v[V]; };
-template <int V, class E>
-__device__ __forceinline__ void rec_ld(const E* p, int n, RecRaw<E, V>& r) {
-  if (V == 2 && n >= 2) {
-    if constexpr (V == 2 && sizeof(E) == 2) {
-      const bf16x2 t = *reinterpret_cast<const bf16x2_any*>(p);
-      r.v[0] = t[0]; r.v[1] = t[1];
-    } else if constexpr (V == 2) {
-      const f32x2 t = *reinterpret_cast<const f32x2_any*>(p);
-      r.v[0] = t[0]; r.v[1] = t[1];
-    }
-  } else {
-    r.v[0] = p[0];
-#pragma unroll
-    for (int e = 1; e < V; ++e) r.v[e] = to_e<E>(0.f);
+// The V channels of a thread's token, as loaded: unpacked where they are used, so that
+// many loads are under way at once.  A row's last thread may have fewer than V channels
+// left: it loads the row's last V (D >= V) and finds its own `shift` elements on.
+template <class E, int V>
+struct RecRaw {
+  typedef E vec __attribute__((ext_vector_type(V)));
+  vec t;
+  __device__ __forceinline__ void load(const E* p, int shift) {
+    typedef vec any __attribute__((aligned(sizeof(E))));
+    t = *reinterpret_cast<const any*>(p - shift);
   }
-}
+  __device__ __forceinline__ float get(int e, int shift) const {
+    float f = to_f(t[e]);
+#pragma unroll
+    for (int s = 1; s < V; ++s)
+      if (e + s < V) f = shift == s ? to_f(t[e + s]) : f;
+    return f;
+  }
+};
+template <> struct RecRaw<bf16, 1> {
+  bf16 t;
+  __device__ __forceinline__ void load(const bf16* p, int) { t = *p; }
+  __device__ __forceinline__ float get(int, int) const { return to_f(t); }
+};
+template <> struct RecRaw<float, 1> {
+  float t;
+  __device__ __forceinline__ void load(const float* p, int) { t = *p; }
+  __device__ __forceinline__ float get(int, int) const { return t; }
+};
 template <int V, class E>
 __device__ __forceinline__ void rec_st(E* p, int n, const float (&f)[V]) {
-  if (V == 2 && n >= 2) {
-    if constexpr (V == 2 && sizeof(E) == 2)
-      __builtin_nontemporal_store(bf16x2{(bf16)f[0], (bf16)f[1]}, reinterpret_cast<bf16x2_any*>(p));
-    else if constexpr (V == 2)
-      __builtin_nontemporal_store(f32x2{f[0], f[1]}, reinterpret_cast<f32x2_any*>(p));
+  typedef E vec __attribute__((ext_vector_type(V)));
+  typedef vec any __attribute__((aligned(sizeof(E))));
+  if (n >= V) {
+    vec t;
+#pragma unroll
+    for (int e = 0; e < V; ++e) t[e] = to_e<E>(f[e]);
+    __builtin_nontemporal_store(t, reinterpret_cast<any*>(p));
   } else {
-    p[0] = to_e<E>(f[0]);
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      if (e < n) p[e] = to_e<E>(f[e]);
   }
 }
 
 // Blocks are numbered channels first over the chunks: neighbours read neighbouring lines.
 template <int V> __host__ __device__ __forceinline__ uint32_t rec_width(int D) { return ((uint32_t)D + 64 * V - 1) / (64 * V); }
-template <int V> __device__ __forceinline__ int rec_chunk(const RecParams& p) { return (int)(blockIdx.x / rec_width<V>(p.D)); }
-// Channels of this block: a wave's 64 threads, V each.  false: none for this thread.
-template <int V>
-__device__ __forceinline__ bool rec_channels(const RecParams& p, int& c, int& n) {
-  c = (int)(blockIdx.x % rec_width<V>(p.D) * 64 + (threadIdx.x & 63)) * V;
-  n = p.D - c;
-  return n > 0;
-}
 template <int V>
 __device__ __forceinline__ void rec_vec(const float* base, int64_t row, int D, int c, int n, float (&f)[V]) {
 #pragma unroll
@@ -154,347 +177,404 @@ __device__ __forceinline__ void rec_put(float* base, int64_t row, int D, int c, 
     if (e < n) base[row * D + c + e] = f[e];
 }
 
-constexpr int REC_AHEAD = 8;  // tokens requested together
-
-// The tokens [t0, t1) of one chunk, in order: begin(n) where a sequence starts,
-// each(t, x, g, i), finish(n) behind a sequence's last token.  The chunk's rows behind
-// the last sequence are not visited.
-template <class E, class GT, int V, bool IN, class FB, class FE, class FF>
-__device__ __forceinline__ void rec_walk(const RecParams& p, int c, int n, FB begin, FE each, FF finish) {
-  const int t0 = rec_chunk<V>(p) * p.chunk, t1 = min(t0 + p.chunk, p.tokens);
-  RecSeq s(p);
-  if (t0 >= t1 || !s.seek(t0)) return;
-  const E* xp = static_cast<const E*>(p.x) + t0 * p.x_stride + c;
-  const GT* gp = static_cast<const GT*>(p.g) + t0 * p.g_stride + c;
-  const E* ip = static_cast<const E*>(p.i) + (IN ? t0 * p.i_stride + c : 0);
-  if (t0 == s.start) begin(s.n);
-  for (int t = t0; t < t1; t += REC_AHEAD) {
-    RecRaw<E, V> x[REC_AHEAD], i[REC_AHEAD];
-    RecRaw<GT, V> g[REC_AHEAD];
-#pragma unroll
-    for (int k = 0; k < REC_AHEAD; ++k) {
-      if (t + k < t1) {
-        rec_ld<V>(xp, n, x[k]);
-        rec_ld<V>(gp, n, g[k]);
-        if (IN) rec_ld<V>(ip, n, i[k]);
-      }
-      xp += p.x_stride;
-      gp += p.g_stride;
-      if (IN) ip += p.i_stride;
-    }
-#pragma unroll
-    for (int k = 0; k < REC_AHEAD; ++k) {
-      if (t + k >= t1) break;
-      if (t + k == s.end) {
-        if (!s.next()) return;
-        begin(s.n);
-      }
-      each(t + k, x[k], g[k], i[k]);
-      if (t + k == s.end - 1) finish(s.n);
-    }
-  }
-}
-
-// Each chunk's (A, U).
-template <class E, class GT, bool SC, bool IN>
-__global__ __launch_bounds__(64) void rec_sum_kernel(RecParams p) {
-  constexpr int V = kRV<E>;
-  int c, n;
-  if (!rec_channels<V>(p, c, n)) return;
-  float scale[V], A[V], U[V] = {};
-  rec_vec<V>(p.scale, 0, p.D, c, n, scale);
-#pragma unroll
-  for (int e = 0; e < V; ++e) A[e] = 1.f;
-  bool cut = false;
-  rec_walk<E, GT, V, IN>(p, c, n,
-    [&](int q) {
-      cut = true;
-      rec_vec<V>(p.h0, q, p.D, c, n, U);
-    },
-    [&](int, const RecRaw<E, V>& x, const RecRaw<GT, V>& g, const RecRaw<E, V>& i) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const RecGate<SC, IN> w(to_f(x.v[e]), to_f(g.v[e]), IN ? to_f(i.v[e]) : 0.f, scale[e]);
-        U[e] = fmaf(w.a, U[e], w.u);
-        A[e] *= w.a;
-      }
-    },
-    [](int) {});
-#pragma unroll
-  for (int e = 0; e < V; ++e)
-    if (e < n) p.sum[(int64_t)rec_chunk<V>(p) * p.D + c + e] = make_float2(cut ? -1.f : A[e], U[e]);
-}
-
-// The same for the gradient's chain, backwards: carry leaving the chunk's front.
-template <class E, class GT, bool SC>
-__global__ __launch_bounds__(64) void rec_rev_sum_kernel(RecParams p) {
-  constexpr int V = kRV<E>;
-  int c, n;
-  if (!rec_channels<V>(p, c, n)) return;
-  float scale[V], A[V], U[V] = {};
-  rec_vec<V>(p.scale, 0, p.D, c, n, scale);
-#pragma unroll
-  for (int e = 0; e < V; ++e) A[e] = 1.f;
-  bool cut = false;  // behind the first sequence's end nothing more reaches the front
-  RecParams w = p;   // walks dy in x's place
-  w.x = p.dy;
-  w.x_stride = p.D;
-  rec_walk<E, GT, V, false>(w, c, n, [](int) {},
-    [&](int, const RecRaw<E, V>& dy, const RecRaw<GT, V>& g, const RecRaw<E, V>&) {
-      if (cut) return;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        float L = to_f(g.v[e]);
-        if (SC) L = -scale[e] * fast_sigmoid<float>(L);
-        A[e] *= __builtin_amdgcn_exp2f(1.44269504f * L);
-        U[e] = fmaf(A[e], to_f(dy.v[e]), U[e]);
-      }
-    },
-    [&](int q) {
-      if (cut) return;
-      cut = true;
-      if (!p.dhT) return;
-      float d[V];
-      rec_vec<V>(p.dhT, q, p.D, c, n, d);
-#pragma unroll
-      for (int e = 0; e < V; ++e) U[e] = fmaf(A[e], d[e], U[e]);
-    });
-#pragma unroll
-  for (int e = 0; e < V; ++e)
-    if (e < n) p.sum[(int64_t)rec_chunk<V>(p) * p.D + c + e] = make_float2(cut ? -1.f : A[e], U[e]);
-}
-
-// States entering the chunks (REV: gradients leaving them): JOIN_S threads a channel
-// compose a run of chunks each, then walk it again from what the runs before make.
-constexpr int RJ_C = 32, RJ_S = 32;
 __device__ __forceinline__ float rec_apply(float2 s, float h) { return s.x < 0.f ? s.y : fmaf(s.x, h, s.y); }
-template <bool REV>
-__global__ __launch_bounds__(RJ_C * RJ_S) void rec_join_kernel(RecParams p) {
-  __shared__ float2 runs[RJ_S][RJ_C + 1];
-  const int cl = threadIdx.x % RJ_C, s = threadIdx.x / RJ_C;
-  const int c = blockIdx.x * RJ_C + cl;
-  const int per = (p.nchunk + RJ_S - 1) / RJ_S, b0 = min(p.nchunk, s * per), b1 = min(p.nchunk, b0 + per);
-  auto at = [&](int b) { return (int64_t)(REV ? p.nchunk - 1 - b : b) * p.D + c; };
-  float2 r = make_float2(1.f, 0.f);
-  if (c < p.D) {
-#pragma unroll 8
-    for (int b = b0; b < b1; ++b) {
-      const float2 v = p.sum[at(b)];
-      r = v.x < 0.f ? v : make_float2(r.x < 0.f ? -1.f : r.x * v.x, fmaf(v.x, r.y, v.y));
+// first r, then v
+__device__ __forceinline__ float2 rec_then(float2 r, float2 v) {
+  return v.x < 0.f ? v : make_float2(r.x < 0.f ? -1.f : r.x * v.x, fmaf(v.x, r.y, v.y));
+}
+
+// ---------------------------------------------------------------- the chunks' chain
+// A pair as a word that is never 0 (the first half inverted: 0 would be a NaN of all ones,
+// which NaNs are replaced by another for).
+__device__ __forceinline__ uint64_t rec_word(float2 v) {
+  const uint32_t a = v.x != v.x ? 0x7fc00000u : __builtin_bit_cast(uint32_t, v.x);
+  return (uint64_t)~a << 32 | __builtin_bit_cast(uint32_t, v.y);
+}
+__device__ __forceinline__ float2 rec_pair(uint64_t w) {
+  return make_float2(__builtin_bit_cast(float, ~(uint32_t)(w >> 32)), __builtin_bit_cast(float, (uint32_t)w));
+}
+__device__ __forceinline__ void rec_publish(uint64_t* p, float2 v) {
+  __hip_atomic_store(p, rec_word(v), __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t rec_peek(const uint64_t* p) {
+  return __hip_atomic_load(p, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ uint64_t rec_await(const uint64_t* p) {
+  uint64_t w = rec_peek(p);
+  while (w == 0) {
+    __builtin_amdgcn_s_sleep(1);
+    w = rec_peek(p);
+  }
+  return w;
+}
+// Words in front of the chunks': a counter for each workgroup's width of channels (the
+// narrowest, fp32's), each in a line of its own.
+constexpr int REC_LINE = 16;
+__host__ __device__ __forceinline__ int64_t rec_counters(int D) { return (int64_t)rec_width<REC_BYTES / 4>(D) * REC_LINE; }
+constexpr int REC_GROUP = 16;  // chunks of a group: about as many words are read as groups wait for each other
+constexpr int REC_PEEK = 4;    // words requested together
+
+// Publishes the pair of chunk k (counted in the chain's direction) and returns the state
+// entering it.  One wave; e: the thread's channel, of which all V exist up to n.
+template <int V>
+__device__ __forceinline__ void rec_chain(const RecParams& p, int k, int c, int n, const float2 (&own)[V], float (&h)[V]) {
+  const int first = k / REC_GROUP * REC_GROUP;
+  uint64_t* pairs = p.words + rec_counters(p.D);          // [nchunk][D]
+  uint64_t* ends = pairs + (int64_t)p.nchunk * p.D;       // [groups][D]: (-1, the state leaving a group)
+  const bool last = k == first + REC_GROUP - 1;
+#pragma unroll
+  for (int e = 0; e < V; ++e)
+    if (e < n && !last) rec_publish(pairs + (int64_t)k * p.D + c + e, own[e]);
+  float2 r[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) r[e] = make_float2(1.f, 0.f);
+  for (int j = first; j < k; j += REC_PEEK) {
+    uint64_t w[REC_PEEK][V];
+#pragma unroll
+    for (int q = 0; q < REC_PEEK; ++q)
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (j + q < k && e < n) w[q][e] = rec_peek(pairs + (int64_t)(j + q) * p.D + c + e);
+#pragma unroll
+    for (int q = 0; q < REC_PEEK; ++q)
+#pragma unroll
+      for (int e = 0; e < V; ++e)
+        if (j + q < k && e < n) {
+          if (w[q][e] == 0) w[q][e] = rec_await(pairs + (int64_t)(j + q) * p.D + c + e);
+          r[e] = rec_then(r[e], rec_pair(w[q][e]));
+        }
+  }
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    float in = 0.f;
+    if (first > 0 && e < n) in = rec_pair(rec_await(ends + (int64_t)(k / REC_GROUP - 1) * p.D + c + e)).y;
+    h[e] = rec_apply(r[e], in);
+    if (e < n && last) rec_publish(ends + (int64_t)(k / REC_GROUP) * p.D + c + e, make_float2(-1.f, rec_apply(own[e], h[e])));
+  }
+}
+
+// The chunk of this workgroup, counted in the chain's direction: its own number where it
+// waits for nobody, else by its channels' counter.
+template <int V>
+__device__ __forceinline__ int rec_ticket(const RecParams& p) {
+  const uint32_t wide = rec_width<V>(p.D), own = blockIdx.x / wide;
+  if (!p.words || own >= (uint32_t)p.nchunk) return (int)own;
+  __shared__ uint32_t id;
+  if (threadIdx.x == 0)
+    id = __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(p.words + blockIdx.x % wide * REC_LINE), 1u, __ATOMIC_RELAXED,
+                                __HIP_MEMORY_SCOPE_AGENT);
+  __syncthreads();
+  return (int)__builtin_amdgcn_readfirstlane(id);
+}
+
+// Where sequences start and end among the tokens [t0, t0 + S) of a wave: bit k, token t0 +
+// k.  `count` tokens from t0 on belong to sequences; none do behind them.
+template <int S>
+struct RecSpan {
+  uint32_t starts = 0, ends = 0;
+  int count = 0;
+  __device__ __forceinline__ RecSpan(const RecParams& p, int t0, int t1) {
+    RecSeq s(p);
+    t1 = min(t1, s.all());
+    if (t0 >= t1 || !s.seek(t0)) return;
+    if (s.start == t0) starts = 1;
+    count = t1 - t0;
+    while (s.end <= t1) {
+      ends |= 1u << (s.end - 1 - t0);
+      if (s.end == t1) break;
+      if (!s.next()) {
+        count = s.end - t0;  // (a bad device copy of cu: a gap)
+        break;
+      }
+      starts |= 1u << (s.start - t0);
     }
   }
-  runs[s][cl] = r;
-  __syncthreads();
-  float h = 0.f;
-  for (int q = 0; q < s; ++q) h = rec_apply(runs[q][cl], h);
-  if (c >= p.D) return;
-  float* out = REV ? p.carry : p.enter;
-#pragma unroll 8
-  for (int b = b0; b < b1; ++b) {
-    out[at(b)] = h;
-    h = rec_apply(p.sum[at(b)], h);
-  }
-}
-
-// Blocks past the chunks write the final states of sequences without tokens.
-template <int V>
-__device__ __forceinline__ bool rec_empty_seq(const RecParams& p, const float* src, float* dst, int c, int n) {
-  if (rec_chunk<V>(p) < p.nchunk) return false;
+};
+// The sequence of token t.
+__device__ __forceinline__ int rec_seq_of(const RecParams& p, int t) {
   RecSeq s(p);
-  s.n = rec_chunk<V>(p) - p.nchunk;
+  s.seek(t);
+  return s.n;
+}
+template <int V>
+__device__ __forceinline__ void rec_state(const RecParams& p, const float* states, int t, int c, int n, float (&h)[V]) {
+  rec_vec<V>(states, states ? rec_seq_of(p, t) : 0, p.D, c, n, h);
+}
+
+// Workgroups past the chunks write the final states of sequences without tokens.
+template <int V>
+__device__ __forceinline__ void rec_empty_seq(const RecParams& p, int seq, const float* src, float* dst, int c, int n) {
+  RecSeq s(p);
+  s.n = seq;
   s.bounds();
-  if (s.end > s.start || !dst) return true;
+  if (threadIdx.x >= 64 || n <= 0 || s.end > s.start || !dst) return;
   float h[V];
-  rec_vec<V>(src, s.n, p.D, c, n, h);
-  rec_put<V>(dst, s.n, p.D, c, n, h);
-  return true;
+  rec_vec<V>(src, seq, p.D, c, n, h);
+  rec_put<V>(dst, seq, p.D, c, n, h);
 }
 
-template <class E, class GT, bool SC, bool IN>
-__global__ __launch_bounds__(64) void rec_fwd_kernel(RecParams p) {
-  constexpr int V = kRV<E>;
-  int c, n;
-  if (!rec_channels<V>(p, c, n)) return;
-  if (rec_empty_seq<V>(p, p.h0, p.hT, c, n)) return;
-  float scale[V], h[V];
-  rec_vec<V>(p.scale, 0, p.D, c, n, scale);
-  rec_vec<V>(p.enter, rec_chunk<V>(p), p.D, c, n, h);
-  E* yp = static_cast<E*>(p.y) + c;
-  rec_walk<E, GT, V, IN>(p, c, n,
-    [&](int q) { rec_vec<V>(p.h0, q, p.D, c, n, h); },
-    [&](int t, const RecRaw<E, V>& x, const RecRaw<GT, V>& g, const RecRaw<E, V>& i) {
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const RecGate<SC, IN> w(to_f(x.v[e]), to_f(g.v[e]), IN ? to_f(i.v[e]) : 0.f, scale[e]);
-        h[e] = fmaf(w.a, h[e], w.u);
-      }
-      rec_st<V>(yp + (int64_t)t * p.D, n, h);
-    },
-    [&](int q) {
-      if (p.hT) rec_put<V>(p.hT, q, p.D, c, n, h);
-    });
-}
-
-// Gradient.  A chunk is one workgroup, a wave to every REC_SUB tokens, whose inputs lie
-// in registers: a first walk forms the waves' pairs of both chains, exchanged through
-// LDS; a second the states before every token from the state entering; the third goes
-// back with the gradient.
-template <class E, class GT, bool SC, bool IN>
-__global__ __launch_bounds__(512) void rec_bwd_kernel(RecParams p) {
-  constexpr int V = kRV<E>, S = REC_SUB;
-  __shared__ float2 fw[8][64 * V], bw[8][64 * V];
-  int c, n;
-  const bool any = rec_channels<V>(p, c, n);
-  const int ch = rec_chunk<V>(p);
+template <class E, class GT, int V, bool SC, bool IN>
+__global__ __launch_bounds__(64 * REC_W, 4) void rec_fwd_kernel(RecParams p) {
+  constexpr int S = REC_FS, W = REC_W;
+  __shared__ float2 pairs[W][64 * V];
+  __shared__ float entering[64 * V];
+  const int ch = rec_ticket<V>(p);
+  const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
+  const int c = (int)(blockIdx.x % rec_width<V>(p.D) * 64 + lane) * V, n = p.D - c, shift = max(V - n, 0);
   if (ch >= p.nchunk) {
-    if (any && threadIdx.x < 64) rec_empty_seq<V>(p, p.dhT, p.dh0, c, n);
+    rec_empty_seq<V>(p, ch - p.nchunk, p.h0, p.hT, c, n);
     return;
   }
-  const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), W = blockDim.x / 64;
-  const int t0 = ch * p.chunk + w * S;
-  RecSeq s(p);
-  const int t1 = min(t0 + S, s.all());
-  const bool live = any && t0 < t1 && s.seek(t0);
-  const int n0 = s.n;
-  RecRaw<E, V> x[S], i[S], dy[S];
-  RecRaw<GT, V> g[S];
-  float a[S][V], h[S][V], scale[V];
+  const int t0 = ch * (W * S) + w * S;
+  const RecSpan<S> span(p, t0, min(t0 + S, p.tokens));
+  float a[S][V], u[S][V], scale[V];
+  float2 f[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) f[e] = make_float2(1.f, 0.f);
+  if (n > 0 && span.count) {
+    RecRaw<E, V> x[S], i[S];
+    RecRaw<GT, V> g[S];
+    rec_vec<V>(p.scale, 0, p.D, c, n, scale);
+    const E* xp = static_cast<const E*>(p.x) + t0 * p.x_stride + c;
+    const GT* gp = static_cast<const GT*>(p.g) + t0 * p.g_stride + c;
+    const E* ip = static_cast<const E*>(p.i) + (IN ? t0 * p.i_stride + c : 0);
+#pragma unroll
+    for (int k = 0; k < S; ++k) {  // (behind the last token: that one again)
+      const int t = min(k, span.count - 1);
+      g[k].load(gp + t * p.g_stride, shift);
+      x[k].load(xp + t * p.x_stride, shift);
+      if (IN) i[k].load(ip + t * p.i_stride, shift);
+    }
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      if (k < span.count) {
+        if (span.starts >> k & 1) {
+          float t[V];
+          rec_state<V>(p, p.h0, t0 + k, c, n, t);
+#pragma unroll
+          for (int e = 0; e < V; ++e) f[e].y = t[e];
+        }
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const RecGate<E, GT, SC, IN> q(x[k].get(e, shift), g[k].get(e, shift), IN ? i[k].get(e, shift) : 0.f, scale[e]);
+          a[k][e] = q.a;
+          u[k][e] = q.u;
+          f[e] = make_float2(f[e].x * q.a, fmaf(q.a, f[e].y, q.u));
+        }
+      }
+    }
+    if (span.starts) {
+#pragma unroll
+      for (int e = 0; e < V; ++e) f[e].x = -1.f;
+    }
+  }
+  if (n > 0) {
+#pragma unroll
+    for (int e = 0; e < V; ++e) pairs[w][lane * V + e] = f[e];
+  }
+  __syncthreads();
+  if (p.words) {
+    if (w == 0 && n > 0) {
+      float2 own[V];
+      float h[V];
+#pragma unroll
+      for (int e = 0; e < V; ++e) {
+        own[e] = pairs[0][lane * V + e];
+#pragma unroll
+        for (int q = 1; q < W; ++q) own[e] = rec_then(own[e], pairs[q][lane * V + e]);
+      }
+      rec_chain<V>(p, ch, c, n, own, h);
+#pragma unroll
+      for (int e = 0; e < V; ++e) entering[lane * V + e] = h[e];
+    }
+    __syncthreads();
+  }
+  if (n <= 0) return;
+  float h[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) {
+    h[e] = p.words ? entering[lane * V + e] : 0.f;
+    for (int q = 0; q < w; ++q) h[e] = rec_apply(pairs[q][lane * V + e], h[e]);
+  }
+  if (p.enter && w % (REC_STATE / S) == 0 && t0 < p.tokens) rec_put<V>(p.enter, t0 / REC_STATE, p.D, c, n, h);
+  E* yp = static_cast<E*>(p.y) + (int64_t)t0 * p.D + c;
+#pragma unroll
+  for (int k = 0; k < S; ++k) {
+    if (k < span.count) {
+      if (span.starts >> k & 1) rec_state<V>(p, p.h0, t0 + k, c, n, h);
+#pragma unroll
+      for (int e = 0; e < V; ++e) h[e] = fmaf(a[k][e], h[e], u[k][e]);
+      if (p.y) rec_st<V>(yp + (int64_t)k * p.D, n, h);
+      if ((span.ends >> k & 1) && p.hT) rec_put<V>(p.hT, rec_seq_of(p, t0 + k), p.D, c, n, h);
+    }
+  }
+}
+
+// Gradient.  The first walk forms the gates and the waves' pairs of both chains; while one
+// wave waits for the carry from behind, the others walk forward from the state entering
+// the chunk (kept by the forward pass) to the states before every token; then back.
+template <class E, class GT, int V, bool SC, bool IN>
+__global__ __launch_bounds__(64 * REC_W, 4) void rec_bwd_kernel(RecParams p) {
+  constexpr int S = REC_BS, W = REC_W;
+  __shared__ float2 fw[W][64 * V], bw[W][64 * V];
+  __shared__ float leaving[64 * V];
+  const int k_chain = rec_ticket<V>(p);
+  const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
+  const int c = (int)(blockIdx.x % rec_width<V>(p.D) * 64 + lane) * V, n = p.D - c, shift = max(V - n, 0);
+  if (k_chain >= p.nchunk) {
+    rec_empty_seq<V>(p, k_chain - p.nchunk, p.dhT, p.dh0, c, n);
+    return;
+  }
+  const int ch = p.nchunk - 1 - k_chain, t0 = ch * (W * S) + w * S;
+  const RecSpan<S> span(p, t0, min(t0 + S, p.tokens));
+  RecRaw<E, V> x[S], dy[S];
+  float a[S][V], m[S][V], sg[S][V], si[S][V], h[S][V], scale[V];
   float2 f[V], b[V];
 #pragma unroll
   for (int e = 0; e < V; ++e) f[e] = b[e] = make_float2(1.f, 0.f);
+  const bool live = n > 0 && span.count;
   if (live) {
+    RecRaw<E, V> i[S];
+    RecRaw<GT, V> g[S];
     rec_vec<V>(p.scale, 0, p.D, c, n, scale);
     const E* xp = static_cast<const E*>(p.x) + t0 * p.x_stride + c;
     const GT* gp = static_cast<const GT*>(p.g) + t0 * p.g_stride + c;
     const E* ip = static_cast<const E*>(p.i) + (IN ? t0 * p.i_stride + c : 0);
     const E* dp = static_cast<const E*>(p.dy) + (int64_t)t0 * p.D + c;
 #pragma unroll
-    for (int k = 0; k < S; ++k) {
-      if (t0 + k < t1) {
-        rec_ld<V>(gp + k * p.g_stride, n, g[k]);
-        rec_ld<V>(xp + k * p.x_stride, n, x[k]);
-        if (IN) rec_ld<V>(ip + k * p.i_stride, n, i[k]);
-        rec_ld<V>(dp + (int64_t)k * p.D, n, dy[k]);
-      }
+    for (int k = 0; k < S; ++k) {  // (behind the last token: that one again)
+      const int t = min(k, span.count - 1);
+      g[k].load(gp + t * p.g_stride, shift);
+      x[k].load(xp + t * p.x_stride, shift);
+      if (IN) i[k].load(ip + t * p.i_stride, shift);
+      dy[k].load(dp + (int64_t)t * p.D, shift);
     }
-    bool cutf = false, cutb = false;
-    if (t0 == s.start) {
-      cutf = true;
-      float t[V];
-      rec_vec<V>(p.h0, s.n, p.D, c, n, t);
-#pragma unroll
-      for (int e = 0; e < V; ++e) f[e].y = t[e];
-    }
+    bool cut = false;  // behind the first sequence's end nothing more reaches the front
 #pragma unroll
     for (int k = 0; k < S; ++k) {
-      if (t0 + k >= t1) break;
-      if (t0 + k == s.end) {
-        if (!s.next()) break;
-        cutf = true;
-        float t[V];
-        rec_vec<V>(p.h0, s.n, p.D, c, n, t);
+      if (k < span.count) {
+        if (span.starts >> k & 1) {
+          float t[V];
+          rec_state<V>(p, p.h0, t0 + k, c, n, t);
 #pragma unroll
-        for (int e = 0; e < V; ++e) f[e].y = t[e];
-      }
+          for (int e = 0; e < V; ++e) f[e].y = t[e];
+        }
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const RecGate<SC, IN> q(to_f(x[k].v[e]), to_f(g[k].v[e]), IN ? to_f(i[k].v[e]) : 0.f, scale[e]);
-        a[k][e] = q.a;
-        h[k][e] = q.u;
-        f[e] = make_float2(f[e].x * q.a, fmaf(q.a, f[e].y, q.u));
-        if (!cutb) b[e] = make_float2(b[e].x * q.a, fmaf(b[e].x * q.a, to_f(dy[k].v[e]), b[e].y));
-      }
-      if (t0 + k == s.end - 1 && !cutb) {
-        cutb = true;
-        float t[V];
-        rec_vec<V>(p.dhT, s.n, p.D, c, n, t);
+        for (int e = 0; e < V; ++e) {
+          const RecGate<E, GT, SC, IN> q(x[k].get(e, shift), g[k].get(e, shift), IN ? i[k].get(e, shift) : 0.f, scale[e]);
+          a[k][e] = q.a;
+          if (SC) { m[k][e] = q.m; sg[k][e] = q.sg; }
+          if (IN) si[k][e] = q.si;
+          h[k][e] = q.u;
+          f[e] = make_float2(f[e].x * q.a, fmaf(q.a, f[e].y, q.u));
+          if (!cut) b[e] = make_float2(b[e].x * q.a, fmaf(b[e].x * q.a, dy[k].get(e, shift), b[e].y));
+        }
+        if ((span.ends >> k & 1) && !cut) {
+          cut = true;
+          float t[V];
+          rec_state<V>(p, p.dhT, t0 + k, c, n, t);
 #pragma unroll
-        for (int e = 0; e < V; ++e) b[e].y = fmaf(b[e].x, t[e], b[e].y);
+          for (int e = 0; e < V; ++e) b[e].y = fmaf(b[e].x, t[e], b[e].y);
+        }
       }
     }
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      if (cutf) f[e].x = -1.f;
-      if (cutb) b[e].x = -1.f;
+      if (span.starts) f[e].x = -1.f;
+      if (cut) b[e].x = -1.f;
     }
   }
+  if (n > 0) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) {
-    fw[w][lane * V + e] = f[e];
-    bw[w][lane * V + e] = b[e];
+    for (int e = 0; e < V; ++e) {
+      fw[w][lane * V + e] = f[e];
+      bw[w][lane * V + e] = b[e];
+    }
+  }
+  __syncthreads();
+  if (p.words && w == 0 && n > 0) {
+    float2 own[V];
+    float d[V];
+#pragma unroll
+    for (int e = 0; e < V; ++e) {
+      own[e] = bw[W - 1][lane * V + e];
+#pragma unroll
+      for (int q = W - 2; q >= 0; --q) own[e] = rec_then(own[e], bw[q][lane * V + e]);
+    }
+    rec_chain<V>(p, k_chain, c, n, own, d);
+#pragma unroll
+    for (int e = 0; e < V; ++e) leaving[lane * V + e] = d[e];
+  }
+  if (live) {  // the states before every token
+    float hc[V];
+    rec_vec<V>(p.enter, ch, p.D, c, n, hc);
+#pragma unroll
+    for (int e = 0; e < V; ++e)
+      for (int q = 0; q < w; ++q) hc[e] = rec_apply(fw[q][lane * V + e], hc[e]);
+#pragma unroll
+    for (int k = 0; k < S; ++k) {
+      if (k < span.count) {
+        if (span.starts >> k & 1) rec_state<V>(p, p.h0, t0 + k, c, n, hc);
+#pragma unroll
+        for (int e = 0; e < V; ++e) {
+          const float t = fmaf(a[k][e], hc[e], h[k][e]);
+          h[k][e] = hc[e];
+          hc[e] = t;
+        }
+      }
+    }
   }
   __syncthreads();
   float ds[V] = {};
   if (live) {
-    float hc[V], dc[V];
-    rec_vec<V>(p.enter, ch, p.D, c, n, hc);
-    rec_vec<V>(p.carry, ch, p.D, c, n, dc);
+    float dc[V];
 #pragma unroll
     for (int e = 0; e < V; ++e) {
-      for (int q = 0; q < w; ++q) hc[e] = rec_apply(fw[q][lane * V + e], hc[e]);
+      dc[e] = p.words ? leaving[lane * V + e] : 0.f;
       for (int q = W - 1; q > w; --q) dc[e] = rec_apply(bw[q][lane * V + e], dc[e]);
     }
-    // the states before every token
-    s.n = n0;
-    s.bounds();
-    if (t0 == s.start) rec_vec<V>(p.h0, s.n, p.D, c, n, hc);
-    int last = t0;  // past the last token that belongs to a sequence
-#pragma unroll
-    for (int k = 0; k < S; ++k) {
-      if (t0 + k >= t1) break;
-      if (t0 + k == s.end) {
-        if (!s.next()) break;
-        rec_vec<V>(p.h0, s.n, p.D, c, n, hc);
-      }
-      last = t0 + k + 1;
-#pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float t = fmaf(a[k][e], hc[e], h[k][e]);
-        h[k][e] = hc[e];
-        hc[e] = t;
-      }
-    }
-    // back in time
-    if (s.n >= s.N || !(last > s.start && last <= s.end)) s.seek(last - 1);
+    E* dxp = static_cast<E*>(p.dx) + (int64_t)t0 * p.D + c;
+    GT* dgp = static_cast<GT*>(p.dg) + (int64_t)t0 * p.D + c;
+    E* dip = static_cast<E*>(p.di) + (IN ? (int64_t)t0 * p.D + c : 0);
 #pragma unroll
     for (int k = S - 1; k >= 0; --k) {
-      const int t = t0 + k;
-      if (t >= last) continue;
-      if (t < s.start) s.seek(t);
-      if (t == s.end - 1) rec_vec<V>(p.dhT, s.n, p.D, c, n, dc);
-      float dx[V], dg[V], di[V];
+      if (k < span.count) {
+        if (span.ends >> k & 1) rec_state<V>(p, p.dhT, t0 + k, c, n, dc);
+        float dx[V], dg[V], di[V];
 #pragma unroll
-      for (int e = 0; e < V; ++e) {
-        const float xv = to_f(x[k].v[e]);
-        const RecGate<SC, IN> q(xv, to_f(g[k].v[e]), IN ? to_f(i[k].v[e]) : 0.f, scale[e]);
-        const float dh = to_f(dy[k].v[e]) + dc[e], dhs = IN ? dh * q.si : dh;
-        dc[e] = a[k][e] * dh;
-        dx[e] = SC ? dhs * q.m : dhs;
-        di[e] = dx[e] * xv * (1.f - q.si);
-        float dl = dc[e] * h[k][e];
-        if (SC) {
-          dl -= dhs * xv * (q.a * q.a) * q.im;
-          dg[e] = -dl * scale[e] * (q.sg - q.sg * q.sg);
-          ds[e] -= dl * q.sg;
-        } else {
-          dg[e] = dl;
+        for (int e = 0; e < V; ++e) {
+          const float xv = x[k].get(e, shift), dh = dy[k].get(e, shift) + dc[e], dhs = IN ? dh * si[k][e] : dh;
+          dc[e] = a[k][e] * dh;
+          dx[e] = SC ? dhs * m[k][e] : dhs;
+          if (IN) di[e] = dx[e] * xv * (1.f - si[k][e]);
+          float dl = dc[e] * h[k][e];
+          if (SC) {
+            const float im = m[k][e] == 0.f ? 0.f : __builtin_amdgcn_rcpf(m[k][e]);
+            dl -= dhs * xv * (a[k][e] * a[k][e]) * im;
+            dg[e] = -dl * scale[e] * (sg[k][e] - sg[k][e] * sg[k][e]);
+            ds[e] -= dl * sg[k][e];
+          } else {
+            dg[e] = dl;
+          }
         }
+        rec_st<V>(dxp + (int64_t)k * p.D, n, dx);
+        rec_st<V>(dgp + (int64_t)k * p.D, n, dg);
+        if (IN) rec_st<V>(dip + (int64_t)k * p.D, n, di);
+        if ((span.starts >> k & 1) && p.dh0) rec_put<V>(p.dh0, rec_seq_of(p, t0 + k), p.D, c, n, dc);
       }
-      rec_st<V>(static_cast<E*>(p.dx) + (int64_t)t * p.D + c, n, dx);
-      rec_st<V>(static_cast<GT*>(p.dg) + (int64_t)t * p.D + c, n, dg);
-      if (IN) rec_st<V>(static_cast<E*>(p.di) + (int64_t)t * p.D + c, n, di);
-      if (t == s.start && p.dh0) rec_put<V>(p.dh0, s.n, p.D, c, n, dc);
     }
   }
   if (!SC) return;
-  __syncthreads();
+  if (n > 0) {
 #pragma unroll
-  for (int e = 0; e < V; ++e) fw[w][lane * V + e].x = ds[e];
+    for (int e = 0; e < V; ++e) fw[w][lane * V + e].x = ds[e];  // (last read before the barrier above)
+  }
   __syncthreads();
-  if (w == 0 && any) {
+  if (w == 0 && n > 0) {
 #pragma unroll
     for (int e = 0; e < V; ++e) {
       float t = 0.f;
+#pragma unroll
       for (int q = 0; q < W; ++q) t += fw[q][lane * V + e].x;
       ds[e] = t;
     }
@@ -502,90 +582,95 @@ __global__ __launch_bounds__(512) void rec_bwd_kernel(RecParams p) {
   }
 }
 
-template <class E, class GT, bool SC, bool IN>
+// Zeros: words that are not written yet, and the counter.
+__global__ __launch_bounds__(256) void rec_clear_kernel(uint64_t* p, int64_t words) {
+  for (int64_t i = blockIdx.x * 256ll + threadIdx.x; i < words; i += gridDim.x * 256ll) p[i] = 0;
+}
+
+template <class E, class GT, int V, bool SC, bool IN>
 __global__ __launch_bounds__(64) void rec_step_kernel(RecStepParams p) {
-  constexpr int V = kRV<E>;
   const uint32_t wide = rec_width<V>(p.D);
-  const int c = (int)(blockIdx.x % wide * 64 + threadIdx.x) * V, n = p.D - c, r = (int)(blockIdx.x / wide);
+  const int c = (int)(blockIdx.x % wide * 64 + threadIdx.x) * V, n = p.D - c, r = (int)(blockIdx.x / wide), shift = max(V - n, 0);
   if (n <= 0) return;
   const int slot = p.state_idx ? p.state_idx[r] : r;
   if (slot < 0 || slot >= p.num_slots) return;
   RecRaw<E, V> x, i;
   RecRaw<GT, V> g;
-  rec_ld<V>(static_cast<const E*>(p.x) + r * p.x_stride + c, n, x);
-  rec_ld<V>(static_cast<const GT*>(p.g) + r * p.g_stride + c, n, g);
-  if (IN) rec_ld<V>(static_cast<const E*>(p.i) + r * p.i_stride + c, n, i);
+  x.load(static_cast<const E*>(p.x) + r * p.x_stride + c, shift);
+  g.load(static_cast<const GT*>(p.g) + r * p.g_stride + c, shift);
+  if (IN) i.load(static_cast<const E*>(p.i) + r * p.i_stride + c, shift);
   float h[V], scale[V];
   rec_vec<V>(p.state, slot, p.D, c, n, h);
   rec_vec<V>(p.scale, 0, p.D, c, n, scale);
 #pragma unroll
   for (int e = 0; e < V; ++e) {
-    const RecGate<SC, IN> w(to_f(x.v[e]), to_f(g.v[e]), IN ? to_f(i.v[e]) : 0.f, scale[e]);
+    const RecGate<E, GT, SC, IN> w(x.get(e, shift), g.get(e, shift), IN ? i.get(e, shift) : 0.f, scale[e]);
     h[e] = fmaf(w.a, h[e], w.u);
   }
   rec_put<V>(p.state, slot, p.D, c, n, h);
   rec_st<V>(static_cast<E*>(p.y) + (int64_t)r * p.D + c, n, h);
 }
 
-// f<E, GT, SC, IN>() by the call's types and optional inputs.
-template <class E, class GT, class F>
+// f<E, GT, V, SC, IN>() by the call's types and optional inputs; rows of fewer channels
+// than a thread takes go one by one.
+template <class E, class GT, int V, class F>
 void rec_pick(bool sc, bool in, F f) {
-  if (sc && in) f.template operator()<E, GT, true, true>();
-  else if (sc) f.template operator()<E, GT, true, false>();
-  else if (in) f.template operator()<E, GT, false, true>();
-  else f.template operator()<E, GT, false, false>();
+  if (sc && in) f.template operator()<E, GT, V, true, true>();
+  else if (sc) f.template operator()<E, GT, V, true, false>();
+  else if (in) f.template operator()<E, GT, V, false, true>();
+  else f.template operator()<E, GT, V, false, false>();
+}
+template <class E, class GT, class F>
+void rec_width_of(int D, bool sc, bool in, F f) {
+  if constexpr (kRV<E> > 1)
+    if (D < kRV<E>) return rec_pick<E, GT, 1>(sc, in, f);
+  rec_pick<E, GT, kRV<E>>(sc, in, f);
 }
 template <class F>
-hipError_t rec_types(int dtype, int g_f32, bool sc, bool in, F f) {
-  if (dtype == GDN_F32) rec_pick<float, float>(sc, in, f);
-  else if (g_f32) rec_pick<bf16, float>(sc, in, f);
-  else rec_pick<bf16, bf16>(sc, in, f);
+hipError_t rec_types(int dtype, int g_f32, int D, bool sc, bool in, F f) {
+  if (dtype == GDN_F32) rec_width_of<float, float>(D, sc, in, f);
+  else if (g_f32) rec_width_of<bf16, float>(D, sc, in, f);
+  else rec_width_of<bf16, bf16>(D, sc, in, f);
   return hipGetLastError();
 }
 struct RecLaunch {
-  enum { SUM, RSUM, FWD, BWD } what;
+  bool bwd;
   const RecParams& p;
   hipStream_t st;
-  template <class E, class GT, bool SC, bool IN>
+  template <class E, class GT, int V, bool SC, bool IN>
   void operator()() const {
-    const int more = what == FWD && p.hT || what == BWD && p.dh0 ? p.N : 0;
-    const dim3 grid(rec_width<kRV<E>>(p.D) * (uint32_t)(p.nchunk + more));
+    const int more = (bwd ? p.dh0 : p.hT) ? p.N : 0;
+    const dim3 grid(rec_width<V>(p.D) * (uint32_t)(p.nchunk + more));
     if (grid.x == 0) return;
-    if (what == SUM) hipLaunchKernelGGL((rec_sum_kernel<E, GT, SC, IN>), grid, dim3(64), 0, st, p);
-    else if (what == RSUM) hipLaunchKernelGGL((rec_rev_sum_kernel<E, GT, SC>), grid, dim3(64), 0, st, p);
-    else if (what == FWD) hipLaunchKernelGGL((rec_fwd_kernel<E, GT, SC, IN>), grid, dim3(64), 0, st, p);
-    else hipLaunchKernelGGL((rec_bwd_kernel<E, GT, SC, IN>), grid, dim3(64 * (p.chunk / REC_SUB)), 0, st, p);
+    if (bwd) hipLaunchKernelGGL((rec_bwd_kernel<E, GT, V, SC, IN>), grid, dim3(64 * REC_W), 0, st, p);
+    else hipLaunchKernelGGL((rec_fwd_kernel<E, GT, V, SC, IN>), grid, dim3(64 * REC_W), 0, st, p);
   }
 };
 struct RecStepLaunch {
   const RecStepParams& p;
   hipStream_t st;
-  template <class E, class GT, bool SC, bool IN>
+  template <class E, class GT, int V, bool SC, bool IN>
   void operator()() const {
-    const dim3 grid(rec_width<kRV<E>>(p.D) * (uint32_t)p.N);
-    hipLaunchKernelGGL((rec_step_kernel<E, GT, SC, IN>), grid, dim3(64), 0, st, p);
+    const dim3 grid(rec_width<V>(p.D) * (uint32_t)p.N);
+    hipLaunchKernelGGL((rec_step_kernel<E, GT, V, SC, IN>), grid, dim3(64), 0, st, p);
   }
 };
 
 }  // namespace
 
-hipError_t launch_rec_sum(int dtype, const RecParams& p, bool rev, hipStream_t st) {
-  return rec_types(dtype, p.g_f32, p.scale, p.i, RecLaunch{rev ? RecLaunch::RSUM : RecLaunch::SUM, p, st});
+int64_t rec_words(int nchunk, int D) { return rec_counters(D) + ((int64_t)nchunk + nchunk / REC_GROUP) * D; }
+static hipError_t rec_run(int dtype, const RecParams& p, bool bwd, hipStream_t st) {
+  if (p.words) {
+    const int64_t n = rec_words(p.nchunk, p.D);
+    hipLaunchKernelGGL(rec_clear_kernel, dim3((uint32_t)std::min<int64_t>((n + 1023) / 1024, 1024)), dim3(256), 0, st, p.words, n);
+    if (hipError_t e = hipGetLastError(); e != hipSuccess) return e;
+  }
+  return rec_types(dtype, p.g_f32, p.D, p.scale, p.i, RecLaunch{bwd, p, st});
 }
-hipError_t launch_rec_join(const RecParams& p, bool rev, hipStream_t st) {
-  const dim3 grid((p.D + RJ_C - 1) / RJ_C);
-  if (rev) hipLaunchKernelGGL((rec_join_kernel<true>), grid, dim3(RJ_C * RJ_S), 0, st, p);
-  else hipLaunchKernelGGL((rec_join_kernel<false>), grid, dim3(RJ_C * RJ_S), 0, st, p);
-  return hipGetLastError();
-}
-hipError_t launch_rec_fwd(int dtype, const RecParams& p, hipStream_t st) {
-  return rec_types(dtype, p.g_f32, p.scale, p.i, RecLaunch{RecLaunch::FWD, p, st});
-}
-hipError_t launch_rec_bwd(int dtype, const RecParams& p, hipStream_t st) {
-  return rec_types(dtype, p.g_f32, p.scale, p.i, RecLaunch{RecLaunch::BWD, p, st});
-}
+hipError_t launch_rec_fwd(int dtype, const RecParams& p, hipStream_t st) { return rec_run(dtype, p, false, st); }
+hipError_t launch_rec_bwd(int dtype, const RecParams& p, hipStream_t st) { return rec_run(dtype, p, true, st); }
 hipError_t launch_rec_step(int dtype, const RecStepParams& p, hipStream_t st) {
-  return rec_types(dtype, p.g_f32, p.scale, p.i, RecStepLaunch{p, st});
+  return rec_types(dtype, p.g_f32, p.D, p.scale, p.i, RecStepLaunch{p, st});
 }
 
 }  // namespace gdn
