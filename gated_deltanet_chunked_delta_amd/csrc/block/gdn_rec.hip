@@ -93,6 +93,13 @@ __device__ __forceinline__ float expm1_neg(float L, float a) {
   return L > -0.1f ? s : a - 1.f;
 }
 
+// (The fp32 gate holds its argument to a range, a NaN too: here it stays one.)
+template <class E>
+__device__ __forceinline__ float rec_sigmoid(float x) {
+  const float s = fast_sigmoid<E>(x);
+  return sizeof(E) == 4 && x != x ? x : s;
+}
+
 // Decay, input and what the gradient needs of them, of one token and channel.
 template <class E, class GT, bool SC, bool IN>
 struct RecGate {
@@ -100,7 +107,7 @@ struct RecGate {
   __device__ __forceinline__ RecGate(float x, float g, float i, float scale) {
     float L = g;
     if (SC) {
-      sg = fast_sigmoid<GT>(g);
+      sg = rec_sigmoid<GT>(g);
       L = -scale * sg;
     }
     a = __builtin_amdgcn_exp2f(1.44269504f * L);
@@ -112,7 +119,7 @@ struct RecGate {
       u *= m;
     }
     if (IN) {
-      si = fast_sigmoid<E>(i);
+      si = rec_sigmoid<E>(i);
       u *= si;
     }
   }
