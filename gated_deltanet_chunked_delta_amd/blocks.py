@@ -103,43 +103,40 @@ def _on_gpu(name, t):
     return _layers._on_gpu(name, t)
 
 
-def _flat(t, inner=1):
-    """The number of rows in front of the last `inner` dimensions."""
-    n = 1
-    for s in t.shape[:t.dim() - inner]:
-        n *= s
-    return n
-
-
 def _row_input(name, t):
-    if t.dim() < 2:
+    """(shape, width, number of rows)"""
+    shape = t.shape
+    if len(shape) < 2:
         raise GDNError(f"{name} must be [..., D]")
-    D = t.shape[-1]
-    if D >> 31 or _flat(t) >> 31:
+    D, R = shape[-1], 1
+    for n in shape[:-1]:
+        R *= n
+    if (D | R) >> 31:
         _past_32_bits()
-    return D
+    return shape, D, R
+
+
+def _like(t, dtype):
+    """A contiguous tensor of t's shape (t's rows lie evenly apart: only a contiguous t is dense)."""
+    return torch.empty_like(t) if dtype is t.dtype else torch.empty_like(t, dtype=dtype)
 
 
 # ------------------------------------------------------------------ residual norm, rows in 8 bits
 def _addnorm_args(x, weight, residual, eps):
-    D = _row_input("x", x)
+    shape, D, R = _row_input("x", x)
     dt, dev = x.dtype, x.device
-    a = AddNormFwdArgs()
-    a.dtype = a.res_dtype = _dtype_code(x)
-    a.R, a.D, a.eps = _flat(x), D, eps
-    a.x, a.x_stride = x.data_ptr(), _rows("x", x, x.shape, 1, dt, dev)
+    code = res = _dtype_code(x)
+    xs, rs, s = _rows("x", x, shape, 1, dt, dev), 0, x
     _t("weight", weight, (D,), dt, dev)
-    a.w = weight.data_ptr()
-    s = x
     if residual is not None:
-        if residual.dtype not in (dt, torch.float32):
-            raise GDNError(f"residual must be {dt} or float32, got {residual.dtype}")
-        a.res_dtype = _dtype_code(residual)
-        a.r, a.r_stride = residual.data_ptr(), _rows("residual", residual, x.shape, 1, residual.dtype, dev)
-        s = torch.empty(x.shape, dtype=residual.dtype, device=dev)
-        a.s = s.data_ptr()
+        rdt = residual.dtype
+        if rdt is not dt and rdt is not torch.float32:
+            raise GDNError(f"residual must be {dt} or float32, got {rdt}")
+        res, rs = _dtype_code(residual), _rows("residual", residual, shape, 1, rdt, dev)
+        s = _like(x, rdt)
     _on_gpu("x", x)
-    return a, s
+    return AddNormFwdArgs(code, res, R, D, eps, x.data_ptr(), xs, _ptr(residual), rs, weight.data_ptr(),
+                          None if residual is None else s.data_ptr()), s
 
 
 def gdn_addnorm_fwd(x, weight, residual=None, eps: float = 1e-6):
@@ -147,7 +144,7 @@ def gdn_addnorm_fwd(x, weight, residual=None, eps: float = 1e-6):
     if _compiling():
         return _outside(gdn_addnorm_fwd, x, weight, residual, eps)
     a, s = _addnorm_args(x, weight, residual, eps)
-    y = torch.empty(x.shape, dtype=x.dtype, device=x.device)
+    y = torch.empty_like(x)
     a.y = y.data_ptr()
     _call(lib().gdn_addnorm_fwd, a, x.device)
     return y, s
@@ -159,7 +156,7 @@ def gdn_addnorm_bwd(s, weight, dy, ds=None, eps: float = 1e-6, need=(True, True,
     dresidual in s's, one tensor where the two are alike."""
     if _compiling():
         return _outside(gdn_addnorm_bwd, s, weight, dy, ds, eps, need)
-    D = _row_input("s", s)
+    _, D, R = _row_input("s", s)
     dt, dev = dy.dtype, s.device
     if s.dtype not in (dt, torch.float32):
         raise GDNError(f"s must be {dt} or float32, got {s.dtype}")
@@ -168,14 +165,14 @@ def gdn_addnorm_bwd(s, weight, dy, ds=None, eps: float = 1e-6, need=(True, True,
     _t("weight", weight, (D,), dt, dev)
     a = AddNormBwdArgs()
     a.dtype, a.res_dtype = _dtype_code(dy), _dtype_code(s)
-    a.R, a.D, a.eps = _flat(s), D, eps
+    a.R, a.D, a.eps = R, D, eps
     a.s, a.s_stride = s.data_ptr(), _rows("s", s, s.shape, 1, s.dtype, dev)
     a.w, a.dy, a.ds = weight.data_ptr(), dy.data_ptr(), _ptr(ds)
     _on_gpu("s", s)
     same = s.dtype == dt
-    dx = torch.empty(s.shape, dtype=dt, device=dev) if need[0] or same and need[1] else None
-    dr = torch.empty(s.shape, dtype=s.dtype, device=dev) if need[1] and not same else None
-    dw = torch.empty(D, dtype=dt, device=dev) if need[2] else None
+    dx = torch.empty_like(dy) if need[0] or same and need[1] else None
+    dr = torch.empty_like(s) if need[1] and not same else None
+    dw = torch.empty_like(weight) if need[2] else None
     a.dx, a.dr, a.dw = _ptr(dx), _ptr(dr), _ptr(dw)
     with _on(dev):
         ws = _workspace(lib().gdn_addnorm_bwd_workspace_size(ctypes.byref(a)), dev)
@@ -225,8 +222,7 @@ def add_rms_norm(x, weight, residual=None, eps: float = 1e-6):
 
 
 def _q8(x):
-    return (torch.empty(x.shape, dtype=torch.float8_e4m3fn, device=x.device),
-            torch.empty(x.shape[:-1], dtype=torch.float32, device=x.device))
+    return torch.empty_like(x, dtype=torch.float8_e4m3fn), x.new_empty(x.shape[:-1], dtype=torch.float32)
 
 
 def add_rms_norm_8bit(x, weight, residual=None, eps: float = 1e-6):
@@ -250,13 +246,11 @@ def quantize_rows(x):
     if _compiling():
         return _outside(quantize_rows, x)
     _no_derivative("quantize_rows", (x,))
-    D = _row_input("x", x)
-    a = QuantArgs()
-    a.dtype, a.R, a.D = _dtype_code(x), _flat(x), D
-    a.x, a.x_stride = x.data_ptr(), _rows("x", x, x.shape, 1, x.dtype, x.device)
+    shape, D, R = _row_input("x", x)
+    code, stride = _dtype_code(x), _rows("x", x, shape, 1, x.dtype, x.device)
     _on_gpu("x", x)
     q, scale = _q8(x)
-    a.q, a.q_scale = q.data_ptr(), scale.data_ptr()
+    a = QuantArgs(code, R, D, x.data_ptr(), stride, q.data_ptr(), scale.data_ptr())
     _call(lib().gdn_quant_rows, a, x.device)
     return q, scale
 
@@ -269,34 +263,33 @@ _ACTS = {None: 0, "silu": 1, "gelu": 2}
 def _linear_args(x, weight, bias, activation, residual, out_dtype):
     if weight.dim() != 2:
         raise GDNError("weight must be [N, K]")
-    K = _row_input("x", x)
-    N, dev = weight.shape[0], x.device
+    xshape, K, M = _row_input("x", x)
+    N, dev, dt = weight.shape[0], x.device, x.dtype
     if N >> 31:
         _past_32_bits()
     if activation not in _ACTS:
         raise GDNError(f"unknown activation {activation!r} (None, 'silu' or 'gelu')")
-    a = LinearArgs()
-    a.M, a.N, a.K, a.act = _flat(x), N, K, _ACTS[activation]
-    a.x, a.x_stride = x.data_ptr(), _rows("x", x, x.shape, 1, x.dtype, dev)
-    _t("weight", weight, (N, K), x.dtype, dev)
+    xs, rs = _rows("x", x, xshape, 1, dt, dev), 0
+    _t("weight", weight, (N, K), dt, dev)
     _t("bias", bias, (N,), out_dtype, dev, optional=True)
-    shape = (*x.shape[:-1], N)
+    shape = (*xshape[:-1], N)
     if residual is not None:
-        a.r, a.r_stride = residual.data_ptr(), _rows("residual", residual, shape, 1, out_dtype, dev)
-    a.w, a.bias = weight.data_ptr(), _ptr(bias)
+        rs = _rows("residual", residual, shape, 1, out_dtype, dev)
     _on_gpu("x", x)
-    return a, shape
+    return LinearArgs(0, 0, M, N, K, x.data_ptr(), xs, weight.data_ptr(), None, None, _ptr(bias), _ptr(residual), rs,
+                      _ACTS[activation]), shape
 
 
 def _linear_run(a, shape, out_dtype, dev, save):
-    args = LinearFwdArgs()
     y = torch.empty(shape, dtype=out_dtype, device=dev)
     v = torch.empty(shape, dtype=torch.float32, device=dev) if save else None
-    args.a, args.y, args.v_save = a, y.data_ptr(), _ptr(v)
-    with _on(dev):
-        ws = _workspace(lib().gdn_linear_fwd_workspace_size(ctypes.byref(args)), dev)
-    args.a.workspace, args.a.workspace_bytes = ws.data_ptr(), ws.numel()
-    _call(lib().gdn_linear_fwd, args, dev)
+    args = LinearFwdArgs(a, y.data_ptr(), _ptr(v))
+    L = lib()
+    if a.M > 64:  # (up to that many rows a product takes no workspace)
+        with _on(dev):
+            ws = _workspace(L.gdn_linear_fwd_workspace_size(ctypes.byref(args)), dev)
+        args.a.workspace, args.a.workspace_bytes = ws.data_ptr(), ws.numel()
+    _call(L.gdn_linear_fwd, args, dev)
     return y, v
 
 
@@ -426,7 +419,7 @@ def gdn_rec_fwd(x, g, i=None, scale=None, h0=None, cu_seqlens=None, cu_seqlens_h
     a, unchecked = _rec_args(x, g, i, scale, h0, cu_seqlens, cu_seqlens_host)
     dev, L = x.device, lib()
     args = RecFwdArgs()
-    y = _rows_like(x, unchecked)
+    y = _rows_like(x, True) if unchecked else torch.empty_like(x)
     hT = torch.empty((a.num_seqs, a.D), dtype=torch.float32, device=dev) if output_final_state else None
     args.a, args.y, args.hT = a, y.data_ptr(), _ptr(hT)
     states = None
@@ -536,7 +529,7 @@ def gdn_rec_step(x, g, state, i=None, scale=None, state_idx=None, y=None):
     _t("state_idx", state_idx, (N,), torch.int32, dev, optional=True)
     _on_gpu("x", x)
     if y is None:
-        y = x.new_empty((N, D))
+        y = torch.empty_like(x)
     else:
         _t("y", y, (N, D), dt, dev)
     a = RecStepArgs(code, _dtype_code(g), N, D, x.data_ptr(), xs, g.data_ptr(), gs, _ptr(i), ist, _ptr(scale),

@@ -391,7 +391,7 @@ gdn_status gdn_linear_fwd(const gdn_linear_fwd_args* args, void* stream) {
   if (!args->y) return fail(GDN_E_INVALID, "null output y");
   if (!aligned(args->y, esize(a.out_dtype)) || !aligned(args->v_save, 4)) return fail(GDN_E_INVALID, "a pointer is misaligned");
   const LinearPlan pl = linear_plan(a);
-  if (gdn_status st = check_ws(a.workspace, a.workspace_bytes, pl.total); st != GDN_OK) return st;
+  if (gdn_status st = pl.skinny ? GDN_OK : check_ws(a.workspace, a.workspace_bytes, pl.total); st != GDN_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   const int64_t es = (int64_t)bytes_of(a.dtype), row = row16(a.K, a.dtype);
   if (pl.skinny) {

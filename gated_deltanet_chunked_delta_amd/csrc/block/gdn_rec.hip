@@ -28,10 +28,11 @@
 // the sum of dy_t times the decays up to t, cut off at the first sequence's end.
 //
 // Measured (bf16, scale and i): 65,536 tokens of 2,048 channels in 326 us (1.07 GB, 3.3
-// TB/s; three kernels that read the inputs twice: 950), its gradient in 697 (1.88 GB, 2.7
-// TB/s); 16,384 of 2,304 in 95 and 197 us.  Four bytes of a row a thread and 16 (gradient: 8)
-// tokens: with eight bytes and half the tokens 413 and 1,075 us, by spilled registers in the
-// gradient; 8 tokens forwards 342 us; 16 waves of half the tokens and eight bytes 433 and 803.
+// TB/s; three kernels that read the inputs twice: 950), its gradient in 580 (1.88 GB, 3.2
+// TB/s); 16,384 of 2,304 in 95 and 161 us.  Four bytes of a row a thread and 16 (gradient: 8)
+// tokens, eight waves: with eight bytes and half the tokens 413 and 1,075 us (the gradient's
+// registers spill); 8 tokens forwards 342; the gradient with 4 tokens 792, with chunks of
+// four or two waves 611 and 801.  A gradient that keeps its inputs' products too spills: 697.
 #include "gdn_block.h"
 
 namespace gdn {
@@ -472,7 +473,6 @@ __global__ __launch_bounds__(64 * REC_W, 4) void rec_bwd_kernel(RecParams p) {
           a[k][e] = q.a;
           if (SC) { m[k][e] = q.m; sg[k][e] = q.sg; }
           if (IN) si[k][e] = q.si;
-          h[k][e] = q.u;
           f[e] = make_float2(f[e].x * q.a, fmaf(q.a, f[e].y, q.u));
           if (!cut) b[e] = make_float2(b[e].x * q.a, fmaf(b[e].x * q.a, dy[k].get(e, shift), b[e].y));
         }
@@ -524,9 +524,11 @@ __global__ __launch_bounds__(64 * REC_W, 4) void rec_bwd_kernel(RecParams p) {
         if (span.starts >> k & 1) rec_state<V>(p, p.h0, t0 + k, c, n, hc);
 #pragma unroll
         for (int e = 0; e < V; ++e) {
-          const float t = fmaf(a[k][e], hc[e], h[k][e]);
+          float u = x[k].get(e, shift);  // (formed again: the products of the gate, in its order)
+          if (SC) u *= m[k][e];
+          if (IN) u *= si[k][e];
           h[k][e] = hc[e];
-          hc[e] = t;
+          hc[e] = fmaf(a[k][e], hc[e], u);
         }
       }
     }
