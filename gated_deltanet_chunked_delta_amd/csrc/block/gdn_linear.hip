@@ -363,56 +363,74 @@ __global__ __launch_bounds__(256) void gemm_join_kernel(GemmParams p) {
 
 // Up to 16 MT rows of x by 16 outputs: eight waves take every eighth 128 bytes of k.
 // Bound: the weight's bytes (latency where there are few).
+typedef u32x4 u32x4_any __attribute__((aligned(1)));
 __device__ __forceinline__ u32x4 ld_piece(const char* row, int k, int kbytes) {
-  typedef u32x4 u32x4_any __attribute__((aligned(1)));
   if (k + 16 <= kbytes) return *reinterpret_cast<const u32x4_any*>(row + k);
   u32x4 v = {};
   for (int i = 0; i < 16 && k + i < kbytes; ++i) v[i / 4] |= (uint32_t)(uint8_t)row[k + i] << (8 * (i % 4));
   return v;
 }
-template <int T, class O, int MT>
+// With more rows a workgroup takes 16 NT outputs, so that the rows of x, which every
+// workgroup reads whole, are read less often (32 and 64 rows
+// of 2,048 to 6,144: 10.3 and 13.4 us with 32 outputs, 12.8 and 20.3 with 16).
+template <int T, class O, int MT, int NT>
 __global__ __launch_bounds__(512) void skinny_kernel(SkinnyParams p) {
   constexpr int W = 8;
-  __shared__ f32x4 red[W][MT][64];
+  __shared__ f32x4 red[W][NT * MT][64];
   const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), q = lane >> 4, r16 = lane & 15;
-  const int n0 = blockIdx.x * 16;
-  const char* wr = static_cast<const char*>(p.w) + (int64_t)min(n0 + r16, p.N - 1) * p.w_stride;
-  const char* xr[MT];
+  const int n0 = blockIdx.x * (16 * NT);
+  const char *wr[NT], *xr[MT];
+#pragma unroll
+  for (int j = 0; j < NT; ++j) wr[j] = static_cast<const char*>(p.w) + (int64_t)min(n0 + j * 16 + r16, p.N - 1) * p.w_stride;
 #pragma unroll
   for (int i = 0; i < MT; ++i) xr[i] = static_cast<const char*>(p.x) + (int64_t)min(i * 16 + r16, p.M - 1) * p.x_stride;
-  f32x4 acc[MT];
+  f32x4 acc[NT][MT];
 #pragma unroll
-  for (int i = 0; i < MT; ++i) acc[i] = zero4();
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) acc[j][i] = zero4();
   constexpr int U = MT <= 2 ? 4 : 2;  // steps requested together
-  for (int k = w * 128; k < p.kbytes; k += U * W * 128) {
-    Pieces b[U], a[U][MT];
+  auto steps = [&](int k, auto piece) {
+    Pieces b[U][NT], a[U][MT];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       const int ku = k + u * W * 128 + q * 16;
-      b[u].lo = ld_piece(wr, ku, p.kbytes);
-      b[u].hi = ld_piece(wr, ku + 64, p.kbytes);
+#pragma unroll
+      for (int j = 0; j < NT; ++j) {
+        b[u][j].lo = piece(wr[j], ku);
+        b[u][j].hi = piece(wr[j], ku + 64);
+      }
 #pragma unroll
       for (int i = 0; i < MT; ++i) {
-        a[u][i].lo = ld_piece(xr[i], ku, p.kbytes);
-        a[u][i].hi = ld_piece(xr[i], ku + 64, p.kbytes);
+        a[u][i].lo = piece(xr[i], ku);
+        a[u][i].hi = piece(xr[i], ku + 64);
       }
     }
 #pragma unroll
     for (int u = 0; u < U; ++u)
 #pragma unroll
-      for (int i = 0; i < MT; ++i) mma_step<T, sizeof(O) == 4>(acc[i], b[u], a[u][i]);
-  }
+      for (int j = 0; j < NT; ++j)
 #pragma unroll
-  for (int i = 0; i < MT; ++i) red[w][i][lane] = acc[i];
+        for (int i = 0; i < MT; ++i) mma_step<T, sizeof(O) == 4>(acc[j][i], b[u][j], a[u][i]);
+  };
+  int k = w * 128;
+  // whole steps without a test in front of each load, which would keep them apart
+  for (; k + (U - 1) * W * 128 + 128 <= p.kbytes; k += U * W * 128)
+    steps(k, [](const char* row, int at) { return *reinterpret_cast<const u32x4_any*>(row + at); });
+  for (; k < p.kbytes; k += U * W * 128) steps(k, [&](const char* row, int at) { return ld_piece(row, at, p.kbytes); });
+#pragma unroll
+  for (int j = 0; j < NT; ++j)
+#pragma unroll
+    for (int i = 0; i < MT; ++i) red[w][j * MT + i][lane] = acc[j][i];
   __syncthreads();
-  // four outputs of a row a thread: entry (i, lane) holds rows n 4 (lane / 16) of column m = lane % 16
-  for (int t = threadIdx.x; t < MT * 64; t += 512) {
-    const int i = t / 64, l = t % 64;
-    f32x4 s = red[0][i][l];
+  // four outputs of a row a thread: entry (j MT + i, lane) holds columns 16 j + 4 (lane / 16) of row 16 i + lane % 16
+  for (int t = threadIdx.x; t < NT * MT * 64; t += 512) {
+    const int ji = t / 64, l = t % 64;
+    f32x4 s = red[0][ji][l];
 #pragma unroll
-    for (int v = 1; v < W; ++v) s += red[v][i][l];
-    const int m = i * 16 + (l & 15);
-    if (m < p.M) finish4<O>(p.e, m, p.N, n0 + 4 * (l >> 4), s);
+    for (int v = 1; v < W; ++v) s += red[v][ji][l];
+    const int m = ji % MT * 16 + (l & 15);
+    if (m < p.M) finish4<O>(p.e, m, p.N, n0 + ji / MT * 16 + 4 * (l >> 4), s);
   }
 }
 
@@ -498,10 +516,10 @@ hipError_t gemm_any(const GemmParams& p, const GemmPlan& g, hipStream_t st) {
 }
 template <int T, class O>
 hipError_t skinny_any(const SkinnyParams& p, hipStream_t st) {
-  const dim3 grid((p.N + 15) / 16);
-  if (p.M <= 16) hipLaunchKernelGGL((skinny_kernel<T, O, 1>), grid, dim3(512), 0, st, p);
-  else if (p.M <= 32) hipLaunchKernelGGL((skinny_kernel<T, O, 2>), grid, dim3(512), 0, st, p);
-  else hipLaunchKernelGGL((skinny_kernel<T, O, 4>), grid, dim3(512), 0, st, p);
+  auto grid = [&](int nt) { return dim3((p.N + 16 * nt - 1) / (16 * nt)); };
+  if (p.M <= 16) hipLaunchKernelGGL((skinny_kernel<T, O, 1, 1>), grid(1), dim3(512), 0, st, p);
+  else if (p.M <= 32) hipLaunchKernelGGL((skinny_kernel<T, O, 2, 2>), grid(2), dim3(512), 0, st, p);
+  else hipLaunchKernelGGL((skinny_kernel<T, O, 4, 2>), grid(2), dim3(512), 0, st, p);
   return hipGetLastError();
 }
 
@@ -509,11 +527,12 @@ hipError_t skinny_any(const SkinnyParams& p, hipStream_t st) {
 
 // The cheapest of both tiles and a few splits of k, by a model of their times in us that
 // was fitted to bf16 products of 64 to 16,384 rows (a step: 128 bytes of k).  A round of
-// 256 x 256 tiles, one a compute unit, takes 1.8 a step and 8 to start and end; 128 x 128
-// tiles take 0.69 and 5 one a compute unit, 1.1 and 6 two.  Splits add a join: its bytes,
-// and a launch.  Measured against the other choice: 4,096 x 2,048 -> 2,048 in tiles of 128
-// 37 us, of 256 60; 8,192 rows 73 and 67; 128 rows -> 6,144 in 4 parts 20, whole 25; a sum
-// over 32,768 to 2,048 x 2,048 of 256 in 4 parts 276, whole 652, of 128 in 2 parts 310.
+// 256 x 256 tiles, one a compute unit, takes 1.55 a step and 11 to start and end; 128 x
+// 128 tiles take 0.69 and 5 one a compute unit, 1 and 5 two.  Splits add a join: its bytes
+// (mostly from cache), and a launch.  Measured against the other choice: 4,096 x 2,048 ->
+// 2,048 in tiles of 128 37 us, of 256 60; 8,192 rows 72 and 61; 128 rows -> 6,144 in 4 parts
+// 20, whole 25; sums over 8,192 to 2,048 x 2,048 of 128 in 2 parts 80, whole 89, of 256 in 4
+// parts 93; over 32,768 of 256 in 4 parts 276, whole 652, of 128 in 2 parts 310.
 GemmPlan gemm_plan(int64_t M, int N, int64_t kbytes, int esize, int cus) {
   const int steps = (int)((kbytes + 127) / 128);
   const double slow = esize == 4 ? 8. : 1.;  // fp32's matrix instructions against bf16's
@@ -526,12 +545,12 @@ GemmPlan gemm_plan(int64_t M, int N, int64_t kbytes, int esize, int cus) {
       const int64_t n = tiles * s;
       double t;
       if (tile == 256) {
-        t = (double)((n + cus - 1) / cus) * (1.8 * k + 8.);
+        t = (double)((n + cus - 1) / cus) * (1.55 * k + 11.);
       } else {
         const int64_t rest = n % (2 * cus);
-        t = (double)(n / (2 * cus)) * (1.1 * k + 6.) + (rest == 0 ? 0. : rest <= cus ? 0.69 * k + 5. : 1.1 * k + 6.);
+        t = (double)(n / (2 * cus)) * (k + 5.) + (rest == 0 ? 0. : rest <= cus ? 0.69 * k + 5. : k + 5.);
       }
-      if (s > 1) t += 4. + (double)M * N * (8. * s + 2.) / 4e6;
+      if (s > 1) t += 4. + (double)M * N * (8. * s + 2.) / 6e6;
       if (least == 0. || t < least) {
         least = t;
         best = GemmPlan{tile, s, (steps + s - 1) / s};
