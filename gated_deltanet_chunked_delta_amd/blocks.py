@@ -369,7 +369,7 @@ def linear_8bit(x, x_scale, weight, weight_scale, bias=None, activation=None, re
     or fp32).  No derivative."""
     if _compiling():
         return _outside(linear_8bit, x, x_scale, weight, weight_scale, bias, activation, residual, out_dtype)
-    _no_derivative("linear_8bit", (bias, residual, x_scale, weight_scale))
+    _no_derivative("linear_8bit", (x, x_scale, weight, weight_scale, bias, residual))
     if x.dtype is not torch.float8_e4m3fn:
         raise GDNError(f"x must be {torch.float8_e4m3fn}, got {x.dtype}")
     if out_dtype not in (torch.bfloat16, torch.float32):

@@ -87,7 +87,7 @@ RecPlan rec_plan(const gdn_rec_args& a, bool bwd, bool own_states) {
 }
 gdn_status check_rec_grid(const gdn_rec_args& a, const RecPlan& pl) {
   const double per = 64. * gdn::REC_BYTES / esize(a.dtype);
-  if (!launchable(((double)pl.bwd + a.num_seqs) * std::ceil(a.D / per) * 64 * gdn::REC_W))
+  if (!launchable(((double)pl.bwd + a.num_seqs / 64. + 1) * std::ceil(a.D / per) * 64 * gdn::REC_W))
     return fail(GDN_E_INVALID, "problem too large: %d chunks and %d sequences of %d channels", pl.bwd, a.num_seqs, a.D);
   return GDN_OK;
 }
@@ -128,8 +128,9 @@ gdn_status check_linear(const gdn_linear_args& a, bool bwd) {
   if (!aligned(a.x, es) || !aligned(a.w, es) || !aligned(a.bias, os) || !aligned(a.r, os) || !aligned(a.x_scale, 4) ||
       !aligned(a.w_scale, 4))
     return fail(GDN_E_INVALID, "a pointer is misaligned");
-  const double tiles = ((a.M + 127) / 128. + 1) * ((a.N + 127) / 128. + 1);
-  if (!launchable(256. * 16 * tiles)) return fail(GDN_E_INVALID, "problem too large");
+  // (tiles of 128 x 128 and up to 16 parts of k; the gradients' products too)
+  auto fits = [](double m, double n) { return launchable(256. * 16 * (m / 128 + 2) * (n / 128 + 2)); };
+  if (!fits(a.M, a.N) || (bwd && (!fits(a.M, a.K) || !fits(a.N, a.K)))) return fail(GDN_E_INVALID, "problem too large");
   return GDN_OK;
 }
 // Whether a product can read these rows as they lie.

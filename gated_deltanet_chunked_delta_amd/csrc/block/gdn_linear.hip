@@ -79,18 +79,28 @@ __device__ __forceinline__ void mma_step(f32x4& acc, const Pieces& a, const Piec
   }
 }
 
+// sigmoid(u) for an activation of v: fp32's gate stops at sigmoid(-88), which a v near the
+// type's lowest value would still turn into a result of order 1.
+template <class E>
+__device__ __forceinline__ float act_gate(float u) {
+  const float s = fast_sigmoid<E>(u);
+  return sizeof(E) == 4 && u < -87.f ? 0.f : s;
+}
 // act(v); derivative in d.  E: the type that the result is rounded to
 template <class E, bool D>
 __device__ __forceinline__ float act_of(int act, float v, float& d) {
   if (act == GDN_ACT_SILU) {
-    const float s = fast_sigmoid<E>(v);
+    const float s = act_gate<E>(v);
     if (D) d = dsilu_gate(v, s);
     return v * s;
   }
   if (act == GDN_ACT_GELU) {
     constexpr float c = 1.5957691216057308f;  // 2 sqrt(2 / pi)
-    const float s = fast_sigmoid<E>(c * fmaf(0.044715f * v * v, v, v));
-    if (D) d = fmaf(v * (s - s * s), c * fmaf(3.f * 0.044715f * v, v, 1.f), s);
+    const float s = act_gate<E>(c * fmaf(0.044715f * v * v, v, v));
+    if (D) {  // (past +-16, where s is 0 or 1, the square may not grow until 0 times it is a NaN)
+      const float t = __builtin_amdgcn_fmed3f(v, -16.f, 16.f);
+      d = fmaf(v * (s - s * s), c * fmaf(3.f * 0.044715f * t, t, 1.f), s);
+    }
     return v * s;
   }
   d = 1.f;

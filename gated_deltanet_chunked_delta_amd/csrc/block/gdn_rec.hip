@@ -309,16 +309,21 @@ __device__ __forceinline__ void rec_state(const RecParams& p, const float* state
   rec_vec<V>(states, states ? rec_seq_of(p, t) : 0, p.D, c, n, h);
 }
 
-// Workgroups past the chunks write the final states of sequences without tokens.
+// Workgroups past the chunks write the final states of sequences without tokens, each
+// looking at REC_EMPTY of them.
+constexpr int REC_EMPTY = 64;
 template <int V>
-__device__ __forceinline__ void rec_empty_seq(const RecParams& p, int seq, const float* src, float* dst, int c, int n) {
+__device__ __forceinline__ void rec_empty_seqs(const RecParams& p, int group, const float* src, float* dst, int c, int n) {
+  if (n <= 0) return;
   RecSeq s(p);
-  s.n = seq;
-  s.bounds();
-  if (threadIdx.x >= 64 || n <= 0 || s.end > s.start || !dst) return;
-  float h[V];
-  rec_vec<V>(src, seq, p.D, c, n, h);
-  rec_put<V>(dst, seq, p.D, c, n, h);
+  for (int q = group * REC_EMPTY + wave_id(); q < min((group + 1) * REC_EMPTY, p.N); q += REC_W) {
+    s.n = q;
+    s.bounds();
+    if (s.end > s.start) continue;
+    float h[V];
+    rec_vec<V>(src, q, p.D, c, n, h);
+    rec_put<V>(dst, q, p.D, c, n, h);
+  }
 }
 
 template <class E, class GT, int V, bool SC, bool IN>
@@ -330,7 +335,7 @@ __global__ __launch_bounds__(64 * REC_W, 4) void rec_fwd_kernel(RecParams p) {
   const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
   const int c = (int)(blockIdx.x % rec_width<V>(p.D) * 64 + lane) * V, n = p.D - c, shift = max(V - n, 0);
   if (ch >= p.nchunk) {
-    rec_empty_seq<V>(p, ch - p.nchunk, p.h0, p.hT, c, n);
+    rec_empty_seqs<V>(p, ch - p.nchunk, p.h0, p.hT, c, n);
     return;
   }
   const int t0 = ch * (W * S) + w * S;
@@ -430,7 +435,7 @@ __global__ __launch_bounds__(64 * REC_W, 4) void rec_bwd_kernel(RecParams p) {
   const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
   const int c = (int)(blockIdx.x % rec_width<V>(p.D) * 64 + lane) * V, n = p.D - c, shift = max(V - n, 0);
   if (k_chain >= p.nchunk) {
-    rec_empty_seq<V>(p, k_chain - p.nchunk, p.dhT, p.dh0, c, n);
+    rec_empty_seqs<V>(p, k_chain - p.nchunk, p.dhT, p.dh0, c, n);
     return;
   }
   const int ch = p.nchunk - 1 - k_chain, t0 = ch * (W * S) + w * S;
@@ -648,7 +653,8 @@ struct RecLaunch {
   hipStream_t st;
   template <class E, class GT, int V, bool SC, bool IN>
   void operator()() const {
-    const int more = (bwd ? p.dh0 : p.hT) ? p.N : 0;
+    // (sequences of one length are empty all or none)
+    const int more = (bwd ? p.dh0 : p.hT) && (p.cu || p.tokens == 0) ? (p.N + REC_EMPTY - 1) / REC_EMPTY : 0;
     const dim3 grid(rec_width<V>(p.D) * (uint32_t)(p.nchunk + more));
     if (grid.x == 0) return;
     if (bwd) hipLaunchKernelGGL((rec_bwd_kernel<E, GT, V, SC, IN>), grid, dim3(64 * REC_W), 0, st, p);

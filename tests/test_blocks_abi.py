@@ -99,7 +99,8 @@ def test_linear_refusals(L, kw, status):
         assert L.gdn_linear_fwd_workspace_size(ref(f)) == 0
 
 
-@pytest.mark.parametrize("kw,status", BAD_LINEAR + [(Q, 2), (dict(M=1 << 22), 1), (dict(N=1 << 22), 1)])
+@pytest.mark.parametrize("kw,status", BAD_LINEAR + [(Q, 2), (dict(M=1 << 22), 1), (dict(N=1 << 22), 1),
+                                                    (dict(M=1 << 20, K=1 << 19, x_stride=1 << 19), 1), (dict(N=1 << 20, K=1 << 19, x_stride=1 << 19), 1)])
 def test_linear_gradient_refusals(L, kw, status):
     b = fill(blocks.LinearBwdArgs(), a=lin(**kw), dy=FAKE, dx=FAKE, dw=FAKE, dbias=FAKE)
     assert L.gdn_linear_bwd(ref(b), None) == status
@@ -146,7 +147,7 @@ def test_recurrence_missing_buffers_and_sizes(L):
     kept = L.gdn_rec_bwd_workspace_size(ref(fill(blocks.RecBwdArgs(), a=rec(), h_saved=FAKE, **ok)))
     assert own - kept == 4 * 4 * 64
     # more sequences' final states than one launch has threads
-    many = rec(B=1, T=8, D=1 << 20, x_stride=1 << 20, g_stride=1 << 20, i_stride=1 << 20, cu_seqlens=FAKE, num_seqs=1 << 12)
+    many = rec(B=1, T=8, D=1 << 20, x_stride=1 << 20, g_stride=1 << 20, i_stride=1 << 20, cu_seqlens=FAKE, num_seqs=1 << 17)
     assert L.gdn_rec_fwd(ref(fill(blocks.RecFwdArgs(), a=many, y=FAKE, hT=FAKE)), None) == 1 and b"too large" in L.gdn_last_error()
 
 

@@ -314,6 +314,24 @@ def test_linear_without_rows():
     assert y.shape == (0, 10) and dx.shape == (0, 24) and not dw.any() and not db.any()
 
 
+@pytest.mark.parametrize("dt", ["bf16", "f32"])
+@pytest.mark.parametrize("act", ["silu", "gelu"])
+def test_activations_at_the_types_ends(act, dt):
+    """A bias of the type's lowest value (a mask) gives 0 and no gradient, its largest passes through."""
+    dt = DT[dt]
+    top = torch.finfo(dt).max
+    b = torch.tensor([-top, -1e19, -100., -20., 20., 100., 1e19, top], device="cuda").to(dt)
+    for M in (3, 70):
+        x, w = torch.zeros(M, 16, device="cuda", dtype=dt), torch.zeros(8, 16, device="cuda", dtype=dt)
+        leaves = [t.requires_grad_(True) for t in (x, w, b)]
+        y = gdn.linear(x, w, b, act)
+        g = torch.autograd.grad(y, leaves, torch.ones_like(y))
+        assert bool((y[:, :3].abs() < 1e-30).all()) and torch.equal(y[:, 4:], b[4:].expand(M, 4)) and bool((y[:, 3].abs() < 1e-7).all())
+        assert all(bool(t.isfinite().all()) for t in g)
+        # (silu'(-20) = -19 e^-20 = -3.92e-8 a row, gelu's less)
+        assert bool((g[2][:4].abs() < M * 4e-8).all()) and bool(((g[2][4:] - M).abs() < 1e-5).all())
+
+
 def test_linear_keeps_what_is_not_finite_to_its_row():
     for M in (20, 300):
         x, w = rn(1, M, 72, dt=torch.bfloat16), rn(2, 130, 72, dt=torch.bfloat16)
@@ -477,6 +495,39 @@ def test_recurrence_rows_behind_the_last_sequence():
     grads = blocks.gdn_rec_bwd(x, g, dy, cu_seqlens=cu)
     wg = blocks.gdn_rec_bwd(x[:, :250].contiguous(), g[:, :250].contiguous(), dy[:, :250].contiguous(), cu_seqlens=cu)
     assert all(torch.equal(a[:, :250], b) and not a[:, 250:].any() for a, b in zip(grads[:2], wg[:2]))
+
+
+@pytest.mark.parametrize("lens", [None, [0, 0, 0]])
+def test_recurrence_without_tokens(lens):
+    N = 3
+    x, g, sc, h0, dh = torch.zeros(1 if lens else N, 0, 70, device="cuda"), None, ru(1, .1, .2, 70), rn(2, N, 70), rn(3, N, 70)
+    g = torch.zeros_like(x)
+    cu = torch.zeros(4, dtype=torch.int32)
+    leaves = [t.requires_grad_(True) for t in (x, g, sc, h0)]
+    y, hT = gdn.gated_recurrence(x, g, scale=sc, initial_state=h0, output_final_state=True,
+                                 **(dict(cu_seqlens=cu.cuda(), cu_seqlens_host=cu) if lens else {}))
+    dx, dg, ds, d0 = torch.autograd.grad([y, hT], leaves, [torch.zeros_like(y), dh])
+    assert y.shape == x.shape and torch.equal(hT, h0) and torch.equal(d0, dh) and not ds.any()
+
+
+def test_recurrence_of_many_sequences():
+    """A thousand sequences of up to 40 tokens, a third of them empty, against each alone."""
+    g0 = torch.Generator().manual_seed(5)
+    lens = (torch.randint(0, 41, (1000,), generator=g0) * (torch.rand(1000, generator=g0) > .33)).tolist()
+    cu = torch.tensor([0] + lens).cumsum(0).to(torch.int32)
+    T, D = int(cu[-1]), 66
+    x, g, h0, dy, dh = rn(1, 1, T, D), -rn(2, 1, T, D).abs() * .1, rn(3, 1000, D), rn(4, 1, T, D), rn(5, 1000, D)
+    seqs = dict(cu_seqlens=cu.cuda(), cu_seqlens_host=cu)
+    y, hT = gdn.gated_recurrence(x, g, initial_state=h0, output_final_state=True, **seqs)
+    dx, dg, _, _, d0 = blocks.gdn_rec_bwd(x, g, dy, h0=h0, dhT=dh, **seqs)
+    for n in list(range(0, 1000, 37)) + [999]:
+        lo, hi = int(cu[n]), int(cu[n + 1])
+        q = [t.double().requires_grad_(True) for t in (x[0, lo:hi], g[0, lo:hi], h0[n:n + 1])]
+        wy, wT = ref_rec(q[0], q[1], None, None, q[2], [(0, hi - lo)])
+        wx, wg, w0 = torch.autograd.grad([wy, wT], q, [dy[0, lo:hi].double(), dh[n:n + 1].double()], allow_unused=True)
+        pairs = [(hT[n:n + 1], wT), (d0[n:n + 1], w0)] + ([(y[0, lo:hi], wy), (dx[0, lo:hi], wx), (dg[0, lo:hi], wg)] if hi > lo else [])
+        for a, b in pairs:   # forty tokens' roundings, four each
+            within(str(n), a, b, b.abs().max().expand_as(b), 400)
 
 
 def test_recurrence_takes_slices():
