@@ -51,7 +51,7 @@ def build(verbose: bool = False, out: str = LIB, sanitize: bool = False, phase_c
     (GDN_PHASE_CLOCK; objects in a separate folder, default output LIB_CLOCK)."""
     obj_dir = OBJ + ("_san" if sanitize else "") + ("_clock" if phase_clock else "")
     os.makedirs(obj_dir, exist_ok=True)
-    extra = (SAN_FLAGS if sanitize else ()) + (("-DGDN_PHASE_CLOCK",) if phase_clock else ())
+    extra = (tuple(SAN_FLAGS) if sanitize else ()) + (("-DGDN_PHASE_CLOCK",) if phase_clock else ())
     with cf.ThreadPoolExecutor(max_workers=min(8, len(SOURCES))) as ex:
         objs = list(ex.map(lambda s_: _compile(s_, obj_dir, extra), SOURCES))
     tmp = out + ".tmp"
