@@ -217,7 +217,13 @@ struct PackParams {
   int64_t ldt;
   float* sums;               // nullable
 };
-hipError_t launch_pack(int dtype, const PackParams& p, hipStream_t st);
+// Several of them in one launch (8-bit rows: one).
+struct PackJobs {
+  PackParams job[3];
+  int n = 0;
+  __host__ __device__ int64_t blocks(int i) const { return (job[i].R + 63) / 64 * ((job[i].C + 63) / 64); }
+};
+hipError_t launch_pack(int dtype, const PackJobs& jobs, hipStream_t st);
 
 // ---------------------------------------------------------------- sums of parts
 // out[c] = sum over rows of part[row][c], in 64 bits and a fixed order, rounded once.

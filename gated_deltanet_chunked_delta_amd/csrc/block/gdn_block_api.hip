@@ -195,9 +195,9 @@ gdn::Epilogue epilogue(const gdn_linear_fwd_args& f) {
   e.out = f.y; e.v_save = f.v_save;
   return e;
 }
-gdn_status run_pack(int dtype, const gdn::PackParams& p, hipStream_t s) {
-  if (p.R == 0) return GDN_OK;
-  hipError_t e = timed("linear_pack", s, [&] { return gdn::launch_pack(dtype, p, s); });
+gdn_status run_pack(int dtype, const gdn::PackJobs& jobs, hipStream_t s) {
+  if (jobs.n == 0) return GDN_OK;
+  hipError_t e = timed("linear_pack", s, [&] { return gdn::launch_pack(dtype, jobs, s); });
   return e == hipSuccess ? GDN_OK : hip_fail(e, "row copy launch");
 }
 gdn_status run_gemm(const char* name, int dtype, int out_dtype, gdn::GemmParams p, const gdn::GemmPlan& g, hipStream_t s) {
@@ -408,9 +408,10 @@ gdn_status gdn_linear_fwd(const gdn_linear_fwd_args* args, void* stream) {
   p.part = at<float>(a.workspace, pl.o_part);
   p.e = epilogue(*args);
   auto relay = [&](const void* in, int64_t stride, int64_t R, size_t off) {
-    gdn::PackParams k{};
+    gdn::PackJobs jobs{};
+    gdn::PackParams& k = jobs.job[jobs.n++];
     k.in = in; k.ld = stride; k.R = R; k.C = a.K; k.rows = at<char>(a.workspace, off); k.ldo = row / es;
-    return run_pack(a.dtype, k, s);
+    return run_pack(a.dtype, jobs, s);
   };
   if (!rows_fit(a.x, a.x_stride, a.K, a.dtype)) {
     if (gdn_status st = relay(a.x, a.x_stride, a.M, pl.o_x); st != GDN_OK) return st;
@@ -441,15 +442,26 @@ gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* args, void* stream) {
   hipStream_t s = static_cast<hipStream_t>(stream);
   void* ws = a.workspace;
   const int64_t rn = row16(a.N, a.dtype), rm = row16(a.M, a.dtype);
-  // dy act'(v): as it lies, turned, and its column sums
-  gdn::PackParams k{};
+  // dy act'(v): as it lies, turned, and its column sums; w and x turned
+  gdn::PackParams k{}, wt{}, xt{};
   k.in = args->dy; k.ld = a.N; k.R = a.M; k.C = a.N;
   k.v = a.act ? args->v_saved : nullptr; k.act = a.act;
   if (pl.pre) { k.rows = at<char>(ws, pl.o_pre); k.ldo = rn / es; }
   if (args->dw) { k.cols = at<char>(ws, pl.o_pre_t); k.ldt = rm / es; }
   if (args->dbias) k.sums = at<float>(ws, pl.o_sums);
-  if (k.rows || k.cols || k.sums)
-    if (gdn_status st = run_pack(a.dtype, k, s); st != GDN_OK) return st;
+  gdn::PackJobs jobs{};
+  if (a.M > 0) {
+    if (k.rows || k.cols || k.sums) jobs.job[jobs.n++] = k;
+    if (args->dx) {
+      wt.in = a.w; wt.ld = a.K; wt.R = a.N; wt.C = a.K; wt.cols = at<char>(ws, pl.o_w_t); wt.ldt = rn / es;
+      jobs.job[jobs.n++] = wt;
+    }
+    if (args->dw) {
+      xt.in = a.x; xt.ld = a.x_stride; xt.R = a.M; xt.C = a.K; xt.cols = at<char>(ws, pl.o_x_t); xt.ldt = rm / es;
+      jobs.job[jobs.n++] = xt;
+    }
+  }
+  if (gdn_status st = run_pack(a.dtype, jobs, s); st != GDN_OK) return st;
   if (args->dbias) {
     hipError_t e = timed("linear_dbias", s, [&] { return gdn::launch_join_parts(a.dtype, k.sums, (a.M + 63) / 64, a.N, args->dbias, s); });
     if (e != hipSuccess) return hip_fail(e, "bias gradient launch");
@@ -457,20 +469,14 @@ gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* args, void* stream) {
   gdn::GemmParams p{};
   p.part = at<float>(ws, pl.o_part);
   if (args->dx && a.M > 0) {
-    gdn::PackParams t{};
-    t.in = a.w; t.ld = a.K; t.R = a.N; t.C = a.K; t.cols = at<char>(ws, pl.o_w_t); t.ldt = rn / es;
-    if (gdn_status st = run_pack(a.dtype, t, s); st != GDN_OK) return st;
-    p.a = pl.pre ? k.rows : args->dy; p.lda = rn; p.b = t.cols; p.ldb = rn;
+    p.a = pl.pre ? k.rows : args->dy; p.lda = rn; p.b = wt.cols; p.ldb = rn;
     p.M = a.M; p.N = a.K; p.kbytes = (int)rn;
     p.e = gdn::Epilogue{};
     p.e.out = args->dx;
     if (gdn_status st = run_gemm("linear_dx", a.dtype, a.dtype, p, pl.gx, s); st != GDN_OK) return st;
   }
   if (args->dw) {
-    gdn::PackParams t{};
-    t.in = a.x; t.ld = a.x_stride; t.R = a.M; t.C = a.K; t.cols = at<char>(ws, pl.o_x_t); t.ldt = rm / es;
-    if (gdn_status st = run_pack(a.dtype, t, s); st != GDN_OK) return st;
-    p.a = k.cols; p.lda = rm; p.b = t.cols; p.ldb = rm;
+    p.a = k.cols; p.lda = rm; p.b = at<char>(ws, pl.o_x_t); p.ldb = rm;
     p.M = a.N; p.N = a.K; p.kbytes = (int)rm;
     p.e = gdn::Epilogue{};
     p.e.out = args->dw;

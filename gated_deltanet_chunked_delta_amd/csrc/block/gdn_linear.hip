@@ -466,11 +466,14 @@ __device__ __forceinline__ void put8(bf16* p, const float (&f)[8], bool) { store
 // the 64 values that a wave touches at once on 64 banks both ways.  Bound: memory (16,384 x
 // 6,144 with v, both copies: 1.0 GB in 219 us, 4.6 TB/s).
 template <class E>
-__global__ __launch_bounds__(256) void pack_kernel(PackParams p) {
+__global__ __launch_bounds__(256) void pack_kernel(PackJobs jobs) {
   __shared__ float tile[64][65];
+  int64_t blk = block_2d();
+  int job = 0;
+  while (job < jobs.n - 1 && blk >= jobs.blocks(job)) blk -= jobs.blocks(job++);
+  const PackParams& p = jobs.job[job];
   const int cols_n = (p.C + 63) / 64;
-  const int64_t blk = block_2d(), br = blk / cols_n;
-  const int64_t r0 = br * 64;
+  const int64_t br = blk / cols_n, r0 = br * 64;
   const int c0 = (int)(blk - br * cols_n) * 64;
   if (r0 >= p.R) return;
   const int ti = threadIdx.x / 8, tj = threadIdx.x % 8 * 8;
@@ -590,13 +593,15 @@ hipError_t launch_skinny(int dtype, int out_dtype, const SkinnyParams& p, hipStr
   if (dtype == GDN_F32) return skinny_any<GDN_F32, float>(p, st);
   return out_dtype == GDN_BF16 ? skinny_any<GDN_E4M3, bf16>(p, st) : skinny_any<GDN_E4M3, float>(p, st);
 }
-hipError_t launch_pack(int dtype, const PackParams& p, hipStream_t st) {
+hipError_t launch_pack(int dtype, const PackJobs& jobs, hipStream_t st) {
   if (dtype == GDN_E4M3) {
+    const PackParams& p = jobs.job[0];
     hipLaunchKernelGGL(pack_bytes_kernel, blocks_2d((p.R * (p.ldo / 16) + 255) / 256), dim3(256), 0, st, p);
   } else {
-    const dim3 grid = blocks_2d((p.R + 63) / 64 * ((p.C + 63) / 64));
-    if (dtype == GDN_BF16) hipLaunchKernelGGL((pack_kernel<bf16>), grid, dim3(256), 0, st, p);
-    else hipLaunchKernelGGL((pack_kernel<float>), grid, dim3(256), 0, st, p);
+    int64_t blocks = 0;
+    for (int i = 0; i < jobs.n; ++i) blocks += jobs.blocks(i);
+    if (dtype == GDN_BF16) hipLaunchKernelGGL((pack_kernel<bf16>), blocks_2d(blocks), dim3(256), 0, st, jobs);
+    else hipLaunchKernelGGL((pack_kernel<float>), blocks_2d(blocks), dim3(256), 0, st, jobs);
   }
   return hipGetLastError();
 }
