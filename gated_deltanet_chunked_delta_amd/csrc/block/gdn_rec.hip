@@ -27,10 +27,10 @@
 // The gradient's chain runs the other way with pairs of its own: in token order its U is
 // the sum of dy_t times the decays up to t, cut off at the first sequence's end.
 //
-// Measured (bf16, scale and i): 65,536 tokens of 2,048 channels in 326 us (1.07 GB, 3.3
-// TB/s; three kernels that read the inputs twice: 950), its gradient in 580 (1.88 GB, 3.2
-// TB/s); 16,384 of 2,304 in 95 and 161 us.  Four bytes of a row a thread and 16 (gradient: 8)
-// tokens, eight waves: with eight bytes and half the tokens 413 and 1,075 us (the gradient's
+// Measured (bf16, scale and i): 65,536 tokens of 2,048 channels in 320 us (1.07 GB, 3.4
+// TB/s; three kernels that read the inputs twice: 950), its gradient in 551 (1.88 GB, 3.4
+// TB/s); 16,384 of 2,304 in 91 and 155 us.  Four bytes of a row a thread and 16 (gradient: 8)
+// tokens, eight waves (groups of 16 in all of these: 326, 580): with eight bytes and half the tokens 413 and 1,075 us (the gradient's
 // registers spill); 8 tokens forwards 342; the gradient with 4 tokens 792, with chunks of
 // four or two waves 611 and 801.  A gradient that keeps its inputs' products too spills: 697.
 #include "gdn_block.h"
@@ -219,17 +219,22 @@ __device__ __forceinline__ uint64_t rec_await(const uint64_t* p) {
 // narrowest, fp32's), each in a line of its own.
 constexpr int REC_LINE = 16;
 __host__ __device__ __forceinline__ int64_t rec_counters(int D) { return (int64_t)rec_width<REC_BYTES / 4>(D) * REC_LINE; }
-constexpr int REC_GROUP = 16;  // chunks of a group: about as many words are read as groups wait for each other
+// Chunks of a group.  Groups wait for each other, some 1.2 us a time; a chunk reads half a
+// group's words.  Many channels bring enough other workgroups for the first and pay for the
+// second.  Measured with 8, 16, 32 chunks (65,536 tokens, forward and gradient): 2,048 channels
+// 320 + 551, 329 + 569, 353 + 604 us; 512 88 + 153, 88 + 152, 94 + 164; 128 59 + 94, 46 + 65, 41 + 60.
+constexpr int REC_GROUP_MIN = 8;
+template <int V> __device__ __forceinline__ int rec_group(int D) { return rec_width<V>(D) >= 8 ? REC_GROUP_MIN : 16; }
 constexpr int REC_PEEK = 4;    // words requested together
 
 // Publishes the pair of chunk k (counted in the chain's direction) and returns the state
 // entering it.  One wave; e: the thread's channel, of which all V exist up to n.
 template <int V>
 __device__ __forceinline__ void rec_chain(const RecParams& p, int k, int c, int n, const float2 (&own)[V], float (&h)[V]) {
-  const int first = k / REC_GROUP * REC_GROUP;
+  const int len = rec_group<V>(p.D), group = k / len, first = group * len;
   uint64_t* pairs = p.words + rec_counters(p.D);          // [nchunk][D]
   uint64_t* ends = pairs + (int64_t)p.nchunk * p.D;       // [groups][D]: (-1, the state leaving a group)
-  const bool last = k == first + REC_GROUP - 1;
+  const bool last = k == first + len - 1;
 #pragma unroll
   for (int e = 0; e < V; ++e)
     if (e < n && !last) rec_publish(pairs + (int64_t)k * p.D + c + e, own[e]);
@@ -255,9 +260,9 @@ __device__ __forceinline__ void rec_chain(const RecParams& p, int k, int c, int 
 #pragma unroll
   for (int e = 0; e < V; ++e) {
     float in = 0.f;
-    if (first > 0 && e < n) in = rec_pair(rec_await(ends + (int64_t)(k / REC_GROUP - 1) * p.D + c + e)).y;
+    if (first > 0 && e < n) in = rec_pair(rec_await(ends + (int64_t)(group - 1) * p.D + c + e)).y;
     h[e] = rec_apply(r[e], in);
-    if (e < n && last) rec_publish(ends + (int64_t)(k / REC_GROUP) * p.D + c + e, make_float2(-1.f, rec_apply(own[e], h[e])));
+    if (e < n && last) rec_publish(ends + (int64_t)group * p.D + c + e, make_float2(-1.f, rec_apply(own[e], h[e])));
   }
 }
 
@@ -673,7 +678,7 @@ struct RecStepLaunch {
 
 }  // namespace
 
-int64_t rec_words(int nchunk, int D) { return rec_counters(D) + ((int64_t)nchunk + nchunk / REC_GROUP) * D; }
+int64_t rec_words(int nchunk, int D) { return rec_counters(D) + ((int64_t)nchunk + nchunk / REC_GROUP_MIN) * D; }
 static hipError_t rec_run(int dtype, const RecParams& p, bool bwd, hipStream_t st) {
   if (p.words) {
     const int64_t n = rec_words(p.nchunk, p.D);

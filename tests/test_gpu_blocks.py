@@ -372,7 +372,7 @@ def ref_rec(x, g, i, scale, h0, spans):
 REC = [("bf16", None, 1, 1, 5, 1, 1, 0, 1), ("bf16", None, 3, 16, 1, 1, 1, 0, 1), ("f32", [3, 0, 1, 0, 0, 64, 7], 0, 0, 33, 1, 1, 0, 1),
        ("bf16", [0, 0, 5, 128, 127, 129, 1, 1, 1, 0], 0, 0, 130, 1, 0, 1, 1), ("f32", None, 3, 65, 64, 0, 1, 0, 0),
        ("bf16", None, 2, 300, 257, 0, 0, 1, 1), ("f32", None, 1, 257, 129, 1, 1, 0, 0), ("bf16", None, 1, 600, 2, 1, 1, 1, 0),
-       ("f32", [128, 128, 64, 1, 15, 16, 17], 0, 0, 65, 1, 0, 0, 1), ("bf16", [2049, 1], 0, 0, 6, 1, 1, 0, 1)]
+       ("f32", [128, 128, 64, 1, 15, 16, 17], 0, 0, 65, 1, 0, 0, 1), ("bf16", [2049, 1], 0, 0, 6, 1, 1, 0, 1), ("bf16", [1300, 3, 200], 0, 0, 1030, 1, 1, 0, 1)]
 
 
 @pytest.mark.parametrize("dt,lens,B,T,D,scaled,inp,g32,init", REC)
