@@ -12,16 +12,22 @@
 // 16 rows that a fragment read takes at once fall on all 64 banks.
 //
 // The products are formed turned (b's rows are the matrix core's rows), and the four 16-row
-// blocks of a wave's 64 outputs take rows 16 q + 4 j + i of b for block j: a lane then
-// holds 16 outputs side by side, and four lanes a whole line of a row.
+// blocks of a wave's 64 outputs take rows 32 (j / 2) + 8 q + 4 (j % 2) + i of b for block j: a
+// lane (of group q) then holds twice eight outputs side by side, and a store of 16 bytes a
+// lane fills 64 of a row by its four lanes (16 side by side, whose stores lie 32 bytes
+// apart: 8 bits 413 us instead of 403, SiLU with v kept 470 instead of 435).
 //
 // Bound: the matrix cores, and between a tile's main loops its epilogue, which nothing
 // hides (two buffers of a 256 x 256 tile take 128 of 160 KB of LDS: one workgroup a
-// compute unit).  Measured: bf16 8,192^3 809 us (1,360 TFLOP/s; the library's product 1,267
-// on the same card); 16,384 x 2,048 -> 6,144 in 352 us' worth of main loops 392 with SiLU,
-// 470 with v kept in fp32 as well (402 MB more); its dx 331 us, dw 394.  8 bits: 32,768 x
-// 2,048 -> 6,144 382-411 us (2,160-2,010 TFLOP/s; the library 395).  fp32 4,096^3 980 us (140 of
-// the 157 TFLOP/s of its matrix instructions; the library 153).
+// compute unit).  Measured: bf16 8,192^3 808-818 us (1,345-1,360 TFLOP/s; the library's
+// product 1,267 on such a card); 16,384 x 2,048 -> 6,144 with SiLU 386 (1,068; the library
+// without it 349), 435 with v kept in fp32 as well (402 MB more); its dx 331 us, dw 394.  8
+// bits: 32,768 x 2,048 -> 6,144 382-404 us (2,160-2,040 TFLOP/s; the library 395).  fp32 4,096^3
+// 980 us (140 of the 157 TFLOP/s of its matrix instructions; the library 153).  No better:
+// other groups of tile rows (4: 347 instead of 331 in dx, 16: 869 in 8,192^3), a raised
+// priority around the products, the next fragment requested by hand, requests between the
+// products, non-temporal stores (481 instead of 413), a persistent workgroup that requests its
+// next tile's first step with this one's last (its registers spill: 869 in 8,192^3).
 #include "gdn_block.h"
 
 namespace gdn {
@@ -149,30 +155,35 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int N, int
   }
 }
 
-// Sixteen outputs side by side of each of a lane's rows: what belongs to the columns is
-// loaded once, and one branch decides for all sixteen (a tile's epilogue runs while its
-// compute unit's matrix cores wait).
+// Block j's first row of b among a wave's 64, which is its outputs' first column too.
+__device__ __forceinline__ constexpr int blk_b(int j) { return 32 * (j >> 1) + 4 * (j & 1); }
+
+// A lane's sixteen outputs of each of its rows, eight at column n and eight at n + 32:
+// what belongs to the columns is loaded once, and one branch decides for all sixteen (a
+// tile's epilogue runs while its compute unit's matrix cores wait).
 template <class O>
 struct Columns {
   float b[16], ws[16];
-  int n, c;
-  __device__ __forceinline__ Columns(const Epilogue& e, int N, int n_) : n(n_), c(N - n_) {
-    if (c < 16) return;
+  int n;
+  bool whole;  // all sixteen exist
+  static constexpr __device__ __forceinline__ int col(int j) { return j < 8 ? j : j + 24; }
+  __device__ __forceinline__ Columns(const Epilogue& e, int N, int n_) : n(n_), whole(N - n_ >= 40) {
+    if (!whole) return;
 #pragma unroll
     for (int j = 0; j < 16; j += 4) {
       float t[4] = {};
-      if (e.bias) ld_full<4>(static_cast<const O*>(e.bias) + n + j, t);
+      if (e.bias) ld_full<4>(static_cast<const O*>(e.bias) + n + col(j), t);
 #pragma unroll
       for (int i = 0; i < 4; ++i) b[j + i] = t[i];
-      if (e.w_scale) ld_full<4>(e.w_scale + n + j, t);
+      if (e.w_scale) ld_full<4>(e.w_scale + n + col(j), t);
 #pragma unroll
       for (int i = 0; i < 4; ++i) ws[j + i] = t[i];
     }
   }
   __device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int N, const f32x4 (&v)[4]) const {
-    if (c < 16) {
+    if (!whole) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) finish4<O>(e, m, N, n + 4 * j, v[j]);
+      for (int j = 0; j < 4; ++j) finish4<O>(e, m, N, n + blk_b(j), v[j]);
       return;
     }
     float f[16];
@@ -191,7 +202,7 @@ struct Columns {
     if (e.v_save) {
 #pragma unroll
       for (int j = 0; j < 16; j += 4)
-        reinterpret_cast<f32x4_any*>(e.v_save + at)[j / 4] = f32x4{f[j], f[j + 1], f[j + 2], f[j + 3]};
+        *reinterpret_cast<f32x4_any*>(e.v_save + at + col(j)) = f32x4{f[j], f[j + 1], f[j + 2], f[j + 3]};
     }
     float d;
     if (e.act == GDN_ACT_SILU) {
@@ -206,7 +217,7 @@ struct Columns {
 #pragma unroll
       for (int j = 0; j < 16; j += V) {
         float t[V];
-        ld_full<V>(static_cast<const O*>(e.r) + m * e.r_stride + n + j, t);
+        ld_full<V>(static_cast<const O*>(e.r) + m * e.r_stride + n + col(j), t);
 #pragma unroll
         for (int i = 0; i < V; ++i) f[j + i] += t[i];
       }
@@ -216,9 +227,9 @@ struct Columns {
     for (int j = 0; j < 16; j += V) {
       if constexpr (V == 8) {
         const float t[8] = {f[j], f[j + 1], f[j + 2], f[j + 3], f[j + 4], f[j + 5], f[j + 6], f[j + 7]};
-        *reinterpret_cast<bf16x8_any*>(p + j) = VecIO<bf16, 8>::pack(t);
+        *reinterpret_cast<bf16x8_any*>(p + col(j)) = VecIO<bf16, 8>::pack(t);
       } else {
-        *reinterpret_cast<f32x4_any*>(p + j) = f32x4{f[j], f[j + 1], f[j + 2], f[j + 3]};
+        *reinterpret_cast<f32x4_any*>(p + col(j)) = f32x4{f[j], f[j + 1], f[j + 2], f[j + 3]};
       }
     }
   }
@@ -239,7 +250,7 @@ __device__ __forceinline__ void load_lds(u32x4 rsrc, uint32_t off, uint32_t lds)
 __device__ __forceinline__ void lds_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ int swz_a(int row) { return (row >> 1) & 7; }
-__device__ __forceinline__ int swz_b(int row) { return ((row >> 1) & 1) | ((row >> 4) & 3) << 1; }
+__device__ __forceinline__ int swz_b(int row) { return ((row >> 1) & 1) | ((row >> 3) & 3) << 1; }
 
 // BM x BN tile, WM x WN waves, each TM 16-row blocks of a and 64 rows of b.
 template <int T, class O, int BM, int BN, int WM, int WN>
@@ -299,12 +310,12 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmParams p) {
     for (int j = 0; j < NB; ++j) ob[j] += 128;
   };
   const int wm = w / WN, wn = w % WN, q = lane >> 4, r16 = lane & 15;
-  // fragment addresses: a's block i, row 16 i + r16; b's block j, row 16 (r16 / 4) + 4 j + r16 % 4
+  // fragment addresses: a's block i, row 16 i + r16; b's block j, row blk_b(j) + 8 (r16 / 4) + r16 % 4
   const char* fa = smem + (wm * TM * 16 + r16) * 128;
   const int sa = swz_a(r16);  // (the same for every block: they lie 16 rows apart)
-  const int rb0 = 16 * (r16 >> 2) + (r16 & 3);
+  const int rb0 = 8 * (r16 >> 2) + (r16 & 3);
   const char* fb = smem + BM * 128 + (wn * 64 + rb0) * 128;
-  const int sb = swz_b(rb0);  // (4 j leaves it as it is)
+  const int sb = swz_b(rb0);  // (blk_b leaves it as it is)
   f32x4 acc[TM][TN];
 #pragma unroll
   for (int i = 0; i < TM; ++i)
@@ -320,8 +331,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmParams p) {
     Pieces b[TN];
 #pragma unroll
     for (int j = 0; j < TN; ++j) {
-      b[j].lo = *reinterpret_cast<const u32x4*>(pb + j * 512 + ((q ^ sb) << 4));
-      b[j].hi = *reinterpret_cast<const u32x4*>(pb + j * 512 + (((q + 4) ^ sb) << 4));
+      b[j].lo = *reinterpret_cast<const u32x4*>(pb + blk_b(j) * 128 + ((q ^ sb) << 4));
+      b[j].hi = *reinterpret_cast<const u32x4*>(pb + blk_b(j) * 128 + (((q + 4) ^ sb) << 4));
     }
 #pragma unroll
     for (int i = 0; i < TM; ++i) {
@@ -335,7 +346,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmParams p) {
     __syncthreads();
     buf ^= 1;
   }
-  const int n = n0 + wn * 64 + 16 * q;
+  const int n = n0 + wn * 64 + 8 * q;
   if (n >= p.N) return;
   if (p.splits > 1) {
 #pragma unroll
@@ -344,8 +355,8 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmParams p) {
       if (m >= p.M) break;
 #pragma unroll
       for (int j = 0; j < TN; ++j) {
-        float* t = p.part + (split * p.M + m) * p.N + n + 4 * j;
-        const int c = p.N - n - 4 * j;
+        float* t = p.part + (split * p.M + m) * p.N + n + blk_b(j);
+        const int c = p.N - n - blk_b(j);
         if (c >= 4) *reinterpret_cast<f32x4_any*>(t) = acc[i][j];
         else
           for (int x = 0; x < c; ++x) t[x] = acc[i][j][x];
