@@ -55,6 +55,9 @@ __device__ __forceinline__ void ld_part(const E* p, int n, float (&f)[V]) {
     for (int i = 0; i < V; ++i) f[i] = i < n ? to_f(p[i]) : 0.f;
   }
 }
+// Stored past the L2, as outputs that stream through memory (norm forward of 16,384 x
+// 2,304 on an fp32 stream: 76 us, 90 with ordinary stores; of 2,303 channels, whose lines are
+// shared, 77 and 100).
 template <int V, class E>
 __device__ __forceinline__ void st_part(E* p, int n, const float (&f)[V]) {
   if (n >= V) {

@@ -233,6 +233,18 @@ def test_tracers(stub, name):
             torch.jit.trace(f, (x,), check_trace=False)
 
 
+@pytest.mark.parametrize("name", DIFFERENTIABLE)
+def test_one_operation_of_a_jit_trace(stub, name):
+    """A trace holds the operator as one operation, whose replay calls the library."""
+    f, x = entries()[name]
+    with torch.no_grad():
+        t = torch.jit.trace(f, (x,), check_trace=False)
+        n = len(stub)
+        assert n >= 1
+        t(x)
+    assert len(stub) == n + 1
+
+
 @pytest.mark.parametrize("name", list(entries()))
 def test_compiled_functions_leave_their_graph(stub, name):
     f, x = entries()[name]

@@ -134,6 +134,51 @@ def test_norm_only_the_gradients_asked_for():
     assert torch.equal(g, dy)
 
 
+@pytest.mark.parametrize("shape", [(0, 40), (3, 0, 40)])
+def test_norm_without_rows(shape):
+    x, w, r = torch.zeros(shape, device="cuda"), rn(1, 40), torch.zeros(shape, device="cuda")
+    leaves = [t.requires_grad_(True) for t in (x, w, r)]
+    y, s = gdn.add_rms_norm(x, w, r)
+    dx, dw, dr = torch.autograd.grad([y, s], leaves, [torch.zeros_like(y), torch.zeros_like(s)])
+    assert y.shape == s.shape == dx.shape == dr.shape == shape and not dw.any()
+    with torch.no_grad():
+        q, scale, _ = gdn.add_rms_norm_8bit(x, w, r)
+    assert q.shape == shape and scale.shape == shape[:-1]
+
+
+def test_calls_with_more_dimensions():
+    """[..., D] in, [..., N] out, as the same rows flattened."""
+    x, w, r, W = rn(1, 2, 3, 5, 48), rn(2, 48), rn(3, 2, 3, 5, 48), rn(4, 20, 48, std=.2)
+    flat = lambda t: t.reshape(30, -1)
+    for a, b in zip(gdn.add_rms_norm(x, w, r), gdn.add_rms_norm(flat(x), w, flat(r))):
+        assert a.shape == (2, 3, 5, 48) and torch.equal(flat(a), b)
+    q, s = gdn.quantize_rows(x)
+    q2, s2 = gdn.quantize_rows(flat(x))
+    assert s.shape == (2, 3, 5) and torch.equal(flat(q.view(torch.uint8)), q2.view(torch.uint8)) and torch.equal(s.reshape(30), s2)
+    p, t = gdn.quantize_rows(W)
+    y = gdn.linear_8bit(q, s, p, t, out_dtype=torch.float32)
+    assert y.shape == (2, 3, 5, 20) and torch.equal(flat(y), gdn.linear_8bit(q2, s2, p, t, out_dtype=torch.float32))
+    assert torch.equal(flat(gdn.linear(x, W, None, "gelu")), gdn.linear(flat(x), W, None, "gelu"))
+
+
+def test_training_step_by_backward():
+    """.backward() with a summed loss (an expanded gradient), one leaf used twice."""
+    x, w = rn(1, 70, 64, dt=torch.bfloat16).requires_grad_(True), (1 + rn(2, 64, std=.1)).to(torch.bfloat16).requires_grad_(True)
+    W = rn(3, 64, 64, std=.1, dt=torch.bfloat16).requires_grad_(True)
+    y, s = gdn.add_rms_norm(x, w, x)
+    z = gdn.linear(y, W, None, "silu", s)
+    h = gdn.gated_recurrence(z[None], z[None], z[None], scale=ru(4, .1, .2, 64))
+    h.sum().backward()
+    X, w_, W_ = (t.detach().double().requires_grad_(True) for t in (x, w, W))
+    S = 2 * X
+    Y = S / torch.sqrt(S.square().mean(-1, keepdim=True) + 1e-6) * w_
+    v = Y @ W_.t()
+    Z = v * torch.sigmoid(v) + S
+    ref_rec(Z, Z, Z, ru(4, .1, .2, 64).double(), None, [(0, 70)])[0].sum().backward()
+    for a, b in ((x, X), (w, w_), (W, W_)):   # some ten roundings of bf16 along the way, of 1.7e-3 (rms) each
+        assert rms(a.grad, b.grad) <= 3e-2
+
+
 def test_norm_takes_slices_and_leaves_its_inputs():
     wide, wr = rn(1, 33, 500, dt=torch.bfloat16), rn(2, 33, 301)
     x, r, w = wide[:, 3:252], wr[:, 5:254], rn(3, 249, dt=torch.bfloat16)
@@ -303,6 +348,18 @@ def test_linear_takes_slices_and_any_alignment():
                 a = blocks.gdn_linear_bwd(x, w, dy, "silu", v)
                 b = blocks.gdn_linear_bwd(x.contiguous(), w.clone(), dy, "silu", v)
                 assert all(torch.equal(p, q) for p, q in zip(a, b))
+
+
+@pytest.mark.parametrize("act", [None, "gelu"])
+@pytest.mark.parametrize("K", [64, 37])
+def test_linear_only_the_gradients_asked_for(act, K):
+    x, w, b, dy = (rn(k, *s, dt=torch.bfloat16) for k, s in enumerate([(90, K), (50, K), (50,), (90, 50)]))
+    v = blocks.gdn_linear_fwd(x, w, b, act, save=True)[1]
+    full = blocks.gdn_linear_bwd(x, w, dy, act, v)
+    for bits in range(8):
+        need = tuple(bool(bits >> k & 1) for k in range(3))
+        part = blocks.gdn_linear_bwd(x, w, dy, act, v, need=need)
+        assert all((p is None) if not n else torch.equal(p, q) for p, q, n in zip(part, full, need))
 
 
 def test_linear_without_rows():
