@@ -18,7 +18,7 @@ import torch
 from torch.autograd.function import once_differentiable
 
 from . import layers as _layers
-from .binding import GDNError, _compiling, _dtype_code, _outside, _ptr, _vp, lib as _load
+from .binding import GDNError, _check, _compiling, _dtype_code, _outside, _ptr, _vp, lib as _load
 from .layers import (_as_one_op, _call, _no_derivative, _on, _own_lengths, _past_32_bits, _rows, _rows_like, _seqs, _t, _wants_grad, _workspace)
 
 __all__ = ["add_rms_norm", "add_rms_norm_8bit", "quantize_rows", "linear", "linear_8bit", "gated_recurrence", "gdn_rec_step"]
@@ -295,12 +295,18 @@ def _linear_run(a, shape, out_dtype, dev, save):
 
 def gdn_linear_fwd(x, weight, bias=None, activation=None, residual=None, save: bool = False):
     """(y, v) of the projection (see linear): v [..., N] fp32 is the value before the activation,
-    for gdn_linear_bwd, with an activation and save; else None."""
+    for gdn_linear_bwd, with an activation and save; else None.  With save, sizes whose gradient
+    is too large are refused."""
     if _compiling():
         return _outside(gdn_linear_fwd, x, weight, bias, activation, residual, save)
     code = _dtype_code(x)
     a, shape = _linear_args(x, weight, bias, activation, residual, x.dtype)
     a.dtype = a.out_dtype = code
+    if save and (a.M | a.N | a.K) >> 16:  # (below: no gradient is too large)
+        b = LinearBwdArgs(a)
+        with _on(x.device):
+            if lib().gdn_linear_bwd_workspace_size(ctypes.byref(b)) == 0:
+                _check(1)
     return _linear_run(a, shape, x.dtype, x.device, save and activation is not None)
 
 
@@ -355,7 +361,8 @@ def linear(x, weight, bias=None, activation=None, residual=None):
 
     x [..., K], weight [N, K], bias [N], residual [..., N], all of one dtype (bf16 or fp32);
     activation None, "silu" or "gelu" (its tanh form).  Sums are fp32 and y is rounded once.  With
-    an activation a training pass keeps the value before it in fp32 (4 bytes an output)."""
+    an activation a training pass keeps the value before it in fp32 (4 bytes an output).  A
+    training pass takes fewer than 2^22 rows in bf16, 2^21 in fp32."""
     if _compiling():
         return _outside(linear, x, weight, bias, activation, residual)
     if not _wants_grad(x, weight, bias, residual):

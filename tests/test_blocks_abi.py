@@ -291,3 +291,28 @@ def test_python_checks(stub):
         with pytest.raises(GDNError, match=text):
             f()
     assert not stub
+
+
+@pytest.mark.parametrize("M,N,K,dt", [(1 << 22, 3, 1, torch.bfloat16), (1 << 21, 2, 1, torch.float32)])
+@pytest.mark.parametrize("activation", (None, "silu"))
+def test_training_calls_whose_gradient_would_be_refused_are_refused_at_once(stub, monkeypatch, M, N, K, dt, activation):
+    """Rows along which the weight's gradient sums are below 2^23 bytes: a call that asks for one
+    is refused by its forward pass, not later; one without a gradient runs, as do fewer rows."""
+    L, recorded = B.lib(), blocks.lib()
+
+    class Sizes:   # the library's sizes, launches recorded
+        def __getattr__(self, name):
+            if not name.endswith("_size"):
+                return getattr(recorded, name)
+            fn = getattr(L, name)
+            fn.argtypes, fn.restype = [ctypes.POINTER(dict(blocks._SIZES)[name])], ctypes.c_size_t
+            return fn
+    monkeypatch.setattr(blocks, "lib", Sizes)
+    x, w = torch.zeros(M, K, dtype=dt), torch.zeros(N, K, dtype=dt)
+    for leaf in ("x", "w"):
+        with pytest.raises(GDNError, match="too large"):
+            blocks.linear(x.clone().requires_grad_(leaf == "x"), w.clone().requires_grad_(leaf == "w"), None, activation)
+    assert stub == []
+    blocks.linear(x, w, None, activation)
+    blocks.linear(x[:M - 8].clone().requires_grad_(True), w, None, activation)
+    assert stub == ["gdn_linear_fwd"] * 2
