@@ -26,7 +26,8 @@ ARCH = os.environ.get("GDN_OFFLOAD_ARCH", "gfx950")
 
 FLAGS = ["-O3", "-std=c++17", "-fPIC", f"--offload-arch={ARCH}", "-I", INC, "-I", CSRC,
          "-Xclang", "-target-feature", "-Xclang", "-packed-fp32-ops",
-         "-Wno-unused-command-line-argument"]
+         # (registers that inline assembly may not name: "may lead to undefined behaviour")
+         "-Werror=inline-asm", "-Wno-unused-command-line-argument"]
 
 
 # Host-side sanitizers only (the device code is built as always): for CPU runs of

@@ -242,11 +242,15 @@ __device__ __forceinline__ u32x4 make_rsrc(const void* base, uint32_t bytes) {
   return u32x4{(uint32_t)p, (uint32_t)(p >> 32) & 0xffffu, bytes, 0x00027000u};
 }
 // 16 bytes a lane from rsrc + off to LDS at `lds` + 16 * lane; past the buffer's end: zeros.
-// The compiler does not see these loads: what reads their target waits by hand (lds_wait).
+// The compiler does not see these loads: what reads their target waits by hand (lds_wait). It
+// sets m0, an input, itself: m0 is not to be written behind its back. The s_nop is the wait
+// state between that and the load; descriptors_ready() is theirs for the descriptors.
 __device__ __forceinline__ void load_lds(u32x4 rsrc, uint32_t off, uint32_t lds) {
-  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds"
-               :: "s"(lds), "v"(off), "s"(rsrc) : "memory", "m0");
+  asm volatile("s_nop 0\n\tbuffer_load_dwordx4 %1, %2, 0 offen lds" :: "{m0}"(lds), "v"(off), "s"(rsrc) : "memory");
 }
+// A memory access may read scalars that vector instructions wrote (v_readfirstlane) five
+// wait states later.
+__device__ __forceinline__ void descriptors_ready(u32x4 a, u32x4 b) { asm volatile("s_nop 4" :: "s"(a), "s"(b)); }
 __device__ __forceinline__ void lds_wait() { asm volatile("s_waitcnt vmcnt(0)" ::: "memory"); }
 
 __device__ __forceinline__ int swz_a(int row) { return (row >> 1) & 7; }
@@ -321,6 +325,7 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmParams p) {
   for (int i = 0; i < TM; ++i)
 #pragma unroll
     for (int j = 0; j < TN; ++j) acc[i][j] = zero4();
+  descriptors_ready(ra, rb);
   if (k0 < k1) request(k0, 0);
   lds_wait();
   __syncthreads();
