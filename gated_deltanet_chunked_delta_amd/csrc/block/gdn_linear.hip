@@ -113,6 +113,12 @@ __device__ __forceinline__ float act_of(int act, float v, float& d) {
   return v;
 }
 
+// f xs ws of 8-bit rows' sums.  The scales' own product may leave fp32's range where the
+// result does not (7e-22 each: a result of 1e-37 is off by 2^-10 of it), so f comes first: a
+// sum is 0 or between 2^-18 and 2^42 and a scale at least 2^-109, so that f times a scale of 1 at
+// most stays in range, and with xs above 1 f ws leaves it only where the result does too.
+__device__ __forceinline__ float scaled(float f, float xs, float ws) { return xs <= 1.f ? f * xs * ws : f * ws * xs; }
+
 // Four outputs side by side of row m, from column n on (c of them exist).
 template <class O>
 __device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int N, int n, f32x4 v) {
@@ -123,7 +129,7 @@ __device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int N, int
     const float xs = e.x_scale[m];
     ld_part<4>(e.w_scale + n, c, t);
 #pragma unroll
-    for (int i = 0; i < 4; ++i) f[i] *= xs * t[i];
+    for (int i = 0; i < 4; ++i) f[i] = scaled(f[i], xs, t[i]);
   }
   if (e.bias) {
     ld_part<4>(static_cast<const O*>(e.bias) + n, c, t);
@@ -191,8 +197,14 @@ struct Columns {
     for (int j = 0; j < 16; ++j) f[j] = v[j / 4][j % 4];
     if (e.x_scale) {
       const float xs = e.x_scale[m];
+      // (32,768 x 2,048 -> 6,144: 0.7 % more time than the scales' product first; chosen by the entry 1.9 %)
+      if (__all(xs <= 1.f)) {
 #pragma unroll
-      for (int j = 0; j < 16; ++j) f[j] *= xs * ws[j];
+        for (int j = 0; j < 16; ++j) f[j] = f[j] * xs * ws[j];
+      } else {
+#pragma unroll
+        for (int j = 0; j < 16; ++j) f[j] = scaled(f[j], xs, ws[j]);
+      }
     }
     if (e.bias) {
 #pragma unroll
