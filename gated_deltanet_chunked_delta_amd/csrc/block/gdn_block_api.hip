@@ -116,7 +116,8 @@ gdn_status check_linear(const gdn_linear_args& a, bool bwd) {
     return fail(GDN_E_UNSUPPORTED, "out_dtype %d does not go with dtype %d", a.out_dtype, a.dtype);
   if (a.M < 0 || a.N < 1 || a.K < 1) return fail(GDN_E_INVALID, "bad sizes M=%lld N=%d K=%d", (long long)a.M, a.N, a.K);
   if (a.act < GDN_ACT_NONE || a.act > GDN_ACT_GELU) return fail(GDN_E_UNSUPPORTED, "unknown activation %d", a.act);
-  if (a.M >= (1LL << 31) || row16(a.K, a.dtype) >= ROW_BYTES || a.M >= (1LL << 40) / std::max(a.N, a.K) ||
+  constexpr int64_t most = 1LL << 39;  // of a tensor's elements: more than the card's memory in any type
+  if (a.M >= (1LL << 31) || a.N >= (1LL << 31) - 1024 || row16(a.K, a.dtype) >= ROW_BYTES || a.M * a.N >= most || a.M * a.K >= most || (int64_t)a.N * a.K >= most ||
       (bwd && (row16(a.N, a.dtype) >= ROW_BYTES || row16(a.M, a.dtype) >= ROW_BYTES)))
     return fail(GDN_E_INVALID, "problem too large");
   if (!a.w) return fail(GDN_E_INVALID, "null weight");
@@ -128,9 +129,6 @@ gdn_status check_linear(const gdn_linear_args& a, bool bwd) {
   if (!aligned(a.x, es) || !aligned(a.w, es) || !aligned(a.bias, os) || !aligned(a.r, os) || !aligned(a.x_scale, 4) ||
       !aligned(a.w_scale, 4))
     return fail(GDN_E_INVALID, "a pointer is misaligned");
-  // (tiles of 128 x 128 and up to 16 parts of k; the gradients' products too)
-  auto fits = [](double m, double n) { return launchable(256. * 16 * (m / 128 + 2) * (n / 128 + 2)); };
-  if (!fits(a.M, a.N) || (bwd && (!fits(a.M, a.K) || !fits(a.N, a.K)))) return fail(GDN_E_INVALID, "problem too large");
   return GDN_OK;
 }
 // Whether a product can read these rows as they lie.

@@ -281,8 +281,9 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmParams p) {
   // groups of eight tile rows, so that its L2 sees the same rows of a and b again.
   const int tn_n = (p.N + BN - 1) / BN;
   const int64_t tm_n = (p.M + BM - 1) / BM, tiles = tm_n * tn_n;
-  int64_t id = blockIdx.x;
+  int64_t id = block_2d();
   const int split = (int)(id / tiles);
+  if (split >= p.splits) return;
   id -= split * tiles;
   {
     const int64_t per = tiles / 8, more = tiles % 8, die = id % 8;
@@ -425,10 +426,12 @@ __global__ __launch_bounds__(512) void skinny_kernel(SkinnyParams p) {
   constexpr int W = 8;
   __shared__ f32x4 red[W][NT * MT][64];
   const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id()), q = lane >> 4, r16 = lane & 15;
-  const int n0 = blockIdx.x * (16 * NT);
+  const int64_t first = block_2d() * (16 * NT);
+  if (first >= p.N) return;
+  const int n0 = (int)first;
   const char *wr[NT], *xr[MT];
 #pragma unroll
-  for (int j = 0; j < NT; ++j) wr[j] = static_cast<const char*>(p.w) + (int64_t)min(n0 + j * 16 + r16, p.N - 1) * p.w_stride;
+  for (int j = 0; j < NT; ++j) wr[j] = static_cast<const char*>(p.w) + min(first + j * 16 + r16, (int64_t)p.N - 1) * p.w_stride;
 #pragma unroll
   for (int i = 0; i < MT; ++i) xr[i] = static_cast<const char*>(p.x) + (int64_t)min(i * 16 + r16, p.M - 1) * p.x_stride;
   f32x4 acc[NT][MT];
@@ -558,7 +561,7 @@ __global__ __launch_bounds__(256) void pack_bytes_kernel(PackParams p) {
 template <int T, class O>
 hipError_t gemm_any(const GemmParams& p, const GemmPlan& g, hipStream_t st) {
   const int64_t tiles = (p.M + g.tile - 1) / g.tile * ((p.N + g.tile - 1) / g.tile);
-  const dim3 grid((uint32_t)(tiles * g.splits));
+  const dim3 grid = blocks_2d(tiles * g.splits);
   if (g.tile == 256) hipLaunchKernelGGL((gemm_kernel<T, O, 256, 256, 2, 4>), grid, dim3(512), 0, st, p);
   else hipLaunchKernelGGL((gemm_kernel<T, O, 128, 128, 2, 2>), grid, dim3(256), 0, st, p);
   if (hipError_t e = hipGetLastError(); e != hipSuccess || g.splits == 1) return e;
@@ -567,7 +570,7 @@ hipError_t gemm_any(const GemmParams& p, const GemmPlan& g, hipStream_t st) {
 }
 template <int T, class O>
 hipError_t skinny_any(const SkinnyParams& p, hipStream_t st) {
-  auto grid = [&](int nt) { return dim3((p.N + 16 * nt - 1) / (16 * nt)); };
+  auto grid = [&](int nt) { return blocks_2d(((int64_t)p.N + 16 * nt - 1) / (16 * nt)); };
   if (p.M <= 16) hipLaunchKernelGGL((skinny_kernel<T, O, 1, 1>), grid(1), dim3(512), 0, st, p);
   else if (p.M <= 32) hipLaunchKernelGGL((skinny_kernel<T, O, 2, 2>), grid(2), dim3(512), 0, st, p);
   else hipLaunchKernelGGL((skinny_kernel<T, O, 4, 2>), grid(2), dim3(512), 0, st, p);

@@ -71,3 +71,20 @@ def test_scales_whose_product_is_infinite(M):
     q[0, :32] = q[2, 40]
     y = gdn.linear_8bit(q, s, p, t, out_dtype=torch.float32)
     assert bool(y[1].isnan().all()) and not bool(y[:, 3].isfinite().any())
+
+
+# ------------------------------------------------------------------ sizes
+@pytest.mark.parametrize("M,N", [(131077, 131103), ((1 << 30) + 130, 17), (5, (1 << 30) + 71)])
+def test_products_of_1e10_outputs(M, N):
+    """Each of them checked (more than 2^22 workgroups in the last two): small whole numbers, whose
+    products every type holds."""
+    K = 8
+    g = torch.Generator(device="cuda").manual_seed(1)
+    x, w = (torch.randint(-5, 6, (n, K), generator=g, device="cuda", dtype=torch.int8).to(torch.bfloat16) for n in (M, N))
+    y = gdn.linear(x, w)
+    step = max(1, (1 << 29) // N)
+    for m in range(0, M, step):
+        want = torch.zeros_like(y[m:m + step])
+        for k in range(K):          # (whole numbers up to 8 x 25 = 200 fit bf16's 8 bits)
+            want.addcmul_(x[m:m + step, k, None], w[None, :, k])
+        assert torch.equal(y[m:m + step], want), m
