@@ -49,7 +49,8 @@ gdn_status check_rec(const gdn_rec_args& a) {
     return fail(GDN_E_UNSUPPORTED, "g_dtype %d: g is in x's type or fp32", a.g_dtype);
   if (a.B < 1 || a.T < 0 || a.D < 1) return fail(GDN_E_INVALID, "bad sizes B=%d T=%d D=%d", a.B, a.T, a.D);
   const long long tokens = (long long)a.B * a.T;
-  if (tokens >= std::min((1LL << 40) / a.D, (1LL << 31) - 1024) || a.D >= (1 << 24)) return fail(GDN_E_INVALID, "problem too large");
+  if (tokens >= std::min((1LL << 40) / a.D, (1LL << 31) - 1024) || a.num_seqs >= (1LL << 37) / a.D || a.D >= (1 << 24))
+    return fail(GDN_E_INVALID, "problem too large");
   if (a.cu_seqlens) {
     if (a.B != 1) return fail(GDN_E_INVALID, "cu_seqlens requires B == 1 (got %d)", a.B);
     if (a.num_seqs < 1) return fail(GDN_E_INVALID, "num_seqs must be >= 1 with cu_seqlens");
@@ -84,12 +85,6 @@ RecPlan rec_plan(const gdn_rec_args& a, bool bwd, bool own_states) {
   }
   p.total = off;
   return p;
-}
-gdn_status check_rec_grid(const gdn_rec_args& a, const RecPlan& pl) {
-  const double per = 64. * gdn::REC_BYTES / esize(a.dtype);
-  if (!launchable(((double)pl.bwd + a.num_seqs / 64. + 1) * std::ceil(a.D / per) * 64 * gdn::REC_W))
-    return fail(GDN_E_INVALID, "problem too large: %d chunks and %d sequences of %d channels", pl.bwd, a.num_seqs, a.D);
-  return GDN_OK;
 }
 gdn::RecParams rec_params(const gdn_rec_args& a, const RecPlan& pl, int nchunk) {
   gdn::RecParams p{};
@@ -302,7 +297,6 @@ gdn_status gdn_rec_fwd(const gdn_rec_fwd_args* args, void* stream) {
   if (!aligned(args->y, esize(a.dtype)) || !aligned(args->hT, 4) || !aligned(args->h_save, 4))
     return fail(GDN_E_INVALID, "a pointer is misaligned");
   const RecPlan pl = rec_plan(a, false, !args->h_save);
-  if (gdn_status st = check_rec_grid(a, pl); st != GDN_OK) return st;
   if (gdn_status st = check_ws(a.workspace, a.workspace_bytes, pl.total); st != GDN_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   gdn::RecParams p = rec_params(a, pl, pl.fwd);
@@ -324,7 +318,6 @@ gdn_status gdn_rec_bwd(const gdn_rec_bwd_args* args, void* stream) {
       !aligned(args->dscale, 4) || !aligned(args->dh0, 4) || !aligned(args->dhT, 4) || !aligned(args->h_saved, 4))
     return fail(GDN_E_INVALID, "a gradient pointer is misaligned");
   const RecPlan pl = rec_plan(a, true, !args->h_saved);
-  if (gdn_status st = check_rec_grid(a, pl); st != GDN_OK) return st;
   if (gdn_status st = check_ws(a.workspace, a.workspace_bytes, pl.total); st != GDN_OK) return st;
   hipStream_t s = static_cast<hipStream_t>(stream);
   gdn::RecParams p = rec_params(a, pl, pl.bwd);

@@ -173,6 +173,8 @@ __device__ __forceinline__ void rec_st(E* p, int n, const float (&f)[V]) {
 }
 
 // Blocks are numbered channels first over the chunks: neighbours read neighbouring lines.
+// (Fewer than 2^32: 2^40 entries of at least 2,048 a block, or 2^25 chunks.)
+__device__ __forceinline__ uint32_t rec_block() { return (uint32_t)block_2d(); }
 template <int V> __host__ __device__ __forceinline__ uint32_t rec_width(int D) { return ((uint32_t)D + 64 * V - 1) / (64 * V); }
 template <int V>
 __device__ __forceinline__ void rec_vec(const float* base, int64_t row, int D, int c, int n, float (&f)[V]) {
@@ -271,11 +273,11 @@ __device__ __forceinline__ void rec_chain(const RecParams& p, int k, int c, int 
 // waits for nobody, else by its channels' counter.
 template <int V>
 __device__ __forceinline__ int rec_ticket(const RecParams& p) {
-  const uint32_t wide = rec_width<V>(p.D), own = blockIdx.x / wide;
+  const uint32_t wide = rec_width<V>(p.D), own = rec_block() / wide;
   if (!p.words || own >= (uint32_t)p.nchunk) return (int)own;
   __shared__ uint32_t id;
   if (threadIdx.x == 0)
-    id = __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(p.words + blockIdx.x % wide * REC_LINE), 1u, __ATOMIC_RELAXED,
+    id = __hip_atomic_fetch_add(reinterpret_cast<uint32_t*>(p.words + rec_block() % wide * REC_LINE), 1u, __ATOMIC_RELAXED,
                                 __HIP_MEMORY_SCOPE_AGENT);
   __syncthreads();
   return (int)__builtin_amdgcn_readfirstlane(id);
@@ -339,7 +341,7 @@ __global__ __launch_bounds__(64 * REC_W, 4) void rec_fwd_kernel(RecParams p) {
   __shared__ float entering[64 * V];
   const int ch = rec_ticket<V>(p);
   const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
-  const int c = (int)(blockIdx.x % rec_width<V>(p.D) * 64 + lane) * V, n = p.D - c, shift = max(V - n, 0);
+  const int c = (int)(rec_block() % rec_width<V>(p.D) * 64 + lane) * V, n = p.D - c, shift = max(V - n, 0);
   if (ch >= p.nchunk) {
     rec_empty_seqs<V>(p, ch - p.nchunk, p.h0, p.hT, c, n);
     return;
@@ -439,7 +441,7 @@ __global__ __launch_bounds__(64 * REC_W, 4) void rec_bwd_kernel(RecParams p) {
   __shared__ float leaving[64 * V];
   const int k_chain = rec_ticket<V>(p);
   const int lane = lane_id(), w = __builtin_amdgcn_readfirstlane(wave_id());
-  const int c = (int)(blockIdx.x % rec_width<V>(p.D) * 64 + lane) * V, n = p.D - c, shift = max(V - n, 0);
+  const int c = (int)(rec_block() % rec_width<V>(p.D) * 64 + lane) * V, n = p.D - c, shift = max(V - n, 0);
   if (k_chain >= p.nchunk) {
     rec_empty_seqs<V>(p, k_chain - p.nchunk, p.dhT, p.dh0, c, n);
     return;
@@ -661,8 +663,8 @@ struct RecLaunch {
   void operator()() const {
     // (sequences of one length are empty all or none)
     const int more = (bwd ? p.dh0 : p.hT) && (p.cu || p.tokens == 0) ? (p.N + REC_EMPTY - 1) / REC_EMPTY : 0;
-    const dim3 grid(rec_width<V>(p.D) * (uint32_t)(p.nchunk + more));
-    if (grid.x == 0) return;
+    if (p.nchunk + more == 0) return;
+    const dim3 grid = blocks_2d(rec_width<V>(p.D) * (int64_t)(p.nchunk + more));
     if (bwd) hipLaunchKernelGGL((rec_bwd_kernel<E, GT, V, SC, IN>), grid, dim3(64 * REC_W), 0, st, p);
     else hipLaunchKernelGGL((rec_fwd_kernel<E, GT, V, SC, IN>), grid, dim3(64 * REC_W), 0, st, p);
   }

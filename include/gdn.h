@@ -603,7 +603,7 @@ gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* args, void* stream);
  * L <= 0 in the intended domain (scale >= 0); where m_t = 0 (scale 0, or a sigmoid that
  * vanishes) its derivative counts as 0.  cu_seqlens as for the convolution: no host copy is
  * needed, tokens at or past cu_seqlens[N] belong to no sequence and are left as they were.
- * States are fp32.  B * T below 2^31 - 1024. */
+ * States are fp32.  B * T below 2^31 - 1024, B * T * D below 2^40, N * D below 2^37. */
 typedef struct {
   int32_t dtype;               /* of x, i, y (dy, dx, di) */
   int32_t g_dtype;             /* of g (dg): dtype, or GDN_F32 */

@@ -1,4 +1,4 @@
-"""Sizes that the projections take and refuse (C ABI, no GPU: nothing here reaches a launch)."""
+"""Sizes that a block's operators take and refuse (C ABI, no GPU: nothing here reaches a launch)."""
 import ctypes
 
 import pytest
@@ -51,3 +51,27 @@ def test_large_gradients_are_taken(L):
     for kw in (dict(M=131077, N=131103, K=8), dict(M=131077, N=8, K=131104), dict(M=100, N=131103, K=131104)):
         b = blocks.LinearBwdArgs(lin(**kw), None, FAKE, FAKE, FAKE, FAKE)
         assert L.gdn_linear_bwd(ref(b), None) == 3 and L.gdn_linear_bwd_workspace_size(ref(b)) > 0, kw
+
+
+def rec(B_, T, D, N=None, **kw):
+    a = blocks.RecArgs()
+    d = dict(dtype=B.GDN_BF16, g_dtype=B.GDN_BF16, B=B_, T=T, D=D, x=FAKE, x_stride=D, g=FAKE, g_stride=D, num_seqs=N or B_)
+    for k, v in dict(d, **kw).items():
+        setattr(a, k, v)
+    return a
+
+
+@pytest.mark.parametrize("T,D", [((1 << 31) - 1025, 1), (600_000_007, 3), (1 << 20, 1 << 17), (1 << 10, 1 << 23)])
+@pytest.mark.parametrize("dt", [B.GDN_BF16, B.GDN_F32])
+def test_long_recurrences_are_taken(L, T, D, dt):
+    """Below 2^31 - 1024 tokens and 2^40 entries: such a call comes as far as its missing workspace."""
+    a = rec(1, T, D, dtype=dt, g_dtype=dt, cu_seqlens=FAKE)
+    assert L.gdn_rec_fwd(ref(blocks.RecFwdArgs(a, FAKE, FAKE)), None) == 3, L.gdn_last_error()
+    b = blocks.RecBwdArgs(a, None, FAKE, None, FAKE, FAKE)
+    assert L.gdn_rec_bwd(ref(b), None) == 3 and L.gdn_rec_bwd_workspace_size(ref(b)) > 0
+
+
+def test_longer_recurrences_are_refused(L):
+    for a in (rec(1, (1 << 31) - 1024, 1), rec(1, 1 << 23, 1 << 17), rec(1, 8, 1 << 20, N=1 << 17, cu_seqlens=FAKE)):
+        f = blocks.RecFwdArgs(a, FAKE, FAKE)
+        assert L.gdn_rec_fwd(ref(f), None) == 1 and b"too large" in L.gdn_last_error() and L.gdn_rec_fwd_workspace_size(ref(f)) == 0
