@@ -295,15 +295,19 @@ def _linear_run(a, shape, out_dtype, dev, save):
 
 def gdn_linear_fwd(x, weight, bias=None, activation=None, residual=None, save: bool = False):
     """(y, v) of the projection (see linear): v [..., N] fp32 is the value before the activation,
-    for gdn_linear_bwd, with an activation and save; else None.  With save, sizes whose gradient
-    is too large are refused."""
+    for gdn_linear_bwd, with an activation and save; else None."""
     if _compiling():
         return _outside(gdn_linear_fwd, x, weight, bias, activation, residual, save)
+    return _linear_fwd(x, weight, bias, activation, residual, save, False)
+
+
+def _linear_fwd(x, weight, bias, activation, residual, save, train):
+    """gdn_linear_fwd; with train, sizes of which a gradient is too large are refused."""
     code = _dtype_code(x)
     a, shape = _linear_args(x, weight, bias, activation, residual, x.dtype)
     a.dtype = a.out_dtype = code
-    if save and (a.M | a.N | a.K) >> 16:  # (below: no gradient is too large)
-        b = LinearBwdArgs(a)
+    if train and (a.M | a.N | a.K) >> 16:  # (below: no gradient is too large)
+        b = LinearBwdArgs(a, dx=a.x, dw=a.w)  # (its size alone is asked for)
         with _on(x.device):
             if lib().gdn_linear_bwd_workspace_size(ctypes.byref(b)) == 0:
                 _check(1)
@@ -340,7 +344,7 @@ class _Linear(torch.autograd.Function):
     def forward(ctx, x, weight, bias, residual, activation):
         need = ctx.needs_input_grad
         with _as_one_op():
-            y, v = gdn_linear_fwd(x, weight, bias, activation, residual, save=any(need[:3]))
+            y, v = _linear_fwd(x, weight, bias, activation, residual, any(need[:3]), any(need[:3]))
         ctx.save_for_backward(x, weight, v)
         ctx.act = activation
         return y
@@ -362,7 +366,8 @@ def linear(x, weight, bias=None, activation=None, residual=None):
     x [..., K], weight [N, K], bias [N], residual [..., N], all of one dtype (bf16 or fp32);
     activation None, "silu" or "gelu" (its tanh form).  Sums are fp32 and y is rounded once.  With
     an activation a training pass keeps the value before it in fp32 (4 bytes an output).  A
-    training pass takes fewer than 2^22 rows in bf16, 2^21 in fp32."""
+    training pass takes fewer than 2^22 rows in bf16, 2^21 in fp32, along which the weight's
+    gradient sums (gdn_linear_bwd takes more for the other gradients)."""
     if _compiling():
         return _outside(linear, x, weight, bias, activation, residual)
     if not _wants_grad(x, weight, bias, residual):

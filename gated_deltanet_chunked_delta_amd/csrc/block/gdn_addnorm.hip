@@ -362,7 +362,7 @@ template <class E>
 __global__ __launch_bounds__(32 * JOIN_ROWS) void join_parts_kernel(const float* part, int64_t rows, int64_t cols, E* out) {
   __shared__ double red[JOIN_ROWS][33];
   const int cl = threadIdx.x & 31, rl = threadIdx.x >> 5;
-  const int64_t col = blockIdx.x * 32ll + cl;
+  const int64_t col = block_2d() * 32 + cl;
   double s = 0.;
   if (col < cols) {
 #pragma unroll 8
@@ -453,7 +453,7 @@ hipError_t launch_addnorm_bwd(int dtype, int res_dtype, const AddNormParams& p, 
   return res_dtype == GDN_F32 ? an_bwd_any<bf16, float>(p, st) : an_bwd_any<bf16, bf16>(p, st);
 }
 hipError_t launch_join_parts(int dtype, const float* part, int64_t rows, int64_t cols, void* out, hipStream_t st) {
-  const dim3 grid((uint32_t)((cols + 31) / 32));
+  const dim3 grid = blocks_2d((cols + 31) / 32);
   if (dtype == GDN_BF16)
     hipLaunchKernelGGL((join_parts_kernel<bf16>), grid, dim3(32 * JOIN_ROWS), 0, st, part, rows, cols, static_cast<bf16*>(out));
   else

@@ -112,8 +112,7 @@ gdn_status check_linear(const gdn_linear_args& a, bool bwd) {
   if (a.M < 0 || a.N < 1 || a.K < 1) return fail(GDN_E_INVALID, "bad sizes M=%lld N=%d K=%d", (long long)a.M, a.N, a.K);
   if (a.act < GDN_ACT_NONE || a.act > GDN_ACT_GELU) return fail(GDN_E_UNSUPPORTED, "unknown activation %d", a.act);
   constexpr int64_t most = 1LL << 39;  // of a tensor's elements: more than the card's memory in any type
-  if (a.M >= (1LL << 31) || a.N >= (1LL << 31) - 1024 || row16(a.K, a.dtype) >= ROW_BYTES || a.M * a.N >= most || a.M * a.K >= most || (int64_t)a.N * a.K >= most ||
-      (bwd && (row16(a.N, a.dtype) >= ROW_BYTES || row16(a.M, a.dtype) >= ROW_BYTES)))
+  if (a.M >= (1LL << 31) || a.N >= (1LL << 31) - 1024 || row16(a.K, a.dtype) >= ROW_BYTES || a.M * a.N >= most || a.M * a.K >= most || (int64_t)a.N * a.K >= most)
     return fail(GDN_E_INVALID, "problem too large");
   if (!a.w) return fail(GDN_E_INVALID, "null weight");
   if (a.M > 0 && !a.x) return fail(GDN_E_INVALID, "null input x");
@@ -124,6 +123,13 @@ gdn_status check_linear(const gdn_linear_args& a, bool bwd) {
   if (!aligned(a.x, es) || !aligned(a.w, es) || !aligned(a.bias, os) || !aligned(a.r, os) || !aligned(a.x_scale, 4) ||
       !aligned(a.w_scale, 4))
     return fail(GDN_E_INVALID, "a pointer is misaligned");
+  return GDN_OK;
+}
+// dx sums along N, dw along M: those are their operands' rows.
+gdn_status check_linear_bwd(const gdn_linear_bwd_args& b) {
+  if (gdn_status st = check_linear(b.a, true); st != GDN_OK) return st;
+  if ((b.dx && row16(b.a.N, b.a.dtype) >= ROW_BYTES) || (b.dw && row16(b.a.M, b.a.dtype) >= ROW_BYTES))
+    return fail(GDN_E_INVALID, "problem too large");
   return GDN_OK;
 }
 // Whether a product can read these rows as they lie.
@@ -371,7 +377,7 @@ size_t gdn_linear_fwd_workspace_size(const gdn_linear_fwd_args* args) {
 }
 size_t gdn_linear_bwd_workspace_size(const gdn_linear_bwd_args* args) {
   if (!args) { fail(GDN_E_INVALID, "null args"); return 0; }
-  if (check_linear(args->a, true) != GDN_OK) return 0;
+  if (check_linear_bwd(*args) != GDN_OK) return 0;
   return linear_bwd_plan(*args).total;
 }
 
@@ -420,7 +426,7 @@ gdn_status gdn_linear_fwd(const gdn_linear_fwd_args* args, void* stream) {
 gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* args, void* stream) {
   if (!args) return fail(GDN_E_INVALID, "null args");
   const gdn_linear_args& a = args->a;
-  if (gdn_status st = check_linear(a, true); st != GDN_OK) return st;
+  if (gdn_status st = check_linear_bwd(*args); st != GDN_OK) return st;
   if (a.M > 0 && !args->dy) return fail(GDN_E_INVALID, "null gradient pointer");
   if (!args->dx && !args->dw && !args->dbias) return fail(GDN_E_INVALID, "no gradient asked for");
   if (a.act && a.M > 0 && !args->v_saved) return fail(GDN_E_INVALID, "an activation's gradient needs v_saved");

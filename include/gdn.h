@@ -554,8 +554,8 @@ gdn_status gdn_quant_rows(const gdn_quant_args* args, void* stream);
  * (products of bf16 and 8 bits are exact), rounded once into y.  The gradient's dy act'(v)
  * is rounded to dtype before its products (bf16: it is their operand); dbias sums it unrounded.
  * M below 2^31, N below 2^31 - 1024; x, w and y below 2^39 elements; rows of x and w below 2^23
- * bytes.  The gradient also sums along N and M: N and M values of dtype below 2^23 bytes (its
- * workspace query tells before the forward call).
+ * bytes.  dx also sums along N and dw along M: then as many values of dtype are below 2^23 bytes
+ * too (the gradient's workspace query tells before the forward call).
  * The forward call of up to 64 rows takes no workspace. */
 typedef enum { GDN_ACT_NONE = 0, GDN_ACT_SILU = 1, GDN_ACT_GELU = 2 } gdn_act;
 typedef struct {

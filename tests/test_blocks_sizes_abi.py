@@ -53,6 +53,18 @@ def test_large_gradients_are_taken(L):
         assert L.gdn_linear_bwd(ref(b), None) == 3 and L.gdn_linear_bwd_workspace_size(ref(b)) > 0, kw
 
 
+@pytest.mark.parametrize("kw,taken", [
+    (dict(M=1 << 22, N=48, K=32), "xb"), (dict(M=(1 << 22) - 8, N=48, K=32), "xwb"), (dict(M=40, N=1 << 22, K=32), "wb"),
+    (dict(M=1 << 22, N=1 << 16, K=8), "xb"), (dict(M=1 << 21, N=48, K=32, dtype=B.GDN_F32, out_dtype=B.GDN_F32), "xb"),
+    (dict(M=8, N=1 << 30, K=8), "wb"), (dict(M=(1 << 31) - 1, N=8, K=8), "xb")])
+def test_each_gradient_is_refused_for_its_own_sums(L, kw, taken):
+    """dx sums along N, dw along M, the bias's gradient has no product."""
+    for name, field in zip("xwb", ("dx", "dw", "dbias")):
+        b = blocks.LinearBwdArgs(lin(**kw), None, FAKE, **{field: FAKE})
+        status = L.gdn_linear_bwd(ref(b), None)
+        assert status == (3 if name in taken else 1) and (L.gdn_linear_bwd_workspace_size(ref(b)) > 0) == (name in taken), name
+
+
 def rec(B_, T, D, N=None, **kw):
     a = blocks.RecArgs()
     d = dict(dtype=B.GDN_BF16, g_dtype=B.GDN_BF16, B=B_, T=T, D=D, x=FAKE, x_stride=D, g=FAKE, g_stride=D, num_seqs=N or B_)

@@ -21,6 +21,7 @@ def dev():
 
 
 import gated_deltanet_chunked_delta_amd as gdn  # noqa: E402
+from gated_deltanet_chunked_delta_amd import GDNError, blocks  # noqa: E402
 
 
 def rn(seed, *s, std=1.0, dt=torch.float32):
@@ -88,3 +89,35 @@ def test_products_of_1e10_outputs(M, N):
         for k in range(K):          # (whole numbers up to 8 x 25 = 200 fit bf16's 8 bits)
             want.addcmul_(x[m:m + step, k, None], w[None, :, k])
         assert torch.equal(y[m:m + step], want), m
+
+
+@pytest.mark.parametrize("act", [None, "silu"])
+def test_gradients_of_more_rows_than_the_weights_takes(act):
+    """x's and the bias's gradients of 2^22 rows and more, row by row those of the same rows alone;
+    the weight's is refused."""
+    M, K, N = (1 << 22) + 77, 16, 24
+    x, w, dy = rn(1, M, K, dt=torch.bfloat16), rn(2, N, K, dt=torch.bfloat16), rn(3, M, N, dt=torch.bfloat16)
+    v = blocks.gdn_linear_fwd(x, w, None, act, save=True)[1]
+    dx, _, db = blocks.gdn_linear_bwd(x, w, dy, act, v, need=(True, False, True))
+    total = torch.zeros(N, device="cuda", dtype=torch.float64)
+    for m in range(0, M, 1 << 20):
+        s = slice(m, m + (1 << 20))
+        vs = None if v is None else v[s].contiguous()
+        a, _, _ = blocks.gdn_linear_bwd(x[s], w, dy[s], act, vs, need=(True, False, False))
+        assert torch.equal(a, dx[s])
+        sig = None if v is None else torch.sigmoid(v[s].double())
+        total += (dy[s].double() * (1 if v is None else sig + v[s] * sig * (1 - sig))).sum(0)
+    # of terms whose magnitudes add up to at most 1.1 sum |dy|: 90 roundings each, as fp32 sums hold 64 rows
+    within(db, total, 1.1 * dy.double().abs().sum(0), 90)
+    with pytest.raises(GDNError, match="too large"):
+        blocks.gdn_linear_bwd(x, w, dy, act, v)
+
+
+def test_bias_gradient_of_very_wide_rows():
+    """2^28 outputs and more, past one dimension of the joining launch: sums of a few whole numbers."""
+    N = (1 << 28) + 45
+    x, w = torch.ones(3, 1, device="cuda", dtype=torch.bfloat16), torch.zeros(N, 1, device="cuda", dtype=torch.bfloat16)
+    dy = torch.randint(-9, 10, (3, N), device="cuda", dtype=torch.int8).to(torch.bfloat16)
+    _, dw, db = blocks.gdn_linear_bwd(x, w, dy, need=(False, True, True))
+    want = (dy[0] + dy[1]) + dy[2]
+    assert torch.equal(db, want) and torch.equal(dw[:, 0], want)
