@@ -199,10 +199,12 @@ gdn_status run_pack(int dtype, const gdn::PackJobs& jobs, hipStream_t s) {
   hipError_t e = timed("linear_pack", s, [&] { return gdn::launch_pack(dtype, jobs, s); });
   return e == hipSuccess ? GDN_OK : hip_fail(e, "row copy launch");
 }
-gdn_status run_gemm(const char* name, int dtype, int out_dtype, gdn::GemmParams p, const gdn::GemmPlan& g, hipStream_t s) {
+// A product's names among the timed kernels, by its tiles.
+struct GemmName { const char *large, *small; };
+gdn_status run_gemm(GemmName name, int dtype, int out_dtype, gdn::GemmParams p, const gdn::GemmPlan& g, hipStream_t s) {
   p.splits = g.splits;
   p.steps = g.steps;
-  hipError_t e = timed(name, s, [&] { return gdn::launch_gemm(dtype, out_dtype, p, g, s); });
+  hipError_t e = timed(g.tile == 256 ? name.large : name.small, s, [&] { return gdn::launch_gemm(dtype, out_dtype, p, g, s); });
   return e == hipSuccess ? GDN_OK : hip_fail(e, "product launch");
 }
 
@@ -420,7 +422,7 @@ gdn_status gdn_linear_fwd(const gdn_linear_fwd_args* args, void* stream) {
     p.b = at<char>(a.workspace, pl.o_w);
     p.ldb = row;
   }
-  return run_gemm("linear_fwd", a.dtype, a.out_dtype, p, pl.g, s);
+  return run_gemm({"linear_fwd_256", "linear_fwd_128"}, a.dtype, a.out_dtype, p, pl.g, s);
 }
 
 gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* args, void* stream) {
@@ -472,7 +474,7 @@ gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* args, void* stream) {
     p.M = a.M; p.N = a.K; p.kbytes = (int)rn;
     p.e = gdn::Epilogue{};
     p.e.out = args->dx;
-    if (gdn_status st = run_gemm("linear_dx", a.dtype, a.dtype, p, pl.gx, s); st != GDN_OK) return st;
+    if (gdn_status st = run_gemm({"linear_dx_256", "linear_dx_128"}, a.dtype, a.dtype, p, pl.gx, s); st != GDN_OK) return st;
   }
   if (args->dw) {
     if (x_late && a.M > 0) {
@@ -484,7 +486,7 @@ gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* args, void* stream) {
     p.M = a.N; p.N = a.K; p.kbytes = (int)rm;
     p.e = gdn::Epilogue{};
     p.e.out = args->dw;
-    if (gdn_status st = run_gemm("linear_dw", a.dtype, a.dtype, p, pl.gw, s); st != GDN_OK) return st;
+    if (gdn_status st = run_gemm({"linear_dw_256", "linear_dw_128"}, a.dtype, a.dtype, p, pl.gw, s); st != GDN_OK) return st;
   }
   return GDN_OK;
 }
