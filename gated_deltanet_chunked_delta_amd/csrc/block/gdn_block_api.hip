@@ -448,8 +448,14 @@ gdn_status gdn_linear_bwd(const gdn_linear_bwd_args* args, void* stream) {
   if (pl.pre) { k.rows = at<char>(ws, pl.o_pre); k.ldo = rn / es; }
   if (args->dw) { k.cols = at<char>(ws, pl.o_pre_t); k.ldt = rm / es; }
   if (args->dbias) k.sums = at<float>(ws, pl.o_sums);
-  // x's copy of 34 MB in one launch with the others saves 3 us; one of 67 MB, made after dx, 22
-  const bool x_late = args->dx && (double)a.K * rm > 48e6;
+  // One launch for all copies, or x's own right before dw's product, its reader: made earlier it
+  // leaves the 256 MB cache in front of the memory, as the sizes where this turns suggest, once the
+  // turned copies of x and dy with dx's product between them fill enough of it.  Late against
+  // early (us, bf16): copies of 67 + 67 MB 317, 310 (16,384 x 2,048 -> 2,048) and 228, 218 (32,768 x
+  // 1,024 -> 1,024); 34 + 101 MB 418, 416; 101 + 50 MB 703, 731 (6,144 x 8,192 -> 4,096); 50 + 134 MB
+  // 513, 510; 67 + 201 MB 832, 855 (16,384 x 2,048 -> 6,144); 134 + 134 MB 944, 983 (16,384 x 4,096
+  // -> 4,096) and 418, 414 (65,536 x 1,024 -> 1,024).
+  const bool x_late = args->dx && ((double)a.K + a.N) * rm > 144e6;
   gdn::PackJobs jobs{};
   if (a.M > 0) {
     if (k.rows || k.cols || k.sums) jobs.job[jobs.n++] = k;

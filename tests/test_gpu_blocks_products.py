@@ -199,6 +199,16 @@ def test_every_output_of_many_ragged_tiles(M, K, N, dt, act, tile):
     within(grads[2], dv.sum(0), (dv.abs() * 90 + dd).sum(0), 1)
 
 
+@pytest.mark.parametrize("M,K,N,launches", [(32768, 1024, 1024, 1), (16384, 2048, 2048, 1), (6144, 8192, 4096, 2)])
+def test_when_the_gradient_copies_x(M, K, N, launches):
+    """With the other copies, or after the product of dx where the copies are large: the same gradients."""
+    x, w, dy = rn(1, M, K, dt=torch.bfloat16), rn(2, N, K, dt=torch.bfloat16), rn(3, M, N, dt=torch.bfloat16)
+    (dx, dw, _), names = kernels(lambda: blocks.gdn_linear_bwd(x, w, dy, need=(True, True, False)))
+    assert names["linear_pack"] == launches
+    assert torch.equal(dx, blocks.gdn_linear_bwd(x, w, dy, need=(True, False, False))[0])
+    assert torch.equal(dw, blocks.gdn_linear_bwd(x, w, dy, need=(False, True, False))[1])
+
+
 @pytest.mark.parametrize("out", ["bf16", "f32"])
 @pytest.mark.parametrize("M,K,N,tile", [(16301, 2041, 6131, 256), (16304, 2064, 6136, 256), (3001, 522, 2100, 128), (300, 8190, 300, 128)])
 def test_every_8bit_output_of_many_ragged_tiles(M, K, N, tile, out):
