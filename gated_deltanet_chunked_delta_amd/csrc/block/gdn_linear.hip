@@ -28,6 +28,8 @@
 // priority around the products, the next fragment requested by hand, requests between the
 // products, non-temporal stores (481 instead of 413), a persistent workgroup that requests its
 // next tile's first step with this one's last (its registers spill: 869 in 8,192^3).
+#include <utility>
+
 #include "gdn_block.h"
 
 namespace gdn {
@@ -119,13 +121,13 @@ __device__ __forceinline__ float act_of(int act, float v, float& d) {
 // most stays in range, and with xs above 1 f ws leaves it only where the result does too.
 __device__ __forceinline__ float scaled(float f, float xs, float ws) { return xs <= 1.f ? f * xs * ws : f * ws * xs; }
 
-// Four outputs side by side of row m, from column n on (c of them exist).
-template <class O>
+// Four outputs side by side of row m, from column n on (c of them exist).  Q: there may be scales
+template <class O, bool Q = true>
 __device__ __forceinline__ void finish4(const Epilogue& e, int64_t m, int N, int n, f32x4 v) {
   const int c = N - n;
   if (c <= 0) return;
   float f[4] = {v[0], v[1], v[2], v[3]}, t[4];
-  if (e.x_scale) {
+  if (Q && e.x_scale) {
     const float xs = e.x_scale[m];
     ld_part<4>(e.w_scale + n, c, t);
 #pragma unroll
@@ -167,7 +169,7 @@ __device__ __forceinline__ constexpr int blk_b(int j) { return 32 * (j >> 1) + 4
 // A lane's sixteen outputs of each of its rows, eight at column n and eight at n + 32:
 // what belongs to the columns is loaded once, and one branch decides for all sixteen (a
 // tile's epilogue runs while its compute unit's matrix cores wait).
-template <class O>
+template <class O, bool Q>
 struct Columns {
   float b[16], ws[16];
   int n;
@@ -181,30 +183,26 @@ struct Columns {
       if (e.bias) ld_full<4>(static_cast<const O*>(e.bias) + n + col(j), t);
 #pragma unroll
       for (int i = 0; i < 4; ++i) b[j + i] = t[i];
-      if (e.w_scale) ld_full<4>(e.w_scale + n + col(j), t);
+      if (Q) ld_full<4>(e.w_scale + n + col(j), t);
 #pragma unroll
       for (int i = 0; i < 4; ++i) ws[j + i] = t[i];
     }
   }
   __device__ __forceinline__ void finish(const Epilogue& e, int64_t m, int N, const f32x4 (&v)[4]) const {
-    if (!whole) {
+    // (the branch for scales above 1, which are rare, is a wave's: one for every entry took 1.9 % of
+    // 32,768 x 2,048 -> 6,144 in 8 bits)
+    const float xs = Q ? e.x_scale[m] : 1.f;
+    if (!whole || (Q && !__all(xs <= 1.f))) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) finish4<O>(e, m, N, n + blk_b(j), v[j]);
+      for (int j = 0; j < 4; ++j) finish4<O, Q>(e, m, N, n + blk_b(j), v[j]);
       return;
     }
     float f[16];
 #pragma unroll
     for (int j = 0; j < 16; ++j) f[j] = v[j / 4][j % 4];
-    if (e.x_scale) {
-      const float xs = e.x_scale[m];
-      // (32,768 x 2,048 -> 6,144: 0.7 % more time than the scales' product first; chosen by the entry 1.9 %)
-      if (__all(xs <= 1.f)) {
+    if (Q) {
 #pragma unroll
-        for (int j = 0; j < 16; ++j) f[j] = f[j] * xs * ws[j];
-      } else {
-#pragma unroll
-        for (int j = 0; j < 16; ++j) f[j] = scaled(f[j], xs, ws[j]);
-      }
+      for (int j = 0; j < 16; ++j) f[j] = f[j] * xs * ws[j];
     }
     if (e.bias) {
 #pragma unroll
@@ -267,6 +265,13 @@ __device__ __forceinline__ void lds_wait() { asm volatile("s_waitcnt vmcnt(0)" :
 
 __device__ __forceinline__ int swz_a(int row) { return (row >> 1) & 7; }
 __device__ __forceinline__ int swz_b(int row) { return ((row >> 1) & 1) | ((row >> 3) & 3) << 1; }
+
+// f(0) .. f(N - 1), each with its number as a constant: past a size of its body a loop is not
+// unrolled, and the accumulators that it indexes lie in memory (fp32 4,096^3: 1,670 us, not 980).
+template <int... I, class F>
+__device__ __forceinline__ void each_of(std::integer_sequence<int, I...>, F f) { (f(std::integral_constant<int, I>{}), ...); }
+template <int N, class F>
+__device__ __forceinline__ void each(F f) { each_of(std::make_integer_sequence<int, N>{}, f); }
 
 // BM x BN tile, WM x WN waves, each TM 16-row blocks of a and 64 rows of b.
 template <int T, class O, int BM, int BN, int WM, int WN>
@@ -382,13 +387,11 @@ __global__ __launch_bounds__(64 * WM * WN) void gemm_kernel(GemmParams p) {
     }
     return;
   }
-  const Columns<O> cols(p.e, p.N, n);
-#pragma unroll
-  for (int i = 0; i < TM; ++i) {
+  const Columns<O, T == GDN_E4M3> cols(p.e, p.N, n);
+  each<TM>([&](auto i) {
     const int64_t m = m0 + (wm * TM + i) * 16 + r16;
-    if (m >= p.M) break;
-    cols.finish(p.e, m, p.N, acc[i]);
-  }
+    if (m < p.M) cols.finish(p.e, m, p.N, acc[i]);
+  });
 }
 
 // The splits' sums, in order, and the epilogue: four outputs a thread.
