@@ -235,8 +235,8 @@ __global__ __launch_bounds__(AN_NT) void addnorm_fwd_long_kernel(AddNormParams p
 }
 
 // Gradient.  p.blocks workgroups walk the rows, each thread always on the same
-// columns, and keep dw in registers: at most ADDNORM_ROWS rows a thread and fp32 sum;
-// the parts are joined in 64 bits (join_parts_kernel).
+// columns, and keep dw in registers: at most ADDNORM_ROWS rows a thread.  A workgroup's threads
+// of one column are added in fp32, the workgroups' parts in 64 bits (join_parts_kernel).
 template <class E, class RT, int TPR, int NV>
 __global__ __launch_bounds__(AN_NT) void addnorm_bwd_kernel(AddNormParams p) {
   constexpr int V = kAV<E>, RPB = AN_NT / TPR;

@@ -21,11 +21,6 @@ typedef bf16x8 bf16x8_any __attribute__((aligned(2)));
 typedef bf16x4 bf16x4_any __attribute__((aligned(2)));
 typedef f32x4 f32x4_any __attribute__((aligned(4)));
 
-typedef __attribute__((__vector_size__(2 * sizeof(__bf16)))) __bf16 bf16x2;
-typedef bf16x2 bf16x2_any __attribute__((aligned(2)));
-typedef __attribute__((__vector_size__(2 * sizeof(float)))) float f32x2;
-typedef f32x2 f32x2_any __attribute__((aligned(4)));
-
 template <int V> __device__ __forceinline__ void ld_full(const bf16* p, float (&f)[V]) {
   if constexpr (V == 8) {
     const bf16x8 v = *reinterpret_cast<const bf16x8_any*>(p);
@@ -109,7 +104,9 @@ struct AddNormParams {
   float* part;               // [blocks][D]
   int blocks;
 };
-// One fp32 sum takes at most these many rows' terms of the weight's gradient.
+// A thread sums at most these many rows' terms of the weight's gradient in fp32; the sums of a
+// workgroup's threads of one column (2 to 16 with short rows) are added in fp32 too, the
+// workgroups' in 64 bits.
 constexpr int ADDNORM_ROWS = 64;
 // Workgroups (rows of parts) of the gradient.
 int addnorm_blocks(int64_t R, int D, int esize, int cus);
@@ -195,7 +192,8 @@ struct GemmPlan { int tile, splits, steps; };
 GemmPlan gemm_plan(int64_t M, int N, int64_t kbytes, int esize, int cus);
 inline size_t gemm_part_bytes(const GemmPlan& g, int64_t M, int N) { return g.splits > 1 ? 4ull * g.splits * M * N : 0; }
 hipError_t launch_gemm(int dtype, int out_dtype, const GemmParams& p, const GemmPlan& g, hipStream_t st);
-// Few rows: a workgroup to 16 outputs, its waves along k.  Any strides and alignment.
+// Few rows: a workgroup to 16 outputs (32 from 17 rows on), its waves along k.  Any strides and
+// alignment.
 constexpr int SKINNY_M = 64;
 struct SkinnyParams {
   const void* x;

@@ -19,15 +19,17 @@
 //
 // Bound: the matrix cores, and between a tile's main loops its epilogue, which nothing
 // hides (two buffers of a 256 x 256 tile take 128 of 160 KB of LDS: one workgroup a
-// compute unit).  Measured: bf16 8,192^3 808-818 us (1,345-1,360 TFLOP/s; the library's
-// product 1,267 on such a card); 16,384 x 2,048 -> 6,144 with SiLU 386 (1,068; the library
-// without it 349), 435 with v kept in fp32 as well (402 MB more); its dx 331 us, dw 394.  8
-// bits: 32,768 x 2,048 -> 6,144 382-404 us (2,160-2,040 TFLOP/s; the library 395).  fp32 4,096^3
-// 980 us (140 of the 157 TFLOP/s of its matrix instructions; the library 153).  No better:
-// other groups of tile rows (4: 347 instead of 331 in dx, 16: 869 in 8,192^3), a raised
-// priority around the products, the next fragment requested by hand, requests between the
-// products, non-temporal stores (481 instead of 413), a persistent workgroup that requests its
-// next tile's first step with this one's last (its registers spill: 869 in 8,192^3).
+// compute unit).  Measured: bf16 8,192^3 806-833 us (1,365-1,320 TFLOP/s; the library's
+// product 1,267 on such a card); 16,384 x 2,048 -> 6,144 with SiLU 355-399 (1,160-1,030; the
+// library without it 349), 432-449 with v kept in fp32 as well (402 MB more), its dx 324-339, its
+// dw 391-410.  8 bits: 32,768 x 2,048 -> 6,144 382-412 us (2,160-2,000 TFLOP/s; the library 395),
+// to fp32 (bf16 products) 658-670.  fp32 4,096^3 967-987 us (142-139 of the 157 TFLOP/s of its
+// matrix instructions; the library 153).  Sums stay in the matrix cores' fp32: those of 2^20 like
+// terms come out within 2e-6 (rms), of few rows within 7e-6.  No better: other groups of tile rows (4: 347 instead of 331
+// in dx, 16: 869 in 8,192^3), a raised priority around the products, the next fragment requested
+// by hand, requests between the products, non-temporal stores (481 instead of 413), a persistent
+// workgroup that requests its next tile's first step with this one's last (its registers spill:
+// 869 in 8,192^3).
 #include <utility>
 
 #include "gdn_block.h"

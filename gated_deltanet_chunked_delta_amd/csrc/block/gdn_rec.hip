@@ -27,12 +27,14 @@
 // The gradient's chain runs the other way with pairs of its own: in token order its U is
 // the sum of dy_t times the decays up to t, cut off at the first sequence's end.
 //
-// Measured (bf16, scale and i): 65,536 tokens of 2,048 channels in 320 us (1.07 GB, 3.4
-// TB/s; three kernels that read the inputs twice: 950), its gradient in 551 (1.88 GB, 3.4
-// TB/s); 16,384 of 2,304 in 91 and 155 us.  Four bytes of a row a thread and 16 (gradient: 8)
-// tokens, eight waves (groups of 16 in all of these: 326, 580): with eight bytes and half the tokens 413 and 1,075 us (the gradient's
-// registers spill); 8 tokens forwards 342; the gradient with 4 tokens 792, with chunks of
-// four or two waves 611 and 801.  A gradient that keeps its inputs' products too spills: 697.
+// Measured (bf16, scale and i): 65,536 tokens of 2,048 channels in 299-320 us (1.07 GB, 3.6-3.4
+// TB/s; three kernels that read the inputs twice: 950), its gradient in 545-556 (1.88 GB, 3.4
+// TB/s); 16,384 of 2,304 in 87-93 and 150-156 us.  fp32, one channel a thread: 420 and 752 us (2.15
+// and 3.76 GB, 5.1 and 5.0 TB/s), 16,384 of 2,304 121 and 218.  Four bytes of a row a thread and 16
+// (gradient: 8) tokens, eight waves (groups of 16 in all of these: 326, 580): with eight bytes and
+// half the tokens 413 and 1,075 us (the gradient's registers spill); 8 tokens forwards 342; the
+// gradient with 4 tokens 792, with chunks of four or two waves 611 and 801.  A gradient that
+// keeps its inputs' products too spills: 697.
 #include "gdn_block.h"
 
 namespace gdn {

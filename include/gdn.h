@@ -495,7 +495,8 @@ gdn_status gdn_norm_bwd(const gdn_norm_bwd_args* args, void* stream);
  *     s = x + r  (rounded to r's type; x itself without r),   y = s / sqrt(mean(s^2) + eps) w
  * The norm reads s as it is stored, so that the backward pass and whatever reads
  * the stream later see the same values.  r is in x's type or fp32.  Either y or
- * (q, q_scale) is written.  R below 2^31. */
+ * (q, q_scale) is written.  Sums are fp32: where that of s^2 is past its range (entries of
+ * 1e19 / sqrt(D) and more) y is 0.  R below 2^31. */
 typedef struct {
   int32_t dtype;               /* of x, w, y (dy, dx, dw) */
   int32_t res_dtype;           /* of r and s (ds, dr): GDN_F32 or dtype; dtype without r */
@@ -551,7 +552,7 @@ gdn_status gdn_quant_rows(const gdn_quant_args* args, void* stream);
  * act: none, SiLU, or GELU in its tanh form, v sigmoid(2 sqrt(2 / pi) (v + 0.044715 v^3)).
  * With GDN_E4M3, x and w are 8-bit rows as gdn_quant_rows makes them (a scale a token,
  * a scale an output), bias, r and y in out_dtype, and no gradient exists.  Sums are fp32
- * (products of bf16 and 8 bits are exact), rounded once into y.  The gradient's dy act'(v)
+ * (products of bf16 and 8 bits are exact; 8 bits to bf16: sums of about 17 bits), rounded once into y.  The gradient's dy act'(v)
  * is rounded to dtype before its products (bf16: it is their operand); dbias sums it unrounded.
  * M below 2^31, N below 2^31 - 1024; x, w and y below 2^39 elements; rows of x and w below 2^23
  * bytes.  dx also sums along N and dw along M: then as many values of dtype are below 2^23 bytes
