@@ -307,7 +307,7 @@ def _linear_fwd(x, weight, bias, activation, residual, save, train):
     a, shape = _linear_args(x, weight, bias, activation, residual, x.dtype)
     a.dtype = a.out_dtype = code
     if train and (a.M | a.N | a.K) >> 16:  # (below: no gradient is too large)
-        b = LinearBwdArgs(a, dx=a.x, dw=a.w)  # (its size alone is asked for)
+        b = LinearBwdArgs(a, dx=1, dw=1)  # (its size alone is asked for; without rows x is null)
         with _on(x.device):
             if lib().gdn_linear_bwd_workspace_size(ctypes.byref(b)) == 0:
                 _check(1)

@@ -2,9 +2,10 @@
 import ctypes
 
 import pytest
+import torch
 
+from gated_deltanet_chunked_delta_amd import GDNError, blocks, layers
 from gated_deltanet_chunked_delta_amd import binding as B
-from gated_deltanet_chunked_delta_amd import blocks
 
 FAKE = 1 << 20  # a 16-byte aligned fake device address; never dereferenced
 ref = ctypes.byref
@@ -63,6 +64,16 @@ def test_each_gradient_is_refused_for_its_own_sums(L, kw, taken):
         b = blocks.LinearBwdArgs(lin(**kw), None, FAKE, **{field: FAKE})
         status = L.gdn_linear_bwd(ref(b), None)
         assert status == (3 if name in taken else 1) and (L.gdn_linear_bwd_workspace_size(ref(b)) > 0) == (name in taken), name
+
+
+@pytest.mark.parametrize("M,N", [(0, 1 << 22), (3, 1 << 22), (1 << 22, 2)])
+def test_training_calls_are_refused_by_their_forward_pass(monkeypatch, M, N):
+    """Whatever the rows, none among them: not later, by the gradient."""
+    monkeypatch.setattr(layers, "_on_gpu", lambda name, t: t.device)
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: None)
+    x, w = torch.zeros(M, 1, dtype=torch.bfloat16), torch.zeros(N, 1, dtype=torch.bfloat16, requires_grad=True)
+    with pytest.raises(GDNError, match="too large"):
+        blocks.linear(x, w)
 
 
 def rec(B_, T, D, N=None, **kw):
