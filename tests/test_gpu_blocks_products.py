@@ -76,6 +76,35 @@ def test_scales_whose_product_is_infinite(M):
     assert bool(y[1].isnan().all()) and not bool(y[:, 3].isfinite().any())
 
 
+# ------------------------------------------------------------------ values that are not finite
+@pytest.mark.parametrize("out", ["bf16", "f32"])
+@pytest.mark.parametrize("M", [5, 70, 700])
+def test_8bit_rows_that_are_not_finite_stay_rows(M, out):
+    """Rows and weights that hold an infinity or a NaN (NaN in 8 bits): their outputs, and no others."""
+    out = DT[out]
+    x, w = rn(1, M, 200), rn(2, 330, 200)
+    clean = gdn.linear_8bit(*rows8(x)[:2], *rows8(w)[:2], out_dtype=out)
+    x[1, 3], x[4, 199], w[7, 0], w[329, 130] = float("inf"), float("nan"), float("nan"), -float("inf")
+    y = gdn.linear_8bit(*rows8(x)[:2], *rows8(w)[:2], out_dtype=out)
+    bad = torch.zeros_like(y, dtype=torch.bool)
+    bad[[1, 4]] = True
+    bad[:, [7, 329]] = True
+    assert bool(y[bad].isnan().all()) and torch.equal(y[~bad], clean[~bad])
+
+
+@pytest.mark.parametrize("M", [5, 70, 700])
+def test_fp32_rows_that_are_not_finite_stay_rows(M):
+    x, w, dy = rn(1, M, 72), rn(2, 330, 72), rn(3, M, 330)
+    clean, cx = gdn.linear(x, w), blocks.gdn_linear_bwd(x, w, dy, need=(True, False, False))[0]
+    x[1, 71], x[4, 0] = float("inf"), float("nan")
+    dy[2, 329] = float("nan")
+    y, dx = gdn.linear(x, w), blocks.gdn_linear_bwd(x, w, dy, need=(True, False, False))[0]
+    rest = [m for m in range(M) if m not in (1, 4)]
+    assert not bool(y[[1, 4]].isfinite().any()) and torch.equal(y[rest], clean[rest])
+    rest = [m for m in range(M) if m != 2]
+    assert bool(dx[2].isnan().all()) and torch.equal(dx[rest], cx[rest])
+
+
 # ------------------------------------------------------------------ sizes
 @pytest.mark.parametrize("M,N", [(131077, 131103), ((1 << 30) + 130, 17), (5, (1 << 30) + 71)])
 def test_products_of_1e10_outputs(M, N):
